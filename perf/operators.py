@@ -241,13 +241,6 @@ def _empty_q4(NB, Hk, B, D):
 
 
 # ------------------------------------------------------------------------------- the library's calls
-def _kept(st, name, make):
-    """What a program makes once and keeps: a workspace, a plan, an output buffer."""
-    if name not in st:
-        st[name] = make()
-    return st[name]
-
-
 def _rope_args(case):
     more = {"none": {}, "linear": {"factor": 4.0}, "base": {"factor": 4.0},
             "bands": {"factor": 8.0, "low_freq_factor": 1.0, "high_freq_factor": 4.0, "original_len": 8192},
@@ -255,52 +248,58 @@ def _rope_args(case):
     return {"rotary_dim": case["rd"], "base": case["base"], "layout": case["layout"], "scaling": case["scaling"], **more}
 
 
-def _own(st):
+def _calls(st):
+    """The library's calls of one pass, prepared as a serving loop prepares them, and their outputs."""
     from paged_kv_cache_47_gb300 import binding as b
 
     case = st["case"]
     kind = case["kind"]
+    i32 = functools.partial(torch.empty, dtype=torch.int32, device="cuda")
     if kind == "tables":
         S = case["S"]
-        i32 = functools.partial(torch.empty, dtype=torch.int32, device="cuda")
-        mid, last, freed, left = _kept(st, "after", lambda: (i32(S), i32(S), i32(1), i32(1)))
-        slots, pos, offs = _kept(st, "plan", lambda: (torch.empty(st["max_tokens"], dtype=torch.int64, device="cuda"),
-                                                      i32(st["max_tokens"]), i32(S + 1)))
-        ws = _kept(st, "ws", b.alloc_tables_workspace)
-        b.tables_release(st["tables"], st["lens"], st["done"], st["free"], st["num_free"], case["B"], workspace=ws,
-                         context_lens_out=mid, num_free_out=freed)
-        b.tables_append(st["tables"], mid, st["add"], st["free"], freed, case["B"], slots, pos, offs, workspace=ws,
-                        context_lens_out=last, num_free_out=left)
-        return {"tables": st["tables"], "free": st["free"], "lens": last, "num_free": left, "slots": slots,
-                "positions": pos, "offsets": offs}
+        mid, last, freed, left = i32(S), i32(S), i32(1), i32(1)
+        slots = torch.empty(st["max_tokens"], dtype=torch.int64, device="cuda")
+        pos, offs = i32(st["max_tokens"]), i32(S + 1)
+        ws = b.alloc_tables_workspace()
+        calls = (b.prepared_tables_release(st["tables"], st["lens"], st["done"], st["free"], st["num_free"], case["B"],
+                                           workspace=ws, context_lens_out=mid, num_free_out=freed),
+                 b.prepared_tables_append(st["tables"], mid, st["add"], st["free"], freed, case["B"], slots, pos, offs,
+                                          workspace=ws, context_lens_out=last, num_free_out=left))
+        return calls, {"tables": st["tables"], "free": st["free"], "lens": last, "num_free": left, "slots": slots,
+                       "positions": pos, "offsets": offs}
     if kind == "rope":
-        plan = _kept(st, "rope", lambda: b.RopePlan(**_rope_args(case)))
-        b.rope_append(st["q"], st["k"], st["v"], st["pos"], st["slots"], plan, st["k_pool"], st["v_pool"],
-                      q_out=st["q_out"])
-        return {"q": st["q_out"], "k_pool": st["k_pool"], "v_pool": st["v_pool"]}
+        plan = b.RopePlan(**_rope_args(case))
+        call = b.prepared_rope_append(st["q"], st["k"], st["v"], st["pos"], st["slots"], plan, st["k_pool"],
+                                      st["v_pool"], q_out=st["q_out"])
+        return (call,), {"q": st["q_out"], "k_pool": st["k_pool"], "v_pool": st["v_pool"]}
     if kind == "sparse":
-        W = case["top"] + case["first"] + case["last"]
-        sel = _kept(st, "sel", lambda: (torch.empty(case["S"], case["Hk"], W, dtype=torch.int32, device="cuda"),
-                                        torch.empty(case["S"], case["Hk"], dtype=torch.int32, device="cuda")))
-        ws = _kept(st, "ws", lambda: b.alloc_sparse_workspace(st["k_pool"], case["S"], case["Hq"],
-                                                              st["tables"].shape[1]))
-        out = _kept(st, "out", lambda: torch.empty_like(st["q"]))
-        b.block_means(st["slots"], st["k_pool"], st["k_means"])
-        b.decode_attention_sparse(st["q"], st["k_pool"], st["v_pool"], st["k_means"], st["tables"], st["lens"],
-                                  st["scale"], top_blocks=case["top"], first_blocks=case["first"],
-                                  last_blocks=case["last"], out=out, sel_tables=sel[0], sel_lens=sel[1], workspace=ws)
-        return {"out": out, "sel_tables": sel[0], "sel_lens": sel[1], "k_means": st["k_means"]}
-    cache = _kept(st, "cache", lambda: b.Q4Cache(st["k_codes"], st["v_codes"], st["k_params"], st["v_params"],
-                                                 DT[case["dt"]]))
+        sel = i32(case["S"], case["Hk"], case["top"] + case["first"] + case["last"]), i32(case["S"], case["Hk"])
+        ws = b.alloc_sparse_workspace(st["k_pool"], case["S"], case["Hq"], st["tables"].shape[1])
+        out = torch.empty_like(st["q"])
+        calls = (b.prepared_block_means(st["slots"], st["k_pool"], st["k_means"]),
+                 b.prepared_decode_attention_sparse(
+                     st["q"], st["k_pool"], st["v_pool"], st["k_means"], st["tables"], st["lens"], st["scale"],
+                     top_blocks=case["top"], first_blocks=case["first"], last_blocks=case["last"], out=out,
+                     sel_tables=sel[0], sel_lens=sel[1], workspace=ws))
+        return calls, {"out": out, "sel_tables": sel[0], "sel_lens": sel[1], "k_means": st["k_means"]}
+    cache = b.Q4Cache(st["k_codes"], st["v_codes"], st["k_params"], st["v_params"], DT[case["dt"]])
     if kind == "store":
-        k, v = _kept(st, "out", lambda: (torch.empty_like(st["k"]), torch.empty_like(st["v"])))
-        b.append_q4(st["k"], st["v"], st["slots"], cache)
-        b.gather_q4(st["slots"], cache, k, v)
-        return {"k": k, "v": v}
-    ws = _kept(st, "ws", lambda: b.alloc_q4_workspace(cache, case["Hq"]))
-    out = _kept(st, "out", lambda: torch.empty_like(st["q"]))
-    b.decode_attention_q4(st["q"], cache, st["tables"], st["lens"], st["scale"], out=out, workspace=ws)
-    return {"out": out}
+        k, v = torch.empty_like(st["k"]), torch.empty_like(st["v"])
+        calls = (b.prepared_append_q4(st["k"], st["v"], st["slots"], cache),
+                 b.prepared_gather_q4(st["slots"], cache, k, v))
+        return calls, {"k": k, "v": v}
+    out = torch.empty_like(st["q"])
+    call = b.prepared_decode_attention_q4(st["q"], cache, st["tables"], st["lens"], st["scale"], out=out,
+                                          workspace=b.alloc_q4_workspace(cache, case["Hq"]))
+    return (call,), {"out": out}
+
+
+def _own(st):
+    if "calls" not in st:       # what a program makes once and keeps: plans, workspaces, outputs, arguments
+        st["calls"] = _calls(st)
+    calls, outputs = st["calls"]
+    [call() for call in calls]
+    return outputs
 
 
 # -------------------------------------------------------------------------------------- plain forms
