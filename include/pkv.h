@@ -75,6 +75,8 @@ typedef enum {
 #define PKV_DEVERR_CONTEXT    0x2u  /* a context length < 0 or > max_blocks*block_size */
 #define PKV_DEVERR_TIMEOUT    0x4u  /* an on-chip barrier wait ran out of time */
 #define PKV_DEVERR_SLOT       0x8u  /* an append slot outside the pool */
+#define PKV_DEVERR_NO_BLOCKS  0x10u /* device tables: not enough free blocks (pkv_tables.h) */
+#define PKV_DEVERR_TOKENS     0x20u /* device tables: a bad or too large token count */
 
 /* Shape of one paged K/V pool pair. */
 typedef struct {

@@ -22,6 +22,7 @@ CODE_DTYPE = {v: k for k, v in DTYPE_CODE.items()}
 STATUS = {0: "PKV_OK", -1: "PKV_ERR_INVALID_ARG", -2: "PKV_ERR_UNSUPPORTED", -3: "PKV_ERR_CUDA",
           -4: "PKV_ERR_OUT_OF_RANGE", -5: "PKV_ERR_TIMEOUT", -6: "PKV_ERR_WORKSPACE"}
 DEVERR_BLOCK_ID, DEVERR_CONTEXT, DEVERR_TIMEOUT, DEVERR_SLOT = 0x1, 0x2, 0x4, 0x8
+DEVERR_NO_BLOCKS, DEVERR_TOKENS = 0x10, 0x20
 
 
 class CacheDesc(ctypes.Structure):
@@ -942,3 +943,553 @@ class PreparedDecodePrefix:
             opts.timing_events[i] = None if ev is None else ev.cuda_event
         _check(self._fn(*self._args, _stream(stream), ctypes.byref(opts)))
         return self.out
+
+
+# ------------------------------------------------------------- device block tables
+TABLES_WORKSPACE_BYTES = 64
+
+
+def _ops_lib():
+    """libpkv with the signatures of pkv_tables.h, pkv_rope.h, pkv_q4.h and pkv_sparse.h."""
+    L = lib()
+    if not getattr(L, "_ops_ready", False):
+        vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
+                                 ctypes.c_size_t)
+        dp, q4, pools = (ctypes.POINTER(CacheDesc), ctypes.POINTER(Q4CacheDesc),
+                         ctypes.POINTER(Q4Pools))
+        plan, sel = ctypes.POINTER(_RopePlan), ctypes.POINTER(SparseSelect)
+        for name, args in {
+            "pkv_tables_append": [i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp,
+                                  vp, vp],
+            "pkv_tables_release": [i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp],
+            "pkv_rope_plan_init": [ctypes.POINTER(RopeDesc), plan],
+            "pkv_rope": [i32, i32, plan, vp, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp],
+            "pkv_rope_append": [dp, plan, vp, vp, i32, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp,
+                                vp, vp],
+            "pkv_append_q4": [q4, vp, vp, vp, i32, pools, vp],
+            "pkv_gather_q4": [q4, pools, vp, i32, vp, vp, i32, vp],
+            "pkv_decode_attention_q4": [q4, vp, i32, i32, pools, vp, i32, vp, f32, vp, i32, vp, sz,
+                                        vp, ctypes.POINTER(DecodeOptions)],
+            "pkv_block_copy_q4": [q4, vp, i32, pools, vp],
+            "pkv_block_means": [dp, vp, i32, vp, vp, vp],
+            "pkv_select_blocks": [dp, vp, i32, i32, vp, vp, i32, vp, sel, vp, vp, vp, sz, vp],
+            "pkv_decode_attention_sparse": [dp, vp, i32, i32, vp, vp, vp, vp, i32, vp, f32, sel, vp,
+                                            vp, vp, i32, vp, sz, vp],
+        }.items():
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = i32
+        for name, args in {
+            "pkv_decode_q4_workspace_bytes": [q4, i32, i32],
+            "pkv_select_workspace_bytes": [dp, i32, i32],
+            "pkv_decode_sparse_workspace_bytes": [dp, i32, i32, i32],
+        }.items():
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = sz
+        L._ops_ready = True
+    return L
+
+
+class PreparedCall:
+    """A call whose arguments are checked and marshalled once, for repeated steps on stable
+    buffers (the usual serving loop, and CUDA-graph capture): each call only passes the stream
+    (None: the current one) and returns `out`. The buffers are kept alive by this object and
+    rewritten in place by the caller between steps."""
+
+    def __init__(self, name: str, args, keep, out=None, after=()):
+        self._fn = getattr(_ops_lib(), name)
+        devices = {t.device for t in keep if isinstance(t, torch.Tensor)}
+        for c in keep:
+            if isinstance(c, Q4Cache):
+                devices |= {t.device for t in (c.k_codes, c.v_codes, c.k_params, c.v_params)}
+        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+            raise ValueError(f"{name}: the tensors are not on one GPU ({sorted(map(str, devices))})")
+        self._device = next(iter(devices)).index
+        # plain numbers become ctypes objects once, not at each call
+        kinds = self._fn.argtypes
+        self._args = tuple(k(a) if a is None or isinstance(a, (int, float)) else a
+                           for k, a in zip(kinds, args))
+        self._after, self._keep, self.out = tuple(after), keep, out
+
+    def __call__(self, stream=None):
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device)
+        if torch.cuda.current_device() != self._device:
+            with torch.cuda.device(self._device):
+                _check(self._fn(*self._args, _stream(stream), *self._after))
+        else:
+            _check(self._fn(*self._args, _stream(stream), *self._after))
+        return self.out
+
+
+def _need(t: torch.Tensor, name: str, dtype, shape=None) -> torch.Tensor:
+    """`t`, which has to be contiguous, of this dtype and (None: any) shape."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return t
+
+
+def alloc_tables_workspace(device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of tables_append / tables_release; one for calls that may overlap."""
+    return torch.zeros(TABLES_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def _tables_state(block_tables, context_lens, free_blocks, num_free, context_lens_out, num_free_out):
+    S, M = block_tables.shape
+    i32 = torch.int32
+    _need(block_tables, "block_tables", i32)
+    _need(context_lens, "context_lens", i32, (S,))
+    _need(free_blocks, "free_blocks", i32)
+    _need(num_free, "num_free", i32, (1,))
+    lens_out = context_lens if context_lens_out is None else context_lens_out
+    free_out = num_free if num_free_out is None else num_free_out
+    _need(lens_out, "context_lens_out", i32, (S,))
+    _need(free_out, "num_free_out", i32, (1,))
+    return S, M, free_blocks.numel(), lens_out, free_out
+
+
+def prepared_tables_append(block_tables, context_lens, new_tokens, free_blocks, num_free,
+                           block_size: int, slot_mapping, positions, token_offsets, workspace,
+                           context_lens_out: Optional[torch.Tensor] = None,
+                           num_free_out: Optional[torch.Tensor] = None) -> PreparedCall:
+    """tables_append as a PreparedCall."""
+    S, M, NB, lens_out, free_out = _tables_state(block_tables, context_lens, free_blocks, num_free,
+                                                 context_lens_out, num_free_out)
+    _need(new_tokens, "new_tokens", torch.int32, (S,))
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    n = slot_mapping.numel()
+    _need(positions, "positions", torch.int32, (n,))
+    _need(token_offsets, "token_offsets", torch.int32, (S + 1,))
+    if workspace.numel() * workspace.element_size() < TABLES_WORKSPACE_BYTES:
+        raise ValueError("workspace is too small")
+    return PreparedCall("pkv_tables_append", (
+        NB, block_size, S, _ptr(new_tokens), _ptr(block_tables), M, _ptr(context_lens), _ptr(lens_out),
+        _ptr(free_blocks), _ptr(num_free), _ptr(free_out), _ptr(slot_mapping), _ptr(positions), n,
+        _ptr(token_offsets), _ptr(workspace)),
+        keep=(block_tables, context_lens, new_tokens, free_blocks, num_free, lens_out, free_out,
+              slot_mapping, positions, token_offsets, workspace),
+        out=(slot_mapping, positions, token_offsets))
+
+
+def tables_append(block_tables, context_lens, new_tokens, free_blocks, num_free, block_size: int,
+                  slot_mapping, positions, token_offsets, workspace,
+                  context_lens_out: Optional[torch.Tensor] = None,
+                  num_free_out: Optional[torch.Tensor] = None, stream=None):
+    """Blocks and slots of one step's new tokens, on the device (pkv_tables_append): fills
+    slot_mapping / positions [max_tokens] and token_offsets [S + 1], writes the new blocks
+    into block_tables [S][M], and updates the lengths and the free count (in place unless
+    the *_out tensors are given). free_blocks [num_blocks] is the stack of free blocks.
+    Returns the three outputs."""
+    return prepared_tables_append(block_tables, context_lens, new_tokens, free_blocks, num_free,
+                                  block_size, slot_mapping, positions, token_offsets, workspace,
+                                  context_lens_out, num_free_out)(stream)
+
+
+def prepared_tables_release(block_tables, context_lens, released, free_blocks, num_free,
+                            block_size: int, workspace,
+                            context_lens_out: Optional[torch.Tensor] = None,
+                            num_free_out: Optional[torch.Tensor] = None) -> PreparedCall:
+    """tables_release as a PreparedCall."""
+    S, M, NB, lens_out, free_out = _tables_state(block_tables, context_lens, free_blocks, num_free,
+                                                 context_lens_out, num_free_out)
+    _need(released, "released", torch.bool if released.dtype == torch.bool else torch.uint8, (S,))
+    if workspace.numel() * workspace.element_size() < TABLES_WORKSPACE_BYTES:
+        raise ValueError("workspace is too small")
+    return PreparedCall("pkv_tables_release", (
+        NB, block_size, S, _ptr(released), _ptr(block_tables), M, _ptr(context_lens), _ptr(lens_out),
+        _ptr(free_blocks), _ptr(num_free), _ptr(free_out), _ptr(workspace)),
+        keep=(block_tables, context_lens, released, free_blocks, num_free, lens_out, free_out, workspace),
+        out=None)
+
+
+def tables_release(block_tables, context_lens, released, free_blocks, num_free, block_size: int,
+                   workspace, context_lens_out: Optional[torch.Tensor] = None,
+                   num_free_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Push the blocks of the requests with released[s] (bool or uint8 [S]) onto the stack of
+    free blocks and set their lengths to 0 (pkv_tables_release)."""
+    return prepared_tables_release(block_tables, context_lens, released, free_blocks, num_free,
+                                   block_size, workspace, context_lens_out, num_free_out)(stream)
+
+
+# ------------------------------------------------------------------ rotary positions
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4}
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_len", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low_freq_factor", ctypes.c_double), ("high_freq_factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attention_factor", ctypes.c_double)]
+
+
+class _RopePlan(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
+
+
+class RopePlan:
+    """Frequencies of a rotary embedding, made once (pkv_rope_plan_init). layout: "half" or
+    "interleaved"; scaling: "none", "linear", "base", "bands" or "yarn" (include/pkv_rope.h)."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, layout: str = "half",
+                 scaling: str = "none", factor: float = 1.0, original_len: int = 0,
+                 low_freq_factor: float = 1.0, high_freq_factor: float = 4.0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, attention_factor: float = 0.0):
+        desc = RopeDesc(rotary_dim, ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], original_len, base, factor,
+                        low_freq_factor, high_freq_factor, beta_fast, beta_slow, attention_factor)
+        self.c = _RopePlan()
+        _check(_ops_lib().pkv_rope_plan_init(ctypes.byref(desc), ctypes.byref(self.c)))
+
+
+def _heads(t: torch.Tensor, name: str, dtype=None, rows=None):
+    """(heads, token stride) of a [T][H][D] tensor whose heads are contiguous."""
+    if t.dim() != 3 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]) or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens][heads][head_dim] with each token's heads contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if rows is not None and t.shape[0] != rows:
+        raise ValueError(f"{name} has {t.shape[0]} tokens, not {rows}")
+    # the stride of a single token says nothing
+    return t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def prepared_rope(q, k, positions, plan: RopePlan, q_out: Optional[torch.Tensor] = None,
+                  k_out: Optional[torch.Tensor] = None) -> PreparedCall:
+    """rope as a PreparedCall."""
+    T, _, D = q.shape
+    (Hq, qs), (Hk, ks) = _heads(q, "q"), _heads(k, "k", q.dtype, T)
+    if k.shape[2] != D:
+        raise ValueError("q and k differ in head_dim")
+    q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(T, Hk, D, dtype=q.dtype, device=q.device) if k_out is None else k_out
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out have the shapes of q and k")
+    (_, qos), (_, kos) = _heads(q_out, "q_out", q.dtype, T), _heads(k_out, "k_out", q.dtype, T)
+    _need(positions, "positions", torch.int32, (T,))
+    return PreparedCall("pkv_rope", (
+        DTYPE_CODE[q.dtype], D, ctypes.byref(plan.c), _ptr(positions), T, _ptr(q), qs,
+                               Hq, _ptr(q_out), qos, _ptr(k), ks, Hk, _ptr(k_out), kos),
+        keep=(q, k, positions, plan, q_out, k_out),
+        out=(q_out, k_out))
+
+
+def rope(q, k, positions, plan: RopePlan, q_out: Optional[torch.Tensor] = None,
+         k_out: Optional[torch.Tensor] = None, stream=None):
+    """q [T][Hq][D] and k [T][Hk][D] (token-strided views allowed) turned to their positions
+    (int32 [T]); into new tensors unless q_out / k_out are given (q and k themselves allowed)."""
+    return prepared_rope(q, k, positions, plan, q_out, k_out)(stream)
+
+
+def prepared_rope_append(q, k_new, v_new, positions, slot_mapping, plan: RopePlan, k_pool, v_pool,
+                         q_out: Optional[torch.Tensor] = None) -> PreparedCall:
+    """rope_append as a PreparedCall."""
+    desc = _pools(k_pool, v_pool)
+    T, _, D = q.shape
+    dt = k_pool.dtype
+    (Hq, qs), (Hk, ks), (Hv, vs) = _heads(q, "q", dt), _heads(k_new, "k_new", dt, T), _heads(v_new, "v_new", dt, T)
+    if Hk != desc.num_kv_heads or Hv != Hk or not D == k_new.shape[2] == v_new.shape[2] == desc.head_dim:
+        raise ValueError("q, k_new or v_new do not fit the pools")
+    q_out = torch.empty(T, Hq, D, dtype=dt, device=q.device) if q_out is None else q_out
+    if q_out.shape != q.shape:
+        raise ValueError("q_out has the shape of q")
+    _, qos = _heads(q_out, "q_out", dt, T)
+    _need(positions, "positions", torch.int32, (T,))
+    _need(slot_mapping, "slot_mapping", torch.int64, (T,))
+    return PreparedCall("pkv_rope_append", (
+        ctypes.byref(desc), ctypes.byref(plan.c), _ptr(positions), _ptr(slot_mapping), T, _ptr(q), qs, Hq,
+        _ptr(q_out), qos, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(k_pool), _ptr(v_pool)),
+        keep=(q, k_new, v_new, positions, slot_mapping, plan, k_pool, v_pool, q_out, desc),
+        out=q_out)
+
+
+def rope_append(q, k_new, v_new, positions, slot_mapping, plan: RopePlan, k_pool, v_pool,
+                q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """rope and append in one launch (pkv_rope_append): returns the turned q; the turned k and
+    v go to slot_mapping [T] (int64). q, k_new, v_new: [T][heads][D], token-strided views allowed."""
+    return prepared_rope_append(q, k_new, v_new, positions, slot_mapping, plan, k_pool, v_pool,
+                                q_out)(stream)
+
+
+# --------------------------------------------------------------------- 4-bit KV cache
+class Q4CacheDesc(ctypes.Structure):
+    _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32)]
+
+
+class Q4Pools(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_params", ctypes.c_void_p), ("v_params", ctypes.c_void_p)]
+
+
+class Q4Cache:
+    """A 4-bit K/V cache (include/pkv_q4.h): code pools [NB][Hk][B][D/2] uint8, K parameters
+    [NB][Hk][B][2 NG] and V parameters [NB][Hk][2 NG][B] fp16, NG = D / 32."""
+
+    def __init__(self, k_codes, v_codes, k_params, v_params, act_dtype: torch.dtype):
+        NB, Hk, B, half = k_codes.shape
+        NG = half // 16
+        _need(k_codes, "k_codes", torch.uint8)
+        _need(v_codes, "v_codes", torch.uint8, k_codes.shape)
+        _need(k_params, "k_params", torch.float16, (NB, Hk, B, 2 * NG))
+        _need(v_params, "v_params", torch.float16, (NB, Hk, 2 * NG, B))
+        self.k_codes, self.v_codes, self.k_params, self.v_params = k_codes, v_codes, k_params, v_params
+        self.act_dtype = act_dtype
+        self.desc = Q4CacheDesc(NB, B, Hk, 2 * half, DTYPE_CODE[act_dtype])
+        self.pools = Q4Pools(k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(),
+                             v_params.data_ptr())
+
+    @classmethod
+    def empty(cls, num_blocks, num_kv_heads, block_size, head_dim, act_dtype=torch.bfloat16,
+              device="cuda") -> "Q4Cache":
+        NG = head_dim // 32
+        codes = [torch.zeros(num_blocks, num_kv_heads, block_size, head_dim // 2, dtype=torch.uint8,
+                             device=device) for _ in range(2)]
+        return cls(*codes, torch.zeros(num_blocks, num_kv_heads, block_size, 2 * NG, dtype=torch.float16,
+                                       device=device),
+                   torch.zeros(num_blocks, num_kv_heads, 2 * NG, block_size, dtype=torch.float16,
+                               device=device), act_dtype)
+
+    def head_view(self) -> "Q4Cache":
+        """The same memory as a pool of one-head blocks [NB * Hk][1], for the tables of select_blocks."""
+        NB, Hk = self.k_codes.shape[:2]
+        return Q4Cache(*(t.view(NB * Hk, 1, *t.shape[2:]) for t in
+                         (self.k_codes, self.v_codes, self.k_params, self.v_params)), self.act_dtype)
+
+
+def prepared_append_q4(k_new, v_new, slot_mapping, cache: Q4Cache) -> PreparedCall:
+    """append_q4 as a PreparedCall."""
+    d = cache.desc
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    shape = (slot_mapping.numel(), d.num_kv_heads, d.head_dim)
+    _need(k_new, "k_new", cache.act_dtype, shape)
+    _need(v_new, "v_new", cache.act_dtype, shape)
+    return PreparedCall("pkv_append_q4", (
+        ctypes.byref(d), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), shape[0],
+                                    ctypes.byref(cache.pools)),
+        keep=(k_new, v_new, slot_mapping, cache),
+        out=None)
+
+
+def append_q4(k_new, v_new, slot_mapping, cache: Q4Cache, stream=None) -> None:
+    """Quantize k_new/v_new [T][Hk][D] into the cache at slot_mapping [T] (int64)."""
+    return prepared_append_q4(k_new, v_new, slot_mapping, cache)(stream)
+
+
+def prepared_gather_q4(slot_mapping, cache: Q4Cache, k_out: Optional[torch.Tensor] = None,
+                       v_out: Optional[torch.Tensor] = None,
+                       out_dtype: Optional[torch.dtype] = None) -> PreparedCall:
+    """gather_q4 as a PreparedCall."""
+    d = cache.desc
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    shape = (slot_mapping.numel(), d.num_kv_heads, d.head_dim)
+    dt = k_out.dtype if k_out is not None else out_dtype or cache.act_dtype
+    k_out = torch.empty(shape, dtype=dt, device=cache.k_codes.device) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=dt, device=cache.k_codes.device) if v_out is None else v_out
+    _need(k_out, "k_out", dt, shape)
+    _need(v_out, "v_out", dt, shape)
+    return PreparedCall("pkv_gather_q4", (
+        ctypes.byref(d), ctypes.byref(cache.pools), _ptr(slot_mapping), shape[0],
+                                    _ptr(k_out), _ptr(v_out), DTYPE_CODE[dt]),
+        keep=(slot_mapping, cache, k_out, v_out),
+        out=(k_out, v_out))
+
+
+def gather_q4(slot_mapping, cache: Q4Cache, k_out: Optional[torch.Tensor] = None,
+              v_out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, stream=None):
+    """The cached rows at slot_mapping [T] as values: (k, v) [T][Hk][D]."""
+    return prepared_gather_q4(slot_mapping, cache, k_out, v_out, out_dtype)(stream)
+
+
+def q4_workspace_bytes(cache: Q4Cache, num_q_heads: int, num_ctas: int = 0) -> int:
+    return int(_ops_lib().pkv_decode_q4_workspace_bytes(ctypes.byref(cache.desc), num_q_heads, num_ctas))
+
+
+def alloc_q4_workspace(cache: Q4Cache, num_q_heads: int, num_ctas: int = 0) -> torch.Tensor:
+    """Zero-filled workspace of decode_attention_q4 (every call leaves its counters zero)."""
+    n = q4_workspace_bytes(cache, num_q_heads, num_ctas)
+    if n == 0:
+        raise PkvError(-1, "workspace size query failed")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k_codes.device)
+
+
+def prepared_decode_attention_q4(q, cache: Q4Cache, block_tables, context_lens, scale: float,
+                                 out: Optional[torch.Tensor] = None,
+                                 out_dtype: Optional[torch.dtype] = None,
+                                 workspace: Optional[torch.Tensor] = None, num_ctas: int = 0,
+                                 lse_out: Optional[torch.Tensor] = None,
+                                 tables_ready: bool = False,
+                                 timing_events: Optional[Sequence] = None) -> PreparedCall:
+    """decode_attention_q4 as a PreparedCall."""
+    d = cache.desc
+    S, Hq, D = q.shape
+    _need(q, "q", cache.act_dtype, (S, Hq, d.head_dim))
+    _need(block_tables, "block_tables", torch.int32, (S, block_tables.shape[-1]))
+    _need(context_lens, "context_lens", torch.int32, (S,))
+    if out is None:
+        out = torch.empty(S, Hq, D, dtype=out_dtype or q.dtype, device=q.device)
+    _need(out, "out", out.dtype, q.shape)
+    if workspace is None:
+        workspace = alloc_q4_workspace(cache, Hq, num_ctas)
+    opts = DecodeOptions()
+    opts.num_ctas = num_ctas
+    opts.tables_ready = int(tables_ready)
+    if timing_events is not None:
+        for i, ev in enumerate(timing_events):
+            opts.timing_events[i] = None if ev is None else ev.cuda_event
+    if lse_out is not None:
+        opts.lse_out = _need(lse_out, "lse_out", torch.float32, (S, Hq)).data_ptr()
+    return PreparedCall("pkv_decode_attention_q4", (
+        ctypes.byref(d), _ptr(q), S, Hq, ctypes.byref(cache.pools), _ptr(block_tables), block_tables.shape[1],
+        _ptr(context_lens), float(scale), _ptr(out), DTYPE_CODE[out.dtype], _ptr(workspace),
+        workspace.numel() * workspace.element_size()),
+        keep=(q, cache, block_tables, context_lens, out, workspace, lse_out, opts),
+        out=out, after=(ctypes.byref(opts),))
+
+
+def decode_attention_q4(q, cache: Q4Cache, block_tables, context_lens, scale: float,
+                        out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                        workspace: Optional[torch.Tensor] = None, num_ctas: int = 0, stream=None,
+                        lse_out: Optional[torch.Tensor] = None, tables_ready: bool = False,
+                        timing_events: Optional[Sequence] = None) -> torch.Tensor:
+    """decode_attention over a 4-bit cache; q [S][Hq][D] in the cache's activation dtype."""
+    return prepared_decode_attention_q4(q, cache, block_tables, context_lens, scale, out, out_dtype,
+                                        workspace, num_ctas, lse_out, tables_ready, timing_events)(stream)
+
+
+def block_copy_q4(pairs, cache: Q4Cache, stream=None) -> None:
+    """Copy whole blocks src -> dst of a 4-bit cache; pairs is host data [n][2]."""
+    p = torch.as_tensor(pairs, dtype=torch.int64).reshape(-1, 2).contiguous()
+    assert p.device.type == "cpu", "block-copy pairs are host memory"
+    _check(_ops_lib().pkv_block_copy_q4(ctypes.byref(cache.desc), _ptr(p), p.shape[0],
+                                        ctypes.byref(cache.pools), _stream(stream)))
+
+
+# ---------------------------------------------------------------- block-sparse decode
+class SparseSelect(ctypes.Structure):
+    _fields_ = [("top_blocks", ctypes.c_int32), ("first_blocks", ctypes.c_int32),
+                ("last_blocks", ctypes.c_int32)]
+
+
+def _means_desc(k_pool, k_means) -> CacheDesc:
+    desc = cache_desc(k_pool)
+    _need(k_pool, "k_pool", k_pool.dtype)
+    _need(k_means, "k_means", k_pool.dtype, (desc.num_blocks, desc.num_kv_heads, desc.head_dim))
+    return desc
+
+
+def prepared_block_means(slot_mapping, k_pool, k_means) -> PreparedCall:
+    """block_means as a PreparedCall."""
+    desc = _means_desc(k_pool, k_means)
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    return PreparedCall("pkv_block_means", (
+        ctypes.byref(desc), _ptr(slot_mapping), slot_mapping.numel(),
+                                      _ptr(k_pool), _ptr(k_means)),
+        keep=(slot_mapping, k_pool, k_means, desc),
+        out=None)
+
+
+def block_means(slot_mapping, k_pool, k_means, stream=None) -> None:
+    """Mean keys, into k_means [NB][Hk][D], of the blocks that the tokens at slot_mapping [T]
+    (int64) have filled (pkv_block_means); after the append of those tokens."""
+    return prepared_block_means(slot_mapping, k_pool, k_means)(stream)
+
+
+def _selection(q, desc, block_tables, context_lens, select, sel_tables, sel_lens):
+    S, Hq, _ = q.shape
+    W = select.top_blocks + select.first_blocks + select.last_blocks
+    _need(q, "q", CODE_DTYPE[desc.dtype], (S, Hq, desc.head_dim))
+    _need(block_tables, "block_tables", torch.int32, (S, block_tables.shape[-1]))
+    _need(context_lens, "context_lens", torch.int32, (S,))
+    i32 = dict(dtype=torch.int32, device=q.device)
+    shape = (S, desc.num_kv_heads, max(0, W))
+    sel_tables = torch.empty(shape, **i32) if sel_tables is None else sel_tables
+    sel_lens = torch.empty(shape[:2], **i32) if sel_lens is None else sel_lens
+    _need(sel_tables, "sel_tables", torch.int32, shape)
+    _need(sel_lens, "sel_lens", torch.int32, shape[:2])
+    return S, Hq, sel_tables, sel_lens
+
+
+def prepared_select_blocks(q, k_pool, k_means, block_tables, context_lens, top_blocks: int,
+                           first_blocks: int = 1, last_blocks: int = 1,
+                           sel_tables: Optional[torch.Tensor] = None,
+                           sel_lens: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """select_blocks as a PreparedCall."""
+    desc = _means_desc(k_pool, k_means)
+    sel = SparseSelect(top_blocks, first_blocks, last_blocks)
+    S, Hq, st, sl = _selection(q, desc, block_tables, context_lens, sel, sel_tables, sel_lens)
+    M = block_tables.shape[1]
+    if workspace is None:
+        n = int(_ops_lib().pkv_select_workspace_bytes(ctypes.byref(desc), S, M))
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+    return PreparedCall("pkv_select_blocks", (
+        ctypes.byref(desc), _ptr(q), S, Hq, _ptr(k_means), _ptr(block_tables), M, _ptr(context_lens),
+        ctypes.byref(sel), _ptr(st), _ptr(sl), _ptr(workspace),
+        workspace.numel() * workspace.element_size()),
+        keep=(q, k_means, block_tables, context_lens, st, sl, workspace, desc, sel),
+        out=(st, sl))
+
+
+def select_blocks(q, k_pool, k_means, block_tables, context_lens, top_blocks: int, first_blocks: int = 1,
+                  last_blocks: int = 1, sel_tables: Optional[torch.Tensor] = None,
+                  sel_lens: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None):
+    """(sel_tables [S][Hk][W], sel_lens [S][Hk]): the blocks each kv head of each sequence reads
+    (pkv_select_blocks), as tables over the pool viewed as [NB * Hk][1][B][D]. k_pool gives the
+    shape only."""
+    return prepared_select_blocks(q, k_pool, k_means, block_tables, context_lens, top_blocks,
+                                  first_blocks, last_blocks, sel_tables, sel_lens, workspace)(stream)
+
+
+def alloc_sparse_workspace(k_pool, num_seqs: int, num_q_heads: int, max_blocks_per_seq: int) -> torch.Tensor:
+    """Zero-filled workspace of decode_attention_sparse."""
+    desc = cache_desc(k_pool)
+    n = int(_ops_lib().pkv_decode_sparse_workspace_bytes(ctypes.byref(desc), num_seqs, num_q_heads,
+                                                         max_blocks_per_seq))
+    if n == 0:
+        raise PkvError(-1, lib().pkv_last_error_message().decode())
+    return torch.zeros(n, dtype=torch.uint8, device=k_pool.device)
+
+
+def prepared_decode_attention_sparse(q, k_pool, v_pool, k_means, block_tables, context_lens,
+                                     scale: float, top_blocks: int, first_blocks: int = 1,
+                                     last_blocks: int = 1, out: Optional[torch.Tensor] = None,
+                                     out_dtype: Optional[torch.dtype] = None,
+                                     sel_tables: Optional[torch.Tensor] = None,
+                                     sel_lens: Optional[torch.Tensor] = None,
+                                     workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """decode_attention_sparse as a PreparedCall."""
+    _pools(k_pool, v_pool)
+    desc = _means_desc(k_pool, k_means)
+    sel = SparseSelect(top_blocks, first_blocks, last_blocks)
+    S, Hq, st, sl = _selection(q, desc, block_tables, context_lens, sel, sel_tables, sel_lens)
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    _need(out, "out", out.dtype, q.shape)
+    if workspace is None:
+        workspace = alloc_sparse_workspace(k_pool, S, Hq, block_tables.shape[1])
+    return PreparedCall("pkv_decode_attention_sparse", (
+        ctypes.byref(desc), _ptr(q), S, Hq, _ptr(k_pool), _ptr(v_pool), _ptr(k_means), _ptr(block_tables),
+        block_tables.shape[1], _ptr(context_lens), float(scale), ctypes.byref(sel), _ptr(st), _ptr(sl),
+        _ptr(out), DTYPE_CODE[out.dtype], _ptr(workspace), workspace.numel() * workspace.element_size()),
+        keep=(q, k_pool, v_pool, k_means, block_tables, context_lens, st, sl, out, workspace, desc, sel),
+        out=out)
+
+
+def decode_attention_sparse(q, k_pool, v_pool, k_means, block_tables, context_lens, scale: float,
+                            top_blocks: int, first_blocks: int = 1, last_blocks: int = 1,
+                            out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                            sel_tables: Optional[torch.Tensor] = None,
+                            sel_lens: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Decode attention over the blocks that the block means select for each (sequence, kv head):
+    the top_blocks best, the first_blocks first and the last_blocks last (pkv_sparse.h)."""
+    return prepared_decode_attention_sparse(q, k_pool, v_pool, k_means, block_tables, context_lens,
+                                            scale, top_blocks, first_blocks, last_blocks, out,
+                                            out_dtype, sel_tables, sel_lens, workspace)(stream)

@@ -267,6 +267,13 @@ void next_wait_fault(unsigned long long *wait_ns, int *drop_arrival) {
 }
 
 pkv_status device_error_word(unsigned **out) { return device_error_ptr(out); }
+pkv_status check_cache_desc(const pkv_cache_desc *c) { return check_cache(c); }
+pkv_status device_sm_count(int *sms) { return sm_count(sms); }
+cudaError_t record_event(cudaEvent_t ev, cudaStream_t s) { return record_timing_event(ev, s); }
+pkv_status copy_block_pairs(int NB, const int64_t *pairs, int n, void *k_pool, void *v_pool,
+                            size_t block_bytes, cudaStream_t stream) {
+    return copy_blocks(NB, pairs, n, k_pool, v_pool, block_bytes, stream);
+}
 
 pkv_status set_last_error(pkv_status st, const char *fmt, ...) {
     va_list ap;

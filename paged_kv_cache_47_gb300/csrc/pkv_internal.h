@@ -169,6 +169,15 @@ pkv_status decode_flat(const FlatGeom &g, const void *q, int32_t S, int32_t Hq,
                        const pkv_decode_options *o);
 size_t flat_workspace_bytes(const FlatGeom &g, int32_t Hq, int32_t num_ctas);
 
+// Argument checks and device queries shared with the operators' own
+// translation units (defined in pkv_api.cu).
+pkv_status check_cache_desc(const pkv_cache_desc *c);
+pkv_status device_sm_count(int *sms);
+cudaError_t record_event(cudaEvent_t ev, cudaStream_t s);   // as an event node under capture
+// Whole-block copies: pairs checked on the host, block_bytes per block in both pools.
+pkv_status copy_block_pairs(int NB, const int64_t *pairs, int n, void *k_pool, void *v_pool,
+                            size_t block_bytes, cudaStream_t stream);
+
 // The device error word of the current device (PKV_DEVERR_* bits).
 pkv_status device_error_word(unsigned **out);
 

@@ -1,0 +1,113 @@
+// Host replay of the 4-bit decode's split (q4_split.h): random batches of units
+// are cut over CTAs and warps as the kernel cuts them; every subtile must be
+// used once, every unit written once, and the pieces joined must be exactly
+// the unit's.
+#include <cstdio>
+#include <map>
+#include <random>
+#include <set>
+#include <vector>
+
+#include "q4_split.h"
+
+using namespace pkv;
+
+struct Piece { int tu = 0, nu = 0, from = 0, to = 0; };
+
+static bool run(const std::vector<int> &units, int C) {
+    int NT = 0;
+    std::vector<int> start;
+    for (int n : units) { start.push_back(NT); NT += n; }
+    const int CT = q4_active_ctas(NT, C);
+    if (CT > C || (NT > 0) != (CT > 0)) return false;
+    std::map<int, int> covered, written;           // unit start -> subtiles, outputs
+    std::map<int, std::vector<std::pair<int, int>>> parts;   // unit start -> (cta, side)
+    std::map<int, int> part_subtiles;
+    auto unit_of = [&](int t) {
+        size_t u = 0;
+        while (u + 1 < units.size() && start[u + 1] <= t) ++u;
+        return (int)u;
+    };
+    int expect = 0;
+    for (int c = 0; c < CT; ++c) {
+        const int A = q4_cta_cut(c, NT, CT), Z = q4_cta_cut(c + 1, NT, CT);
+        if (A != expect || Z <= A) return false;
+        expect = Z;
+        Piece piece[kQ4Warps][2];
+        int at = A;
+        for (int w = 0; w < kQ4Warps; ++w) {
+            const int a = q4_warp_cut(w, A, Z), z = q4_warp_cut(w + 1, A, Z);
+            if (a != at || z < a) return false;
+            if (w == 0 && z == a) return false;     // the first warp has work
+            at = z;
+            for (int t = a; t < z;) {
+                if (q4_owner(t, NT, CT) != c) return false;
+                const int u = unit_of(t), tu = start[u], end = tu + units[u];
+                const int to = end < z ? end : z;
+                covered[tu] += to - t;
+                if (tu >= a && end <= z) {
+                    ++written[tu];
+                } else {
+                    Piece &p = piece[w][tu < a ? 0 : 1];
+                    if (p.nu) return false;         // a place is used once
+                    p = {tu, units[u], t, to};
+                }
+                t = to;
+            }
+        }
+        if (at != Z) return false;
+        bool open[2] = {false, false};
+        for (int w = 0; w < kQ4Warps; ++w)
+            for (int sl = w == 0 ? 0 : 1; sl < 2; ++sl) {
+                const Piece pc = piece[w][sl];
+                if (!pc.nu) continue;
+                int last = w, sum = pc.to - pc.from;
+                while (last + 1 < kQ4Warps && piece[last + 1][0].nu && piece[last + 1][0].tu == pc.tu) {
+                    ++last;
+                    sum += piece[last][0].to - piece[last][0].from;
+                }
+                const bool done = pc.tu >= A && pc.tu + pc.nu <= Z;
+                if (done) {
+                    if (sum != pc.nu) return false;
+                    ++written[pc.tu];
+                } else {
+                    const int side = pc.tu < A ? 0 : 1;
+                    if (open[side]) return false;
+                    open[side] = true;
+                    parts[pc.tu].push_back({c, side});
+                    part_subtiles[pc.tu] += sum;
+                }
+            }
+    }
+    if (expect != NT) return false;
+    std::set<int> counters;
+    for (auto &kv : parts) {
+        const int tu = kv.first, nu = units[unit_of(tu)];
+        const int first = q4_owner(tu, NT, CT), n = q4_owner(tu + nu - 1, NT, CT) - first + 1;
+        if ((int)kv.second.size() != n || part_subtiles[tu] != nu) return false;
+        if (!counters.insert(first).second) return false;        // a counter serves one unit
+        for (int k = 0; k < n; ++k)
+            if (kv.second[k].first != first + k || kv.second[k].second != (k == 0 ? 1 : 0)) return false;
+        ++written[tu];
+    }
+    for (size_t u = 0; u < units.size(); ++u)
+        if (covered[start[u]] != units[u] || written[start[u]] != 1) return false;
+    return true;
+}
+
+int main() {
+    std::mt19937 rng(1);
+    auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+    for (int i = 0; i < 4000; ++i) {
+        std::vector<int> units(pick(1, 60));
+        const int most = i % 4 == 0 ? 1 : i % 4 == 1 ? 5 : i % 4 == 2 ? 40 : 900;
+        for (int &n : units) n = pick(1, most);
+        const int C = i % 3 == 0 ? pick(1, 4) : i % 3 == 1 ? 152 : pick(1, 600);
+        if (!run(units, C)) {
+            std::printf("FAIL at %d\n", i);
+            return 1;
+        }
+    }
+    std::puts("OK");
+    return 0;
+}
