@@ -1011,14 +1011,23 @@ class PreparedCall:
         self._after, self._keep, self.out = tuple(after), keep, out
 
     def __call__(self, stream=None):
-        if stream is None:
-            stream = torch.cuda.current_stream(self._device)
+        raw = _raw_stream(self._device) if stream is None else _stream(stream)
         if torch.cuda.current_device() != self._device:
             with torch.cuda.device(self._device):
-                _check(self._fn(*self._args, _stream(stream), *self._after))
+                _check(self._fn(*self._args, raw, *self._after))
         else:
-            _check(self._fn(*self._args, _stream(stream), *self._after))
+            status = self._fn(*self._args, raw, *self._after)
+            if status:
+                _check(status)
         return self.out
+
+
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the current stream's handle without a Stream object around it (1 us less a call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None) -> torch.Tensor:

@@ -62,6 +62,7 @@ struct Q4Params {
     int out_dtype, act_f16;
     const int32_t *tables, *lens;
     int S, Hq, Hk, G, NC, GC, U, M, NB, lb;    // block size 1 << lb; U = Hk * NC units a sequence
+    uint32_t code_bytes, par_bytes;  // of one (block, kv head) chunk, K or V
     float scale_log2;
     const uint8_t *kc, *vc;
     const __half *kp, *vp;
@@ -95,11 +96,20 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+// The same with nothing to add to.
+__device__ __forceinline__ void mma16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                           uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void mma8_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
     asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b0));
+        "{%7,%7,%7,%7};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -115,118 +125,228 @@ __device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
 
-// A place in the flattened list of subtiles.
-struct Cursor {
-    int s, u, i, n;      // sequence, unit in it, subtile of the unit, subtiles of the unit
-};
+// cp.async of 16 bytes to dst + OFF; the second form reads only `n` of them.
+template <int OFF>
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1], 16;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
+}
 
-// Copies one warp's subtiles into its stages, ahead of their use.
+// The order of the 16-byte pieces of codes in a stage. Each 128-byte line has
+// its eight pieces exclusive-ored by a number of the line, so that the fragment
+// loads of K and V meet 32 banks.
 template <int D>
+__device__ __forceinline__ int line_xor(int line) {
+    return D == 128 ? (line & ~1) : ((line & 1) << 2 | (line & 2));
+}
+
+// A context's last subtile, or one with a block id outside the pool: what is
+// not there becomes zeros.
+template <int D>
+__device__ __noinline__ void issue_ragged(const Q4Params &p, uint32_t stage, int id0, int id1, int off,
+                                          int head, int left, int lane, uint32_t dst0,
+                                          uint32_t dst1, uint32_t dst_par) {
+    using C = Cfg<D>;
+    const int B = 1 << p.lb;
+    bool ok0 = (unsigned)id0 < (unsigned)p.NB, ok1 = (unsigned)id1 < (unsigned)p.NB;
+    if (lane == 0 && (!ok0 || (!ok1 && left > 8))) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+    if (!ok0) id0 = 0;
+    if (!ok1) id1 = 0;
+    const size_t c0 = (size_t)id0 * p.Hk + head, c1 = (size_t)id1 * p.Hk + head;
+#pragma unroll
+    for (int j = 0; j < C::kCodes / 512; ++j) {
+        const int c = lane + 32 * j, r = c / (D / 32), w = c % (D / 32);
+        const bool hi = r >= 8;
+        const size_t src = ((hi ? c1 : c0) * B + ((off + r) & (B - 1))) * (D / 2) + w * 16;
+        const bool live = (hi ? ok1 : ok0) && r < left;
+        pkv::cp_async_16(stage + (j ? dst1 : dst0), p.kc + src, live);
+        pkv::cp_async_16(stage + (j ? dst1 : dst0) + C::kCodes, p.vc + src, live);
+    }
+    const int l = lane & 15;
+    if (l < C::kPar / 16) {
+        if (lane < 16) {
+            constexpr int kTok = 16 / (4 * C::NG);   // tokens of a piece: 1 or 2
+            const int r = l * kTok;
+            const bool hi = r >= 8;
+            const __half *src = p.kp + ((hi ? c1 : c0) * B + ((off + r) & (B - 1))) * (2 * C::NG);
+            const int live = (hi ? ok1 : ok0) ? min(kTok, max(0, left - r)) : 0;
+            pkv::cp_async_16_n(stage + dst_par, src, live * 4 * C::NG);
+        } else {
+            const bool hi = l & 1;
+            const __half *src = p.vp + ((hi ? c1 : c0) * (2 * C::NG) + (l >> 1)) * B +
+                                ((off + 8 * hi) & (B - 1));
+            const int live = (hi ? ok1 : ok0) ? min(8, max(0, left - 8 * hi)) : 0;
+            pkv::cp_async_16_n(stage + dst_par, src, live * 2);
+        }
+    }
+}
+
+// Copies one warp's subtiles into its stages, ahead of their use. The place of
+// the next subtile is kept as the sequence and unit it belongs to, its first
+// token and the tokens left from there.
+template <int D, bool B8>
 struct Loader {
     using C = Cfg<D>;
     const Q4Params &p;
     const int *prefix, *len;         // shared memory: subtiles before a sequence, its length
     int lane;
-    Cursor at;
+    int s, u, head, t0, left;
     int32_t window, next_window;     // table entries: lane holds entry `base + lane` of each
     int base;
+    uint32_t dst0, dst1;             // this lane's pieces of the codes in a stage
+    uint32_t dst_par;                // and of the parameters
+    const uint8_t *par;              // the parameters' source in chunk 0
+    uint32_t par_tok;                // bytes from one token's to the next's
+    bool par_hi;                     // blocks of 8: from the second block
 
     __device__ __forceinline__ Loader(const Q4Params &p_, const int *prefix_, const int *len_, int lane_)
-        : p(p_), prefix(prefix_), len(len_), lane(lane_) {}
+        : p(p_), prefix(prefix_), len(len_), lane(lane_) {
+        const int line = lane >> 3;
+        dst0 = line * 128 + (((lane & 7) ^ line_xor<D>(line)) << 4);
+        dst1 = (line + 4) * 128 + (((lane & 7) ^ line_xor<D>(line + 4)) << 4);
+        dst_par = 2 * C::kCodes + (lane >> 4) * C::kPar + (lane & 15) * 16;
+        // parameters: lanes 0..15 copy K's (token-major), 16..31 V's: piece l is
+        // tokens 8 (l & 1) .. of row l / 2 of [2 NG][B]
+        const int l = lane & 15;
+        const bool is_v = lane >= 16;
+        par = reinterpret_cast<const uint8_t *>(is_v ? p.vp : p.kp);
+        par_tok = is_v ? 2 : 4 * C::NG;
+        if (B8) {
+            par_hi = is_v ? l & 1 : l * 16 >= C::kPar / 2;
+            par += is_v ? (l >> 1) * 16 : l * 16 - (par_hi ? C::kPar / 2 : 0);
+        } else {
+            par_hi = false;
+            par += is_v ? (((l >> 1) << p.lb) + 8 * (l & 1)) * 2 : l * 16;
+        }
+    }
 
-    __device__ __forceinline__ int32_t entries(int s, int from) const {
+    __device__ __forceinline__ int32_t entries(int from) const {
         const int e = from + lane;
         return e < p.M ? __ldg(p.tables + (int64_t)s * p.M + e) : -1;
     }
-    __device__ __forceinline__ void start(const Cursor &c) {
-        at = c;
-        base = ((at.i * kSub) >> p.lb) & ~31;
-        window = entries(at.s, base);
-        next_window = entries(at.s, base + 32);
+    __device__ __forceinline__ void windows() {
+        base = (t0 >> p.lb) & ~31;
+        window = entries(base);
+        next_window = entries(base + 32);
     }
-    // Next subtile; the sequence's table starts again with each unit.
+    __device__ __forceinline__ void start(int seq, int unit, int subtile) {
+        s = seq;
+        u = unit;
+        head = unit / p.NC;
+        t0 = subtile * kSub;
+        left = len[s] - t0;
+        windows();
+    }
+    // Next subtile; the table's row starts again with each unit.
     __device__ __forceinline__ void advance() {
-        if (++at.i < at.n) {
-            const int b = (at.i * kSub) >> p.lb;
-            if (b >= base + 32) {
+        t0 += kSub;
+        left -= kSub;
+        if (left > 0) {
+            if ((t0 >> p.lb) >= base + 32) {
                 base += 32;
                 window = next_window;
-                next_window = entries(at.s, base + 32);
+                next_window = entries(base + 32);
             }
             return;
         }
-        at.i = 0;
-        if (++at.u == p.U) {
-            at.u = 0;
-            do ++at.s; while (at.s < p.S && prefix[at.s + 1] == prefix[at.s]);
-            if (at.s >= p.S) return;             // the list's end
-            at.n = prefix[at.s + 1] - prefix[at.s];
+        if (++u == p.U) {
+            u = 0;
+            do ++s; while (s < p.S && len[s] == 0);
+            if (s >= p.S) return;                // the list's end
         }
-        base = 0;
-        window = entries(at.s, 0);
-        next_window = entries(at.s, 32);
+        head = u / p.NC;
+        t0 = 0;
+        left = len[s];
+        windows();
     }
     __device__ __forceinline__ void issue(uint32_t stage) {
-        const int t0 = at.i * kSub, L = len[at.s], head = at.u / p.NC;
-        const int B = 1 << p.lb;
-        // block of the subtile's tokens 0..7 and 8..15 (one block unless B is 8)
-        const int b0 = t0 >> p.lb, b1 = (t0 + 8) >> p.lb;
-        int32_t id[2];
-        id[0] = __shfl_sync(~0u, window, b0 - base);
-        id[1] = __shfl_sync(~0u, window, b1 - base);
-        bool ok[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            ok[h] = id[h] >= 0 && id[h] < p.NB;
-            if (!ok[h]) {
-                if (lane == 0 && t0 + 8 * h < L) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-                id[h] = 0;
-            }
-        }
-        // codes: 16-byte pieces; each 128-byte line of shared memory has its
-        // eight pieces exclusive-ored by a number of the line, so that the
-        // fragment loads below meet 32 banks
-#pragma unroll
-        for (int j = 0; j < C::kCodes / 512; ++j) {
-            const int c = lane + 32 * j, r = c / (D / 32), w = c % (D / 32);
-            const int h = r >> 3;
-            const int line = c >> 3;
-            const int x = D == 128 ? (line & ~1) : ((line & 1) << 2 | (line & 2));
-            const uint32_t dst = stage + line * 128 + (((c & 7) ^ x) << 4);
-            const int off = (t0 + r) & (B - 1);
-            const size_t src = (((size_t)id[h] * p.Hk + head) * B + off) * (D / 2) + w * 16;
-            const bool live = ok[h] && t0 + r < L;
-            pkv::cp_async_16(dst, p.kc + src, live);
-            pkv::cp_async_16(dst + C::kCodes, p.vc + src, live);
-        }
-        // parameters: lanes 0..15 K (token-major), 16..31 V (tokens along the row)
-        const uint32_t par = stage + 2 * C::kCodes;
-        constexpr int kPieces = C::kPar / 16;            // 16 or 8
-        const int l = lane & 15;
-        if (l < kPieces) {
-            if (lane < 16) {
-                constexpr int kTok = 16 / (4 * C::NG);   // tokens of a piece: 1 or 2
-                const int r = l * kTok, h = r >> 3, off = (t0 + r) & (B - 1);
-                const __half *src = p.kp + (((size_t)id[h] * p.Hk + head) * B + off) * (2 * C::NG);
-                const int live = ok[h] ? min(kTok, max(0, L - t0 - r)) : 0;
-                pkv::cp_async_16_n(par + l * 16, src, live * 4 * C::NG);
+        // the block of the subtile's tokens 0..7, and of 8..15 (the same unless
+        // a block holds 8)
+        const int at = (t0 >> p.lb) - base;
+        const int id0 = __shfl_sync(~0u, window, at);
+        const int id1 = B8 ? __shfl_sync(~0u, window, at + 1) : id0;
+        const int off = B8 ? 0 : t0 & ((1 << p.lb) - 1);
+        if (left >= kSub && (unsigned)id0 < (unsigned)p.NB && (!B8 || (unsigned)id1 < (unsigned)p.NB)) {
+            // a whole subtile: its codes are 16 D / 2 bytes in a row (two runs
+            // where blocks hold 8)
+            const uint32_t c0 = id0 * p.Hk + head, c1 = B8 ? id1 * p.Hk + head : c0;
+            if (D == 128) {
+                const uint64_t o0 = (uint64_t)c0 * p.code_bytes + (off * (D / 2) + lane * 16);
+                const uint64_t o1 = B8 ? (uint64_t)c1 * p.code_bytes + lane * 16 : o0 + 512;
+                copy16<0>(stage + dst0, p.kc + o0);
+                copy16<0>(stage + dst1, p.kc + o1);
+                copy16<C::kCodes>(stage + dst0, p.vc + o0);
+                copy16<C::kCodes>(stage + dst1, p.vc + o1);
             } else {
-                const int row = l >> 1, h = l & 1, off = (t0 + 8 * h) & (B - 1);
-                const __half *src = p.vp + (((size_t)id[h] * p.Hk + head) * (2 * C::NG) + row) * B + off;
-                const int live = ok[h] ? min(8, max(0, L - t0 - 8 * h)) : 0;
-                pkv::cp_async_16_n(par + C::kPar + l * 16, src, live * 2);
+                // 32 pieces: lanes 16.. are tokens 8..
+                const uint64_t o = B8 ? (uint64_t)(lane >= 16 ? c1 : c0) * p.code_bytes + (lane & 15) * 16
+                                      : (uint64_t)c0 * p.code_bytes + (off * (D / 2) + lane * 16);
+                copy16<0>(stage + dst0, p.kc + o);
+                copy16<C::kCodes>(stage + dst0, p.vc + o);
             }
+            if (C::kPar == 256 || (lane & 15) < 8)
+                copy16<0>(stage + dst_par,
+                          par + ((uint64_t)(B8 && par_hi ? c1 : c0) * p.par_bytes + off * par_tok));
+            return;
         }
+        issue_ragged<D>(p, stage, id0, id1, off, head, left, lane, dst0, dst1, dst_par);
     }
 };
+
+// E neighbouring fp32 values (2 or 4), and E outputs in the output's type.
+template <int E>
+__device__ __forceinline__ void add_scaled(float (&o)[E], const float *src, float f) {
+    if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
+        o[0] = fmaf(v.x, f, o[0]);
+        o[1] = fmaf(v.y, f, o[1]);
+        o[2] = fmaf(v.z, f, o[2]);
+        o[3] = fmaf(v.w, f, o[3]);
+    } else {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        o[0] = fmaf(v.x, f, o[0]);
+        o[1] = fmaf(v.y, f, o[1]);
+    }
+}
+template <int E>
+__device__ __forceinline__ void load_cg(float (&o)[E], const float *src) {
+    if constexpr (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+    } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+        o[0] = v.x, o[1] = v.y;
+    }
+}
+template <int E>
+__device__ __forceinline__ void store_f32(float *dst, const float (&o)[E]) {
+    if constexpr (E == 4) *reinterpret_cast<float4 *>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+    else *reinterpret_cast<float2 *>(dst) = make_float2(o[0], o[1]);
+}
+template <int E>
+__device__ __forceinline__ void store_row(const Q4Params &p, size_t at, const float (&o)[E]) {
+    if (p.out_dtype == PKV_F32) {
+        store_f32(static_cast<float *>(p.out) + at, o);
+        return;
+    }
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+        float a, b;
+        w[i / 2] = p.out_dtype == PKV_F16 ? pkv::Elem<__half>::pack2(o[i], o[i + 1], a, b)
+                                          : pkv::Elem<__nv_bfloat16>::pack2(o[i], o[i + 1], a, b);
+    }
+    uint16_t *dst = static_cast<uint16_t *>(p.out) + at;
+    if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(dst) = w[0];
+}
 
 // What a warp leaves of a unit it does not hold whole.
 struct Piece {
     int tu, nu, s, u;     // the unit's first subtile and length in the list; its place; nu 0: none
 };
 
-template <int D, int NST>
-__global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p) {
+template <int D, int NST, bool B8>
+__global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_constant__ Q4Params p) {
     using C = Cfg<D>;
     constexpr int NG = C::NG;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -234,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
     __shared__ int scan[kWarps];
     __shared__ Piece piece[kWarps][2];
     __shared__ float piece_lse[kWarps][2][kHeads];
-    __shared__ int merge_first[2], merge_n[2];
+    __shared__ int cut_tu[2], cut_nu[2], cut_s[2], cut_u[2];      // units cut at the CTA's start, end
     uint8_t *ring_all = smem;
     float *heads_o = reinterpret_cast<float *>(smem + kWarps * NST * C::kStage);   // [warp][GC][D]
 
@@ -302,23 +422,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
     const int g = lane >> 2, t = lane & 3;
 
     if (a < z) {
-        Cursor c;
-        {   // the sequence holding subtile a: the last whose units begin at or before it
+        int cs, cu, ci;                      // sequence, unit, subtile of the unit
+        {   // the sequence holding subtile a: the last whose units begin at or before
+            // it (of equal prefixes, the empty sequences come first)
             int lo = 0, hi = p.S - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (prefix[mid] * p.U <= a) lo = mid;
                 else hi = mid - 1;
             }
-            // equal prefixes belong to empty sequences before it, not after
-            c.s = lo;
-            c.n = prefix[lo + 1] - prefix[lo];
-            const int r = a - prefix[lo] * p.U;
-            c.u = r / c.n;
-            c.i = r - c.u * c.n;
+            const int n = prefix[lo + 1] - prefix[lo], r = a - prefix[lo] * p.U;
+            cs = lo;
+            cu = r / n;
+            ci = r - cu * n;
         }
-        Loader<D> ld(p, prefix, len, lane);
-        ld.start(c);
+        const uint32_t ring_end = ring + NST * C::kStage;
+        Loader<D, B8> ld(p, prefix, len, lane);
+        ld.start(cs, cu, ci);
         int to_issue = z - a;
 #pragma unroll
         for (int st = 0; st < NST - 1; ++st) {
@@ -328,24 +448,34 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        int stage = 0, fill = NST - 1;      // stage to use, stage to fill
+        uint32_t sk = ring, fill = ring + (NST - 1) * C::kStage;      // stage to use, to fill
+        // this lane's places in a stage (see below)
+        const int r0 = 4 * (g >> 1) + (g & 1);
+        uint32_t k_at, v_at, m_at;
+        if constexpr (NG == 4) {
+            k_at = (r0 >> 1) * 128 + (((4 * (r0 & 1) + t) ^ line_xor<D>(r0 >> 1)) << 4);
+            v_at = 2 * t * 128 + (((g >> 1) ^ (2 * t)) << 4) + 8 * (g & 1);
+        } else {
+            k_at = (r0 >> 2) * 128 + (((2 * (r0 & 3) + (t >> 1)) ^ line_xor<D>(r0 >> 2)) << 4) + 8 * (t & 1);
+            v_at = t * 128 + (((g >> 2) ^ line_xor<D>(t)) << 4) + 4 * (g & 3);
+        }
+        m_at = 2 * NG + (NG == 4 ? 4 * (t & 1) : 0);                 // minima of two groups in a K row
+        const uint32_t vm_at = (NG + (g & (NG - 1))) * 32 + t * 8;   // minima of a group, V
+        const uint32_t one = g == 0 ? 0x3c003c00u : 0u;
 
-        uint32_t qb[NG][2][2];              // q as B operands
-        uint32_t qsum = 0;                  // sums of q over the groups, as a B operand
-        float zs0 = 0.f, zs1 = 0.f;         // scores to log2 units, heads 2t and 2t + 1
-        float me0 = kNone, me1 = kNone;     // reference exponents
-        float room = 15.f;                  // largest score above the reference
-        uint32_t sbound = 0;                // V scales so far stay at or below it (both halves)
-        float acc[NG][2][4], accx[4];
-        bool fresh = true;
-        int tile = a;
-
-        for (; tile < z; ++tile) {
-            if (fresh) {
-                fresh = false;
-                // q of this unit: lane (g, t) holds elements 32 y + 8 t .. + 7 of head g
-                const int gca = min(p.GC, p.G - (c.u % p.NC) * p.GC);
-                const int h0 = (c.u / p.NC) * p.G + (c.u % p.NC) * p.GC;
+        for (int tile = a; tile < z;) {
+            // ---- a unit, or the part of it that lies here: `count` subtiles
+            const int n = prefix[cs + 1] - prefix[cs];
+            const int count = min(n - ci, z - tile);
+            const int chunk = cu % p.NC, kvh = cu / p.NC;
+            const int gca = min(p.GC, p.G - chunk * p.GC);
+            const int h0 = kvh * p.G + chunk * p.GC;
+            int left = len[cs] - ci * kSub;      // tokens from the subtile in hand on
+            uint32_t qb[NG][2][2];               // q as B operands
+            uint32_t qsum;                       // sums of q over the groups, as a B operand
+            float zs0, zs1;                      // scores to log2 units, heads 2t and 2t + 1
+            {
+                // lane (g, t) holds elements 32 y + 8 t .. + 7 of head g
                 float x[NG][8], top = 0.f;
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
@@ -353,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
                     if (g < gca)
                         raw = __ldg(reinterpret_cast<const uint4 *>(
                             static_cast<const uint16_t *>(p.q) +
-                            ((size_t)c.s * p.Hq + h0 + g) * D + 32 * y + 8 * t));
+                            ((size_t)cs * p.Hq + h0 + g) * D + 32 * y + 8 * t));
                     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -391,75 +521,62 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
                     }
                 }
                 // sums as fp16 pairs: k = 0..NG-1 the high parts, then the low ones
-                {
-                    const int y = NG == 4 ? 2 * (t & 1) : 0;
-                    float s0 = sum[0], s1 = sum[1];
-                    if (NG == 4 && y == 2) {
-                        s0 = sum[NG - 2];
-                        s1 = sum[NG - 1];
-                    }
-                    __half2 hi = __floats2half2_rn(s0, s1);
-                    const bool low = NG == 4 ? t >= 2 : t == 1;
-                    if (low) {
-                        const float2 f = __half22float2(hi);
-                        hi = __floats2half2_rn(s0 - f.x, s1 - f.y);
-                    }
-                    qsum = NG == 2 && t >= 2 ? 0u : as_u32(hi);
+                const bool upper = NG == 4 && (t & 1);
+                const float s0 = upper ? sum[NG - 2] : sum[0], s1 = upper ? sum[NG - 1] : sum[1];
+                __half2 hi = __floats2half2_rn(s0, s1);
+                if (NG == 4 ? t >= 2 : t == 1) {
+                    const float2 f = __half22float2(hi);
+                    hi = __floats2half2_rn(s0 - f.x, s1 - f.y);
                 }
+                qsum = NG == 2 && t >= 2 ? 0u : as_u32(hi);
                 const float zq = p.scale_log2 * 0x1p24f * down;
                 zs0 = __shfl_sync(~0u, zq, 8 * t);
                 zs1 = __shfl_sync(~0u, zq, 8 * t + 4);
-                me0 = me1 = kNone;
-                room = 15.f;
-                sbound = 0x3c003c00u;                // 1
-#pragma unroll
-                for (int y = 0; y < NG; ++y)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[y][k][i] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) accx[i] = 0.f;
             }
+            float me0 = kNone, me1 = kNone;      // reference exponents
+            float room = 15.f;                   // largest score above the reference
+            uint32_t sbound = 0x3c003c00u;       // V scales so far stay at or below it (1)
+            float acc[NG][2][4], accx[4];
+#pragma unroll
+            for (int y = 0; y < NG; ++y)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[y][k][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) accx[i] = 0.f;
 
+          for (int it = 0; it < count; ++it) {
             asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
             __syncwarp();
             // the stage used last is free now: fill it
             if (to_issue > 0) {
-                ld.issue(ring + fill * C::kStage);
+                ld.issue(fill);
                 if (--to_issue) ld.advance();
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
 
-            const uint32_t sk = ring + stage * C::kStage, sv = sk + C::kCodes;
-            const uint32_t pk = sv + C::kCodes, pv = pk + C::kPar;
-            fill = stage;
-            stage = stage + 1 == NST ? 0 : stage + 1;
+            const uint32_t sv = sk + C::kCodes, pk = sk + 2 * C::kCodes, pv = pk + C::kPar;
+            const uint32_t k_row = sk + k_at, v_row = sv + v_at, pk_row = pk + r0 * (4 * NG);
+            fill = sk;
 
             // ---- scores: rows g and g + 8 of the product are tokens r0 and r0 + 2,
             // so that after the transpose below lane t holds tokens 4t .. 4t + 3
-            const int r0 = 4 * (g >> 1) + (g & 1);
             float sc[4];
             {
                 uint32_t w[2][NG];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = r0 + 2 * h;
-                    if constexpr (NG == 4) {
-                        const int line = r >> 1, x = line & ~1;
-                        pkv::lds_u32x4(sk + line * 128 + (((4 * (r & 1) + t) ^ x) << 4), w[h][0], w[h][1],
-                                       w[h][2], w[h][3]);
-                    } else {
-                        const int line = r >> 2, x = (line & 1) << 2 | (line & 2);
-                        lds64(sk + line * 128 + (((2 * (r & 3) + (t >> 1)) ^ x) << 4) + 8 * (t & 1), w[h][0],
-                              w[h][1]);
-                    }
+                if constexpr (NG == 4) {
+                    pkv::lds_u32x4(k_row, w[0][0], w[0][1], w[0][2], w[0][3]);
+                    pkv::lds_u32x4(k_row + 128, w[1][0], w[1][1], w[1][2], w[1][3]);
+                } else {
+                    lds64(k_row, w[0][0], w[0][1]);
+                    lds64(k_row ^ 64u, w[1][0], w[1][1]);            // two rows on: piece + 4
                 }
                 float s0[NG], s1[NG];                // scales of tokens r0, r0 + 2
                 uint32_t m0, m1;                     // minima of two groups
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t row = pk + (r0 + 2 * h) * 4 * NG;
+                    const uint32_t row = pk_row + h * (8 * NG);
                     uint32_t u[2];
                     if constexpr (NG == 4) lds64(row, u[0], u[1]);
                     else u[0] = pkv::lds_u32(row);
@@ -469,19 +586,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
                         (h ? s1 : s0)[y] = f.x;
                         (h ? s1 : s0)[y + 1] = f.y;
                     }
-                    uint32_t m = pkv::lds_u32(row + 2 * NG + (NG == 4 ? 4 * (t & 1) : 0));
+                    uint32_t m = pkv::lds_u32(row + m_at);
                     if (NG == 2 && t >= 2) m = 0;
                     (h ? m1 : m0) = m;
                 }
-                float mn[4] = {0.f, 0.f, 0.f, 0.f};
-                mma8(mn, m0, m1, qsum);
+                float mn[4];
+                mma8_zero(mn, m0, m1, qsum);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[i] = mn[i] * 0x1p-18f;
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    float d[4];
                     uint32_t wa = w[0][y], wb = w[1][y];
-                    mma16(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
+                    mma16_zero(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
                           qb[y][0][0], qb[y][0][1]);
                     wa >>= 8;
                     wb >>= 8;
@@ -493,15 +610,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
                     sc[3] = fmaf(d[3], s1[y], sc[3]);
                 }
             }
-            sc[0] *= zs0;
-            sc[1] *= zs1;
-            sc[2] *= zs0;
-            sc[3] *= zs1;
-            const int left = len[c.s] - c.i * kSub;          // valid tokens from here on
+            // exponents of the weights, against the reference
+            const float raw[4] = {sc[0], sc[1], sc[2], sc[3]};
+            sc[0] = fmaf(raw[0], zs0, -me0);
+            sc[1] = fmaf(raw[1], zs1, -me1);
+            sc[2] = fmaf(raw[2], zs0, -me0);
+            sc[3] = fmaf(raw[3], zs1, -me1);
             if (left < kSub) {
                 if (r0 >= left) sc[0] = sc[1] = -INFINITY;
                 if (r0 + 2 >= left) sc[2] = sc[3] = -INFINITY;
             }
+            left -= kSub;
 
             // ---- V scales of tokens 4t .. 4t + 3, and the reference exponent
             uint32_t vs[NG][2];
@@ -511,12 +630,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
                 lds64(pv + y * 32 + t * 8, vs[y][0], vs[y][1]);
                 big = __hmax2(big, __hmax2(as_h2(vs[y][0]), as_h2(vs[y][1])));
             }
-            const float over = fmaxf(fmaxf(sc[0], sc[2]) - me0, fmaxf(sc[1], sc[3]) - me1);
+            const float over = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
             if (__any_sync(~0u, over > room || !__hble2(big, as_h2(sbound)))) {
                 // raise the bound on V scales to this subtile's largest, the
                 // reference to 7 (less where scales are large) below the top score
                 float bs = fmaxf(__low2float(big), __high2float(big));
-                float t0 = fmaxf(sc[0], sc[2]), t1 = fmaxf(sc[1], sc[3]);
+                float zz[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    zz[i] = sc[i] == -INFINITY ? -INFINITY : raw[i] * (i & 1 ? zs1 : zs0);
+                float t0 = fmaxf(zz[0], zz[2]), t1 = fmaxf(zz[1], zz[3]);
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     bs = fmaxf(bs, __shfl_xor_sync(~0u, bs, o));
@@ -534,6 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
                 const float f0 = ex2(me0 - n0), f1 = ex2(me1 - n1);
                 me0 = n0;
                 me1 = n1;
+                sc[0] = zz[0] - n0;
+                sc[1] = zz[1] - n1;
+                sc[2] = zz[2] - n0;
+                sc[3] = zz[3] - n1;
 #pragma unroll
                 for (int y = 0; y < NG; ++y)
 #pragma unroll
@@ -551,26 +678,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
 
             // ---- weights, transposed: lane (g, t) then has head g, tokens 4t .. 4t + 3
             const uint32_t p01 =
-                transpose8(as_u32(__floats2half2_rn(ex2(sc[0] - me0), ex2(sc[1] - me1))));
+                transpose8(as_u32(__floats2half2_rn(ex2(sc[0]), ex2(sc[1]))));
             const uint32_t p23 =
-                transpose8(as_u32(__floats2half2_rn(ex2(sc[2] - me0), ex2(sc[3] - me1))));
+                transpose8(as_u32(__floats2half2_rn(ex2(sc[2]), ex2(sc[3]))));
 
             // ---- V: rows of the product are d, its contracted index the tokens
             uint32_t v01[NG], v23[NG];
             {
+                // tokens 4t .. 4t + 3: two lines of two rows (D 64: one line of four)
                 uint32_t w[4][NG / 2];
+                if constexpr (NG == 4) {
+                    lds64(v_row, w[0][0], w[0][1]);
+                    lds64(v_row ^ 64u, w[1][0], w[1][1]);
+                    lds64(v_row + 128, w[2][0], w[2][1]);
+                    lds64((v_row ^ 64u) + 128, w[3][0], w[3][1]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = 4 * t + j;
-                    if constexpr (NG == 4) {
-                        const int line = r >> 1, x = line & ~1;
-                        lds64(sv + line * 128 + (((4 * (r & 1) + (g >> 1)) ^ x) << 4) + 8 * (g & 1),
-                              w[j][0], w[j][1]);
-                    } else {
-                        const int line = r >> 2, x = (line & 1) << 2 | (line & 2);
-                        w[j][0] = pkv::lds_u32(sv + line * 128 + (((2 * (r & 3) + (g >> 2)) ^ x) << 4) +
-                                               4 * (g & 3));
-                    }
+                    for (int j = 0; j < 4; ++j) w[j][0] = pkv::lds_u32(v_row ^ (32u * j));
                 }
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
@@ -582,9 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
             {
                 // minima as rows 0..NG-1, a row of ones as row 8
                 uint32_t m01, m23;
-                lds64(pv + (NG + (g & (NG - 1))) * 32 + t * 8, m01, m23);
+                lds64(pv + vm_at, m01, m23);
                 if (g >= NG) m01 = m23 = 0;
-                const uint32_t one = g == 0 ? 0x3c003c00u : 0u;
                 mma16(accx, m01, one, m23, one, p01, p23);
             }
 #pragma unroll
@@ -603,181 +726,194 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const Q4Params p
                 }
             }
 
-            // ---- the unit's last subtile here: its output, or a piece
-            if (c.i == c.n - 1 || tile == z - 1) {
-                const int gca = min(p.GC, p.G - (c.u % p.NC) * p.GC);
-                const int h0 = (c.u / p.NC) * p.G + (c.u % p.NC) * p.GC;
-                const int tu = tile - c.i;
-                const bool whole = tu >= a && c.i == c.n - 1;
-                const int slot = tu < a ? 0 : 1;
-                const float l0 = __shfl_sync(~0u, accx[2], t), l1 = __shfl_sync(~0u, accx[3], t);
-                const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
-                // a piece of a unit that goes on in the next warp lies in this
-                // warp's ring, which is read to the end; the other has its own place
-                float *po = slot ? reinterpret_cast<float *>(ring_all + warp * NST * C::kStage)
-                                 : heads_o + (size_t)warp * p.GC * D;
-                if (slot && !whole) __syncwarp();
+            sk += C::kStage;
+            if (sk == ring_end) sk = ring;
+          }
+
+            // ---- the unit's output, or a piece of it
+            const int tu = tile - ci;
+            const bool whole = ci == 0 && count == n;
+            const int slot = ci ? 0 : 1;         // ci > 0: it began before this warp's part
+            const float l0 = __shfl_sync(~0u, accx[2], t), l1 = __shfl_sync(~0u, accx[3], t);
+            const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
+            // a piece of a unit that goes on in the next warp lies in this
+            // warp's ring, which is read to the end; the other has its own place
+            float *po = slot ? reinterpret_cast<float *>(ring_all + warp * NST * C::kStage)
+                             : heads_o + (size_t)warp * p.GC * D;
+            if (slot && !whole) __syncwarp();
 #pragma unroll
-                for (int y = 0; y < NG; ++y) {
-                    const float x0 = __shfl_sync(~0u, accx[0], 4 * y + t);
-                    const float x1 = __shfl_sync(~0u, accx[1], 4 * y + t);
+            for (int y = 0; y < NG; ++y) {
+                const float x0 = __shfl_sync(~0u, accx[0], 4 * y + t);
+                const float x1 = __shfl_sync(~0u, accx[1], 4 * y + t);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {            // head 2t + e
-                        const int h = 2 * t + e;
-                        if (h >= gca) continue;
-                        const float m = e ? x1 : x0, inv = e ? inv1 : inv0;
-                        const float o0 = fmaf(acc[y][0][e], 0x1p24f, m) * inv;
-                        const float o1 = fmaf(acc[y][0][2 + e], 0x1p20f, m) * inv;
-                        const float o2 = fmaf(acc[y][1][e], 0x1p24f, m) * inv;
-                        const float o3 = fmaf(acc[y][1][2 + e], 0x1p20f, m) * inv;
-                        const int d = 32 * y + 4 * g;
-                        if (whole) {
-                            const size_t at = ((size_t)c.s * p.Hq + h0 + h) * D + d;
-                            if (p.out_dtype == PKV_F32) {
-                                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
-                                    make_float4(o0, o1, o2, o3);
-                            } else {
-                                uint2 w;
-                                if (p.out_dtype == PKV_F16) {
-                                    w.x = as_u32(__floats2half2_rn(o0, o1));
-                                    w.y = as_u32(__floats2half2_rn(o2, o3));
-                                } else {
-                                    float u0, u1;
-                                    w.x = pkv::Elem<__nv_bfloat16>::pack2(o0, o1, u0, u1);
-                                    w.y = pkv::Elem<__nv_bfloat16>::pack2(o2, o3, u0, u1);
-                                }
-                                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = w;
-                            }
-                        } else {
-                            *reinterpret_cast<float4 *>(po + h * D + d) = make_float4(o0, o1, o2, o3);
-                        }
+                for (int e = 0; e < 2; ++e) {            // head 2t + e
+                    const int h = 2 * t + e;
+                    if (h >= gca) continue;
+                    const float m = e ? x1 : x0, inv = e ? inv1 : inv0;
+                    const float o0 = fmaf(acc[y][0][e], 0x1p24f, m) * inv;
+                    const float o1 = fmaf(acc[y][0][2 + e], 0x1p20f, m) * inv;
+                    const float o2 = fmaf(acc[y][1][e], 0x1p24f, m) * inv;
+                    const float o3 = fmaf(acc[y][1][2 + e], 0x1p20f, m) * inv;
+                    const int d = 32 * y + 4 * g;
+                    const float o4[4] = {o0, o1, o2, o3};
+                    if (whole) {
+                        store_row<4>(p, ((size_t)cs * p.Hq + h0 + h) * D + d, o4);
+                    } else {
+                        store_f32(po + h * D + d, o4);
                     }
                 }
-                if (g == 0) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int h = 2 * t + e;
-                        if (h >= gca) continue;
-                        const float lse = (e ? me1 : me0) + log2f(e ? l1 : l0);
-                        if (!whole) piece_lse[warp][slot][h] = lse;
-                        else if (p.lse_out) p.lse_out[(size_t)c.s * p.Hq + h0 + h] = lse;
-                    }
-                }
-                if (!whole && lane == 0) piece[warp][slot] = {tu, c.n, c.s, c.u};
-                fresh = true;
             }
-            if (++c.i == c.n) {
-                c.i = 0;
-                if (++c.u == p.U) {
-                    c.u = 0;
-                    do ++c.s; while (c.s < p.S && prefix[c.s + 1] == prefix[c.s]);
-                    if (c.s < p.S) c.n = prefix[c.s + 1] - prefix[c.s];
+            if (g == 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = 2 * t + e;
+                    if (h >= gca) continue;
+                    const float lse = (e ? me1 : me0) + log2f(e ? l1 : l0);
+                    if (!whole) piece_lse[warp][slot][h] = lse;
+                    else if (p.lse_out) p.lse_out[(size_t)cs * p.Hq + h0 + h] = lse;
                 }
+            }
+            if (!whole && lane == 0) piece[warp][slot] = {tu, n, cs, cu};
+
+            tile += count;
+            ci = 0;
+            if (++cu == p.U) {
+                cu = 0;
+                do ++cs; while (cs < p.S && len[cs] == 0);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    if (tid < 2) merge_n[tid] = 0;
+    if (tid < 2) cut_nu[tid] = 0;
     __syncthreads();
 
     // ---- join the pieces of each unit cut between this CTA's warps. A unit's
     // pieces here: one that starts it (slot 1 of some warp, or slot 0 of warp 0
-    // when it began in an earlier CTA), then slot 0 of the warps after
-    bool open0 = false, open1 = false;       // units cut at this CTA's start, at its end
-    for (int w = 0; w < kWarps; ++w) {
-        for (int sl = w == 0 ? 0 : 1; sl < 2; ++sl) {
+    // when it began in an earlier CTA), then slot 0 of the warps after. A warp
+    // takes one head of one unit, a lane 4 (D 64: 2) elements.
+    constexpr int E = D / 32;
+    {
+        static_assert(kWarps == 16 && kHeads <= kWarps, "a lane for each possible start");
+        const bool starts = lane <= kWarps && piece[lane ? lane - 1 : 0][lane ? 1 : 0].nu != 0;
+        unsigned todo = __ballot_sync(~0u, starts);
+        for (int k = 0; todo; ++k, todo &= todo - 1) {
+            const int i = __ffs(todo) - 1, w = i ? i - 1 : 0, sl = i ? 1 : 0;
+            const int h = (warp - k * p.GC) & (kWarps - 1);
+            if (h >= p.GC) continue;
             const Piece pc = piece[w][sl];
-            if (pc.nu == 0) continue;
-            int last = w;
-            while (last + 1 < kWarps && piece[last + 1][0].nu && piece[last + 1][0].tu == pc.tu) ++last;
-            const int gca = min(p.GC, p.G - (pc.u % p.NC) * p.GC);
-            const int h0 = (pc.u / p.NC) * p.G + (pc.u % p.NC) * p.GC;
-            const bool done = pc.tu >= A && pc.tu + pc.nu <= Z;
-            const int side = pc.tu < A ? 0 : 1;
-            for (int e = tid; e < gca * D; e += kThreads) {
-                const int h = e / D;
-                float mx = piece_lse[w][sl][h];
-                for (int k = w + 1; k <= last; ++k) mx = fmaxf(mx, piece_lse[k][0][h]);
-                if (mx == -INFINITY) mx = 0.f;
-                float sum = 0.f, o = 0.f;
-                for (int k = w; k <= last; ++k) {
-                    const int ks = k == w ? sl : 0;
-                    const float f = ex2(piece_lse[k][ks][h] - mx);
-                    const float *src = ks ? reinterpret_cast<const float *>(ring_all + k * NST * C::kStage)
-                                          : heads_o + (size_t)k * p.GC * D;
-                    sum += f;
-                    o = fmaf(f, src[e], o);
-                }
-                o = sum == 0.f ? 0.f : o / sum;
-                const float lse = mx + log2f(sum);
-                if (done) {
-                    pkv::store_out(p.out, ((size_t)pc.s * p.Hq + h0) * D + e, p.out_dtype, o);
-                    if (p.lse_out && e % D == 0) p.lse_out[(size_t)pc.s * p.Hq + h0 + h] = lse;
-                } else {
-                    const size_t at = (size_t)(2 * cta + side) * p.GC;
-                    p.ws_o[at * D + e] = o;
-                    if (e % D == 0) p.ws_lse[at + h] = lse;
+            const int chunk = pc.u % p.NC;
+            if (h >= min(p.GC, p.G - chunk * p.GC)) continue;
+            const int head = pc.u / p.NC * p.G + chunk * p.GC + h;
+            const bool next = lane > w && lane < kWarps && piece[lane & 15][0].nu && piece[lane & 15][0].tu == pc.tu;
+            const int more = __ffs(~(__ballot_sync(~0u, next) >> (w + 1))) - 1;      // pieces after the first
+            float l = -INFINITY;
+            if (lane <= more) l = lane ? piece_lse[w + lane][0][h] : piece_lse[w][sl][h];
+            float mx = l;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+            if (mx == -INFINITY) mx = 0.f;
+            const float f = ex2(l - mx);
+            float sum = f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            float o[E] = {};
+            for (int q = 0; q <= more; ++q) {
+                const float *src = q == 0 && sl ? reinterpret_cast<const float *>(ring_all + w * NST * C::kStage)
+                                                : heads_o + (size_t)(w + q) * p.GC * D;
+                add_scaled(o, src + h * D + lane * E, __shfl_sync(~0u, f, q));
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= inv;
+            const float lse = mx + log2f(sum);
+            if (pc.tu >= A && pc.tu + pc.nu <= Z) {
+                const size_t at = (size_t)pc.s * p.Hq + head;
+                store_row<E>(p, at * D + lane * E, o);
+                if (p.lse_out && lane == 0) p.lse_out[at] = lse;
+            } else {
+                const int side = pc.tu < A ? 0 : 1;
+                const size_t at = (size_t)(2 * cta + side) * p.GC + h;
+                store_f32(p.ws_o + at * D + lane * E, o);
+                if (lane == 0) {
+                    p.ws_lse[at] = lse;
+                    if (h == 0) {
+                        cut_tu[side] = pc.tu;
+                        cut_nu[side] = pc.nu;
+                        cut_s[side] = pc.s;
+                        cut_u[side] = pc.u;
+                    }
                 }
             }
-            open0 |= !done && side == 0;
-            open1 |= !done && side == 1;
         }
     }
-    if (!open0 && !open1) return;
+    __syncthreads();
+    if (!cut_nu[0] && !cut_nu[1]) return;
 
     // ---- units cut between CTAs: count this CTA's part in; the last to come joins
-    __syncthreads();
     if (tid == 0) {
         pkv::fence_acq_rel_gpu();
+#pragma unroll
         for (int side = 0; side < 2; ++side) {
-            if (!(side ? open1 : open0)) continue;
-            const int edge = side == 0 ? A : Z - 1;      // a subtile of the unit in this CTA
-            // its unit, from the pieces: slot 0 of warp 0, or the last piece
-            Piece pc = {0, 0, 0, 0};
-            if (side == 0) pc = piece[0][0];
-            else
-                for (int w = 0; w < kWarps; ++w)
-                    for (int sl = 0; sl < 2; ++sl)
-                        if (piece[w][sl].nu && piece[w][sl].tu <= edge &&
-                            edge < piece[w][sl].tu + piece[w][sl].nu)
-                            pc = piece[w][sl];
-            const int first = pkv::q4_owner(pc.tu, NT, CT);
-            const int n = pkv::q4_owner(pc.tu + pc.nu - 1, NT, CT) - first + 1;
-            if (atomicAdd(p.cnt + first, 1u) == (unsigned)n - 1) {
-                p.cnt[first] = 0;
-                merge_first[side] = first;
-                merge_n[side] = n;
-                scan[2 * side] = pc.s;
-                scan[2 * side + 1] = pc.u;
-            }
+            const int nu = cut_nu[side];
+            if (nu == 0) continue;
+            const int first = pkv::q4_owner(cut_tu[side], NT, CT);
+            const int n = pkv::q4_owner(cut_tu[side] + nu - 1, NT, CT) - first + 1;
+            const bool last = atomicAdd(p.cnt + first, 1u) == (unsigned)n - 1;
+            if (last) p.cnt[first] = 0;
+            cut_nu[side] = last ? n : 0;
+            cut_tu[side] = first;
         }
         pkv::fence_acq_rel_gpu();
     }
     __syncthreads();
     for (int side = 0; side < 2; ++side) {
-        const int n = merge_n[side], first = merge_first[side];
+        const int n = cut_nu[side], first = cut_tu[side];
         if (n == 0) continue;
-        const int s = scan[2 * side], u = scan[2 * side + 1];
-        const int gca = min(p.GC, p.G - (u % p.NC) * p.GC);
-        const int h0 = (u / p.NC) * p.G + (u % p.NC) * p.GC;
-        for (int e = tid; e < gca * D; e += kThreads) {
-            const int h = e / D;
-            // the first CTA's part is its side 1, the others' their side 0
-            float mx = -INFINITY;
-            for (int k = 0; k < n; ++k)
-                mx = fmaxf(mx, __ldcg(p.ws_lse + (size_t)(2 * (first + k) + (k == 0)) * p.GC + h));
-            if (mx == -INFINITY) mx = 0.f;
-            float sum = 0.f, o = 0.f;
-            for (int k = 0; k < n; ++k) {
-                const size_t at = (size_t)(2 * (first + k) + (k == 0)) * p.GC;
-                const float f = ex2(__ldcg(p.ws_lse + at + h) - mx);
-                sum += f;
-                o = fmaf(f, __ldcg(p.ws_o + at * D + e), o);
+        const int u = cut_u[side], chunk = u % p.NC;
+        const int gca = min(p.GC, p.G - chunk * p.GC);
+        // the warps of a head take every ways-th part; they meet in shared memory
+        const int ways = kWarps / gca, h = warp % gca, sub = warp / gca;
+        float o[E] = {}, m = kNone, sum = 0.f;
+        if (sub < ways) {
+#pragma unroll 4
+            for (int k = sub; k < n; k += ways) {
+                // the first CTA's part is its side 1, the others' their side 0
+                const size_t at = (size_t)(2 * (first + k) + (k == 0)) * p.GC + h;
+                const float l = __ldcg(p.ws_lse + at);
+                float x[E];
+                load_cg(x, p.ws_o + at * D + lane * E);
+                const float nm = fmaxf(m, l), f = ex2(m - nm), fx = ex2(l - nm);
+                m = nm;
+                sum = fmaf(sum, f, fx);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f, x[e] * fx);
             }
-            pkv::store_out(p.out, ((size_t)s * p.Hq + h0) * D + e, p.out_dtype,
-                           sum == 0.f ? 0.f : o / sum);
-            if (p.lse_out && e % D == 0) p.lse_out[(size_t)s * p.Hq + h0 + h] = mx + log2f(sum);
+            store_f32(heads_o + (size_t)warp * D + lane * E, o);
+            if (lane == 0) {
+                piece_lse[warp][0][0] = m;
+                piece_lse[warp][0][1] = sum;
+            }
         }
+        __syncthreads();
+        if (sub == 0) {
+            float mx = kNone, total = 0.f;
+            for (int q = 0; q < ways; ++q) mx = fmaxf(mx, piece_lse[h + q * gca][0][0]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = 0.f;
+            for (int q = 0; q < ways; ++q) {
+                const int w = h + q * gca;
+                const float f = ex2(piece_lse[w][0][0] - mx);
+                total = fmaf(piece_lse[w][0][1], f, total);
+                add_scaled(o, heads_o + (size_t)w * D + lane * E, f);
+            }
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= inv;
+            const size_t at = (size_t)cut_s[side] * p.Hq + u / p.NC * p.G + chunk * p.GC + h;
+            store_row<E>(p, at * D + lane * E, o);
+            if (p.lse_out && lane == 0) p.lse_out[at] = mx + log2f(total);
+        }
+        __syncthreads();
     }
 }
 
@@ -787,7 +923,7 @@ size_t smem_bytes(int GC) {
     return (size_t)kWarps * (NST * Cfg<D>::kStage + GC * D * sizeof(float));
 }
 
-template <int D, int NST>
+template <int D, int NST, bool B8>
 cudaError_t launch(const Q4Params &p, cudaStream_t stream) {
     // the attribute is per device and idempotent; set once for each
     static std::atomic<uint64_t> ready{0};
@@ -796,12 +932,12 @@ cudaError_t launch(const Q4Params &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(decode_q4_kernel<D, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(decode_q4_kernel<D, NST, B8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem_bytes<D, NST>(NST == 4 ? 4 : kHeads));
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_chained(decode_q4_kernel<D, NST>, dim3((unsigned)p.C), kThreads, smem_bytes<D, NST>(p.GC),
+    return launch_chained(decode_q4_kernel<D, NST, B8>, dim3((unsigned)p.C), kThreads, smem_bytes<D, NST>(p.GC),
                           stream, p);
 }
 
@@ -880,6 +1016,8 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
     if (tokens > INT32_MAX / 2 ||
         seqs * Hk * NC * ((tokens + kSub - 1) / kSub) >= (int64_t)INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
+    if ((int64_t)cache->num_blocks * Hk > INT32_MAX)     // 2^31 chunks are over 500 GB
+        return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");
     if (C == 0 && (st = pkv::device_sm_count(&C)) != PKV_OK) return st;
     const size_t need = workspace_for(C, GC, D);
     if (!workspace || workspace_bytes < need)
@@ -900,6 +1038,8 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
     p.M = M;
     p.NB = cache->num_blocks;
     p.lb = cache->block_size == 8 ? 3 : cache->block_size == 16 ? 4 : 5;
+    p.code_bytes = (uint32_t)(cache->block_size * D / 2);
+    p.par_bytes = (uint32_t)(cache->block_size * D / 32 * 4);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.kc = static_cast<const uint8_t *>(pools->k_codes);
     p.vc = static_cast<const uint8_t *>(pools->v_codes);
@@ -923,8 +1063,12 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
             (e = pkv::record_event(static_cast<cudaEvent_t>(o->timing_events[0]), s)) != cudaSuccess)
             return pkv::set_last_error(PKV_ERR_CUDA, "cudaEventRecord: %s", cudaGetErrorString(e));
         // up to 4 heads a unit leave room for a fourth stage
-        if (D == 128) e = GC <= 4 ? launch<128, 4>(p, s) : launch<128, 3>(p, s);
-        else e = GC <= 4 ? launch<64, 4>(p, s) : launch<64, 3>(p, s);
+        const bool b8 = p.lb == 3;
+        auto *go = D == 128 ? (GC <= 4 ? (b8 ? &launch<128, 4, true> : &launch<128, 4, false>)
+                                       : (b8 ? &launch<128, 3, true> : &launch<128, 3, false>))
+                            : (GC <= 4 ? (b8 ? &launch<64, 4, true> : &launch<64, 4, false>)
+                                       : (b8 ? &launch<64, 3, true> : &launch<64, 3, false>));
+        e = go(p, s);
         if (e != cudaSuccess)
             return pkv::set_last_error(PKV_ERR_CUDA, "decode_q4 launch: %s", cudaGetErrorString(e));
         if (s0 == 0 && o && o->timing_events[1] &&
