@@ -48,7 +48,7 @@ namespace {
 
 using pkv::launch_chained;
 
-constexpr int kSub = 16;             // tokens of a subtile
+constexpr int kSub = 32;             // tokens of a subtile: two halves of 16, the m and k of the mma
 constexpr int kHeads = 8;            // q heads of a unit (the n of the mma)
 constexpr int kWarps = pkv::kQ4Warps;
 constexpr int kThreads = 32 * kWarps;
@@ -68,6 +68,7 @@ struct Q4Params {
     const __half *kp, *vp;
     unsigned *cnt;                   // [C] arrivals, zero between calls
     float *ws_o, *ws_lse;            // [C][2][GC][D], [C][2][GC]
+    float *ws_pieces;                // [C][warps][GC][D], or NULL: on chip
     int C;
     float *lse_out;
     int tables_ready;
@@ -79,7 +80,9 @@ struct Cfg {
     static constexpr int NG = D / 32;
     static constexpr int kCodes = kSub * D / 2;          // bytes of a subtile's K (or V) codes
     static constexpr int kPar = kSub * 4 * NG;           // bytes of its K (or V) parameters
-    static constexpr int kStage = 2 * kCodes + 2 * kPar;
+    static constexpr int kStage = 2 * kCodes + 2 * kPar; // K codes, V codes, K parameters, V parameters
+    static constexpr int kStages = 2;
+    static constexpr int kRing = kStages * kStage;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -125,98 +128,103 @@ __device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
 
-// cp.async of 16 bytes to dst + OFF; the second form reads only `n` of them.
+// cp.async of 16 bytes to dst + OFF.
 template <int OFF>
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0+%2], [%1], 16;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
 }
 
 // The order of the 16-byte pieces of codes in a stage. Each 128-byte line has
-// its eight pieces exclusive-ored by a number of the line, so that the fragment
-// loads of K and V meet 32 banks.
+// its eight pieces exclusive-ored by a number of the line (counted within a
+// half of 16 tokens), so that the fragment loads of K and V meet 32 banks.
 template <int D>
 __device__ __forceinline__ int line_xor(int line) {
-    return D == 128 ? (line & ~1) : ((line & 1) << 2 | (line & 2));
+    return D == 128 ? (line & 6) : ((line & 1) << 2 | (line & 2));
 }
+
+// A lane's piece of the parameters: of which block of the subtile, where in the
+// block's chunk (K and V alike), where in the stage. At D 128 every lane copies
+// a piece of K and one of V; at D 64 lanes 0..15 copy K and 16..31 V.
+template <int D, int LB>
+struct ParPiece {
+    using C = Cfg<D>;
+    static constexpr int B = 1 << LB;
+    static constexpr int kPieces = B * 4 * C::NG / 16;       // a block's, K or V
+    __device__ __forceinline__ static int index(int lane) { return D == 128 ? lane : lane & 15; }
+    __device__ __forceinline__ static int block(int lane) { return index(lane) / kPieces; }
+    __device__ __forceinline__ static int source(int lane) { return index(lane) % kPieces * 16; }
+    __device__ __forceinline__ static int dst_k(int lane) { return 2 * C::kCodes + index(lane) * 16; }
+    // V: piece i of a block is tokens 8 (i % (B / 8)) .. of row i / (B / 8)
+    __device__ __forceinline__ static int dst_v(int lane) {
+        const int i = index(lane) % kPieces;
+        return 2 * C::kCodes + C::kPar + i / (B / 8) * (2 * kSub) + block(lane) * (2 * B) + i % (B / 8) * 16;
+    }
+};
 
 // A context's last subtile, or one with a block id outside the pool: what is
 // not there becomes zeros.
-template <int D>
-__device__ __noinline__ void issue_ragged(const Q4Params &p, uint32_t stage, int id0, int id1, int off,
-                                          int head, int left, int lane, uint32_t dst0,
-                                          uint32_t dst1, uint32_t dst_par) {
+template <int D, int LB>
+__device__ __noinline__ void issue_ragged(const Q4Params &p, uint32_t stage, int32_t window, int at,
+                                          int head, int left, int lane) {
     using C = Cfg<D>;
-    const int B = 1 << p.lb;
-    bool ok0 = (unsigned)id0 < (unsigned)p.NB, ok1 = (unsigned)id1 < (unsigned)p.NB;
-    if (lane == 0 && (!ok0 || (!ok1 && left > 8))) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-    if (!ok0) id0 = 0;
-    if (!ok1) id1 = 0;
-    const size_t c0 = (size_t)id0 * p.Hk + head, c1 = (size_t)id1 * p.Hk + head;
-#pragma unroll
+    using P = ParPiece<D, LB>;
+    constexpr int B = 1 << LB;
+#pragma unroll 1
     for (int j = 0; j < C::kCodes / 512; ++j) {
         const int c = lane + 32 * j, r = c / (D / 32), w = c % (D / 32);
-        const bool hi = r >= 8;
-        const size_t src = ((hi ? c1 : c0) * B + ((off + r) & (B - 1))) * (D / 2) + w * 16;
-        const bool live = (hi ? ok1 : ok0) && r < left;
-        pkv::cp_async_16(stage + (j ? dst1 : dst0), p.kc + src, live);
-        pkv::cp_async_16(stage + (j ? dst1 : dst0) + C::kCodes, p.vc + src, live);
+        int id = __shfl_sync(~0u, window, at + (r >> LB));
+        const bool ok = (unsigned)id < (unsigned)p.NB;
+        if (!ok && r < left) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+        if (!ok) id = 0;
+        const size_t src = (((size_t)id * p.Hk + head) * B + (r & (B - 1))) * (D / 2) + w * 16;
+        constexpr int kHalfLines = 16 * D / 2 / 128;
+        const int line = c >> 3;
+        const uint32_t dst = stage + line * 128 + (((c & 7) ^ line_xor<D>(line & (kHalfLines - 1))) << 4);
+        pkv::cp_async_16(dst, p.kc + src, ok && r < left);
+        pkv::cp_async_16(dst + C::kCodes, p.vc + src, ok && r < left);
     }
-    const int l = lane & 15;
-    if (l < C::kPar / 16) {
-        if (lane < 16) {
-            constexpr int kTok = 16 / (4 * C::NG);   // tokens of a piece: 1 or 2
-            const int r = l * kTok;
-            const bool hi = r >= 8;
-            const __half *src = p.kp + ((hi ? c1 : c0) * B + ((off + r) & (B - 1))) * (2 * C::NG);
-            const int live = (hi ? ok1 : ok0) ? min(kTok, max(0, left - r)) : 0;
-            pkv::cp_async_16_n(stage + dst_par, src, live * 4 * C::NG);
-        } else {
-            const bool hi = l & 1;
-            const __half *src = p.vp + ((hi ? c1 : c0) * (2 * C::NG) + (l >> 1)) * B +
-                                ((off + 8 * hi) & (B - 1));
-            const int live = (hi ? ok1 : ok0) ? min(8, max(0, left - 8 * hi)) : 0;
-            pkv::cp_async_16_n(stage + dst_par, src, live * 2);
-        }
+    int id = __shfl_sync(~0u, window, at + P::block(lane));
+    const bool ok = (unsigned)id < (unsigned)p.NB;
+    if (!ok) id = 0;
+    const size_t src = ((size_t)id * p.Hk + head) * p.par_bytes + P::source(lane);
+    const int t0 = P::block(lane) * B;               // first token of the piece's block
+    if (D == 128 || lane < 16) {
+        constexpr int kTok = 16 / (4 * C::NG);       // tokens of a K piece: 1 or 2
+        const int r = t0 + P::source(lane) / 16 * kTok;
+        const int live = ok ? min(kTok, max(0, left - r)) : 0;
+        pkv::cp_async_16_n(stage + P::dst_k(lane), reinterpret_cast<const uint8_t *>(p.kp) + src, live * 4 * C::NG);
+    }
+    if (D == 128 || lane >= 16) {
+        const int r = t0 + P::source(lane) / 16 % (B / 8) * 8;
+        const int live = ok ? min(8, max(0, left - r)) : 0;
+        pkv::cp_async_16_n(stage + P::dst_v(lane), reinterpret_cast<const uint8_t *>(p.vp) + src, live * 2);
     }
 }
 
 // Copies one warp's subtiles into its stages, ahead of their use. The place of
 // the next subtile is kept as the sequence and unit it belongs to, its first
 // token and the tokens left from there.
-template <int D, bool B8>
+template <int D, int LB>
 struct Loader {
     using C = Cfg<D>;
+    using P = ParPiece<D, LB>;
+    static constexpr int kBlocks = kSub >> LB;       // of a subtile: 4, 2 or 1
     const Q4Params &p;
-    const int *prefix, *len;         // shared memory: subtiles before a sequence, its length
+    const int *len;                  // shared memory: a sequence's length
     int lane;
     int s, u, head, t0, left;
     int32_t window, next_window;     // table entries: lane holds entry `base + lane` of each
     int base;
     uint32_t dst0, dst1;             // this lane's pieces of the codes in a stage
-    uint32_t dst_par;                // and of the parameters
-    const uint8_t *par;              // the parameters' source in chunk 0
-    uint32_t par_tok;                // bytes from one token's to the next's
-    bool par_hi;                     // blocks of 8: from the second block
+    uint32_t dst_k, dst_v;           // and of the parameters
 
-    __device__ __forceinline__ Loader(const Q4Params &p_, const int *prefix_, const int *len_, int lane_)
-        : p(p_), prefix(prefix_), len(len_), lane(lane_) {
+    __device__ __forceinline__ Loader(const Q4Params &p_, const int *len_, int lane_)
+        : p(p_), len(len_), lane(lane_) {
         const int line = lane >> 3;
         dst0 = line * 128 + (((lane & 7) ^ line_xor<D>(line)) << 4);
         dst1 = (line + 4) * 128 + (((lane & 7) ^ line_xor<D>(line + 4)) << 4);
-        dst_par = 2 * C::kCodes + (lane >> 4) * C::kPar + (lane & 15) * 16;
-        // parameters: lanes 0..15 copy K's (token-major), 16..31 V's: piece l is
-        // tokens 8 (l & 1) .. of row l / 2 of [2 NG][B]
-        const int l = lane & 15;
-        const bool is_v = lane >= 16;
-        par = reinterpret_cast<const uint8_t *>(is_v ? p.vp : p.kp);
-        par_tok = is_v ? 2 : 4 * C::NG;
-        if (B8) {
-            par_hi = is_v ? l & 1 : l * 16 >= C::kPar / 2;
-            par += is_v ? (l >> 1) * 16 : l * 16 - (par_hi ? C::kPar / 2 : 0);
-        } else {
-            par_hi = false;
-            par += is_v ? (((l >> 1) << p.lb) + 8 * (l & 1)) * 2 : l * 16;
-        }
+        dst_k = P::dst_k(lane);
+        dst_v = P::dst_v(lane);
     }
 
     __device__ __forceinline__ int32_t entries(int from) const {
@@ -224,7 +232,7 @@ struct Loader {
         return e < p.M ? __ldg(p.tables + (int64_t)s * p.M + e) : -1;
     }
     __device__ __forceinline__ void windows() {
-        base = (t0 >> p.lb) & ~31;
+        base = (t0 >> LB) & ~31;
         window = entries(base);
         next_window = entries(base + 32);
     }
@@ -241,7 +249,7 @@ struct Loader {
         t0 += kSub;
         left -= kSub;
         if (left > 0) {
-            if ((t0 >> p.lb) >= base + 32) {
+            if ((t0 >> LB) >= base + 32) {
                 base += 32;
                 window = next_window;
                 next_window = entries(base + 32);
@@ -258,37 +266,53 @@ struct Loader {
         left = len[s];
         windows();
     }
+    // Piece J of the codes, K and V, from `src` on.
+    template <int J>
+    __device__ __forceinline__ void codes(uint32_t stage, uint64_t src) const {
+        // at D 128 a half has eight lines, two pieces' worth; at D 64 four
+        constexpr int OFF = D == 128 ? J / 2 * 1024 : J * 512;
+        const uint32_t dst = stage + (D == 128 && J % 2 ? dst1 : dst0);
+        copy16<OFF>(dst, p.kc + src);
+        copy16<OFF + C::kCodes>(dst, p.vc + src);
+    }
     __device__ __forceinline__ void issue(uint32_t stage) {
-        // the block of the subtile's tokens 0..7, and of 8..15 (the same unless
-        // a block holds 8)
-        const int at = (t0 >> p.lb) - base;
-        const int id0 = __shfl_sync(~0u, window, at);
-        const int id1 = B8 ? __shfl_sync(~0u, window, at + 1) : id0;
-        const int off = B8 ? 0 : t0 & ((1 << p.lb) - 1);
-        if (left >= kSub && (unsigned)id0 < (unsigned)p.NB && (!B8 || (unsigned)id1 < (unsigned)p.NB)) {
-            // a whole subtile: its codes are 16 D / 2 bytes in a row (two runs
-            // where blocks hold 8)
-            const uint32_t c0 = id0 * p.Hk + head, c1 = B8 ? id1 * p.Hk + head : c0;
-            if (D == 128) {
-                const uint64_t o0 = (uint64_t)c0 * p.code_bytes + (off * (D / 2) + lane * 16);
-                const uint64_t o1 = B8 ? (uint64_t)c1 * p.code_bytes + lane * 16 : o0 + 512;
-                copy16<0>(stage + dst0, p.kc + o0);
-                copy16<0>(stage + dst1, p.kc + o1);
-                copy16<C::kCodes>(stage + dst0, p.vc + o0);
-                copy16<C::kCodes>(stage + dst1, p.vc + o1);
-            } else {
-                // 32 pieces: lanes 16.. are tokens 8..
-                const uint64_t o = B8 ? (uint64_t)(lane >= 16 ? c1 : c0) * p.code_bytes + (lane & 15) * 16
-                                      : (uint64_t)c0 * p.code_bytes + (off * (D / 2) + lane * 16);
-                copy16<0>(stage + dst0, p.kc + o);
-                copy16<C::kCodes>(stage + dst0, p.vc + o);
-            }
-            if (C::kPar == 256 || (lane & 15) < 8)
-                copy16<0>(stage + dst_par,
-                          par + ((uint64_t)(B8 && par_hi ? c1 : c0) * p.par_bytes + off * par_tok));
+        const int at = (t0 >> LB) - base;
+        uint32_t chunk[kBlocks];
+        bool ok = left >= kSub;
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+            const int id = __shfl_sync(~0u, window, at + k);
+            ok &= (unsigned)id < (unsigned)p.NB;
+            chunk[k] = id * p.Hk + head;
+        }
+        if (!ok) {
+            issue_ragged<D, LB>(p, stage, window, at, head, left, lane);
             return;
         }
-        issue_ragged<D>(p, stage, id0, id1, off, head, left, lane, dst0, dst1, dst_par);
+        // a chunk's codes lie in a row: lanes take neighbouring pieces
+        const uint32_t piece = lane * 16;
+        if constexpr (D == 128) {
+            constexpr int PER = 1 << (LB - 3);           // 512-byte pieces of a chunk
+            codes<0>(stage, (uint64_t)chunk[0] * p.code_bytes + piece);
+            codes<1>(stage, (uint64_t)chunk[1 / PER] * p.code_bytes + (piece + 1 % PER * 512));
+            codes<2>(stage, (uint64_t)chunk[2 / PER] * p.code_bytes + (piece + 2 % PER * 512));
+            codes<3>(stage, (uint64_t)chunk[3 / PER] * p.code_bytes + (piece + 3 % PER * 512));
+        } else if constexpr (LB == 3) {
+            const bool up = lane >= 16;                  // 256-byte chunks: two in a piece
+            const uint32_t half = (lane & 15) * 16;
+            codes<0>(stage, (uint64_t)(up ? chunk[1] : chunk[0]) * p.code_bytes + half);
+            codes<1>(stage, (uint64_t)(up ? chunk[3] : chunk[2]) * p.code_bytes + half);
+        } else {
+            constexpr int PER = 1 << (LB - 4);
+            codes<0>(stage, (uint64_t)chunk[0] * p.code_bytes + piece);
+            codes<1>(stage, (uint64_t)chunk[1 / PER] * p.code_bytes + (piece + 1 % PER * 512));
+        }
+        uint32_t c = chunk[0];
+#pragma unroll
+        for (int k = 1; k < kBlocks; ++k) c = P::block(lane) == k ? chunk[k] : c;
+        const uint64_t src = (uint64_t)c * p.par_bytes + P::source(lane);
+        if (D == 128 || lane < 16) copy16<0>(stage + dst_k, reinterpret_cast<const uint8_t *>(p.kp) + src);
+        if (D == 128 || lane >= 16) copy16<0>(stage + dst_v, reinterpret_cast<const uint8_t *>(p.vp) + src);
     }
 };
 
@@ -345,7 +369,7 @@ struct Piece {
     int tu, nu, s, u;     // the unit's first subtile and length in the list; its place; nu 0: none
 };
 
-template <int D, int NST, bool B8>
+template <int D, int LB>
 __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_constant__ Q4Params p) {
     using C = Cfg<D>;
     constexpr int NG = C::NG;
@@ -356,7 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
     __shared__ float piece_lse[kWarps][2][kHeads];
     __shared__ int cut_tu[2], cut_nu[2], cut_s[2], cut_u[2];      // units cut at the CTA's start, end
     uint8_t *ring_all = smem;
-    float *heads_o = reinterpret_cast<float *>(smem + kWarps * NST * C::kStage);   // [warp][GC][D]
+    // places of the pieces that end in a warp, [warp][GC][D]: behind the rings
+    // where they fit, else this CTA's part of the workspace
+    float *heads_o = p.ws_pieces ? p.ws_pieces + (size_t)blockIdx.x * kWarps * p.GC * D
+                                 : reinterpret_cast<float *>(smem + kWarps * C::kRing);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pkv::grid_dependents_launch();
@@ -418,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
     const int A = pkv::q4_cta_cut(cta, NT, CT), Z = pkv::q4_cta_cut(cta + 1, NT, CT);
     const int a = pkv::q4_warp_cut(warp, A, Z), z = pkv::q4_warp_cut(warp + 1, A, Z);
 
-    const uint32_t ring = pkv::smem_u32(ring_all) + warp * NST * C::kStage;
+    const uint32_t ring = pkv::smem_u32(ring_all) + warp * C::kRing;
     const int g = lane >> 2, t = lane & 3;
 
     if (a < z) {
@@ -436,19 +463,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             cu = r / n;
             ci = r - cu * n;
         }
-        const uint32_t ring_end = ring + NST * C::kStage;
-        Loader<D, B8> ld(p, prefix, len, lane);
+        Loader<D, LB> ld(p, len, lane);
         ld.start(cs, cu, ci);
         int to_issue = z - a;
 #pragma unroll
-        for (int st = 0; st < NST - 1; ++st) {
+        for (int st = 0; st < C::kStages; ++st) {
             if (to_issue > 0) {
                 ld.issue(ring + st * C::kStage);
                 if (--to_issue) ld.advance();
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        uint32_t sk = ring, fill = ring + (NST - 1) * C::kStage;      // stage to use, to fill
+        uint32_t sk = ring;                  // stage in use
         // this lane's places in a stage (see below)
         const int r0 = 4 * (g >> 1) + (g & 1);
         uint32_t k_at, v_at, m_at;
@@ -460,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             v_at = t * 128 + (((g >> 2) ^ line_xor<D>(t)) << 4) + 4 * (g & 3);
         }
         m_at = 2 * NG + (NG == 4 ? 4 * (t & 1) : 0);                 // minima of two groups in a K row
-        const uint32_t vm_at = (NG + (g & (NG - 1))) * 32 + t * 8;   // minima of a group, V
+        const uint32_t vm_at = (NG + (g & (NG - 1))) * (2 * kSub) + t * 8;   // minima of a group, V
         const uint32_t one = g == 0 ? 0x3c003c00u : 0u;
 
         for (int tile = a; tile < z;) {
@@ -534,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 zs1 = __shfl_sync(~0u, zq, 8 * t + 4);
             }
             float me0 = kNone, me1 = kNone;      // reference exponents
-            float room = 15.f;                   // largest score above the reference
+            float mu0 = 0.f, mu1 = 0.f;          // what scores are taken against: these, or 0
+            float room = -INFINITY;              // largest score above them that needs no new ones
             uint32_t sbound = 0x3c003c00u;       // V scales so far stay at or below it (1)
             float acc[NG][2][4], accx[4];
 #pragma unroll
@@ -547,23 +574,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             for (int i = 0; i < 4; ++i) accx[i] = 0.f;
 
           for (int it = 0; it < count; ++it) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
-            // the stage used last is free now: fill it
-            if (to_issue > 0) {
-                ld.issue(fill);
-                if (--to_issue) ld.advance();
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-
             const uint32_t sv = sk + C::kCodes, pk = sk + 2 * C::kCodes, pv = pk + C::kPar;
-            const uint32_t k_row = sk + k_at, v_row = sv + v_at, pk_row = pk + r0 * (4 * NG);
-            fill = sk;
+            constexpr int kHalfCodes = C::kCodes / 2, kHalfPar = C::kPar / 2;
 
-            // ---- scores: rows g and g + 8 of the product are tokens r0 and r0 + 2,
-            // so that after the transpose below lane t holds tokens 4t .. 4t + 3
-            float sc[4];
-            {
+            // ---- scores: rows g and g + 8 of the product are tokens r0 and r0 + 2 of a
+            // half, so that after the transpose below lane t holds tokens 4t .. 4t + 3
+            float sc[2][4];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t k_row = sk + k_at + half * kHalfCodes;
+                const uint32_t pk_row = pk + r0 * (4 * NG) + half * kHalfPar;
                 uint32_t w[2][NG];
                 if constexpr (NG == 4) {
                     pkv::lds_u32x4(k_row, w[0][0], w[0][1], w[0][2], w[0][3]);
@@ -590,56 +612,59 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     if (NG == 2 && t >= 2) m = 0;
                     (h ? m1 : m0) = m;
                 }
-                float mn[4];
-                mma8_zero(mn, m0, m1, qsum);
+                float x[4];
+                mma8_zero(x, m0, m1, qsum);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[i] = mn[i] * 0x1p-18f;
+                for (int i = 0; i < 4; ++i) x[i] *= 0x1p-18f;
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
                     float d[4];
                     uint32_t wa = w[0][y], wb = w[1][y];
                     mma16_zero(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
-                          qb[y][0][0], qb[y][0][1]);
+                               qb[y][0][0], qb[y][0][1]);
                     wa >>= 8;
                     wb >>= 8;
                     mma16(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
                           qb[y][1][0], qb[y][1][1]);
-                    sc[0] = fmaf(d[0], s0[y], sc[0]);
-                    sc[1] = fmaf(d[1], s0[y], sc[1]);
-                    sc[2] = fmaf(d[2], s1[y], sc[2]);
-                    sc[3] = fmaf(d[3], s1[y], sc[3]);
+                    x[0] = fmaf(d[0], s0[y], x[0]);
+                    x[1] = fmaf(d[1], s0[y], x[1]);
+                    x[2] = fmaf(d[2], s1[y], x[2]);
+                    x[3] = fmaf(d[3], s1[y], x[3]);
                 }
+                // exponents of the weights, against the reference
+                sc[half][0] = fmaf(x[0], zs0, -mu0);
+                sc[half][1] = fmaf(x[1], zs1, -mu1);
+                sc[half][2] = fmaf(x[2], zs0, -mu0);
+                sc[half][3] = fmaf(x[3], zs1, -mu1);
             }
-            // exponents of the weights, against the reference
-            const float raw[4] = {sc[0], sc[1], sc[2], sc[3]};
-            sc[0] = fmaf(raw[0], zs0, -me0);
-            sc[1] = fmaf(raw[1], zs1, -me1);
-            sc[2] = fmaf(raw[2], zs0, -me0);
-            sc[3] = fmaf(raw[3], zs1, -me1);
             if (left < kSub) {
-                if (r0 >= left) sc[0] = sc[1] = -INFINITY;
-                if (r0 + 2 >= left) sc[2] = sc[3] = -INFINITY;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (r0 + 16 * half >= left) sc[half][0] = sc[half][1] = -INFINITY;
+                    if (r0 + 16 * half + 2 >= left) sc[half][2] = sc[half][3] = -INFINITY;
+                }
             }
             left -= kSub;
 
             // ---- V scales of tokens 4t .. 4t + 3, and the reference exponent
-            uint32_t vs[NG][2];
+            // (the scales are read again where they are used: held, they would spill)
             __half2 big = __float2half2_rn(0.f);
 #pragma unroll
-            for (int y = 0; y < NG; ++y) {
-                lds64(pv + y * 32 + t * 8, vs[y][0], vs[y][1]);
-                big = __hmax2(big, __hmax2(as_h2(vs[y][0]), as_h2(vs[y][1])));
-            }
-            const float over = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int y = 0; y < NG; ++y) {
+                    uint32_t v0, v1;
+                    lds64(pv + y * (2 * kSub) + half * 32 + t * 8, v0, v1);
+                    big = __hmax2(big, __hmax2(as_h2(v0), as_h2(v1)));
+                }
+            const float over = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                                     fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
             if (__any_sync(~0u, over > room || !__hble2(big, as_h2(sbound)))) {
                 // raise the bound on V scales to this subtile's largest, the
                 // reference to 7 (less where scales are large) below the top score
                 float bs = fmaxf(__low2float(big), __high2float(big));
-                float zz[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    zz[i] = sc[i] == -INFINITY ? -INFINITY : raw[i] * (i & 1 ? zs1 : zs0);
-                float t0 = fmaxf(zz[0], zz[2]), t1 = fmaxf(zz[1], zz[3]);
+                float t0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2])) + mu0;
+                float t1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3])) + mu1;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     bs = fmaxf(bs, __shfl_xor_sync(~0u, bs, o));
@@ -650,17 +675,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 }
                 bs = fminf(fmaxf(bs, __low2float(as_h2(sbound))), 65504.f);
                 sbound = as_u32(__float2half2_rn(bs));
-                // scales up to 2^e, e >= 0: weights up to 2^(15 - e)
-                const int e = ((int)(__float_as_uint(bs) >> 23) - 127) + 1;
-                room = 15.f - (float)e;
-                const float n0 = fmaxf(me0, t0 - 7.f + (float)e), n1 = fmaxf(me1, t1 - 7.f + (float)e);
+                // scales up to 2^e, e >= 1: weights up to 2^(15 - e)
+                const float e = (float)((int)(__float_as_uint(bs) >> 23) - 126);
+                const float n0 = fmaxf(me0, t0 - 7.f + e), n1 = fmaxf(me1, t1 - 7.f + e);
                 const float f0 = ex2(me0 - n0), f1 = ex2(me1 - n1);
+                // a head that has had no score but -infinity keeps none, and
+                // the next subtile asks again
+                room = __any_sync(~0u, n0 == kNone || n1 == kNone) ? -INFINITY : 15.f - e;
                 me0 = n0;
                 me1 = n1;
-                sc[0] = zz[0] - n0;
-                sc[1] = zz[1] - n1;
-                sc[2] = zz[2] - n0;
-                sc[3] = zz[3] - n1;
+                const float u0 = n0 == kNone ? 0.f : n0, u1 = n1 == kNone ? 0.f : n1;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    sc[half][0] = sc[half][0] + mu0 - u0;
+                    sc[half][1] = sc[half][1] + mu1 - u1;
+                    sc[half][2] = sc[half][2] + mu0 - u0;
+                    sc[half][3] = sc[half][3] + mu1 - u1;
+                }
+                mu0 = u0;
+                mu1 = u1;
 #pragma unroll
                 for (int y = 0; y < NG; ++y)
 #pragma unroll
@@ -676,58 +709,69 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 accx[3] *= f1;
             }
 
-            // ---- weights, transposed: lane (g, t) then has head g, tokens 4t .. 4t + 3
-            const uint32_t p01 =
-                transpose8(as_u32(__floats2half2_rn(ex2(sc[0]), ex2(sc[1]))));
-            const uint32_t p23 =
-                transpose8(as_u32(__floats2half2_rn(ex2(sc[2]), ex2(sc[3]))));
-
-            // ---- V: rows of the product are d, its contracted index the tokens
-            uint32_t v01[NG], v23[NG];
-            {
-                // tokens 4t .. 4t + 3: two lines of two rows (D 64: one line of four)
-                uint32_t w[4][NG / 2];
-                if constexpr (NG == 4) {
-                    lds64(v_row, w[0][0], w[0][1]);
-                    lds64(v_row ^ 64u, w[1][0], w[1][1]);
-                    lds64(v_row + 128, w[2][0], w[2][1]);
-                    lds64((v_row ^ 64u) + 128, w[3][0], w[3][1]);
-                } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j][0] = pkv::lds_u32(v_row ^ (32u * j));
+            for (int half = 0; half < 2; ++half) {
+                // ---- weights, transposed: lane (g, t) has head g, tokens 4t .. 4t + 3
+                const uint32_t p01 =
+                    transpose8(as_u32(__floats2half2_rn(ex2(sc[half][0]), ex2(sc[half][1]))));
+                const uint32_t p23 =
+                    transpose8(as_u32(__floats2half2_rn(ex2(sc[half][2]), ex2(sc[half][3]))));
+                // ---- V: rows of the product are d, its contracted index the tokens
+                uint32_t v01[NG], v23[NG];
+                {
+                    // tokens 4t .. 4t + 3: two lines of two rows (D 64: one line of four)
+                    const uint32_t v_row = sv + v_at + half * kHalfCodes;
+                    uint32_t w[4][NG / 2];
+                    if constexpr (NG == 4) {
+                        lds64(v_row, w[0][0], w[0][1]);
+                        lds64(v_row ^ 64u, w[1][0], w[1][1]);
+                        lds64(v_row + 128, w[2][0], w[2][1]);
+                        lds64((v_row ^ 64u) + 128, w[3][0], w[3][1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j][0] = pkv::lds_u32(v_row ^ (32u * j));
+                    }
+#pragma unroll
+                    for (int y = 0; y < NG; ++y) {
+                        const uint32_t sel = y & 1 ? 0x7632u : 0x5410u;
+                        v01[y] = __byte_perm(w[0][y / 2], w[1][y / 2], sel);
+                        v23[y] = __byte_perm(w[2][y / 2], w[3][y / 2], sel);
+                    }
+                }
+                {
+                    // minima as rows 0..NG-1, a row of ones as row 8
+                    uint32_t m01, m23;
+                    lds64(pv + vm_at + half * 32, m01, m23);
+                    if (g >= NG) m01 = m23 = 0;
+                    mma16(accx, m01, one, m23, one, p01, p23);
                 }
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
-                    const uint32_t sel = y & 1 ? 0x7632u : 0x5410u;
-                    v01[y] = __byte_perm(w[0][y / 2], w[1][y / 2], sel);
-                    v23[y] = __byte_perm(w[2][y / 2], w[3][y / 2], sel);
-                }
-            }
-            {
-                // minima as rows 0..NG-1, a row of ones as row 8
-                uint32_t m01, m23;
-                lds64(pv + vm_at, m01, m23);
-                if (g >= NG) m01 = m23 = 0;
-                mma16(accx, m01, one, m23, one, p01, p23);
-            }
+                    uint32_t vs0, vs1;
+                    lds64(pv + y * (2 * kSub) + half * 32 + t * 8, vs0, vs1);
+                    const __half2 s01 = as_h2(vs0), s23 = as_h2(vs1);
+                    const __half2 h01 = __hmul2(as_h2(p01), s01), h23 = __hmul2(as_h2(p23), s23);
+                    const uint32_t l01 = as_u32(__hfma2(as_h2(p01), s01, __hneg2(h01)));
+                    const uint32_t l23 = as_u32(__hfma2(as_h2(p23), s23, __hneg2(h23)));
 #pragma unroll
-            for (int y = 0; y < NG; ++y) {
-                const __half2 h01 = __hmul2(as_h2(p01), as_h2(vs[y][0]));
-                const __half2 h23 = __hmul2(as_h2(p23), as_h2(vs[y][1]));
-                const uint32_t l01 = as_u32(__hfma2(as_h2(p01), as_h2(vs[y][0]), __hneg2(h01)));
-                const uint32_t l23 = as_u32(__hfma2(as_h2(p23), as_h2(vs[y][1]), __hneg2(h23)));
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t wa = v01[y] >> (8 * k), wb = v23[y] >> (8 * k);
-                    const uint32_t a0 = wa & 0x000f000fu, a1 = wa & 0x00f000f0u;
-                    const uint32_t a2 = wb & 0x000f000fu, a3 = wb & 0x00f000f0u;
-                    mma16(acc[y][k], a0, a1, a2, a3, as_u32(h01), as_u32(h23));
-                    mma16(acc[y][k], a0, a1, a2, a3, l01, l23);
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t wa = v01[y] >> (8 * k), wb = v23[y] >> (8 * k);
+                        const uint32_t a0 = wa & 0x000f000fu, a1 = wa & 0x00f000f0u;
+                        const uint32_t a2 = wb & 0x000f000fu, a3 = wb & 0x00f000f0u;
+                        mma16(acc[y][k], a0, a1, a2, a3, as_u32(h01), as_u32(h23));
+                        mma16(acc[y][k], a0, a1, a2, a3, l01, l23);
+                    }
                 }
             }
 
-            sk += C::kStage;
-            if (sk == ring_end) sk = ring;
+            // ---- the stage is used up: fill it with the subtile after next
+            __syncwarp();
+            if (to_issue > 0) {
+                ld.issue(sk);
+                if (--to_issue) ld.advance();
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            sk = 2 * ring + C::kStage - sk;
           }
 
             // ---- the unit's output, or a piece of it
@@ -738,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
             // a piece of a unit that goes on in the next warp lies in this
             // warp's ring, which is read to the end; the other has its own place
-            float *po = slot ? reinterpret_cast<float *>(ring_all + warp * NST * C::kStage)
+            float *po = slot ? reinterpret_cast<float *>(ring_all + warp * C::kRing)
                              : heads_o + (size_t)warp * p.GC * D;
             if (slot && !whole) __syncwarp();
 #pragma unroll
@@ -818,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
             float o[E] = {};
             for (int q = 0; q <= more; ++q) {
-                const float *src = q == 0 && sl ? reinterpret_cast<const float *>(ring_all + w * NST * C::kStage)
+                const float *src = q == 0 && sl ? reinterpret_cast<const float *>(ring_all + w * C::kRing)
                                                 : heads_o + (size_t)(w + q) * p.GC * D;
                 add_scaled(o, src + h * D + lane * E, __shfl_sync(~0u, f, q));
             }
@@ -917,13 +961,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
     }
 }
 
-// Shared memory of a variant: the rings, then a piece's place for each warp.
-template <int D, int NST>
+// Whether the warps' pieces fit behind the rings (they do but for more than 4
+// heads at D 128, which take them to the workspace).
+constexpr bool pieces_on_chip(int GC, int D) { return D == 64 || GC <= 4; }
+
+template <int D>
 size_t smem_bytes(int GC) {
-    return (size_t)kWarps * (NST * Cfg<D>::kStage + GC * D * sizeof(float));
+    return (size_t)kWarps * (Cfg<D>::kRing + (pieces_on_chip(GC, D) ? GC * D * sizeof(float) : 0));
 }
 
-template <int D, int NST, bool B8>
+template <int D, int LB>
 cudaError_t launch(const Q4Params &p, cudaStream_t stream) {
     // the attribute is per device and idempotent; set once for each
     static std::atomic<uint64_t> ready{0};
@@ -932,22 +979,22 @@ cudaError_t launch(const Q4Params &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(decode_q4_kernel<D, NST, B8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_bytes<D, NST>(NST == 4 ? 4 : kHeads));
+        const size_t most = smem_bytes<D>(4) > smem_bytes<D>(kHeads) ? smem_bytes<D>(4) : smem_bytes<D>(kHeads);
+        e = cudaFuncSetAttribute(decode_q4_kernel<D, LB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_chained(decode_q4_kernel<D, NST, B8>, dim3((unsigned)p.C), kThreads, smem_bytes<D, NST>(p.GC),
-                          stream, p);
+    return launch_chained(decode_q4_kernel<D, LB>, dim3((unsigned)p.C), kThreads, smem_bytes<D>(p.GC), stream, p);
 }
 
 bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 // workspace: [PKV_MAX_DECODE_CTAS] arrival counters (a fixed region, whatever
-// the launch), then [C][2][GC][D] outputs, then [C][2][GC] log2 denominators
+// the launch), then [C][2][GC][D] outputs, then the warps' pieces where they
+// do not fit on chip, then [C][2][GC] log2 denominators
 constexpr size_t kCounterBytes = PKV_MAX_DECODE_CTAS * sizeof(unsigned);
 size_t workspace_for(int C, int GC, int D) {
-    return kCounterBytes + (size_t)C * 2 * GC * (D + 1) * sizeof(float);
+    return kCounterBytes + (size_t)C * GC * (2 * (D + 1) + (pieces_on_chip(GC, D) ? 0 : kWarps * D)) * sizeof(float);
 }
 
 }  // namespace
@@ -1047,7 +1094,12 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
     p.vp = static_cast<const __half *>(pools->v_params);
     p.cnt = static_cast<unsigned *>(workspace);
     p.ws_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
-    p.ws_lse = p.ws_o + (size_t)C * 2 * GC * D;
+    float *after = p.ws_o + (size_t)C * 2 * GC * D;
+    if (!pieces_on_chip(GC, D)) {
+        p.ws_pieces = after;
+        after += (size_t)C * kWarps * GC * D;
+    }
+    p.ws_lse = after;
     p.C = C;
     p.tables_ready = o && o->tables_ready;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1062,12 +1114,8 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
         if (s0 == 0 && o && o->timing_events[0] &&
             (e = pkv::record_event(static_cast<cudaEvent_t>(o->timing_events[0]), s)) != cudaSuccess)
             return pkv::set_last_error(PKV_ERR_CUDA, "cudaEventRecord: %s", cudaGetErrorString(e));
-        // up to 4 heads a unit leave room for a fourth stage
-        const bool b8 = p.lb == 3;
-        auto *go = D == 128 ? (GC <= 4 ? (b8 ? &launch<128, 4, true> : &launch<128, 4, false>)
-                                       : (b8 ? &launch<128, 3, true> : &launch<128, 3, false>))
-                            : (GC <= 4 ? (b8 ? &launch<64, 4, true> : &launch<64, 4, false>)
-                                       : (b8 ? &launch<64, 3, true> : &launch<64, 3, false>));
+        auto *go = D == 128 ? (p.lb == 3 ? &launch<128, 3> : p.lb == 4 ? &launch<128, 4> : &launch<128, 5>)
+                            : (p.lb == 3 ? &launch<64, 3> : p.lb == 4 ? &launch<64, 4> : &launch<64, 5>);
         e = go(p, s);
         if (e != cudaSuccess)
             return pkv::set_last_error(PKV_ERR_CUDA, "decode_q4 launch: %s", cudaGetErrorString(e));

@@ -177,6 +177,8 @@ def test_q4_workspace_formula(L):
     # 4096 arrival counters, then C CTAs x 2 pieces x heads x (D outputs + 1 denominator)
     assert L.pkv_decode_q4_workspace_bytes(REF(_q4desc(hk=8)), 32, 10) == 4096 * 4 + 10 * 2 * 4 * 129 * 4
     assert L.pkv_decode_q4_workspace_bytes(REF(_q4desc(hk=1, d=64)), 12, 3) == 4096 * 4 + 3 * 2 * 8 * 65 * 4
+    # more than 4 heads at head size 128: and 16 warps' pieces a CTA
+    assert L.pkv_decode_q4_workspace_bytes(REF(_q4desc(hk=1)), 8, 3) == 4096 * 4 + 3 * 8 * (2 * 129 + 16 * 128) * 4
     assert L.pkv_decode_q4_workspace_bytes(REF(_q4desc()), 3, 10) == 0
     assert L.pkv_decode_q4_workspace_bytes(REF(_q4desc()), 4, 4097) == 0
 
