@@ -53,8 +53,8 @@ constexpr int kHeads = 8;            // q heads of a unit (the n of the mma)
 constexpr int kWarps = pkv::kQ4Warps;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSeqs = 1024;       // sequences of one launch
-constexpr float kNone = -3e38f;      // reference exponent before the first score: finite, so
-                                     // that a score of -infinity still has weight 0
+constexpr float kNone = 2e-38f;      // reference exponent of a head before its first finite
+                                     // score: 0 to any score, and no score's own
 
 struct Q4Params {
     const void *q;
@@ -217,9 +217,15 @@ struct Loader {
     int base;
     uint32_t dst0, dst1;             // this lane's pieces of the codes in a stage
     uint32_t dst_k, dst_v;           // and of the parameters
+    // The warp's place for one unit's q rows [GC][D]. A unit whose turn comes
+    // while the last rows there have been taken up gets its own copied with its
+    // first subtile; read from memory only when they are wanted, under the
+    // stream of K and V, they cost a warp 3 us a unit.
+    uint32_t q_buf;
+    int q_unit;                      // the unit whose rows lie there (s * U + u); -1: none
 
-    __device__ __forceinline__ Loader(const Q4Params &p_, const int *len_, int lane_)
-        : p(p_), len(len_), lane(lane_) {
+    __device__ __forceinline__ Loader(const Q4Params &p_, const int *len_, int lane_, uint32_t q_buf_)
+        : p(p_), len(len_), lane(lane_), q_buf(q_buf_), q_unit(-1) {
         const int line = lane >> 3;
         dst0 = line * 128 + (((lane & 7) ^ line_xor<D>(line)) << 4);
         dst1 = (line + 4) * 128 + (((lane & 7) ^ line_xor<D>(line + 4)) << 4);
@@ -236,6 +242,15 @@ struct Loader {
         window = entries(base);
         next_window = entries(base + 32);
     }
+    __device__ __forceinline__ void fetch_q() {
+        if (q_unit >= 0) return;
+        q_unit = s * p.U + u;
+        const int chunk = u - head * p.NC;
+        const int gca = min(p.GC, p.G - chunk * p.GC);
+        const uint8_t *src = static_cast<const uint8_t *>(p.q) +
+                             ((size_t)s * p.Hq + head * p.G + chunk * p.GC) * (D * 2);
+        for (int i = lane * 16; i < gca * D * 2; i += 512) copy16<0>(q_buf + i, src + i);
+    }
     __device__ __forceinline__ void start(int seq, int unit, int subtile) {
         s = seq;
         u = unit;
@@ -243,9 +258,11 @@ struct Loader {
         t0 = subtile * kSub;
         left = len[s] - t0;
         windows();
+        fetch_q();
     }
-    // Next subtile; the table's row starts again with each unit.
-    __device__ __forceinline__ void advance() {
+    // Next subtile; the table's row starts again with each unit. Returns the
+    // places passed over.
+    __device__ __forceinline__ int advance() {
         t0 += kSub;
         left -= kSub;
         if (left > 0) {
@@ -254,17 +271,18 @@ struct Loader {
                 window = next_window;
                 next_window = entries(base + 32);
             }
-            return;
+            return 0;
         }
         if (++u == p.U) {
             u = 0;
-            do ++s; while (s < p.S && len[s] == 0);
-            if (s >= p.S) return;                // the list's end
+            do ++s; while (s < p.S - 1 && len[s] == 0);
         }
         head = u / p.NC;
         t0 = 0;
         left = len[s];
         windows();
+        fetch_q();
+        return pkv::kQ4UnitCost;
     }
     // Piece J of the codes, K and V, from `src` on.
     template <int J>
@@ -379,17 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
     __shared__ Piece piece[kWarps][2];
     __shared__ float piece_lse[kWarps][2][kHeads];
     __shared__ int cut_tu[2], cut_nu[2], cut_s[2], cut_u[2];      // units cut at the CTA's start, end
+    __shared__ int join_first[2], join_n[2];                      // of them, those to join here: parts
     uint8_t *ring_all = smem;
     // places of the pieces that end in a warp, [warp][GC][D]: behind the rings
     // where they fit, else this CTA's part of the workspace
     float *heads_o = p.ws_pieces ? p.ws_pieces + (size_t)blockIdx.x * kWarps * p.GC * D
-                                 : reinterpret_cast<float *>(smem + kWarps * C::kRing);
+                                 : reinterpret_cast<float *>(smem + kWarps * (C::kRing + p.GC * (D * 2)));
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pkv::grid_dependents_launch();
     if (!p.tables_ready) pkv::grid_dependency_wait();
 
-    // ---- lengths and their prefix of subtiles
+    // ---- lengths, and the places of the sequences' units in the list
     {
         constexpr int K = kMaxSeqs / kThreads;
         int n[K], sum = 0;
@@ -402,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 L = L < 0 ? 0 : p.M << p.lb;
             }
             len[s] = L;
-            n[k] = (L + kSub - 1) / kSub;
+            n[k] = L ? (L + kSub - 1) / kSub + pkv::kQ4UnitCost : 0;
             sum += n[k];
         }
         int inc = sum;
@@ -438,19 +457,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
         }
 
     // ---- this CTA's and this warp's part of the list
-    const int NT = prefix[kMaxSeqs] * p.U;
-    const int CT = pkv::q4_active_ctas(NT, (int)gridDim.x);
+    const int NV = prefix[kMaxSeqs] * p.U;
+    const int CT = pkv::q4_active_ctas(NV, (int)gridDim.x);
     const int cta = blockIdx.x;
     if (cta >= CT) return;
-    const int A = pkv::q4_cta_cut(cta, NT, CT), Z = pkv::q4_cta_cut(cta + 1, NT, CT);
+    const int A = pkv::q4_cta_cut(cta, NV, CT), Z = pkv::q4_cta_cut(cta + 1, NV, CT);
     const int a = pkv::q4_warp_cut(warp, A, Z), z = pkv::q4_warp_cut(warp + 1, A, Z);
 
     const uint32_t ring = pkv::smem_u32(ring_all) + warp * C::kRing;
     const int g = lane >> 2, t = lane & 3;
 
     if (a < z) {
-        int cs, cu, ci;                      // sequence, unit, subtile of the unit
-        {   // the sequence holding subtile a: the last whose units begin at or before
+        // sequence, unit, subtile of the unit; places of a unit of the sequence, and
+        // the place of the unit's first subtile
+        int cs, cu, ci, nv, tu;
+        {   // the sequence holding place a: the last whose units begin at or before
             // it (of equal prefixes, the empty sequences come first)
             int lo = 0, hi = p.S - 1;
             while (lo < hi) {
@@ -458,19 +479,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 if (prefix[mid] * p.U <= a) lo = mid;
                 else hi = mid - 1;
             }
-            const int n = prefix[lo + 1] - prefix[lo], r = a - prefix[lo] * p.U;
+            nv = prefix[lo + 1] - prefix[lo];
+            const int r = a - prefix[lo] * p.U;
             cs = lo;
-            cu = r / n;
-            ci = r - cu * n;
+            cu = r / nv;
+            tu = a - (r - cu * nv) + pkv::kQ4UnitCost;
+            ci = max(0, a - tu);
         }
-        Loader<D, LB> ld(p, len, lane);
+        Loader<D, LB> ld(p, len, lane, pkv::smem_u32(smem) + kWarps * C::kRing + warp * p.GC * (D * 2));
         ld.start(cs, cu, ci);
-        int to_issue = z - a;
+        int rem = z - (tu + ci);             // places from the next subtile to copy on
 #pragma unroll
         for (int st = 0; st < C::kStages; ++st) {
-            if (to_issue > 0) {
+            if (rem > 0) {
                 ld.issue(ring + st * C::kStage);
-                if (--to_issue) ld.advance();
+                if (--rem > 0) rem -= ld.advance();
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
@@ -489,10 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
         const uint32_t vm_at = (NG + (g & (NG - 1))) * (2 * kSub) + t * 8;   // minima of a group, V
         const uint32_t one = g == 0 ? 0x3c003c00u : 0u;
 
-        for (int tile = a; tile < z;) {
+        while (true) {
             // ---- a unit, or the part of it that lies here: `count` subtiles
-            const int n = prefix[cs + 1] - prefix[cs];
-            const int count = min(n - ci, z - tile);
+            const int n = nv - pkv::kQ4UnitCost;
+            const int count = min(n, z - tu) - ci;
+            if (count <= 0) break;
             const int chunk = cu % p.NC, kvh = cu / p.NC;
             const int gca = min(p.GC, p.G - chunk * p.GC);
             const int h0 = kvh * p.G + chunk * p.GC;
@@ -503,13 +527,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             {
                 // lane (g, t) holds elements 32 y + 8 t .. + 7 of head g
                 float x[NG][8], top = 0.f;
+                const bool here = ld.q_unit == cs * p.U + cu;
+                if (here) {
+                    // copied with the unit's first subtile or before
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
                     uint4 raw = make_uint4(0, 0, 0, 0);
-                    if (g < gca)
-                        raw = __ldg(reinterpret_cast<const uint4 *>(
-                            static_cast<const uint16_t *>(p.q) +
-                            ((size_t)cs * p.Hq + h0 + g) * D + 32 * y + 8 * t));
+                    if (g < gca) {
+                        if (here)
+                            pkv::lds_u32x4(ld.q_buf + g * (D * 2) + 64 * y + 16 * t, raw.x, raw.y, raw.z, raw.w);
+                        else
+                            raw = __ldg(reinterpret_cast<const uint4 *>(
+                                static_cast<const uint16_t *>(p.q) +
+                                ((size_t)cs * p.Hq + h0 + g) * D + 32 * y + 8 * t));
+                    }
                     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -519,6 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                         x[y][2 * i + 1] = f.y;
                         top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
+                }
+                if (here) {
+                    __syncwarp();
+                    ld.q_unit = -1;              // taken up
                 }
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
@@ -559,8 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 zs0 = __shfl_sync(~0u, zq, 8 * t);
                 zs1 = __shfl_sync(~0u, zq, 8 * t + 4);
             }
-            float me0 = kNone, me1 = kNone;      // reference exponents
-            float mu0 = 0.f, mu1 = 0.f;          // what scores are taken against: these, or 0
+            float mu0 = kNone, mu1 = kNone;      // reference exponents
             float room = -INFINITY;              // largest score above them that needs no new ones
             uint32_t sbound = 0x3c003c00u;       // V scales so far stay at or below it (1)
             float acc[NG][2][4], accx[4];
@@ -677,14 +714,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 sbound = as_u32(__float2half2_rn(bs));
                 // scales up to 2^e, e >= 1: weights up to 2^(15 - e)
                 const float e = (float)((int)(__float_as_uint(bs) >> 23) - 126);
-                const float n0 = fmaxf(me0, t0 - 7.f + e), n1 = fmaxf(me1, t1 - 7.f + e);
-                const float f0 = ex2(me0 - n0), f1 = ex2(me1 - n1);
+                float u0 = mu0, u1 = mu1;
+                const bool none0 = mu0 == kNone, none1 = mu1 == kNone;
+                if (t0 > -INFINITY) u0 = none0 ? t0 - 7.f + e : fmaxf(mu0, t0 - 7.f + e);
+                if (t1 > -INFINITY) u1 = none1 ? t1 - 7.f + e : fmaxf(mu1, t1 - 7.f + e);
+                // (before the first score there is nothing to rescale)
+                const float f0 = none0 ? 1.f : ex2(mu0 - u0), f1 = none1 ? 1.f : ex2(mu1 - u1);
                 // a head that has had no score but -infinity keeps none, and
                 // the next subtile asks again
-                room = __any_sync(~0u, n0 == kNone || n1 == kNone) ? -INFINITY : 15.f - e;
-                me0 = n0;
-                me1 = n1;
-                const float u0 = n0 == kNone ? 0.f : n0, u1 = n1 == kNone ? 0.f : n1;
+                room = __any_sync(~0u, u0 == kNone || u1 == kNone) ? -INFINITY : 15.f - e;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     sc[half][0] = sc[half][0] + mu0 - u0;
@@ -766,16 +804,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 
             // ---- the stage is used up: fill it with the subtile after next
             __syncwarp();
-            if (to_issue > 0) {
+            if (rem > 0) {
                 ld.issue(sk);
-                if (--to_issue) ld.advance();
+                if (--rem > 0) rem -= ld.advance();
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             sk = 2 * ring + C::kStage - sk;
           }
 
             // ---- the unit's output, or a piece of it
-            const int tu = tile - ci;
             const bool whole = ci == 0 && count == n;
             const int slot = ci ? 0 : 1;         // ci > 0: it began before this warp's part
             const float l0 = __shfl_sync(~0u, accx[2], t), l1 = __shfl_sync(~0u, accx[3], t);
@@ -812,23 +849,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 for (int e = 0; e < 2; ++e) {
                     const int h = 2 * t + e;
                     if (h >= gca) continue;
-                    const float lse = (e ? me1 : me0) + log2f(e ? l1 : l0);
+                    const float lse = (e ? mu1 : mu0) + log2f(e ? l1 : l0);
                     if (!whole) piece_lse[warp][slot][h] = lse;
                     else if (p.lse_out) p.lse_out[(size_t)cs * p.Hq + h0 + h] = lse;
                 }
             }
             if (!whole && lane == 0) piece[warp][slot] = {tu, n, cs, cu};
 
-            tile += count;
             ci = 0;
+            tu += nv;
+            if (tu >= z) break;
             if (++cu == p.U) {
                 cu = 0;
-                do ++cs; while (cs < p.S && len[cs] == 0);
+                do ++cs; while (len[cs] == 0);       // (there is one: the list goes on)
+                nv = prefix[cs + 1] - prefix[cs];
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    if (tid < 2) cut_nu[tid] = 0;
+    if (tid < 2) cut_nu[tid] = join_n[tid] = 0;
     __syncthreads();
 
     // ---- join the pieces of each unit cut between this CTA's warps. A unit's
@@ -894,30 +933,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
     if (!cut_nu[0] && !cut_nu[1]) return;
 
     // ---- units cut between CTAs: count this CTA's part in; the last to come joins
-    if (tid == 0) {
+    if (tid < 2 && cut_nu[tid]) {
+        const int nu = cut_nu[tid];
+        const int first = pkv::q4_owner(cut_tu[tid], NV, CT);
+        const int n = pkv::q4_owner(cut_tu[tid] + nu - 1, NV, CT) - first + 1;
         pkv::fence_acq_rel_gpu();
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int nu = cut_nu[side];
-            if (nu == 0) continue;
-            const int first = pkv::q4_owner(cut_tu[side], NT, CT);
-            const int n = pkv::q4_owner(cut_tu[side] + nu - 1, NT, CT) - first + 1;
-            const bool last = atomicAdd(p.cnt + first, 1u) == (unsigned)n - 1;
-            if (last) p.cnt[first] = 0;
-            cut_nu[side] = last ? n : 0;
-            cut_tu[side] = first;
-        }
+        const bool last = atomicAdd(p.cnt + first, 1u) == (unsigned)n - 1;
+        if (last) p.cnt[first] = 0;
+        join_n[tid] = last ? n : 0;
+        join_first[tid] = first;
         pkv::fence_acq_rel_gpu();
     }
     __syncthreads();
     for (int side = 0; side < 2; ++side) {
-        const int n = cut_nu[side], first = cut_tu[side];
+        const int n = join_n[side], first = join_first[side];
         if (n == 0) continue;
         const int u = cut_u[side], chunk = u % p.NC;
         const int gca = min(p.GC, p.G - chunk * p.GC);
         // the warps of a head take every ways-th part; they meet in shared memory
         const int ways = kWarps / gca, h = warp % gca, sub = warp / gca;
-        float o[E] = {}, m = kNone, sum = 0.f;
+        float o[E] = {}, m = -3e38f, sum = 0.f;
         if (sub < ways) {
 #pragma unroll 4
             for (int k = sub; k < n; k += ways) {
@@ -940,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
         }
         __syncthreads();
         if (sub == 0) {
-            float mx = kNone, total = 0.f;
+            float mx = -3e38f, total = 0.f;
             for (int q = 0; q < ways; ++q) mx = fmaxf(mx, piece_lse[h + q * gca][0][0]);
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -967,7 +1002,7 @@ constexpr bool pieces_on_chip(int GC, int D) { return D == 64 || GC <= 4; }
 
 template <int D>
 size_t smem_bytes(int GC) {
-    return (size_t)kWarps * (Cfg<D>::kRing + (pieces_on_chip(GC, D) ? GC * D * sizeof(float) : 0));
+    return (size_t)kWarps * (Cfg<D>::kRing + GC * D * 2 + (pieces_on_chip(GC, D) ? GC * D * sizeof(float) : 0));
 }
 
 template <int D, int LB>
@@ -1057,11 +1092,11 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
         return pkv::set_last_error(PKV_ERR_INVALID_ARG,
                                    "q must be 16-byte aligned, out to four of its elements");
     const int G = num_q_heads / Hk, GC = G < kHeads ? G : kHeads, NC = (G + GC - 1) / GC;
-    // flattened subtile counts, times the CTAs, are taken in 64 bits; the list itself in 32
+    // the list's places fit 32 bits; products with the CTAs are taken in 64
     const int64_t tokens = (int64_t)M * cache->block_size;
     const int64_t seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
     if (tokens > INT32_MAX / 2 ||
-        seqs * Hk * NC * ((tokens + kSub - 1) / kSub) >= (int64_t)INT32_MAX)
+        seqs * Hk * NC * ((tokens + kSub - 1) / kSub + pkv::kQ4UnitCost) >= (int64_t)INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
     if ((int64_t)cache->num_blocks * Hk > INT32_MAX)     // 2^31 chunks are over 500 GB
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");

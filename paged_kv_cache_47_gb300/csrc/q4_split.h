@@ -1,5 +1,12 @@
-// How the 4-bit decode splits its list of NT subtiles over CTAs and their
-// warps. Plain integer arithmetic, shared by the kernel and a host replay.
+// How the 4-bit decode splits its work over CTAs and their warps. Plain integer
+// arithmetic, shared by the kernel and a host replay.
+//
+// The list: each unit (sequence, kv head, chunk of q heads) takes kQ4UnitCost
+// places and then one for each of its n subtiles, units end to end, NV places
+// in all. CTAs and warps take even shares of the places, so a warp that starts
+// more units gets fewer subtiles. Subtile i of a unit whose places begin at v
+// has place v + kQ4UnitCost + i; a cut among a unit's first places falls before
+// its first subtile.
 #pragma once
 
 #if defined(__CUDACC__)
@@ -11,29 +18,36 @@
 namespace pkv {
 
 constexpr int kQ4Warps = 16;
+// What a warp spends on a unit besides its subtiles (q to operands, the piece
+// it leaves), in subtiles.
+constexpr int kQ4UnitCost = 2;
+// A warp's share is at least this many places: then it holds a subtile.
+constexpr int kQ4LeastShare = kQ4UnitCost + 1;
+// Warps a CTA has work for, at least, before another CTA is used.
+constexpr int kQ4LeastWarps = 8;
 
-// CTAs with work, of C launched: at least a subtile a warp while there is more
-// than one, so that a short list stays on few CTAs and is joined on chip.
-PKV_SPLIT_FN int q4_active_ctas(int NT, int C) {
-    const int most = NT / kQ4Warps;
+// CTAs with work, of C launched.
+PKV_SPLIT_FN int q4_active_ctas(int NV, int C) {
+    const int most = NV / (kQ4LeastWarps * kQ4LeastShare);
     const int ct = most < C ? most : C;
-    return NT == 0 ? 0 : ct < 1 ? 1 : ct;
+    return NV == 0 ? 0 : ct < 1 ? 1 : ct;
 }
 
-// First subtile of CTA c of CT.
-PKV_SPLIT_FN int q4_cta_cut(int c, int NT, int CT) {
-    return (int)((long long)c * NT / CT);
+// First place of CTA c of CT.
+PKV_SPLIT_FN int q4_cta_cut(int c, int NV, int CT) {
+    return (int)((long long)c * NV / CT);
 }
 
-// The CTA whose range holds subtile t.
-PKV_SPLIT_FN int q4_owner(int t, int NT, int CT) {
-    return (int)((((long long)t + 1) * CT - 1) / NT);
+// The CTA whose share holds place v.
+PKV_SPLIT_FN int q4_owner(int v, int NV, int CT) {
+    return (int)((((long long)v + 1) * CT - 1) / NV);
 }
 
-// First subtile of warp w in a CTA's range [A, Z), A < Z. The warps with work
-// come first, each with at least one subtile.
+// First place of warp w in a CTA's share [A, Z), A < Z. The warps with work
+// come first.
 PKV_SPLIT_FN int q4_warp_cut(int w, int A, int Z) {
-    const int nw = Z - A < kQ4Warps ? Z - A : kQ4Warps;
+    const int fit = (Z - A) / kQ4LeastShare;
+    const int nw = fit < 1 ? 1 : fit < kQ4Warps ? fit : kQ4Warps;
     return A + (int)((long long)(w < nw ? w : nw) * (Z - A) / nw);
 }
 

@@ -15,22 +15,18 @@ using namespace pkv;
 struct Piece { int tu = 0, nu = 0, from = 0, to = 0; };
 
 static bool run(const std::vector<int> &units, int C) {
-    int NT = 0;
-    std::vector<int> start;
-    for (int n : units) { start.push_back(NT); NT += n; }
-    const int CT = q4_active_ctas(NT, C);
-    if (CT > C || (NT > 0) != (CT > 0)) return false;
-    std::map<int, int> covered, written;           // unit start -> subtiles, outputs
-    std::map<int, std::vector<std::pair<int, int>>> parts;   // unit start -> (cta, side)
-    std::map<int, int> part_subtiles;
-    auto unit_of = [&](int t) {
-        size_t u = 0;
-        while (u + 1 < units.size() && start[u + 1] <= t) ++u;
-        return (int)u;
-    };
+    int NV = 0;
+    std::vector<int> start;                        // a unit's first place
+    for (int n : units) { start.push_back(NV); NV += n + kQ4UnitCost; }
+    const int CT = q4_active_ctas(NV, C);
+    if (CT > C || (NV > 0) != (CT > 0)) return false;
+    std::map<int, int> covered, written;           // first subtile's place -> subtiles, outputs
+    std::map<int, std::vector<std::pair<int, int>>> parts;   // -> (cta, side)
+    std::map<int, int> part_subtiles, length;
+    for (size_t u = 0; u < units.size(); ++u) length[start[u] + kQ4UnitCost] = units[u];
     int expect = 0;
     for (int c = 0; c < CT; ++c) {
-        const int A = q4_cta_cut(c, NT, CT), Z = q4_cta_cut(c + 1, NT, CT);
+        const int A = q4_cta_cut(c, NV, CT), Z = q4_cta_cut(c + 1, NV, CT);
         if (A != expect || Z <= A) return false;
         expect = Z;
         Piece piece[kQ4Warps][2];
@@ -40,20 +36,35 @@ static bool run(const std::vector<int> &units, int C) {
             if (a != at || z < a) return false;
             if (w == 0 && z == a) return false;     // the first warp has work
             at = z;
-            for (int t = a; t < z;) {
-                if (q4_owner(t, NT, CT) != c) return false;
-                const int u = unit_of(t), tu = start[u], end = tu + units[u];
-                const int to = end < z ? end : z;
-                covered[tu] += to - t;
-                if (tu >= a && end <= z) {
+            if (a == z) continue;
+            size_t u = 0;
+            while (u + 1 < units.size() && start[u + 1] <= a) ++u;
+            int ci = a - start[u] - kQ4UnitCost;
+            if (ci < 0) ci = 0;
+            int used = 0;
+            while (u < units.size()) {
+                const int tu = start[u] + kQ4UnitCost, n = units[u];
+                const int to = z - tu < n ? z - tu : n;
+                if (to <= ci) {
+                    if (ci < n) break;              // the share ends before the unit's first subtile
+                    ci = 0;                         // (a share cannot begin past a unit's end)
+                    return false;
+                }
+                for (int i = ci; i < to; ++i)
+                    if (q4_owner(tu + i, NV, CT) != c) return false;
+                covered[tu] += to - ci;
+                used += to - ci;
+                if (ci == 0 && to == n) {
                     ++written[tu];
                 } else {
-                    Piece &p = piece[w][tu < a ? 0 : 1];
+                    Piece &p = piece[w][ci ? 0 : 1];
                     if (p.nu) return false;         // a place is used once
-                    p = {tu, units[u], t, to};
+                    p = {tu, n, ci, to};
                 }
-                t = to;
+                ci = 0;
+                if (++u < units.size() && start[u] >= z) break;
             }
+            if (used == 0) return false;
         }
         if (at != Z) return false;
         bool open[2] = {false, false};
@@ -79,19 +90,19 @@ static bool run(const std::vector<int> &units, int C) {
                 }
             }
     }
-    if (expect != NT) return false;
+    if (expect != NV) return false;
     std::set<int> counters;
     for (auto &kv : parts) {
-        const int tu = kv.first, nu = units[unit_of(tu)];
-        const int first = q4_owner(tu, NT, CT), n = q4_owner(tu + nu - 1, NT, CT) - first + 1;
+        const int tu = kv.first, nu = length[tu];
+        const int first = q4_owner(tu, NV, CT), n = q4_owner(tu + nu - 1, NV, CT) - first + 1;
         if ((int)kv.second.size() != n || part_subtiles[tu] != nu) return false;
         if (!counters.insert(first).second) return false;        // a counter serves one unit
         for (int k = 0; k < n; ++k)
             if (kv.second[k].first != first + k || kv.second[k].second != (k == 0 ? 1 : 0)) return false;
         ++written[tu];
     }
-    for (size_t u = 0; u < units.size(); ++u)
-        if (covered[start[u]] != units[u] || written[start[u]] != 1) return false;
+    for (auto &kv : length)
+        if (covered[kv.first] != kv.second || written[kv.first] != 1) return false;
     return true;
 }
 
