@@ -211,7 +211,7 @@ struct Loader {
     static constexpr int kBlocks = kSub >> LB;       // of a subtile: 4, 2 or 1
     const Q4Params &p;
     const int *len;                  // shared memory: a sequence's length
-    int lane;
+    int lane, cost;                  // cost: places before a unit's first subtile
     int s, u, head, t0, left;
     int32_t window, next_window;     // table entries: lane holds entry `base + lane` of each
     int base;
@@ -224,8 +224,8 @@ struct Loader {
     uint32_t q_buf;
     int q_unit;                      // the unit whose rows lie there (s * U + u); -1: none
 
-    __device__ __forceinline__ Loader(const Q4Params &p_, const int *len_, int lane_, uint32_t q_buf_)
-        : p(p_), len(len_), lane(lane_), q_buf(q_buf_), q_unit(-1) {
+    __device__ __forceinline__ Loader(const Q4Params &p_, const int *len_, int lane_, int cost_, uint32_t q_buf_)
+        : p(p_), len(len_), lane(lane_), cost(cost_), q_buf(q_buf_), q_unit(-1) {
         const int line = lane >> 3;
         dst0 = line * 128 + (((lane & 7) ^ line_xor<D>(line)) << 4);
         dst1 = (line + 4) * 128 + (((lane & 7) ^ line_xor<D>(line + 4)) << 4);
@@ -282,7 +282,7 @@ struct Loader {
         left = len[s];
         windows();
         fetch_q();
-        return pkv::kQ4UnitCost;
+        return cost;
     }
     // Piece J of the codes, K and V, from `src` on.
     template <int J>
@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
     constexpr int NG = C::NG;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int prefix[kMaxSeqs + 1], len[kMaxSeqs];
-    __shared__ int scan[kWarps];
+    __shared__ uint16_t nonempty[kMaxSeqs + 2];                   // sequences with tokens before a sequence
+    __shared__ int scan[kWarps], scan1[kWarps], scan2[kWarps];
     __shared__ Piece piece[kWarps][2];
     __shared__ float piece_lse[kWarps][2][kHeads];
     __shared__ int cut_tu[2], cut_nu[2], cut_s[2], cut_u[2];      // units cut at the CTA's start, end
@@ -409,9 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
     if (!p.tables_ready) pkv::grid_dependency_wait();
 
     // ---- lengths, and the places of the sequences' units in the list
+    int cost, longest = 0;
     {
         constexpr int K = kMaxSeqs / kThreads;
-        int n[K], sum = 0;
+        int n[K], sum = 0, some = 0;             // subtiles; sequences that have any
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int s = tid * K + k;
@@ -421,28 +423,50 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 L = L < 0 ? 0 : p.M << p.lb;
             }
             len[s] = L;
-            n[k] = L ? (L + kSub - 1) / kSub + pkv::kQ4UnitCost : 0;
+            n[k] = (L + kSub - 1) / kSub;
             sum += n[k];
+            some += L > 0;
+            longest = max(longest, n[k]);
         }
-        int inc = sum;
+        int inc = sum, inc1 = some;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(~0u, inc, o);
-            if (lane >= o) inc += x;
+            const int x = __shfl_up_sync(~0u, inc, o), y = __shfl_up_sync(~0u, inc1, o);
+            if (lane >= o) {
+                inc += x;
+                inc1 += y;
+            }
         }
-        if (lane == 31) scan[warp] = inc;
+        longest = __reduce_max_sync(~0u, longest);
+        if (lane == 31) {
+            scan[warp] = inc;
+            scan1[warp] = inc1;
+            scan2[warp] = longest;
+        }
         if (lane < 2) piece[warp][lane].nu = 0;
         __syncthreads();
-        int before = inc - sum;
+        int before = inc - sum, before1 = inc1 - some, total = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (w < warp) before += scan[w];
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) {
+                before += scan[w];
+                before1 += scan1[w];
+            }
+            total += scan[w];
+            longest = max(longest, scan2[w]);
+        }
+        cost = pkv::q4_unit_cost(total * p.U, (int)gridDim.x);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            prefix[tid * K + k] = before;
+            prefix[tid * K + k] = before + cost * before1;
+            nonempty[tid * K + k] = (uint16_t)before1;
             before += n[k];
+            before1 += n[k] > 0;
         }
-        if (tid == kThreads - 1) prefix[kMaxSeqs] = before;
+        if (tid == kThreads - 1) {
+            prefix[kMaxSeqs] = before + cost * before1;
+            nonempty[kMaxSeqs] = (uint16_t)before1;
+        }
         __syncthreads();
     }
     if (p.tables_ready) pkv::grid_dependency_wait();
@@ -458,11 +482,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 
     // ---- this CTA's and this warp's part of the list
     const int NV = prefix[kMaxSeqs] * p.U;
-    const int CT = pkv::q4_active_ctas(NV, (int)gridDim.x);
     const int cta = blockIdx.x;
-    if (cta >= CT) return;
-    const int A = pkv::q4_cta_cut(cta, NV, CT), Z = pkv::q4_cta_cut(cta + 1, NV, CT);
-    const int a = pkv::q4_warp_cut(warp, A, Z), z = pkv::q4_warp_cut(warp + 1, A, Z);
+    const int units = nonempty[kMaxSeqs] * p.U;
+    int CT, A, Z;
+    if (cost == 0 && units <= (int)gridDim.x && longest <= pkv::kQ4OneCta) {
+        // a unit for each CTA
+        CT = units;
+        if (cta >= CT) return;
+        int lo = 0, hi = p.S - 1;                // the last sequence with at most this many before it
+        const int k = cta / p.U;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (nonempty[mid] <= k) lo = mid;
+            else hi = mid - 1;
+        }
+        const int n = prefix[lo + 1] - prefix[lo];
+        A = prefix[lo] * p.U + (cta - k * p.U) * n;
+        Z = A + n;
+    } else {
+        CT = pkv::q4_active_ctas(NV, (int)gridDim.x, cost);
+        if (cta >= CT) return;
+        A = pkv::q4_cta_cut(cta, NV, CT);
+        Z = pkv::q4_cta_cut(cta + 1, NV, CT);
+    }
+    const int a = pkv::q4_warp_cut(warp, A, Z, cost), z = pkv::q4_warp_cut(warp + 1, A, Z, cost);
 
     const uint32_t ring = pkv::smem_u32(ring_all) + warp * C::kRing;
     const int g = lane >> 2, t = lane & 3;
@@ -483,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             const int r = a - prefix[lo] * p.U;
             cs = lo;
             cu = r / nv;
-            tu = a - (r - cu * nv) + pkv::kQ4UnitCost;
+            tu = a - (r - cu * nv) + cost;
             ci = max(0, a - tu);
         }
-        Loader<D, LB> ld(p, len, lane, pkv::smem_u32(smem) + kWarps * C::kRing + warp * p.GC * (D * 2));
+        Loader<D, LB> ld(p, len, lane, cost, pkv::smem_u32(smem) + kWarps * C::kRing + warp * p.GC * (D * 2));
         ld.start(cs, cu, ci);
         int rem = z - (tu + ci);             // places from the next subtile to copy on
 #pragma unroll
@@ -514,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 
         while (true) {
             // ---- a unit, or the part of it that lies here: `count` subtiles
-            const int n = nv - pkv::kQ4UnitCost;
+            const int n = nv - cost;
             const int count = min(n, z - tu) - ci;
             if (count <= 0) break;
             const int chunk = cu % p.NC, kvh = cu / p.NC;

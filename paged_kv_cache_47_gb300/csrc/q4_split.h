@@ -1,12 +1,12 @@
 // How the 4-bit decode splits its work over CTAs and their warps. Plain integer
 // arithmetic, shared by the kernel and a host replay.
 //
-// The list: each unit (sequence, kv head, chunk of q heads) takes kQ4UnitCost
-// places and then one for each of its n subtiles, units end to end, NV places
-// in all. CTAs and warps take even shares of the places, so a warp that starts
-// more units gets fewer subtiles. Subtile i of a unit whose places begin at v
-// has place v + kQ4UnitCost + i; a cut among a unit's first places falls before
-// its first subtile.
+// The list: each unit (sequence, kv head, chunk of q heads) takes `cost` places
+// and then one for each of its n subtiles, units end to end, NV places in all.
+// CTAs and warps take even shares of the places, so a warp that starts more
+// units gets fewer subtiles. Subtile i of a unit whose places begin at v has
+// place v + cost + i; a cut among a unit's first places falls before its first
+// subtile.
 #pragma once
 
 #if defined(__CUDACC__)
@@ -19,16 +19,23 @@ namespace pkv {
 
 constexpr int kQ4Warps = 16;
 // What a warp spends on a unit besides its subtiles (q to operands, the piece
-// it leaves), in subtiles.
+// it leaves), in subtiles; nothing where warps get a few subtiles each and the
+// time is that of one chain.
 constexpr int kQ4UnitCost = 2;
-// A warp's share is at least this many places: then it holds a subtile.
-constexpr int kQ4LeastShare = kQ4UnitCost + 1;
-// Warps a CTA has work for, at least, before another CTA is used.
-constexpr int kQ4LeastWarps = 8;
+constexpr int kQ4FewSubtiles = 4;
+// Few units, none longer than this many subtiles: a CTA each, nothing to join
+// between CTAs.
+constexpr int kQ4OneCta = 4 * kQ4Warps;
 
-// CTAs with work, of C launched.
-PKV_SPLIT_FN int q4_active_ctas(int NV, int C) {
-    const int most = NV / (kQ4LeastWarps * kQ4LeastShare);
+// The cost to count units with, for NT subtiles on C CTAs.
+PKV_SPLIT_FN int q4_unit_cost(int NT, int C) {
+    return NT < C * kQ4Warps * kQ4FewSubtiles ? 0 : kQ4UnitCost;
+}
+
+// CTAs with work, of C launched: a full CTA has a subtile for every warp (a
+// share of cost + 1 places holds one).
+PKV_SPLIT_FN int q4_active_ctas(int NV, int C, int cost) {
+    const int most = NV / (kQ4Warps * (cost + 1));
     const int ct = most < C ? most : C;
     return NV == 0 ? 0 : ct < 1 ? 1 : ct;
 }
@@ -45,8 +52,8 @@ PKV_SPLIT_FN int q4_owner(int v, int NV, int CT) {
 
 // First place of warp w in a CTA's share [A, Z), A < Z. The warps with work
 // come first.
-PKV_SPLIT_FN int q4_warp_cut(int w, int A, int Z) {
-    const int fit = (Z - A) / kQ4LeastShare;
+PKV_SPLIT_FN int q4_warp_cut(int w, int A, int Z, int cost) {
+    const int fit = (Z - A) / (cost + 1);
     const int nw = fit < 1 ? 1 : fit < kQ4Warps ? fit : kQ4Warps;
     return A + (int)((long long)(w < nw ? w : nw) * (Z - A) / nw);
 }

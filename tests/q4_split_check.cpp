@@ -14,16 +14,16 @@ using namespace pkv;
 
 struct Piece { int tu = 0, nu = 0, from = 0, to = 0; };
 
-static bool run(const std::vector<int> &units, int C) {
+static bool run(const std::vector<int> &units, int C, int cost) {
     int NV = 0;
     std::vector<int> start;                        // a unit's first place
-    for (int n : units) { start.push_back(NV); NV += n + kQ4UnitCost; }
-    const int CT = q4_active_ctas(NV, C);
+    for (int n : units) { start.push_back(NV); NV += n + cost; }
+    const int CT = q4_active_ctas(NV, C, cost);
     if (CT > C || (NV > 0) != (CT > 0)) return false;
     std::map<int, int> covered, written;           // first subtile's place -> subtiles, outputs
     std::map<int, std::vector<std::pair<int, int>>> parts;   // -> (cta, side)
     std::map<int, int> part_subtiles, length;
-    for (size_t u = 0; u < units.size(); ++u) length[start[u] + kQ4UnitCost] = units[u];
+    for (size_t u = 0; u < units.size(); ++u) length[start[u] + cost] = units[u];
     int expect = 0;
     for (int c = 0; c < CT; ++c) {
         const int A = q4_cta_cut(c, NV, CT), Z = q4_cta_cut(c + 1, NV, CT);
@@ -32,18 +32,18 @@ static bool run(const std::vector<int> &units, int C) {
         Piece piece[kQ4Warps][2];
         int at = A;
         for (int w = 0; w < kQ4Warps; ++w) {
-            const int a = q4_warp_cut(w, A, Z), z = q4_warp_cut(w + 1, A, Z);
+            const int a = q4_warp_cut(w, A, Z, cost), z = q4_warp_cut(w + 1, A, Z, cost);
             if (a != at || z < a) return false;
             if (w == 0 && z == a) return false;     // the first warp has work
             at = z;
             if (a == z) continue;
             size_t u = 0;
             while (u + 1 < units.size() && start[u + 1] <= a) ++u;
-            int ci = a - start[u] - kQ4UnitCost;
+            int ci = a - start[u] - cost;
             if (ci < 0) ci = 0;
             int used = 0;
             while (u < units.size()) {
-                const int tu = start[u] + kQ4UnitCost, n = units[u];
+                const int tu = start[u] + cost, n = units[u];
                 const int to = z - tu < n ? z - tu : n;
                 if (to <= ci) {
                     if (ci < n) break;              // the share ends before the unit's first subtile
@@ -114,7 +114,7 @@ int main() {
         const int most = i % 4 == 0 ? 1 : i % 4 == 1 ? 5 : i % 4 == 2 ? 40 : 900;
         for (int &n : units) n = pick(1, most);
         const int C = i % 3 == 0 ? pick(1, 4) : i % 3 == 1 ? 152 : pick(1, 600);
-        if (!run(units, C)) {
+        if (!run(units, C, 0) || !run(units, C, kQ4UnitCost)) {
             std::printf("FAIL at %d\n", i);
             return 1;
         }
