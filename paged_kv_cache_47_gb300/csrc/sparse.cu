@@ -3,26 +3,35 @@
 // block_means: a warp per (token, kv head) whose token filled its block; a
 // lane adds 4 (fp32: 2 x 2) neighbouring elements over the block's rows.
 //
-// block_scores: a warp takes one kv head and 64 of a sequence's blocks. Lanes
-// hold 8 neighbouring elements of a mean each, so a row is 16 lanes (D 128),
-// two rows a load; the q heads of the group sit in registers as fp32. Products
-// of 16-bit elements are exact in fp32, so a fused multiply-add equals the
-// product and the addition the definition names; fp32 caches use the two
-// steps. The sums over lanes halve the heads a lane carries at each step,
-// which leaves the order of the additions as defined: neighbours first.
-// Bound by HBM on long contexts: each mean is read once.
+// Scores. A warp takes one kv head and a run of a sequence's blocks. Lanes hold
+// 8 neighbouring elements of a mean each, so a row is 16 lanes (D 128) and a
+// load two rows; the q heads of the group sit in registers as fp32 pairs, two
+// heads an instruction. Products of 16-bit elements are exact in fp32, so a
+// fused multiply-add equals the product and the addition the definition names;
+// fp32 caches use the two steps. The sums over lanes halve the heads a lane
+// carries at each step, which leaves the order of the additions as defined:
+// neighbours first. What is kept of a score is its key: its bits made
+// monotonic, a NaN as +infinity, -0 as +0. Bound by HBM on long contexts (each
+// mean is read once), by the multiply-adds from 8 heads a group on.
 //
-// block_select: a CTA per (sequence, kv head). The key of a score is its bits
-// made monotonic; the selected ones are those above the top-th largest key and
-// the first of its equals. That key is found bit by bit, counting in registers
-// (no shared-memory histogram: the high bits of scores are nearly all alike
-// and its atomics would queue). Threads hold neighbouring blocks, so two scans
-// over the threads give each selected block its place in ascending order.
+// Selection. The candidates taken are those above the top-th largest key and
+// the first of its equals. That key is found bit by bit, counting keys held in
+// registers (no shared-memory histogram: the high bits of scores are nearly
+// all alike and its atomics would queue); the search ends as soon as a
+// threshold leaves exactly `top`. Threads hold neighbouring candidates, so two
+// scans over them give each its place in ascending order.
+//
+// Rows (sequence, kv head) enough for every SM: one kernel, a CTA a row, keys
+// in shared memory; up to 256 candidates one warp selects alone, with no
+// barrier. Fewer rows: a first kernel scores even runs of blocks all over the
+// GPU, a second one selects, a CTA a row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "../../include/pkv_sparse.h"
 #include "device_utils.cuh"
@@ -33,10 +42,11 @@ namespace {
 
 using pkv::launch_chained;
 
-constexpr int kChunk = 64;           // blocks a warp scores
+constexpr int kRowThreads = 256;     // a CTA that scores and selects one row
 constexpr int kScoreThreads = 256;
 constexpr int kSelThreads = 512;
-constexpr int kPerThread = 16;       // keys a thread holds: 8192 blocks a pass
+constexpr int kPerThread = 16;       // keys a thread holds
+constexpr int kPerLane = 8;          // keys a lane holds where a warp selects alone
 constexpr int kMeanThreads = 256;
 
 template <typename T>
@@ -106,9 +116,9 @@ struct SelectParams {
     const void *q, *means;
     const int32_t *tables, *lens;
     int S, Hq, Hk, G, M, NB, B;
-    int chunks;                      // of kChunk blocks, a table row
     int top, first, last, W;
-    float *scores;                   // [S][Hk][M]
+    uint32_t *keys;                  // [S][Hk][pitch], by candidate; NULL: in shared memory
+    int pitch;
     int32_t *sel_tables, *sel_lens;
     unsigned *err;
 };
@@ -121,110 +131,245 @@ __device__ __forceinline__ int clamp_len(const SelectParams &p, int s, bool repo
     return L < 0 ? 0 : cap;
 }
 
-// GP q heads at a time (a group of any size takes several passes)
-template <typename T, int D, int GP>
-__global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const SelectParams p) {
-    constexpr int LANES = D / 8;     // lanes of a row
-    constexpr int ROWS = 32 / LANES; // rows of a load
-    constexpr int AHEAD = 4;
-    pkv::grid_dependents_launch();
-    pkv::grid_dependency_wait();
-    const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
-    const int64_t task = (int64_t)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
-    const int g = (int)(task % p.Hk);
-    const int64_t sc = task / p.Hk;
-    const int chunk = (int)(sc % p.chunks), s = (int)(sc / p.chunks);
-    if (s >= p.S) return;
-    const int L = clamp_len(p, s, chunk == 0 && g == 0 && lane == 0);
-    const int n = (L + p.B - 1) / p.B;
-    // candidates of this chunk; nothing to score where all of them are taken
-    const int lo = max(p.first, chunk * kChunk), hi = min(n - p.last, (chunk + 1) * kChunk);
-    if (lo >= hi || n - p.last - p.first <= p.top) return;
-    const int32_t *row = p.tables + (int64_t)s * p.M;
-    float *out = p.scores + ((int64_t)s * p.Hk + g) * p.M;
-    for (int h0 = 0; h0 < p.G; h0 += GP) {
-        float q[GP][8];
-#pragma unroll
-        for (int h = 0; h < GP; ++h) {
-            // past the group: its first head again, which changes no maximum
-            const int head = g * p.G + (h0 + h < p.G ? h0 + h : h0);
-            const T *src = static_cast<const T *>(p.q) + ((int64_t)s * p.Hq + head) * D + 8 * l;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[h][i] = pkv::Elem<T>::to_f32(src[i]);
-        }
-        for (int j0 = lo; j0 < hi; j0 += ROWS * AHEAD) {
-            uint4 x[AHEAD][sizeof(T) / 2];
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const int j = j0 + a * ROWS + sub;
-                int id = j < hi ? __ldg(row + j) : -1;
-                const bool ok = id >= 0 && id < p.NB;
-                if (!ok && j < hi && l == 0 && g == 0) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    static_cast<const T *>(p.means) + ((int64_t)(ok ? id : 0) * p.Hk + g) * D + 8 * l);
-#pragma unroll
-                for (int v = 0; v < (int)sizeof(T) / 2; ++v)
-                    x[a][v] = ok ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const int j = j0 + a * ROWS + sub;
-                const T *m = reinterpret_cast<const T *>(x[a]);
-                float acc[GP];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float v = pkv::Elem<T>::to_f32(m[i]);
-#pragma unroll
-                    for (int h = 0; h < GP; ++h) {
-                        if (i == 0) acc[h] = __fmul_rn(q[h][0], v);
-                        else if (sizeof(T) == 4) acc[h] = __fadd_rn(acc[h], __fmul_rn(q[h][i], v));
-                        else acc[h] = fmaf(q[h][i], v, acc[h]);
-                    }
-                }
-                // over the lanes of the row; a lane keeps half of its heads at
-                // each step while it has more than one
-#pragma unroll
-                for (int o = 1, keep = GP; o < LANES; o <<= 1) {
-                    if (keep > 1) {
-                        keep >>= 1;
-                        const bool up = l & o;
-#pragma unroll
-                        for (int h = 0; h < keep; ++h) {
-                            const float give = up ? acc[h] : acc[h + keep];
-                            const float mine = up ? acc[h + keep] : acc[h];
-                            acc[h] = __fadd_rn(mine, __shfl_xor_sync(~0u, give, o));
-                        }
-                    } else {
-                        acc[0] = __fadd_rn(acc[0], __shfl_xor_sync(~0u, acc[0], o));
-                    }
-                }
-                // the largest over the heads: those this lane kept, then over the lanes
-                constexpr int KEPT = GP > LANES ? GP / LANES : 1;
-                float best = acc[0];
-                bool nan = acc[0] != acc[0];
-#pragma unroll
-                for (int h = 1; h < KEPT; ++h) {
-                    best = fmaxf(best, acc[h]);
-                    nan |= acc[h] != acc[h];
-                }
-                if (nan) best = INFINITY;
-#pragma unroll
-                for (int o = 1; o < LANES && o < GP; o <<= 1)
-                    best = fmaxf(best, __shfl_xor_sync(~0u, best, o));
-                if (l == 0 && j < hi) out[j] = h0 ? fmaxf(out[j], best) : best;
-            }
-        }
-    }
-}
-
-// ---------------------------------------------------------------- selection
 __device__ __forceinline__ uint32_t key_of(float x) {
     if (x != x) x = INFINITY;
     const uint32_t b = __float_as_uint(x + 0.f);     // -0 becomes +0
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// Two fp32 values in one register pair.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(Pair x, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The neighbouring 8 elements of a row, as fp32.
+template <typename T>
+__device__ __forceinline__ void widen(const uint4 (&raw)[sizeof(T) / 2], float (&x)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        x[0] = __uint_as_float(raw[0].x), x[1] = __uint_as_float(raw[0].y);
+        x[2] = __uint_as_float(raw[0].z), x[3] = __uint_as_float(raw[0].w);
+        x[4] = __uint_as_float(raw[1].x), x[5] = __uint_as_float(raw[1].y);
+        x[6] = __uint_as_float(raw[1].z), x[7] = __uint_as_float(raw[1].w);
+    } else {
+        const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = pkv::Elem<T>::unpack2(w[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// The stream of means of one warp: loads of 16 bytes a lane, kLoads a stage,
+// kStages stages in the warp's ring in shared memory. A lane reads back only
+// what it copied itself, so nothing is shared and nothing waits but its own
+// copies; the ring only lengthens what registers could hold in flight.
+constexpr int kStages = 3;
+constexpr int kStageBytes = 4096;
+constexpr int kRingBytes = kStages * kStageBytes;
+
+// Scores of blocks [lo, hi) of sequence s for kv head g, as keys by candidate
+// (block - first). One warp. GP q heads at a time: a group of any size takes
+// several passes.
+template <typename T, int D, int GP>
+__device__ __forceinline__ void score_blocks(const SelectParams &p, int s, int g, int lo, int hi,
+                                             uint32_t *keys, uint32_t ring) {
+    constexpr int LANES = D / 8;     // lanes of a row
+    constexpr int ROWS = 32 / LANES; // rows of a load
+    constexpr int V = sizeof(T) / 2; // 16-byte pieces of a lane's elements
+    constexpr int LOADS = kStageBytes / (512 * V);
+    constexpr int STAGE_ROWS = ROWS * LOADS;         // 8, 16 or 32
+    const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
+    const int32_t *row = p.tables + (int64_t)s * p.M;
+    const T *means = static_cast<const T *>(p.means) + (int64_t)g * D + 8 * l;
+    const int64_t pitch = (int64_t)p.Hk * D;
+    const uint32_t mine = ring + lane * 16;
+    const int stages = (hi - lo + STAGE_ROWS - 1) / STAGE_ROWS;
+    // Slot i of a lane holds head i ^ swap: the sums over lanes below keep the
+    // lower half of the slots and give the upper one at each step, and the
+    // lanes' orders differ so that what one keeps the other gives.
+    int swap = 0;
+#pragma unroll
+    for (int t = 0; (GP >> (t + 1)) > 0; ++t) swap |= (l >> t & 1) * (GP >> (t + 1));
+
+    // block ids of 32 rows, and of the 32 after them; -1: none
+    auto ids_from = [&](int r) {
+        const int j = lo + r + lane;
+        int id = j < hi ? __ldg(row + j) : -1;
+        if (j < hi && (unsigned)id >= (unsigned)p.NB) {
+            if (g == 0) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+            id = -1;
+        }
+        return id;
+    };
+    for (int h0 = 0; h0 < p.G; h0 += GP) {
+        int ids = ids_from(0), next_ids = ids_from(32);
+        auto issue = [&](int k) {
+            if (k < stages) {
+                const int r0 = k * STAGE_ROWS;
+                if (k && r0 % 32 == 0) {
+                    ids = next_ids;
+                    next_ids = ids_from(r0 + 32);
+                }
+                const uint32_t dst = mine + (k % kStages) * kStageBytes;
+#pragma unroll
+                for (int a = 0; a < LOADS; ++a) {
+                    const int id = __shfl_sync(~0u, ids, r0 % 32 + a * ROWS + sub);
+                    const T *src = means + (id < 0 ? 0 : id) * pitch;
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        pkv::cp_async_16(dst + (a * V + v) * 512, src + v * (16 / sizeof(T)), id >= 0);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) issue(k);
+        Pair q[(GP + 1) / 2][8];
+#pragma unroll
+        for (int h = 0; h < GP; h += 2) {
+            float x[2][8] = {};
+#pragma unroll
+            for (int e = 0; e < 2 && h + e < GP; ++e) {
+                // past the group: its first head again, which changes no maximum
+                const int hh = h0 + ((h + e) ^ swap), head = g * p.G + (hh < p.G ? hh : h0);
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
+                                                                   ((int64_t)s * p.Hq + head) * D + 8 * l);
+                uint4 raw[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) raw[v] = __ldg(src + v);
+                widen<T>(raw, x[e]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[h / 2][i] = pair_of(x[0][i], x[1][i]);
+        }
+        for (int k = 0; k < stages; ++k) {
+            issue(k + kStages - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            const uint32_t from = mine + (k % kStages) * kStageBytes;
+#pragma unroll 2
+            for (int a = 0; a < LOADS; ++a) {
+                uint4 raw[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    pkv::lds_u32x4(from + (a * V + v) * 512, raw[v].x, raw[v].y, raw[v].z, raw[v].w);
+                float x[8], acc[GP + 1];
+                widen<T>(raw, x);
+                Pair sum[(GP + 1) / 2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const Pair xx = pair_of(x[i], x[i]);
+#pragma unroll
+                    for (int h = 0; h < (GP + 1) / 2; ++h) {
+                        if (i == 0) sum[h] = mul2(q[h][0], xx);
+                        else if (sizeof(T) == 4) sum[h] = add2(sum[h], mul2(q[h][i], xx));
+                        else sum[h] = fma2(q[h][i], xx, sum[h]);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < (GP + 1) / 2; ++h) unpair(sum[h], acc[2 * h], acc[2 * h + 1]);
+                // over the lanes of the row, neighbours first
+#pragma unroll
+                for (int o = 1, keep = GP; o < LANES; o <<= 1) {
+                    if (keep > 1) {
+                        keep >>= 1;
+#pragma unroll
+                        for (int h = 0; h < keep; ++h)
+                            acc[h] = __fadd_rn(acc[h], __shfl_xor_sync(~0u, acc[h + keep], o));
+                    } else {
+                        acc[0] = __fadd_rn(acc[0], __shfl_xor_sync(~0u, acc[0], o));
+                    }
+                }
+                // the largest over the heads, spread over the low lane bits
+                uint32_t best = key_of(acc[0]);
+#pragma unroll
+                for (int o = 1; o < GP; o <<= 1) best = max(best, __shfl_xor_sync(~0u, best, o));
+                const int j = lo + k * STAGE_ROWS + a * ROWS + sub;
+                if (l == 0 && j < hi) {
+                    uint32_t *out = keys + (j - p.first);
+                    *out = h0 ? max(*out, best) : best;
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+}
+
+// Candidates of sequence s, 0 where all of them are taken.
+__device__ __forceinline__ int candidates(const SelectParams &p, int s) {
+    const int n = (clamp_len(p, s, false) + p.B - 1) / p.B, cand = n - p.first - p.last;
+    return cand > p.top ? cand : 0;
+}
+
+// Few rows: the candidates of all sequences end to end, in even runs; a group
+// of Hk warps takes a run, a warp each kv head, so that the heads' means of a
+// block, which lie side by side, are read together.
+template <typename T, int D, int GP>
+__global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const SelectParams p) {
+    extern __shared__ __align__(128) uint8_t rings[];
+    pkv::grid_dependents_launch();
+    pkv::grid_dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t ring = pkv::smem_u32(rings) + warp * kRingBytes;
+    long long total = 0;
+    for (int s0 = 0; s0 < p.S; s0 += 32) {
+        const int s = s0 + lane;
+        total += __reduce_add_sync(~0u, s < p.S ? candidates(p, s) : 0);
+    }
+    const int64_t warps = (int64_t)gridDim.x * (kScoreThreads / 32);
+    const int64_t groups = warps / p.Hk > 0 ? warps / p.Hk : 1;
+    for (int64_t task = (int64_t)blockIdx.x * (kScoreThreads / 32) + warp; task < groups * p.Hk; task += warps) {
+        const int g = (int)(task % p.Hk);
+        long long at = task / p.Hk * total / groups;
+        const long long end = (task / p.Hk + 1) * total / groups;
+        // the sequence that holds `at`, then on to `end`
+        long long before = 0;
+        for (int s0 = 0; s0 < p.S && at < end; s0 += 32) {
+            const int mine = s0 + lane < p.S ? candidates(p, s0 + lane) : 0;
+            const int sum = __reduce_add_sync(~0u, mine);
+            if (before + sum <= at) {
+                before += sum;
+                continue;
+            }
+            for (int i = 0; i < 32 && at < end; ++i) {
+                const int c = __shfl_sync(~0u, mine, i);
+                if (before + c > at) {
+                    const int lo = (int)(at - before), hi = (int)min((long long)c, end - before);
+                    score_blocks<T, D, GP>(p, s0 + i, g, p.first + lo, p.first + hi,
+                                           p.keys + ((int64_t)(s0 + i) * p.Hk + g) * p.pitch, ring);
+                    at = before + hi;
+                }
+                before += c;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- selection
 // Exclusive prefix of `v` over the CTA's threads, and the total.
+template <int THREADS>
 __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int inc = v;
@@ -239,129 +384,275 @@ __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total) {
     int before = inc - v;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += warp_sums[w];
         total += warp_sums[w];
     }
     return before;
 }
 
+// The entry of block j in a selection of kv head g.
+__device__ __forceinline__ int32_t entry_of(const SelectParams &p, const int32_t *row, int j, int g) {
+    const int id = __ldg(row + j);
+    if ((unsigned)id < (unsigned)p.NB) return id * p.Hk + g;
+    if (g == 0) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+    return -1;
+}
+
+// N keys from candidate `at` on (a multiple of 4); 0 past the last, below every key.
+template <int N>
+__device__ __forceinline__ void load_keys(uint32_t (&key)[N], const uint32_t *keys, int at, int cand) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (at + i < cand) v = *reinterpret_cast<const uint4 *>(keys + at + i);
+        key[i] = v.x;
+        key[i + 1] = at + i + 1 < cand ? v.y : 0u;
+        key[i + 2] = at + i + 2 < cand ? v.z : 0u;
+        key[i + 3] = at + i + 3 < cand ? v.w : 0u;
+    }
+}
+
+// Which of N keys are taken; `tie`: those equal to the threshold.
+template <int N>
+__device__ __forceinline__ uint32_t compare_keys(const uint32_t (&key)[N], uint32_t threshold, uint32_t &tie) {
+    uint32_t take = 0;
+    tie = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        take |= (uint32_t)(key[i] > threshold) << i;
+        tie |= (uint32_t)(key[i] == threshold) << i;
+    }
+    return take;
+}
+
+// Adds the first of the ties to `take`: those of rank below `ties`.
+__device__ __forceinline__ uint32_t add_ties(uint32_t take, uint32_t tie, int rank, int ties) {
+    for (; tie && rank < ties; tie &= tie - 1, ++rank) take |= tie & -tie;
+    return take;
+}
+
+// One warp, up to 32 * kPerLane candidates: `top` < cand of them to out.
+__device__ __forceinline__ void warp_select(const SelectParams &p, const uint32_t *keys, int cand,
+                                            const int32_t *row, int g, int32_t *out) {
+    if (p.top == 0) return;
+    const int lane = threadIdx.x & 31;
+    uint32_t key[kPerLane];
+    load_keys(key, keys, lane * kPerLane, cand);
+    uint32_t threshold = 0;
+    int above = 0, ties = INT32_MAX;
+    bool exact = false;
+    for (int bit = 31; bit >= 0 && !exact; --bit) {
+        const uint32_t test = threshold | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) c += key[i] >= test;
+        c = __reduce_add_sync(~0u, c);
+        if (c >= p.top) threshold = test;
+        else above = c;
+        exact = c == p.top;          // these and no others: nothing equal is left out
+    }
+    if (!exact) ties = p.top - above;
+    uint32_t tie;
+    uint32_t take = compare_keys(key, threshold, tie);
+    int rank = __popc(tie), mine = rank;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, rank, o);
+        if (lane >= o) rank += x;
+    }
+    take = add_ties(take, tie, rank - mine, ties);
+    int at = __popc(take);
+    mine = at;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, at, o);
+        if (lane >= o) at += x;
+    }
+    at -= mine;
+    for (; take; take &= take - 1)
+        out[at++] = entry_of(p, row, p.first + lane * kPerLane + __ffs(take) - 1, g);
+}
+
+// The whole CTA, any number of candidates.
+template <int THREADS>
+__device__ __forceinline__ void block_select(const SelectParams &p, const uint32_t *keys, int cand,
+                                             const int32_t *row, int g, int32_t *out, int *sums,
+                                             int (&counts)[2][THREADS / 32]) {
+    if (p.top == 0) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int per_pass = THREADS * kPerThread;
+    uint32_t key[kPerThread];
+    load_keys(key, keys, tid * kPerThread, cand);
+    uint32_t threshold = 0;
+    int above = 0, ties = INT32_MAX;
+    bool exact = false;
+    for (int bit = 31; bit >= 0 && !exact; --bit) {
+        const uint32_t test = threshold | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) c += key[i] >= test;
+        for (int j = per_pass + tid; j < cand; j += THREADS) c += keys[j] >= test;
+        c = __reduce_add_sync(~0u, c);
+        if (lane == 0) counts[bit & 1][warp] = c;
+        __syncthreads();             // the other buffer is free: its readers came before
+        c = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) c += counts[bit & 1][w];
+        if (c >= p.top) threshold = test;
+        else above = c;
+        exact = c == p.top;
+    }
+    if (!exact) ties = p.top - above;
+    int written = 0, tied = 0, total;
+    for (int base = 0; base < cand; base += per_pass) {
+        const int j0 = base + tid * kPerThread;
+        if (base) load_keys(key, keys, j0, cand);
+        uint32_t tie;
+        uint32_t take = compare_keys(key, threshold, tie);
+        const int rank = tied + block_prefix<THREADS>(__popc(tie), sums, total);
+        tied += total;
+        take = add_ties(take, tie, rank, ties);
+        int at = written + block_prefix<THREADS>(__popc(take), sums, total);
+        written += total;
+        for (; take; take &= take - 1)
+            out[at++] = entry_of(p, row, p.first + j0 + __ffs(take) - 1, g);
+    }
+}
+
+// What every row has besides its chosen candidates: the first and last blocks
+// (or all blocks), and its length. Threads from `from` on.
+__device__ __forceinline__ void write_rest(const SelectParams &p, int r, int L, int n, bool all,
+                                           const int32_t *row, int g, int from) {
+    int32_t *out = p.sel_tables + (int64_t)r * p.W;
+    const int step = blockDim.x - from, t = threadIdx.x - from;
+    if (t < 0) return;
+    if (all) {
+        for (int w = t; w < p.W; w += step) out[w] = w < n ? entry_of(p, row, w, g) : -1;
+    } else {
+        for (int w = t; w < p.first; w += step) out[w] = entry_of(p, row, w, g);
+        for (int w = t; w < p.last; w += step) out[p.first + p.top + w] = entry_of(p, row, n - p.last + w, g);
+    }
+    const int count = all ? n : p.W;
+    if (t == 0) p.sel_lens[r] = n ? (count - 1) * p.B + L - (n - 1) * p.B : 0;
+}
+
+// Selects from the keys of block_scores_kernel.
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectParams p) {
     __shared__ int sums[kSelThreads / 32];
     __shared__ int counts[2][kSelThreads / 32];
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int s = blockIdx.x / p.Hk, g = blockIdx.x - s * p.Hk;
-    const int L = clamp_len(p, s, false);
-    const int n = (L + p.B - 1) / p.B;
-    const int32_t *row = p.tables + (int64_t)s * p.M;
-    int32_t *out = p.sel_tables + (int64_t)blockIdx.x * p.W;
-    const float *score = p.scores + (int64_t)blockIdx.x * p.M;
-    // candidates are [first, end); all blocks are listed where they are few
-    const int first = p.first, end = n - p.last, cand = end - first;
+    const int L = clamp_len(p, s, g == 0 && threadIdx.x == 0);
+    const int n = (L + p.B - 1) / p.B, cand = n - p.last - p.first;
     const bool all = cand <= p.top;
+    const int32_t *row = p.tables + (int64_t)s * p.M;
+    write_rest(p, blockIdx.x, L, n, all, row, g, 0);
+    if (!all)
+        block_select<kSelThreads>(p, p.keys + (int64_t)blockIdx.x * p.pitch, cand, row, g,
+                                  p.sel_tables + (int64_t)blockIdx.x * p.W + p.first, sums, counts);
+}
 
-    uint32_t threshold = 0;          // the top-th largest key
-    int ties = 0;                    // how many of its equals are taken, in order
-    const int per_pass = kSelThreads * kPerThread;
-    const bool one_pass = cand <= per_pass;
-    uint32_t key[kPerThread];
-    if (!all) {
-        if (one_pass) {
-#pragma unroll
-            for (int i = 0; i < kPerThread; ++i) {
-                const int j = first + tid * kPerThread + i;
-                key[i] = j < end ? key_of(__ldcg(score + j)) : 0u;   // below every real key
-            }
-        }
-        // the largest key that at least `top` keys reach, bit by bit
-        int above = 0;               // keys above the final threshold
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t test = threshold | (1u << bit);
-            int c = 0;
-            if (one_pass) {
-#pragma unroll
-                for (int i = 0; i < kPerThread; ++i) c += key[i] >= test;
-            } else {
-                for (int j = first + tid; j < end; j += kSelThreads) c += key_of(__ldcg(score + j)) >= test;
-            }
-            c = __reduce_add_sync(~0u, c);
-            if (lane == 0) counts[bit & 1][warp] = c;
-            __syncthreads();         // the other buffer is free: its readers came before
-            c = 0;
-#pragma unroll
-            for (int w = 0; w < kSelThreads / 32; ++w) c += counts[bit & 1][w];
-            if (c >= p.top) threshold = test;
-            else above = c;
-            if (c == p.top) {        // these and no others: nothing equal is left out
-                above = -1;
-                break;
-            }
-        }
-        ties = above < 0 ? INT32_MAX : p.top - above;
-        if (p.top == 0) ties = 0;
+// Scores and selects one row.
+template <typename T, int D, int GP>
+__global__ void __launch_bounds__(kRowThreads, 2) block_rows_kernel(const SelectParams p) {
+    extern __shared__ __align__(128) uint8_t rings[];       // then the row's keys
+    __shared__ int sums[kRowThreads / 32];
+    __shared__ int counts[2][kRowThreads / 32];
+    pkv::grid_dependents_launch();
+    pkv::grid_dependency_wait();
+    constexpr int kWarps = kRowThreads / 32;
+    uint32_t *row_keys = reinterpret_cast<uint32_t *>(rings + kWarps * kRingBytes);
+    const int s = blockIdx.x / p.Hk, g = blockIdx.x - s * p.Hk, warp = threadIdx.x >> 5;
+    const int L = clamp_len(p, s, g == 0 && threadIdx.x == 0);
+    const int n = (L + p.B - 1) / p.B, cand = n - p.last - p.first;
+    const bool all = cand <= p.top;
+    const int32_t *row = p.tables + (int64_t)s * p.M;
+    if (all) {
+        write_rest(p, blockIdx.x, L, n, true, row, g, 0);
+        return;
     }
-
-    // walk the blocks in order; a thread holds neighbours
-    int written = 0, tied = 0;       // over the passes before
-    for (int base = 0; base < n; base += per_pass) {
-        const int j0 = base + tid * kPerThread;
-        uint32_t take = 0, tie = 0;  // a bit for each of the thread's blocks
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int j = j0 + i;
-            if (j >= n) continue;
-            if (all || j < first || j >= end) {
-                take |= 1u << i;
-            } else if (p.top > 0) {
-                const uint32_t k = key_of(__ldcg(score + j));
-                if (k > threshold) take |= 1u << i;
-                else if (k == threshold) tie |= 1u << i;
-            }
-        }
-        int total;
-        int rank = tied + block_prefix(__popc(tie), sums, total);
-        tied += total;
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i)
-            if (tie >> i & 1 && rank++ < ties) take |= 1u << i;
-        int at = written + block_prefix(__popc(take), sums, total);
-        written += total;
-        for (; take; take &= take - 1) {
-            const int id = __ldg(row + j0 + __ffs(take) - 1);
-            const bool ok = id >= 0 && id < p.NB;
-            if (!ok && g == 0) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-            if (at < p.W) out[at] = ok ? id * p.Hk + g : -1;
-            ++at;
-        }
+    // even shares, in whole loads
+    const int share = ((cand + kWarps - 1) / kWarps + 3) & ~3;
+    const int lo = p.first + min(cand, warp * share), hi = p.first + min(cand, (warp + 1) * share);
+    if (lo < hi) score_blocks<T, D, GP>(p, s, g, lo, hi, row_keys, pkv::smem_u32(rings) + warp * kRingBytes);
+    __syncthreads();
+    int32_t *out = p.sel_tables + (int64_t)blockIdx.x * p.W + p.first;
+    if (cand <= 32 * kPerLane) {
+        if (warp == 0) warp_select(p, row_keys, cand, row, g, out);
+        else write_rest(p, blockIdx.x, L, n, false, row, g, 32);
+    } else {
+        write_rest(p, blockIdx.x, L, n, false, row, g, 0);
+        block_select<kRowThreads>(p, row_keys, cand, row, g, out, sums, counts);
     }
-    for (int w = written + tid; w < p.W; w += kSelThreads) out[w] = -1;
-    if (tid == 0) p.sel_lens[blockIdx.x] = n ? (written - 1) * p.B + L - (n - 1) * p.B : 0;
 }
 
 // ---------------------------------------------------------------- host
 bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
+// Keys of a row, padded to whole 16-byte loads.
+int key_pitch(int64_t M) { return (int)((M + 3) / 4 * 4); }
+
+constexpr size_t kRowKeyBytes = 64 << 10;        // keys of a row in shared memory, at most
+
+// Shared memory above the default 48 KB: an attribute of each kernel on each
+// device, set once (`ready`: devices done).
+template <typename K>
+cudaError_t allow_smem(K *kernel, size_t bytes, std::atomic<uint64_t> &ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
+template <typename T, int D, int GP>
+struct Launch {
+    static cudaError_t rows(const SelectParams &p, cudaStream_t stream) {
+        static std::atomic<uint64_t> ready{0};
+        constexpr size_t ring = (size_t)kRowThreads / 32 * kRingBytes;
+        const cudaError_t e = allow_smem(block_rows_kernel<T, D, GP>, ring + kRowKeyBytes, ready);
+        if (e != cudaSuccess) return e;
+        return launch_chained(block_rows_kernel<T, D, GP>, dim3((unsigned)(p.S * p.Hk)), kRowThreads,
+                              ring + (size_t)p.pitch * 4, stream, p);
+    }
+    static cudaError_t runs(const SelectParams &p, int sms, cudaStream_t stream) {
+        static std::atomic<uint64_t> ready{0};
+        constexpr size_t ring = (size_t)kScoreThreads / 32 * kRingBytes;
+        cudaError_t e = allow_smem(block_scores_kernel<T, D, GP>, ring, ready);
+        if (e != cudaSuccess) return e;
+        e = launch_chained(block_scores_kernel<T, D, GP>, dim3((unsigned)(2 * sms)), kScoreThreads, ring, stream, p);
+        if (e != cudaSuccess) return e;
+        return launch_chained(block_select_kernel, dim3((unsigned)(p.S * p.Hk)), kSelThreads, 0, stream, p);
+    }
+};
+
+template <typename T, int D, int GP>
+cudaError_t launch_select(const SelectParams &p, bool rows, int sms, cudaStream_t stream) {
+    return rows ? Launch<T, D, GP>::rows(p, stream) : Launch<T, D, GP>::runs(p, sms, stream);
+}
+
 template <typename T, int D>
-cudaError_t launch_scores(const SelectParams &p, cudaStream_t stream) {
-    const int64_t tasks = (int64_t)p.S * p.chunks * p.Hk;
-    const dim3 grid((unsigned)((tasks + kScoreThreads / 32 - 1) / (kScoreThreads / 32)));
+cudaError_t launch_select_d(const SelectParams &p, bool rows, int sms, cudaStream_t stream) {
     // heads at a time: the registers of q are 8 a head
-    auto *kernel = p.G == 1   ? &block_scores_kernel<T, D, 1>
-                   : p.G == 2 ? &block_scores_kernel<T, D, 2>
-                   : p.G <= 4 ? &block_scores_kernel<T, D, 4>
-                              : &block_scores_kernel<T, D, 8>;
-    return launch_chained(kernel, grid, kScoreThreads, 0, stream, p);
+    auto *go = p.G == 1   ? &launch_select<T, D, 1>
+               : p.G == 2 ? &launch_select<T, D, 2>
+               : p.G <= 4 ? &launch_select<T, D, 4>
+                          : &launch_select<T, D, 8>;
+    return go(p, rows, sms, stream);
 }
 
 template <typename T>
-cudaError_t launch_scores_for(int D, const SelectParams &p, cudaStream_t stream) {
-    return D == 64 ? launch_scores<T, 64>(p, stream) : launch_scores<T, 128>(p, stream);
+cudaError_t launch_select_t(int D, const SelectParams &p, bool rows, int sms, cudaStream_t stream) {
+    return D == 64 ? launch_select_d<T, 64>(p, rows, sms, stream) : launch_select_d<T, 128>(p, rows, sms, stream);
 }
 
 size_t score_bytes(const pkv_cache_desc *c, int64_t S, int64_t M) {
-    return (size_t)(((S * c->num_kv_heads * M * 4) + 15) / 16 * 16);
+    return (size_t)S * c->num_kv_heads * key_pitch(M) * 4;
 }
 
 pkv_status check_select(const pkv_cache_desc *c, int32_t S, int32_t Hq, int32_t M) {
@@ -375,8 +666,7 @@ pkv_status check_select(const pkv_cache_desc *c, int32_t S, int32_t Hq, int32_t 
     if (M < 1) return pkv::set_last_error(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d", M);
     if ((int64_t)c->num_blocks * c->num_kv_heads > INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");
-    if ((int64_t)M * c->block_size > INT32_MAX || (int64_t)S * c->num_kv_heads > INT32_MAX / 64 ||
-        (int64_t)S * c->num_kv_heads * ((M + kChunk - 1) / kChunk) / 8 >= INT32_MAX)
+    if ((int64_t)M * c->block_size > INT32_MAX || (int64_t)S * c->num_kv_heads > INT32_MAX / 64)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
     return PKV_OK;
 }
@@ -469,20 +759,22 @@ pkv_status pkv_select_blocks(const pkv_cache_desc *cache, const void *q, int32_t
     p.M = max_blocks_per_seq;
     p.NB = cache->num_blocks;
     p.B = cache->block_size;
-    p.chunks = (max_blocks_per_seq + kChunk - 1) / kChunk;
     p.top = select->top_blocks;
     p.first = select->first_blocks;
     p.last = select->last_blocks;
     p.W = (int)W;
-    p.scores = static_cast<float *>(workspace);
+    p.pitch = key_pitch(max_blocks_per_seq);
+    p.keys = static_cast<uint32_t *>(workspace);
     p.sel_tables = sel_tables;
     p.sel_lens = sel_lens;
+    int sms = 0;
+    if ((st = pkv::device_sm_count(&sms)) != PKV_OK) return st;
+    // a CTA a row where the rows fill the GPU
+    const bool rows = (int64_t)num_seqs * p.Hk >= sms && (size_t)p.pitch * 4 <= kRowKeyBytes;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cache->dtype == PKV_F32   ? launch_scores_for<float>(cache->head_dim, p, s)
-                    : cache->dtype == PKV_F16 ? launch_scores_for<__half>(cache->head_dim, p, s)
-                                              : launch_scores_for<__nv_bfloat16>(cache->head_dim, p, s);
-    if (e == cudaSuccess)
-        e = launch_chained(block_select_kernel, dim3((unsigned)(num_seqs * p.Hk)), kSelThreads, 0, s, p);
+    const cudaError_t e = cache->dtype == PKV_F32   ? launch_select_t<float>(cache->head_dim, p, rows, sms, s)
+                          : cache->dtype == PKV_F16 ? launch_select_t<__half>(cache->head_dim, p, rows, sms, s)
+                                                    : launch_select_t<__nv_bfloat16>(cache->head_dim, p, rows, sms, s);
     if (e != cudaSuccess)
         return pkv::set_last_error(PKV_ERR_CUDA, "block selection launch: %s", cudaGetErrorString(e));
     return PKV_OK;
