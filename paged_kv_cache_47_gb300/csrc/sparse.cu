@@ -15,11 +15,13 @@
 // mean is read once), by the multiply-adds from 8 heads a group on.
 //
 // Selection. The candidates taken are those above the top-th largest key and
-// the first of its equals. That key is found bit by bit, counting keys held in
-// registers (no shared-memory histogram: the high bits of scores are nearly
-// all alike and its atomics would queue); the search ends as soon as a
-// threshold leaves exactly `top`. Threads hold neighbouring candidates, so two
-// scans over them give each its place in ascending order.
+// the first of its equals. One warp finds that key bit by bit, counting keys in
+// registers; a CTA by digits of 11 bits, a histogram in shared memory each
+// (the first digit begins at the highest bit in which the row's keys differ:
+// above it scores are nearly all alike and the histogram's atomics would
+// queue). Both end as soon as a threshold leaves exactly `top`. Threads hold
+// neighbouring candidates, so two scans over them give each its place in
+// ascending order.
 //
 // Rows (sequence, kv head) enough for every SM: one kernel, a CTA a row, keys
 // in shared memory; up to 256 candidates one warp selects alone, with no
@@ -42,7 +44,7 @@ namespace {
 
 using pkv::launch_chained;
 
-constexpr int kRowThreads = 256;     // a CTA that scores and selects one row
+constexpr int kRowThreads = 128;     // a CTA that scores and selects one row: four fit on an SM
 constexpr int kScoreThreads = 256;
 constexpr int kSelThreads = 512;
 constexpr int kPerThread = 16;       // keys a thread holds
@@ -439,10 +441,19 @@ __device__ __forceinline__ void warp_select(const SelectParams &p, const uint32_
     const int lane = threadIdx.x & 31;
     uint32_t key[kPerLane];
     load_keys(key, keys, lane * kPerLane, cand);
-    uint32_t threshold = 0;
+    uint32_t low = ~0u, high = 0;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        high = max(high, key[i]);
+        if (key[i]) low = min(low, key[i]);
+    }
+    low = __reduce_min_sync(~0u, low);
+    high = __reduce_max_sync(~0u, high);
+    const int bits = 32 - __clz(low ^ high);     // the keys differ in these
+    uint32_t threshold = bits == 32 ? 0 : low >> bits << bits;
     int above = 0, ties = INT32_MAX;
     bool exact = false;
-    for (int bit = 31; bit >= 0 && !exact; --bit) {
+    for (int bit = bits - 1; bit >= 0 && !exact; --bit) {
         const uint32_t test = threshold | (1u << bit);
         int c = 0;
 #pragma unroll
@@ -475,45 +486,115 @@ __device__ __forceinline__ void warp_select(const SelectParams &p, const uint32_
 }
 
 // The whole CTA, any number of candidates.
+constexpr int kDigitBits = 11;
+template <int THREADS>
+struct SelectShared {
+    int sums[THREADS / 32];
+    uint32_t lows[THREADS / 32], highs[THREADS / 32];
+    int bins[1 << kDigitBits];
+    int bin, above;
+};
+
 template <int THREADS>
 __device__ __forceinline__ void block_select(const SelectParams &p, const uint32_t *keys, int cand,
-                                             const int32_t *row, int g, int32_t *out, int *sums,
-                                             int (&counts)[2][THREADS / 32]) {
+                                             const int32_t *row, int g, int32_t *out,
+                                             SelectShared<THREADS> &sh) {
     if (p.top == 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int per_pass = THREADS * kPerThread;
+    constexpr int kBins = 1 << kDigitBits, PER = kBins / THREADS;
     uint32_t key[kPerThread];
     load_keys(key, keys, tid * kPerThread, cand);
-    uint32_t threshold = 0;
-    int above = 0, ties = INT32_MAX;
-    bool exact = false;
-    for (int bit = 31; bit >= 0 && !exact; --bit) {
-        const uint32_t test = threshold | (1u << bit);
-        int c = 0;
+    // smallest and largest key
+    uint32_t low = ~0u, high = 0;
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) c += key[i] >= test;
-        for (int j = per_pass + tid; j < cand; j += THREADS) c += keys[j] >= test;
-        c = __reduce_add_sync(~0u, c);
-        if (lane == 0) counts[bit & 1][warp] = c;
-        __syncthreads();             // the other buffer is free: its readers came before
-        c = 0;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) c += counts[bit & 1][w];
-        if (c >= p.top) threshold = test;
-        else above = c;
-        exact = c == p.top;
+    for (int i = 0; i < kPerThread; ++i) {
+        high = max(high, key[i]);
+        if (key[i]) low = min(low, key[i]);
     }
-    if (!exact) ties = p.top - above;
-    int written = 0, tied = 0, total;
+    for (int j = per_pass + tid; j < cand; j += THREADS) {
+        low = min(low, keys[j]);
+        high = max(high, keys[j]);
+    }
+    low = __reduce_min_sync(~0u, low);
+    high = __reduce_max_sync(~0u, high);
+    if (lane == 0) {
+        sh.lows[warp] = low;
+        sh.highs[warp] = high;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        low = min(low, sh.lows[w]);
+        high = max(high, sh.highs[w]);
+    }
+    // the top-th largest key: its bits from `shift` up are those of `threshold`,
+    // `above` keys are larger in these bits
+    int shift = 32 - __clz(low ^ high), above = 0, total;
+    uint32_t threshold = shift == 32 ? 0 : low >> shift << shift;
+    bool exact = false;
+    while (shift > 0 && !exact) {
+        const int next = max(0, shift - kDigitBits);
+        const uint32_t prefix = shift == 32 ? 0 : threshold >> shift;
+        auto digit_of = [&](uint32_t k, bool &in) {
+            in = k != 0 && (shift == 32 || k >> shift == prefix);
+            return (int)(k >> next) & ((1 << (shift - next)) - 1);
+        };
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sh.bins[tid * PER + i] = 0;
+        __syncthreads();
+        bool in;
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int d = digit_of(key[i], in);
+            if (in) atomicAdd(&sh.bins[d], 1);
+        }
+        for (int j = per_pass + tid; j < cand; j += THREADS) {
+            const int d = digit_of(keys[j], in);
+            if (in) atomicAdd(&sh.bins[d], 1);
+        }
+        __syncthreads();
+        // thread t holds PER bins from the top down; keys in bins above them
+        int c[PER], sum = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            c[i] = sh.bins[kBins - 1 - (tid * PER + i)];
+            sum += c[i];
+        }
+        int before = above + block_prefix<THREADS>(sum, sh.sums, total);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (before < p.top && before + c[i] >= p.top) {
+                sh.bin = kBins - 1 - (tid * PER + i);
+                sh.above = before;
+            }
+            before += c[i];
+        }
+        __syncthreads();
+        const int d = sh.bin;
+        above = sh.above;
+        threshold |= (uint32_t)d << next;
+        exact = above + sh.bins[d] == p.top;     // the whole bin: nothing equal is left out
+        shift = next;
+        __syncthreads();                         // before the bins are cleared
+    }
+    // exact: every key from the threshold's bin up; else those above it and the
+    // first of its equals
+    const int ties = p.top - above;
+    int written = 0, tied = 0;
     for (int base = 0; base < cand; base += per_pass) {
         const int j0 = base + tid * kPerThread;
         if (base) load_keys(key, keys, j0, cand);
-        uint32_t tie;
-        uint32_t take = compare_keys(key, threshold, tie);
-        const int rank = tied + block_prefix<THREADS>(__popc(tie), sums, total);
-        tied += total;
-        take = add_ties(take, tie, rank, ties);
-        int at = written + block_prefix<THREADS>(__popc(take), sums, total);
+        uint32_t tie, take;
+        if (exact) {
+            take = compare_keys(key, threshold - 1, tie);
+        } else {
+            take = compare_keys(key, threshold, tie);
+            const int rank = tied + block_prefix<THREADS>(__popc(tie), sh.sums, total);
+            tied += total;
+            take = add_ties(take, tie, rank, ties);
+        }
+        int at = written + block_prefix<THREADS>(__popc(take), sh.sums, total);
         written += total;
         for (; take; take &= take - 1)
             out[at++] = entry_of(p, row, p.first + j0 + __ffs(take) - 1, g);
@@ -539,8 +620,7 @@ __device__ __forceinline__ void write_rest(const SelectParams &p, int r, int L, 
 
 // Selects from the keys of block_scores_kernel.
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectParams p) {
-    __shared__ int sums[kSelThreads / 32];
-    __shared__ int counts[2][kSelThreads / 32];
+    __shared__ SelectShared<kSelThreads> sh;
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
     const int s = blockIdx.x / p.Hk, g = blockIdx.x - s * p.Hk;
@@ -551,19 +631,18 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectP
     write_rest(p, blockIdx.x, L, n, all, row, g, 0);
     if (!all)
         block_select<kSelThreads>(p, p.keys + (int64_t)blockIdx.x * p.pitch, cand, row, g,
-                                  p.sel_tables + (int64_t)blockIdx.x * p.W + p.first, sums, counts);
+                                  p.sel_tables + (int64_t)blockIdx.x * p.W + p.first, sh);
 }
 
 // Scores and selects one row.
 template <typename T, int D, int GP>
-__global__ void __launch_bounds__(kRowThreads, 2) block_rows_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kRowThreads, 4) block_rows_kernel(const SelectParams p) {
     extern __shared__ __align__(128) uint8_t rings[];       // then the row's keys
-    __shared__ int sums[kRowThreads / 32];
-    __shared__ int counts[2][kRowThreads / 32];
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
     constexpr int kWarps = kRowThreads / 32;
     uint32_t *row_keys = reinterpret_cast<uint32_t *>(rings + kWarps * kRingBytes);
+    static_assert(sizeof(SelectShared<kRowThreads>) <= kWarps * kRingBytes, "it takes the rings' place");
     const int s = blockIdx.x / p.Hk, g = blockIdx.x - s * p.Hk, warp = threadIdx.x >> 5;
     const int L = clamp_len(p, s, g == 0 && threadIdx.x == 0);
     const int n = (L + p.B - 1) / p.B, cand = n - p.last - p.first;
@@ -584,7 +663,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) block_rows_kernel(const Select
         else write_rest(p, blockIdx.x, L, n, false, row, g, 32);
     } else {
         write_rest(p, blockIdx.x, L, n, false, row, g, 0);
-        block_select<kRowThreads>(p, row_keys, cand, row, g, out, sums, counts);
+        // (the rings are used up: the selection's histogram takes their place)
+        block_select<kRowThreads>(p, row_keys, cand, row, g, out,
+                                  *reinterpret_cast<SelectShared<kRowThreads> *>(rings));
     }
 }
 
