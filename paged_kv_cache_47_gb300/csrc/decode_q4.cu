@@ -42,37 +42,36 @@
 #include "launch_utils.h"
 #include "pkv_internal.h"
 #include "q4_internal.h"
-#include "q4_split.h"
+#include "warp_decode.cuh"
 
 namespace {
 
 using pkv::launch_chained;
 
 constexpr int kSub = 32;             // tokens of a subtile: two halves of 16, the m and k of the mma
-constexpr int kHeads = 8;            // q heads of a unit (the n of the mma)
-constexpr int kWarps = pkv::kQ4Warps;
+constexpr int kHeads = pkv::kWdHeads;
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxSeqs = 1024;       // sequences of one launch
-constexpr float kNone = 2e-38f;      // reference exponent of a head before its first finite
-                                     // score: 0 to any score, and no score's own
+constexpr int kMaxSeqs = pkv::kWdMaxSeqs;
+// What a warp spends on a unit besides its subtiles (q to operands, the piece
+// it leaves), in subtiles: 3.1 us against 2.07 us a subtile on the Llama-shaped
+// batch. Counting units as 2 subtiles evened the warps' ends out (loops of 29.6
+// and 29.8 us with one and two units, 31.7 and 35.3 us uncounted).
+constexpr int kUnitCost = 2;
+constexpr float kNone = pkv::kWdNone;
 
 struct Q4Params {
+    pkv::WdList list;
+    pkv::WdOut o;
     const void *q;
-    void *out;
-    int out_dtype, act_f16;
-    const int32_t *tables, *lens;
-    int S, Hq, Hk, G, NC, GC, U, M, NB, lb;    // block size 1 << lb; U = Hk * NC units a sequence
+    int act_f16;
+    int Hk, NB;
     uint32_t code_bytes, par_bytes;  // of one (block, kv head) chunk, K or V
     float scale_log2;
     const uint8_t *kc, *vc;
     const __half *kp, *vp;
-    unsigned *cnt;                   // [C] arrivals, zero between calls
-    float *ws_o, *ws_lse;            // [C][2][GC][D], [C][2][GC]
     float *ws_pieces;                // [C][warps][GC][D], or NULL: on chip
     int C;
-    float *lse_out;
-    int tables_ready;
-    unsigned *err;
 };
 
 template <int D>
@@ -85,11 +84,7 @@ struct Cfg {
     static constexpr int kRing = kStages * kStage;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+using pkv::wd_ex2;
 
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -174,7 +169,7 @@ __device__ __noinline__ void issue_ragged(const Q4Params &p, uint32_t stage, int
         const int c = lane + 32 * j, r = c / (D / 32), w = c % (D / 32);
         int id = __shfl_sync(~0u, window, at + (r >> LB));
         const bool ok = (unsigned)id < (unsigned)p.NB;
-        if (!ok && r < left) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+        if (!ok && r < left) atomicOr(p.list.err, PKV_DEVERR_BLOCK_ID);
         if (!ok) id = 0;
         const size_t src = (((size_t)id * p.Hk + head) * B + (r & (B - 1))) * (D / 2) + w * 16;
         constexpr int kHalfLines = 16 * D / 2 / 128;
@@ -235,7 +230,7 @@ struct Loader {
 
     __device__ __forceinline__ int32_t entries(int from) const {
         const int e = from + lane;
-        return e < p.M ? __ldg(p.tables + (int64_t)s * p.M + e) : -1;
+        return e < p.list.M ? __ldg(p.list.tables + (int64_t)s * p.list.M + e) : -1;
     }
     __device__ __forceinline__ void windows() {
         base = (t0 >> LB) & ~31;
@@ -244,17 +239,15 @@ struct Loader {
     }
     __device__ __forceinline__ void fetch_q() {
         if (q_unit >= 0) return;
-        q_unit = s * p.U + u;
-        const int chunk = u - head * p.NC;
-        const int gca = min(p.GC, p.G - chunk * p.GC);
-        const uint8_t *src = static_cast<const uint8_t *>(p.q) +
-                             ((size_t)s * p.Hq + head * p.G + chunk * p.GC) * (D * 2);
+        q_unit = s * p.list.U + u;
+        const int gca = p.o.heads(u);
+        const uint8_t *src = static_cast<const uint8_t *>(p.q) + ((size_t)s * p.o.Hq + p.o.first_head(u)) * (D * 2);
         for (int i = lane * 16; i < gca * D * 2; i += 512) copy16<0>(q_buf + i, src + i);
     }
     __device__ __forceinline__ void start(int seq, int unit, int subtile) {
         s = seq;
         u = unit;
-        head = unit / p.NC;
+        head = unit / p.o.NC;
         t0 = subtile * kSub;
         left = len[s] - t0;
         windows();
@@ -273,11 +266,11 @@ struct Loader {
             }
             return 0;
         }
-        if (++u == p.U) {
+        if (++u == p.list.U) {
             u = 0;
-            do ++s; while (s < p.S - 1 && len[s] == 0);
+            do ++s; while (s < p.list.S - 1 && len[s] == 0);
         }
-        head = u / p.NC;
+        head = u / p.o.NC;
         t0 = 0;
         left = len[s];
         windows();
@@ -334,204 +327,33 @@ struct Loader {
     }
 };
 
-// E neighbouring fp32 values (2 or 4), and E outputs in the output's type.
-template <int E>
-__device__ __forceinline__ void add_scaled(float (&o)[E], const float *src, float f) {
-    if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        o[0] = fmaf(v.x, f, o[0]);
-        o[1] = fmaf(v.y, f, o[1]);
-        o[2] = fmaf(v.z, f, o[2]);
-        o[3] = fmaf(v.w, f, o[3]);
-    } else {
-        const float2 v = *reinterpret_cast<const float2 *>(src);
-        o[0] = fmaf(v.x, f, o[0]);
-        o[1] = fmaf(v.y, f, o[1]);
-    }
-}
-template <int E>
-__device__ __forceinline__ void load_cg(float (&o)[E], const float *src) {
-    if constexpr (E == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
-    } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-        o[0] = v.x, o[1] = v.y;
-    }
-}
-template <int E>
-__device__ __forceinline__ void store_f32(float *dst, const float (&o)[E]) {
-    if constexpr (E == 4) *reinterpret_cast<float4 *>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-    else *reinterpret_cast<float2 *>(dst) = make_float2(o[0], o[1]);
-}
-template <int E>
-__device__ __forceinline__ void store_row(const Q4Params &p, size_t at, const float (&o)[E]) {
-    if (p.out_dtype == PKV_F32) {
-        store_f32(static_cast<float *>(p.out) + at, o);
-        return;
-    }
-    uint32_t w[E / 2];
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-        float a, b;
-        w[i / 2] = p.out_dtype == PKV_F16 ? pkv::Elem<__half>::pack2(o[i], o[i + 1], a, b)
-                                          : pkv::Elem<__nv_bfloat16>::pack2(o[i], o[i + 1], a, b);
-    }
-    uint16_t *dst = static_cast<uint16_t *>(p.out) + at;
-    if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t *>(dst) = w[0];
-}
-
-// What a warp leaves of a unit it does not hold whole.
-struct Piece {
-    int tu, nu, s, u;     // the unit's first subtile and length in the list; its place; nu 0: none
-};
-
 template <int D, int LB>
 __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_constant__ Q4Params p) {
     using C = Cfg<D>;
     constexpr int NG = C::NG;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int prefix[kMaxSeqs + 1], len[kMaxSeqs];
-    __shared__ uint16_t nonempty[kMaxSeqs + 2];                   // sequences with tokens before a sequence
-    __shared__ int scan[kWarps], scan1[kWarps], scan2[kWarps];
-    __shared__ Piece piece[kWarps][2];
-    __shared__ float piece_lse[kWarps][2][kHeads];
-    __shared__ int cut_tu[2], cut_nu[2], cut_s[2], cut_u[2];      // units cut at the CTA's start, end
-    __shared__ int join_first[2], join_n[2];                      // of them, those to join here: parts
+    __shared__ pkv::WdListShared<kWarps> list;
+    __shared__ pkv::WdJoinShared<kWarps> join;
     uint8_t *ring_all = smem;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // places of the pieces that end in a warp, [warp][GC][D]: behind the rings
     // where they fit, else this CTA's part of the workspace
-    float *heads_o = p.ws_pieces ? p.ws_pieces + (size_t)blockIdx.x * kWarps * p.GC * D
-                                 : reinterpret_cast<float *>(smem + kWarps * (C::kRing + p.GC * (D * 2)));
-
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float *heads_o = p.ws_pieces ? p.ws_pieces + (size_t)blockIdx.x * kWarps * p.o.GC * D
+                                 : reinterpret_cast<float *>(smem + kWarps * (C::kRing + p.o.GC * (D * 2)));
     pkv::grid_dependents_launch();
-    if (!p.tables_ready) pkv::grid_dependency_wait();
-
-    // ---- lengths, and the places of the sequences' units in the list
-    int cost, longest = 0;
-    {
-        constexpr int K = kMaxSeqs / kThreads;
-        int n[K], sum = 0, some = 0;             // subtiles; sequences that have any
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int s = tid * K + k;
-            int L = s < p.S ? __ldg(p.lens + s) : 0;
-            if (L < 0 || L > (p.M << p.lb)) {
-                if (blockIdx.x == 0) atomicOr(p.err, PKV_DEVERR_CONTEXT);
-                L = L < 0 ? 0 : p.M << p.lb;
-            }
-            len[s] = L;
-            n[k] = (L + kSub - 1) / kSub;
-            sum += n[k];
-            some += L > 0;
-            longest = max(longest, n[k]);
-        }
-        int inc = sum, inc1 = some;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(~0u, inc, o), y = __shfl_up_sync(~0u, inc1, o);
-            if (lane >= o) {
-                inc += x;
-                inc1 += y;
-            }
-        }
-        longest = __reduce_max_sync(~0u, longest);
-        if (lane == 31) {
-            scan[warp] = inc;
-            scan1[warp] = inc1;
-            scan2[warp] = longest;
-        }
-        if (lane < 2) piece[warp][lane].nu = 0;
-        __syncthreads();
-        int before = inc - sum, before1 = inc1 - some, total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) {
-                before += scan[w];
-                before1 += scan1[w];
-            }
-            total += scan[w];
-            longest = max(longest, scan2[w]);
-        }
-        cost = pkv::q4_unit_cost(total * p.U, (int)gridDim.x);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            prefix[tid * K + k] = before + cost * before1;
-            nonempty[tid * K + k] = (uint16_t)before1;
-            before += n[k];
-            before1 += n[k] > 0;
-        }
-        if (tid == kThreads - 1) {
-            prefix[kMaxSeqs] = before + cost * before1;
-            nonempty[kMaxSeqs] = (uint16_t)before1;
-        }
-        __syncthreads();
-    }
-    if (p.tables_ready) pkv::grid_dependency_wait();
-
-    // empty contexts: zeros
-    for (int s = blockIdx.x; s < p.S; s += gridDim.x)
-        if (len[s] == 0) {
-            for (int e = tid; e < p.Hq * D; e += kThreads)
-                pkv::store_out(p.out, (size_t)s * p.Hq * D + e, p.out_dtype, 0.f);
-            if (p.lse_out)
-                for (int h = tid; h < p.Hq; h += kThreads) p.lse_out[(size_t)s * p.Hq + h] = -INFINITY;
-        }
-
-    // ---- this CTA's and this warp's part of the list
-    const int NV = prefix[kMaxSeqs] * p.U;
-    const int cta = blockIdx.x;
-    const int units = nonempty[kMaxSeqs] * p.U;
-    int CT, A, Z;
-    if (cost == 0 && units <= (int)gridDim.x && longest <= pkv::kQ4OneCta) {
-        // a unit for each CTA
-        CT = units;
-        if (cta >= CT) return;
-        int lo = 0, hi = p.S - 1;                // the last sequence with at most this many before it
-        const int k = cta / p.U;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (nonempty[mid] <= k) lo = mid;
-            else hi = mid - 1;
-        }
-        const int n = prefix[lo + 1] - prefix[lo];
-        A = prefix[lo] * p.U + (cta - k * p.U) * n;
-        Z = A + n;
-    } else {
-        CT = pkv::q4_active_ctas(NV, (int)gridDim.x, cost);
-        if (cta >= CT) return;
-        A = pkv::q4_cta_cut(cta, NV, CT);
-        Z = pkv::q4_cta_cut(cta + 1, NV, CT);
-    }
-    const int a = pkv::q4_warp_cut(warp, A, Z, cost), z = pkv::q4_warp_cut(warp + 1, A, Z, cost);
+    pkv::wd_join_init(join);
+    const pkv::WdShare share = pkv::wd_share<kWarps, kSub>(p.list, p.o, D, kUnitCost, list);
+    if ((int)blockIdx.x >= share.CT) return;
+    const int cost = share.cost, a = share.a, z = share.z;
 
     const uint32_t ring = pkv::smem_u32(ring_all) + warp * C::kRing;
     const int g = lane >> 2, t = lane & 3;
 
     if (a < z) {
-        // sequence, unit, subtile of the unit; places of a unit of the sequence, and
-        // the place of the unit's first subtile
-        int cs, cu, ci, nv, tu;
-        {   // the sequence holding place a: the last whose units begin at or before
-            // it (of equal prefixes, the empty sequences come first)
-            int lo = 0, hi = p.S - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (prefix[mid] * p.U <= a) lo = mid;
-                else hi = mid - 1;
-            }
-            nv = prefix[lo + 1] - prefix[lo];
-            const int r = a - prefix[lo] * p.U;
-            cs = lo;
-            cu = r / nv;
-            tu = a - (r - cu * nv) + cost;
-            ci = max(0, a - tu);
-        }
-        Loader<D, LB> ld(p, len, lane, cost, pkv::smem_u32(smem) + kWarps * C::kRing + warp * p.GC * (D * 2));
-        ld.start(cs, cu, ci);
-        int rem = z - (tu + ci);             // places from the next subtile to copy on
+        pkv::WdPlace at = pkv::wd_place(p.list, list, a, cost);
+        Loader<D, LB> ld(p, list.len, lane, cost, pkv::smem_u32(smem) + kWarps * C::kRing + warp * p.o.GC * (D * 2));
+        ld.start(at.s, at.u, at.i);
+        int rem = z - (at.tu + at.i);             // places from the next subtile to copy on
 #pragma unroll
         for (int st = 0; st < C::kStages; ++st) {
             if (rem > 0) {
@@ -557,20 +379,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 
         while (true) {
             // ---- a unit, or the part of it that lies here: `count` subtiles
-            const int n = nv - cost;
-            const int count = min(n, z - tu) - ci;
+            const int n = at.nv - cost;
+            const int count = min(n, z - at.tu) - at.i;
             if (count <= 0) break;
-            const int chunk = cu % p.NC, kvh = cu / p.NC;
-            const int gca = min(p.GC, p.G - chunk * p.GC);
-            const int h0 = kvh * p.G + chunk * p.GC;
-            int left = len[cs] - ci * kSub;      // tokens from the subtile in hand on
+            const int gca = p.o.heads(at.u), h0 = p.o.first_head(at.u);
+            int left = list.len[at.s] - at.i * kSub;     // tokens from the subtile in hand on
             uint32_t qb[NG][2][2];               // q as B operands
             uint32_t qsum;                       // sums of q over the groups, as a B operand
             float zs0, zs1;                      // scores to log2 units, heads 2t and 2t + 1
             {
                 // lane (g, t) holds elements 32 y + 8 t .. + 7 of head g
                 float x[NG][8], top = 0.f;
-                const bool here = ld.q_unit == cs * p.U + cu;
+                const bool here = ld.q_unit == at.s * p.list.U + at.u;
                 if (here) {
                     // copied with the unit's first subtile or before
                     asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -585,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                         else
                             raw = __ldg(reinterpret_cast<const uint4 *>(
                                 static_cast<const uint16_t *>(p.q) +
-                                ((size_t)cs * p.Hq + h0 + g) * D + 32 * y + 8 * t));
+                                ((size_t)at.s * p.o.Hq + h0 + g) * D + 32 * y + 8 * t));
                     }
                     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -762,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 if (t0 > -INFINITY) u0 = none0 ? t0 - 7.f + e : fmaxf(mu0, t0 - 7.f + e);
                 if (t1 > -INFINITY) u1 = none1 ? t1 - 7.f + e : fmaxf(mu1, t1 - 7.f + e);
                 // (before the first score there is nothing to rescale)
-                const float f0 = none0 ? 1.f : ex2(mu0 - u0), f1 = none1 ? 1.f : ex2(mu1 - u1);
+                const float f0 = none0 ? 1.f : wd_ex2(mu0 - u0), f1 = none1 ? 1.f : wd_ex2(mu1 - u1);
                 // a head that has had no score but -infinity keeps none, and
                 // the next subtile asks again
                 room = __any_sync(~0u, u0 == kNone || u1 == kNone) ? -INFINITY : 15.f - e;
@@ -794,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             for (int half = 0; half < 2; ++half) {
                 // ---- weights, transposed: lane (g, t) has head g, tokens 4t .. 4t + 3
                 const uint32_t p01 =
-                    transpose8(as_u32(__floats2half2_rn(ex2(sc[half][0]), ex2(sc[half][1]))));
+                    transpose8(as_u32(__floats2half2_rn(wd_ex2(sc[half][0]), wd_ex2(sc[half][1]))));
                 const uint32_t p23 =
-                    transpose8(as_u32(__floats2half2_rn(ex2(sc[half][2]), ex2(sc[half][3]))));
+                    transpose8(as_u32(__floats2half2_rn(wd_ex2(sc[half][2]), wd_ex2(sc[half][3]))));
                 // ---- V: rows of the product are d, its contracted index the tokens
                 uint32_t v01[NG], v23[NG];
                 {
@@ -856,14 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
           }
 
             // ---- the unit's output, or a piece of it
-            const bool whole = ci == 0 && count == n;
-            const int slot = ci ? 0 : 1;         // ci > 0: it began before this warp's part
+            const bool whole = at.i == 0 && count == n;
+            const int slot = at.i ? 0 : 1;       // i > 0: it began before this warp's part
             const float l0 = __shfl_sync(~0u, accx[2], t), l1 = __shfl_sync(~0u, accx[3], t);
             const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
             // a piece of a unit that goes on in the next warp lies in this
             // warp's ring, which is read to the end; the other has its own place
             float *po = slot ? reinterpret_cast<float *>(ring_all + warp * C::kRing)
-                             : heads_o + (size_t)warp * p.GC * D;
+                             : heads_o + (size_t)warp * p.o.GC * D;
             if (slot && !whole) __syncwarp();
 #pragma unroll
             for (int y = 0; y < NG; ++y) {
@@ -881,9 +701,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     const int d = 32 * y + 4 * g;
                     const float o4[4] = {o0, o1, o2, o3};
                     if (whole) {
-                        store_row<4>(p, ((size_t)cs * p.Hq + h0 + h) * D + d, o4);
+                        pkv::wd_store_row<4>(p.o, ((size_t)at.s * p.o.Hq + h0 + h) * D + d, o4);
                     } else {
-                        store_f32(po + h * D + d, o4);
+                        pkv::wd_store_f32(po + h * D + d, o4);
                     }
                 }
             }
@@ -893,150 +713,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     const int h = 2 * t + e;
                     if (h >= gca) continue;
                     const float lse = (e ? mu1 : mu0) + log2f(e ? l1 : l0);
-                    if (!whole) piece_lse[warp][slot][h] = lse;
-                    else if (p.lse_out) p.lse_out[(size_t)cs * p.Hq + h0 + h] = lse;
+                    if (!whole) join.lse[warp][slot][h] = lse;
+                    else if (p.o.lse_out) p.o.lse_out[(size_t)at.s * p.o.Hq + h0 + h] = lse;
                 }
             }
-            if (!whole && lane == 0) piece[warp][slot] = {tu, n, cs, cu};
-
-            ci = 0;
-            tu += nv;
-            if (tu >= z) break;
-            if (++cu == p.U) {
-                cu = 0;
-                do ++cs; while (len[cs] == 0);       // (there is one: the list goes on)
-                nv = prefix[cs + 1] - prefix[cs];
-            }
+            if (!whole && lane == 0) join.piece[warp][slot] = {at.tu, n, at.s, at.u};
+            if (!pkv::wd_next_unit(p.list, list, at, z)) break;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    if (tid < 2) cut_nu[tid] = join_n[tid] = 0;
-    __syncthreads();
-
-    // ---- join the pieces of each unit cut between this CTA's warps. A unit's
-    // pieces here: one that starts it (slot 1 of some warp, or slot 0 of warp 0
-    // when it began in an earlier CTA), then slot 0 of the warps after. A warp
-    // takes one head of one unit, a lane 4 (D 64: 2) elements.
-    constexpr int E = D / 32;
-    {
-        static_assert(kWarps == 16 && kHeads <= kWarps, "a lane for each possible start");
-        const bool starts = lane <= kWarps && piece[lane ? lane - 1 : 0][lane ? 1 : 0].nu != 0;
-        unsigned todo = __ballot_sync(~0u, starts);
-        for (int k = 0; todo; ++k, todo &= todo - 1) {
-            const int i = __ffs(todo) - 1, w = i ? i - 1 : 0, sl = i ? 1 : 0;
-            const int h = (warp - k * p.GC) & (kWarps - 1);
-            if (h >= p.GC) continue;
-            const Piece pc = piece[w][sl];
-            const int chunk = pc.u % p.NC;
-            if (h >= min(p.GC, p.G - chunk * p.GC)) continue;
-            const int head = pc.u / p.NC * p.G + chunk * p.GC + h;
-            const bool next = lane > w && lane < kWarps && piece[lane & 15][0].nu && piece[lane & 15][0].tu == pc.tu;
-            const int more = __ffs(~(__ballot_sync(~0u, next) >> (w + 1))) - 1;      // pieces after the first
-            float l = -INFINITY;
-            if (lane <= more) l = lane ? piece_lse[w + lane][0][h] : piece_lse[w][sl][h];
-            float mx = l;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-            if (mx == -INFINITY) mx = 0.f;
-            const float f = ex2(l - mx);
-            float sum = f;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            float o[E] = {};
-            for (int q = 0; q <= more; ++q) {
-                const float *src = q == 0 && sl ? reinterpret_cast<const float *>(ring_all + w * C::kRing)
-                                                : heads_o + (size_t)(w + q) * p.GC * D;
-                add_scaled(o, src + h * D + lane * E, __shfl_sync(~0u, f, q));
-            }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= inv;
-            const float lse = mx + log2f(sum);
-            if (pc.tu >= A && pc.tu + pc.nu <= Z) {
-                const size_t at = (size_t)pc.s * p.Hq + head;
-                store_row<E>(p, at * D + lane * E, o);
-                if (p.lse_out && lane == 0) p.lse_out[at] = lse;
-            } else {
-                const int side = pc.tu < A ? 0 : 1;
-                const size_t at = (size_t)(2 * cta + side) * p.GC + h;
-                store_f32(p.ws_o + at * D + lane * E, o);
-                if (lane == 0) {
-                    p.ws_lse[at] = lse;
-                    if (h == 0) {
-                        cut_tu[side] = pc.tu;
-                        cut_nu[side] = pc.nu;
-                        cut_s[side] = pc.s;
-                        cut_u[side] = pc.u;
-                    }
-                }
-            }
-        }
-    }
-    __syncthreads();
-    if (!cut_nu[0] && !cut_nu[1]) return;
-
-    // ---- units cut between CTAs: count this CTA's part in; the last to come joins
-    if (tid < 2 && cut_nu[tid]) {
-        const int nu = cut_nu[tid];
-        const int first = pkv::q4_owner(cut_tu[tid], NV, CT);
-        const int n = pkv::q4_owner(cut_tu[tid] + nu - 1, NV, CT) - first + 1;
-        pkv::fence_acq_rel_gpu();
-        const bool last = atomicAdd(p.cnt + first, 1u) == (unsigned)n - 1;
-        if (last) p.cnt[first] = 0;
-        join_n[tid] = last ? n : 0;
-        join_first[tid] = first;
-        pkv::fence_acq_rel_gpu();
-    }
-    __syncthreads();
-    for (int side = 0; side < 2; ++side) {
-        const int n = join_n[side], first = join_first[side];
-        if (n == 0) continue;
-        const int u = cut_u[side], chunk = u % p.NC;
-        const int gca = min(p.GC, p.G - chunk * p.GC);
-        // the warps of a head take every ways-th part; they meet in shared memory
-        const int ways = kWarps / gca, h = warp % gca, sub = warp / gca;
-        float o[E] = {}, m = -3e38f, sum = 0.f;
-        if (sub < ways) {
-#pragma unroll 4
-            for (int k = sub; k < n; k += ways) {
-                // the first CTA's part is its side 1, the others' their side 0
-                const size_t at = (size_t)(2 * (first + k) + (k == 0)) * p.GC + h;
-                const float l = __ldcg(p.ws_lse + at);
-                float x[E];
-                load_cg(x, p.ws_o + at * D + lane * E);
-                const float nm = fmaxf(m, l), f = ex2(m - nm), fx = ex2(l - nm);
-                m = nm;
-                sum = fmaf(sum, f, fx);
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f, x[e] * fx);
-            }
-            store_f32(heads_o + (size_t)warp * D + lane * E, o);
-            if (lane == 0) {
-                piece_lse[warp][0][0] = m;
-                piece_lse[warp][0][1] = sum;
-            }
-        }
-        __syncthreads();
-        if (sub == 0) {
-            float mx = -3e38f, total = 0.f;
-            for (int q = 0; q < ways; ++q) mx = fmaxf(mx, piece_lse[h + q * gca][0][0]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = 0.f;
-            for (int q = 0; q < ways; ++q) {
-                const int w = h + q * gca;
-                const float f = ex2(piece_lse[w][0][0] - mx);
-                total = fmaf(piece_lse[w][0][1], f, total);
-                add_scaled(o, heads_o + (size_t)w * D + lane * E, f);
-            }
-            const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= inv;
-            const size_t at = (size_t)cut_s[side] * p.Hq + u / p.NC * p.G + chunk * p.GC + h;
-            store_row<E>(p, at * D + lane * E, o);
-            if (p.lse_out && lane == 0) p.lse_out[at] = mx + log2f(total);
-        }
-        __syncthreads();
-    }
+    pkv::wd_join<kWarps, D>(p.o, share, join, heads_o, reinterpret_cast<const float *>(ring_all), C::kRing / 4);
 }
 
 // Whether the warps' pieces fit behind the rings (they do but for more than 4
@@ -1062,7 +748,7 @@ cudaError_t launch(const Q4Params &p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_chained(decode_q4_kernel<D, LB>, dim3((unsigned)p.C), kThreads, smem_bytes<D>(p.GC), stream, p);
+    return launch_chained(decode_q4_kernel<D, LB>, dim3((unsigned)p.C), kThreads, smem_bytes<D>(p.o.GC), stream, p);
 }
 
 bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -1139,7 +825,7 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
     const int64_t tokens = (int64_t)M * cache->block_size;
     const int64_t seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
     if (tokens > INT32_MAX / 2 ||
-        seqs * Hk * NC * ((tokens + kSub - 1) / kSub + pkv::kQ4UnitCost) >= (int64_t)INT32_MAX)
+        seqs * Hk * NC * ((tokens + kSub - 1) / kSub + kUnitCost) >= (int64_t)INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
     if ((int64_t)cache->num_blocks * Hk > INT32_MAX)     // 2^31 chunks are over 500 GB
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");
@@ -1151,18 +837,27 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
     if (misaligned(workspace, 16))
         return pkv::set_last_error(PKV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
     Q4Params p = {};
-    if ((st = pkv::device_error_word(&p.err)) != PKV_OK) return st;
-    p.out_dtype = out_dtype;
+    if ((st = pkv::device_error_word(&p.list.err)) != PKV_OK) return st;
+    p.list.M = M;
+    p.list.lb = cache->block_size == 8 ? 3 : cache->block_size == 16 ? 4 : 5;
+    p.list.U = Hk * NC;
+    p.list.tables_ready = o && o->tables_ready;
+    p.o.out_dtype = out_dtype;
+    p.o.Hq = num_q_heads;
+    p.o.G = G;
+    p.o.NC = NC;
+    p.o.GC = GC;
+    p.o.cnt = static_cast<unsigned *>(workspace);
+    p.o.ws_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
+    float *after = p.o.ws_o + (size_t)C * 2 * GC * D;
+    if (!pieces_on_chip(GC, D)) {
+        p.ws_pieces = after;
+        after += (size_t)C * kWarps * GC * D;
+    }
+    p.o.ws_lse = after;
     p.act_f16 = cache->act_dtype == PKV_F16;
-    p.Hq = num_q_heads;
     p.Hk = Hk;
-    p.G = G;
-    p.NC = NC;
-    p.GC = GC;
-    p.U = Hk * NC;
-    p.M = M;
     p.NB = cache->num_blocks;
-    p.lb = cache->block_size == 8 ? 3 : cache->block_size == 16 ? 4 : 5;
     p.code_bytes = (uint32_t)(cache->block_size * D / 2);
     p.par_bytes = (uint32_t)(cache->block_size * D / 32 * 4);
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -1170,30 +865,21 @@ pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q,
     p.vc = static_cast<const uint8_t *>(pools->v_codes);
     p.kp = static_cast<const __half *>(pools->k_params);
     p.vp = static_cast<const __half *>(pools->v_params);
-    p.cnt = static_cast<unsigned *>(workspace);
-    p.ws_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
-    float *after = p.ws_o + (size_t)C * 2 * GC * D;
-    if (!pieces_on_chip(GC, D)) {
-        p.ws_pieces = after;
-        after += (size_t)C * kWarps * GC * D;
-    }
-    p.ws_lse = after;
     p.C = C;
-    p.tables_ready = o && o->tables_ready;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     for (int s0 = 0; s0 < num_seqs; s0 += kMaxSeqs) {
-        p.S = num_seqs - s0 < kMaxSeqs ? num_seqs - s0 : kMaxSeqs;
+        p.list.S = num_seqs - s0 < kMaxSeqs ? num_seqs - s0 : kMaxSeqs;
+        p.list.tables = block_tables + (size_t)s0 * M;
+        p.list.lens = context_lens + s0;
         p.q = static_cast<const uint16_t *>(q) + (size_t)s0 * num_q_heads * D;
-        p.out = static_cast<uint8_t *>(out) + (size_t)s0 * num_q_heads * D * oes;
-        p.tables = block_tables + (size_t)s0 * M;
-        p.lens = context_lens + s0;
-        p.lse_out = o && o->lse_out ? static_cast<float *>(o->lse_out) + (size_t)s0 * num_q_heads : nullptr;
+        p.o.out = static_cast<uint8_t *>(out) + (size_t)s0 * num_q_heads * D * oes;
+        p.o.lse_out = o && o->lse_out ? static_cast<float *>(o->lse_out) + (size_t)s0 * num_q_heads : nullptr;
         cudaError_t e;
         if (s0 == 0 && o && o->timing_events[0] &&
             (e = pkv::record_event(static_cast<cudaEvent_t>(o->timing_events[0]), s)) != cudaSuccess)
             return pkv::set_last_error(PKV_ERR_CUDA, "cudaEventRecord: %s", cudaGetErrorString(e));
-        auto *go = D == 128 ? (p.lb == 3 ? &launch<128, 3> : p.lb == 4 ? &launch<128, 4> : &launch<128, 5>)
-                            : (p.lb == 3 ? &launch<64, 3> : p.lb == 4 ? &launch<64, 4> : &launch<64, 5>);
+        auto *go = D == 128 ? (p.list.lb == 3 ? &launch<128, 3> : p.list.lb == 4 ? &launch<128, 4> : &launch<128, 5>)
+                            : (p.list.lb == 3 ? &launch<64, 3> : p.list.lb == 4 ? &launch<64, 4> : &launch<64, 5>);
         e = go(p, s);
         if (e != cudaSuccess)
             return pkv::set_last_error(PKV_ERR_CUDA, "decode_q4 launch: %s", cudaGetErrorString(e));

@@ -39,6 +39,7 @@
 #include "device_utils.cuh"
 #include "launch_utils.h"
 #include "pkv_internal.h"
+#include "rows_internal.h"
 
 namespace {
 
@@ -736,6 +737,14 @@ size_t score_bytes(const pkv_cache_desc *c, int64_t S, int64_t M) {
     return (size_t)S * c->num_kv_heads * key_pitch(M) * 4;
 }
 
+// Workspace of the decode over a selection: 16-bit caches have a kernel for many
+// short contexts, fp32 ones take the split-K decode.
+size_t selection_decode_bytes(const pkv_cache_desc *c, int Hq) {
+    const size_t n = c->dtype == PKV_F32 ? pkv_decode_workspace_bytes_ex(c, Hq, 0)
+                                         : pkv::rows_workspace_bytes(Hq / c->num_kv_heads, c->head_dim);
+    return (n + 15) / 16 * 16;
+}
+
 pkv_status check_select(const pkv_cache_desc *c, int32_t S, int32_t Hq, int32_t M) {
     pkv_status st = pkv::check_cache_desc(c);
     if (st != PKV_OK) return st;
@@ -864,8 +873,8 @@ pkv_status pkv_select_blocks(const pkv_cache_desc *cache, const void *q, int32_t
 size_t pkv_decode_sparse_workspace_bytes(const pkv_cache_desc *cache, int32_t num_seqs,
                                          int32_t num_q_heads, int32_t max_blocks_per_seq) {
     if (check_select(cache, num_seqs, num_q_heads, max_blocks_per_seq) != PKV_OK) return 0;
-    const size_t dec = pkv_decode_workspace_bytes_ex(cache, num_q_heads, 0);
-    return dec ? (dec + 15) / 16 * 16 + score_bytes(cache, num_seqs, max_blocks_per_seq) : 0;
+    const size_t dec = selection_decode_bytes(cache, num_q_heads);
+    return dec ? dec + score_bytes(cache, num_seqs, max_blocks_per_seq) : 0;
 }
 
 pkv_status pkv_decode_attention_sparse(const pkv_cache_desc *cache, const void *q,
@@ -885,8 +894,9 @@ pkv_status pkv_decode_attention_sparse(const pkv_cache_desc *cache, const void *
     if (num_seqs == 0) return PKV_OK;
     if (!k_pool || !v_pool || !out)
         return pkv::set_last_error(PKV_ERR_INVALID_ARG, "a pointer argument is NULL");
-    if (misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(out, out_dtype == PKV_F32 ? 4 : 2))
-        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "the pools must be 16-byte aligned");
+    if (misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(out, out_dtype == PKV_F32 ? 16 : 8))
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG,
+                                   "the pools must be 16-byte aligned, out to four of its elements");
     const size_t need = pkv_decode_sparse_workspace_bytes(cache, num_seqs, num_q_heads, max_blocks_per_seq);
     if (need == 0) return PKV_ERR_CUDA;      // the message is set
     if (!workspace || workspace_bytes < need)
@@ -894,13 +904,13 @@ pkv_status pkv_decode_attention_sparse(const pkv_cache_desc *cache, const void *
                                    workspace ? workspace_bytes : (size_t)0);
     if (misaligned(workspace, 16))
         return pkv::set_last_error(PKV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    // what one launch of the decode holds: 1024 (sequence, kv head) contexts of W blocks
     const int64_t heads = num_q_heads / cache->num_kv_heads;
-    const int64_t tiles = select ? (((int64_t)select->top_blocks + select->first_blocks +
-                                     select->last_blocks) * cache->block_size + 63) / 64 : 0;
-    if (1024 * ((heads + 15) / 16) * tiles >= INT32_MAX)
+    const int64_t blocks = select ? (int64_t)select->top_blocks + select->first_blocks + select->last_blocks : 0;
+    if (1024 * ((heads + 7) / 8) * (blocks * cache->block_size / 16 + 2) >= INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "selection too large for one launch");
     // [decode workspace][scores]: the decode's counters lie first, as it wants them
-    const size_t dec = (pkv_decode_workspace_bytes_ex(cache, num_q_heads, 0) + 15) / 16 * 16;
+    const size_t dec = selection_decode_bytes(cache, num_q_heads);
     if ((st = pkv_select_blocks(cache, q, num_seqs, num_q_heads, k_means, block_tables,
                                 max_blocks_per_seq, context_lens, select, sel_tables, sel_lens,
                                 static_cast<uint8_t *>(workspace) + dec, workspace_bytes - dec,
@@ -910,10 +920,12 @@ pkv_status pkv_decode_attention_sparse(const pkv_cache_desc *cache, const void *
     pkv_cache_desc view = *cache;
     view.num_blocks = cache->num_blocks * cache->num_kv_heads;
     view.num_kv_heads = 1;
-    return pkv_decode_attention(&view, q, num_seqs * cache->num_kv_heads,
-                                num_q_heads / cache->num_kv_heads, k_pool, v_pool, sel_tables,
-                                select->top_blocks + select->first_blocks + select->last_blocks,
-                                sel_lens, scale, out, out_dtype, workspace, dec, stream);
+    const int S = num_seqs * cache->num_kv_heads, Hq = num_q_heads / cache->num_kv_heads;
+    if (cache->dtype != PKV_F32)
+        return pkv::decode_rows(&view, q, S, Hq, k_pool, v_pool, sel_tables, (int)blocks, sel_lens, scale, out,
+                                out_dtype, workspace, static_cast<cudaStream_t>(stream));
+    return pkv_decode_attention(&view, q, S, Hq, k_pool, v_pool, sel_tables, (int)blocks, sel_lens, scale, out,
+                                out_dtype, workspace, dec, stream);
 }
 
 }  // extern "C"

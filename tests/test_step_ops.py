@@ -339,9 +339,9 @@ def test_select_oracle_pins():
     assert O.block_scores(q, m).tolist() == [32.0, 128.0]
 
 
-def test_q4_split_replay(tmp_path):
-    exe = tmp_path / "q4_split_check"
+def test_warp_split_replay(tmp_path):
+    exe = tmp_path / "warp_split_check"
     subprocess.run(["g++", "-O2", "-std=c++17", "-I", os.path.join(ROOT, "paged_kv_cache_47_gb300", "csrc"),
-                    os.path.join(ROOT, "tests", "q4_split_check.cpp"), "-o", str(exe)], check=True)
+                    os.path.join(ROOT, "tests", "warp_split_check.cpp"), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "OK", r.stdout

@@ -1,24 +1,26 @@
-// Host replay of the 4-bit decode's split (q4_split.h): random batches of units
-// are cut over CTAs and warps as the kernel cuts them; every subtile must be
+// Host replay of the split of a decode whose warps run alone (warp_split.h):
+// random batches of units
+// are cut over CTAs and warps as the kernels cut them; every subtile must be
 // used once, every unit written once, and the pieces joined must be exactly
 // the unit's.
+#include <array>
 #include <cstdio>
 #include <map>
 #include <random>
 #include <set>
 #include <vector>
 
-#include "q4_split.h"
+#include "warp_split.h"
 
 using namespace pkv;
 
 struct Piece { int tu = 0, nu = 0, from = 0, to = 0; };
 
-static bool run(const std::vector<int> &units, int C, int cost) {
+static bool run(const std::vector<int> &units, int C, int W, int cost) {
     int NV = 0;
     std::vector<int> start;                        // a unit's first place
     for (int n : units) { start.push_back(NV); NV += n + cost; }
-    const int CT = q4_active_ctas(NV, C, cost);
+    const int CT = split_active_ctas(NV, C, W, cost);
     if (CT > C || (NV > 0) != (CT > 0)) return false;
     std::map<int, int> covered, written;           // first subtile's place -> subtiles, outputs
     std::map<int, std::vector<std::pair<int, int>>> parts;   // -> (cta, side)
@@ -26,13 +28,13 @@ static bool run(const std::vector<int> &units, int C, int cost) {
     for (size_t u = 0; u < units.size(); ++u) length[start[u] + cost] = units[u];
     int expect = 0;
     for (int c = 0; c < CT; ++c) {
-        const int A = q4_cta_cut(c, NV, CT), Z = q4_cta_cut(c + 1, NV, CT);
+        const int A = split_cta_cut(c, NV, CT), Z = split_cta_cut(c + 1, NV, CT);
         if (A != expect || Z <= A) return false;
         expect = Z;
-        Piece piece[kQ4Warps][2];
+        std::vector<std::array<Piece, 2>> piece(W);
         int at = A;
-        for (int w = 0; w < kQ4Warps; ++w) {
-            const int a = q4_warp_cut(w, A, Z, cost), z = q4_warp_cut(w + 1, A, Z, cost);
+        for (int w = 0; w < W; ++w) {
+            const int a = split_warp_cut(w, A, Z, W, cost), z = split_warp_cut(w + 1, A, Z, W, cost);
             if (a != at || z < a) return false;
             if (w == 0 && z == a) return false;     // the first warp has work
             at = z;
@@ -51,7 +53,7 @@ static bool run(const std::vector<int> &units, int C, int cost) {
                     return false;
                 }
                 for (int i = ci; i < to; ++i)
-                    if (q4_owner(tu + i, NV, CT) != c) return false;
+                    if (split_owner(tu + i, NV, CT) != c) return false;
                 covered[tu] += to - ci;
                 used += to - ci;
                 if (ci == 0 && to == n) {
@@ -68,12 +70,12 @@ static bool run(const std::vector<int> &units, int C, int cost) {
         }
         if (at != Z) return false;
         bool open[2] = {false, false};
-        for (int w = 0; w < kQ4Warps; ++w)
+        for (int w = 0; w < W; ++w)
             for (int sl = w == 0 ? 0 : 1; sl < 2; ++sl) {
                 const Piece pc = piece[w][sl];
                 if (!pc.nu) continue;
                 int last = w, sum = pc.to - pc.from;
-                while (last + 1 < kQ4Warps && piece[last + 1][0].nu && piece[last + 1][0].tu == pc.tu) {
+                while (last + 1 < W && piece[last + 1][0].nu && piece[last + 1][0].tu == pc.tu) {
                     ++last;
                     sum += piece[last][0].to - piece[last][0].from;
                 }
@@ -94,7 +96,7 @@ static bool run(const std::vector<int> &units, int C, int cost) {
     std::set<int> counters;
     for (auto &kv : parts) {
         const int tu = kv.first, nu = length[tu];
-        const int first = q4_owner(tu, NV, CT), n = q4_owner(tu + nu - 1, NV, CT) - first + 1;
+        const int first = split_owner(tu, NV, CT), n = split_owner(tu + nu - 1, NV, CT) - first + 1;
         if ((int)kv.second.size() != n || part_subtiles[tu] != nu) return false;
         if (!counters.insert(first).second) return false;        // a counter serves one unit
         for (int k = 0; k < n; ++k)
@@ -114,7 +116,10 @@ int main() {
         const int most = i % 4 == 0 ? 1 : i % 4 == 1 ? 5 : i % 4 == 2 ? 40 : 900;
         for (int &n : units) n = pick(1, most);
         const int C = i % 3 == 0 ? pick(1, 4) : i % 3 == 1 ? 152 : pick(1, 600);
-        if (!run(units, C, 0) || !run(units, C, kQ4UnitCost)) {
+        bool ok = true;
+        for (int W : {8, 12, 16})
+            for (int cost : {0, 1, 2}) ok = ok && run(units, C, W, cost);
+        if (!ok) {
             std::printf("FAIL at %d\n", i);
             return 1;
         }
