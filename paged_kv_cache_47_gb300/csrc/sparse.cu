@@ -210,12 +210,17 @@ __device__ __forceinline__ void score_blocks(const SelectParams &p, int s, int g
     const int64_t pitch = (int64_t)p.Hk * D;
     const uint32_t mine = ring + lane * 16;
     const int stages = (hi - lo + STAGE_ROWS - 1) / STAGE_ROWS;
-    // Slot i of a lane holds head i ^ swap: the sums over lanes below keep the
-    // lower half of the slots and give the upper one at each step, and the
-    // lanes' orders differ so that what one keeps the other gives.
+    // NV sums are carried at a time, of `JOINT` loads and GP heads. Slot v of a
+    // lane holds sum v ^ swap: the sums over lanes below keep the lower half of
+    // the slots and give the upper one at each step, and the lanes' orders
+    // differ so that what one keeps the other gives. In the end a lane has one
+    // sum: the load is told by its low bits, the head by those after them.
+    constexpr int JOINT = LANES / GP < LOADS ? LANES / GP : LOADS;
+    constexpr int NV = JOINT * GP;
     int swap = 0;
 #pragma unroll
-    for (int t = 0; (GP >> (t + 1)) > 0; ++t) swap |= (l >> t & 1) * (GP >> (t + 1));
+    for (int t = 0; (NV >> (t + 1)) > 0; ++t) swap |= (l >> t & 1) * (NV >> (t + 1));
+    const int swap_head = swap % GP, swap_load = swap / GP;
 
     // block ids of 32 rows, and of the 32 after them; -1: none
     auto ids_from = [&](int r) {
@@ -257,7 +262,7 @@ __device__ __forceinline__ void score_blocks(const SelectParams &p, int s, int g
 #pragma unroll
             for (int e = 0; e < 2 && h + e < GP; ++e) {
                 // past the group: its first head again, which changes no maximum
-                const int hh = h0 + ((h + e) ^ swap), head = g * p.G + (hh < p.G ? hh : h0);
+                const int hh = h0 + ((h + e) ^ swap_head), head = g * p.G + (hh < p.G ? hh : h0);
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
                                                                    ((int64_t)s * p.Hq + head) * D + 8 * l);
                 uint4 raw[V];
@@ -272,48 +277,57 @@ __device__ __forceinline__ void score_blocks(const SelectParams &p, int s, int g
             issue(k + kStages - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             const uint32_t from = mine + (k % kStages) * kStageBytes;
-#pragma unroll 2
-            for (int a = 0; a < LOADS; ++a) {
-                uint4 raw[V];
+            float best = 0.f;
+#pragma unroll 1
+            for (int a0 = 0; a0 < LOADS; a0 += JOINT) {
+                float acc[NV + 1];
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    pkv::lds_u32x4(from + (a * V + v) * 512, raw[v].x, raw[v].y, raw[v].z, raw[v].w);
-                float x[8], acc[GP + 1];
-                widen<T>(raw, x);
-                Pair sum[(GP + 1) / 2];
+                for (int a = 0; a < JOINT; ++a) {
+                    uint4 raw[V];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const Pair xx = pair_of(x[i], x[i]);
+                    for (int v = 0; v < V; ++v)
+                        pkv::lds_u32x4(from + (a0 * V + v) * 512 + ((a ^ swap_load) * V * 512), raw[v].x, raw[v].y,
+                                       raw[v].z, raw[v].w);
+                    float x[8];
+                    widen<T>(raw, x);
+                    Pair sum[(GP + 1) / 2];
 #pragma unroll
-                    for (int h = 0; h < (GP + 1) / 2; ++h) {
-                        if (i == 0) sum[h] = mul2(q[h][0], xx);
-                        else if (sizeof(T) == 4) sum[h] = add2(sum[h], mul2(q[h][i], xx));
-                        else sum[h] = fma2(q[h][i], xx, sum[h]);
+                    for (int i = 0; i < 8; ++i) {
+                        const Pair xx = pair_of(x[i], x[i]);
+#pragma unroll
+                        for (int h = 0; h < (GP + 1) / 2; ++h) {
+                            if (i == 0) sum[h] = mul2(q[h][0], xx);
+                            else if (sizeof(T) == 4) sum[h] = add2(sum[h], mul2(q[h][i], xx));
+                            else sum[h] = fma2(q[h][i], xx, sum[h]);
+                        }
                     }
-                }
 #pragma unroll
-                for (int h = 0; h < (GP + 1) / 2; ++h) unpair(sum[h], acc[2 * h], acc[2 * h + 1]);
+                    for (int h = 0; h < GP; h += 2) unpair(sum[h / 2], acc[a * GP + h], acc[a * GP + h + 1]);
+                }
                 // over the lanes of the row, neighbours first
 #pragma unroll
-                for (int o = 1, keep = GP; o < LANES; o <<= 1) {
+                for (int o = 1, keep = NV; o < LANES; o <<= 1) {
                     if (keep > 1) {
                         keep >>= 1;
 #pragma unroll
-                        for (int h = 0; h < keep; ++h)
-                            acc[h] = __fadd_rn(acc[h], __shfl_xor_sync(~0u, acc[h + keep], o));
+                        for (int v = 0; v < keep; ++v)
+                            acc[v] = __fadd_rn(acc[v], __shfl_xor_sync(~0u, acc[v + keep], o));
                     } else {
                         acc[0] = __fadd_rn(acc[0], __shfl_xor_sync(~0u, acc[0], o));
                     }
                 }
-                // the largest over the heads, spread over the low lane bits
-                uint32_t best = key_of(acc[0]);
+                // the largest over the heads
+                float top = acc[0] != acc[0] ? INFINITY : acc[0];
 #pragma unroll
-                for (int o = 1; o < GP; o <<= 1) best = max(best, __shfl_xor_sync(~0u, best, o));
-                const int j = lo + k * STAGE_ROWS + a * ROWS + sub;
-                if (l == 0 && j < hi) {
-                    uint32_t *out = keys + (j - p.first);
-                    *out = h0 ? max(*out, best) : best;
-                }
+                for (int o = JOINT; o < NV; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                if (l / JOINT == a0 / JOINT) best = top;
+            }
+            // lane l has the score of load l / JOINT * JOINT + swap_load, if there is one
+            const int j = lo + k * STAGE_ROWS + (l / JOINT * JOINT + swap_load) * ROWS + sub;
+            if (l < LOADS && j < hi) {
+                uint32_t *out = keys + (j - p.first);
+                const uint32_t key = key_of(best);
+                *out = h0 ? max(*out, key) : key;
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
