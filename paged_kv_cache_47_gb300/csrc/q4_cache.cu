@@ -4,7 +4,13 @@
 // group of 32, so a group's minimum and maximum are two shuffles. The 8 codes
 // of a K row are exactly one of its 32-bit words, those of a V row two of its
 // half-words. Half the lanes of a warp hold K rows and half the V rows of the
-// same (token, kv head), so both go in one pass.
+// same (token, kv head), so both go in one pass. A CTA takes one kv head of a
+// run of tokens, each warp every eighth of them, several at a time when there
+// are many, so that their loads are under way together.
+//
+// A code is the quotient (x - m) / s rounded to the nearest whole number. The
+// product with 1 / s, off by 2^-23 of it, decides all but quotients within
+// 1e-4 of a half (16 times 2^-23 is 2e-6); only those are divided.
 //
 // What bounds it: HBM. A row of 128 elements is 256 bytes read and 80 written.
 #include <cuda_bf16.h>
@@ -26,21 +32,20 @@ constexpr int kThreads = 256;
 constexpr float kMaxHalf = 65504.f;
 
 struct StoreParams {
-    const void *k, *v;           // append: new rows; gather: outputs (non-const)
-    void *k_out, *v_out;
+    const void *k, *v;           // append: new rows
+    void *k_out, *v_out;         // gather: values
     const int64_t *slots;
-    int64_t rows;                // tokens * Hk
-    int Hk, NB, B;
+    int T, Hk, NB, lb;           // tokens, kv heads, blocks, block size 1 << lb
     pkv_q4cache_pools pools;
     unsigned *err;
 };
 
-// Lane's place: which of K and V, which row of the warp's, which 8 elements.
-// A warp holds 512 / (2 D) rows (2 at D 64, 1 at D 128) of K and of V.
+// Lane's place: K or V, which row of the warp's, which 8 elements. A warp holds
+// 128 / D rows of K and of V at a time, of as many tokens.
 template <int D>
 struct Place {
     static constexpr int kLanes = D / 8;              // lanes a row
-    static constexpr int kRows = 16 / kLanes;         // (token, kv head) rows a warp
+    static constexpr int kRows = 16 / kLanes;
     __device__ Place() {
         const int lane = threadIdx.x & 31;
         is_v = lane >= 16;
@@ -53,50 +58,65 @@ struct Place {
     int row, l, group, t;
 };
 
-// Slot of a row, as chunk (block * Hk + head) and offset; chunk -1: none.
-__device__ __forceinline__ void locate(const StoreParams &p, int64_t r, int64_t &chunk, int &off,
-                                       bool report) {
-    const int64_t tok = r / p.Hk;
-    const int g = (int)(r - tok * p.Hk);
-    const int64_t slot = p.slots[tok];
-    chunk = -1;
-    off = 0;
-    if (slot < 0) return;
-    const int64_t blk = slot / p.B;
-    if (blk >= p.NB) {
-        if (report && g == 0) atomicOr(p.err, PKV_DEVERR_SLOT);
-        return;
+// The run of tokens and the kv head of a CTA: kv heads first, so that the rows
+// of a token, which lie side by side, are read together.
+template <int D, int ITER>
+struct Run {
+    static constexpr int kTokens = kThreads / 32 * Place<D>::kRows * ITER;
+    __device__ __forceinline__ Run(const StoreParams &p) {
+        const int tile = blockIdx.x / p.Hk;
+        g = blockIdx.x - tile * p.Hk;
+        first = tile * kTokens;
     }
-    chunk = blk * p.Hk + g;
-    off = (int)(slot - blk * p.B);
+    int g, first;
+    // token of this lane's row in iteration i
+    __device__ __forceinline__ int token(const Place<D> &at, int i) const {
+        return first + (i * (kThreads / 32) + (threadIdx.x >> 5)) * at.kRows + at.row;
+    }
+};
+
+// A slot as row of the pools ((block * Hk + head) * B + offset); -1: none.
+__device__ __forceinline__ int64_t locate(const StoreParams &p, int64_t slot, int g, bool report) {
+    if (slot < 0) return -1;
+    const int64_t blk = slot >> p.lb;
+    if (blk >= p.NB) {
+        if (report) atomicOr(p.err, PKV_DEVERR_SLOT);
+        return -1;
+    }
+    return ((blk * p.Hk + g) << p.lb) + (slot & ((1 << p.lb) - 1));
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) append_q4_kernel(const StoreParams p) {
+template <int D, typename T, int ITER>
+__global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ StoreParams p) {
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
     const Place<D> at;
+    const Run<D, ITER> run(p);
     constexpr int NG = D / 32;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * at.kRows;
-    int64_t r = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * at.kRows + at.row;
-    const int64_t last = r - at.row;     // uniform over the warp
-    for (int64_t base = last; base < p.rows; base += step, r += step) {
-        int64_t chunk = -1;
-        int off = 0;
-        if (r < p.rows) locate(p, r, chunk, off, at.l == 0 && !at.is_v);
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (chunk >= 0)
-            raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(at.is_v ? p.v : p.k) +
-                                                        r * D) + at.l);
-        const T *e = reinterpret_cast<const T *>(&raw);
+    const T *from = static_cast<const T *>(at.is_v ? p.v : p.k) + 8 * at.l;
+    int64_t row[ITER];
+    uint4 raw[ITER];
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int tok = run.token(at, i);
+        const int64_t slot = tok < p.T ? __ldg(p.slots + tok) : -1;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (slot >= 0) raw[i] = __ldg(reinterpret_cast<const uint4 *>(from + ((int64_t)tok * p.Hk + run.g) * D));
+        row[i] = locate(p, slot, run.g, at.l == 0 && !at.is_v && run.g == 0);
+    }
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         float x[8], lo = INFINITY, hi = -INFINITY;
         bool bad = false;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = pkv::Elem<T>::to_f32(e[i]);
-            lo = fminf(lo, x[i]);
-            hi = fmaxf(hi, x[i]);
-            bad |= !(fabsf(x[i]) <= 3.402823466e38f);
+        for (int e = 0; e < 8; e += 2) {
+            const float2 f = pkv::Elem<T>::unpack2(w[e / 2]);
+            x[e] = f.x;
+            x[e + 1] = f.y;
+            lo = fminf(lo, fminf(f.x, f.y));
+            hi = fmaxf(hi, fmaxf(f.x, f.y));
+            bad |= !(fabsf(f.x) <= 3.402823466e38f) || !(fabsf(f.y) <= 3.402823466e38f);
         }
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
@@ -110,30 +130,48 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const StoreParams p
         const float mf = __half2float(m), sf = __half2float(s);
         uint32_t word = 0;
         if (sf > 0.f) {                   // not 0, not NaN
+            const float inv = __frcp_rn(sf);
+            bool close = false;
+            float c[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float c = rintf(__fdiv_rn(x[i] - mf, sf));
-                word |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * i);
+            for (int e = 0; e < 8; ++e) {
+                const float q = (x[e] - mf) * inv;
+                c[e] = rintf(q);
+                close |= fabsf(q - c[e]) > 0.4999f;
             }
+            if (close) {
+#pragma unroll 1
+                for (int e = 0; e < 8; ++e) {
+                    // (indexed in registers: the loop is rare, its code small)
+                    float v = x[0];
+#pragma unroll
+                    for (int k = 1; k < 8; ++k) v = e == k ? x[k] : v;
+                    const float q = rintf(__fdiv_rn(v - mf, sf));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) c[k] = e == k ? q : c[k];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) word |= (uint32_t)fminf(fmaxf(c[e], 0.f), 15.f) << (4 * e);
         }
-        if (chunk < 0) continue;
-        const int64_t tr = chunk * p.B + off;
+        const int64_t r = row[i];
+        if (r < 0) continue;
         if (!at.is_v) {
-            uint32_t *row = reinterpret_cast<uint32_t *>(p.pools.k_codes) + tr * (D / 8);
-            row[at.t * NG + at.group] = word;
+            static_cast<uint32_t *>(p.pools.k_codes)[r * (D / 8) + at.t * NG + at.group] = word;
             if (at.t == 0) {
-                __half *par = static_cast<__half *>(p.pools.k_params) + tr * 2 * NG;
-                par[at.group] = s;
-                par[NG + at.group] = m;
+                __half *par = static_cast<__half *>(p.pools.k_params) + r * 2 * NG + at.group;
+                par[0] = s;
+                par[NG] = m;
             }
         } else {
-            uint16_t *row = reinterpret_cast<uint16_t *>(p.pools.v_codes) + tr * (D / 4);
-            row[2 * at.t * NG + at.group] = (uint16_t)word;
-            row[(2 * at.t + 1) * NG + at.group] = (uint16_t)(word >> 16);
+            uint16_t *codes = static_cast<uint16_t *>(p.pools.v_codes) + r * (D / 4) + 2 * at.t * NG + at.group;
+            codes[0] = (uint16_t)word;
+            codes[NG] = (uint16_t)(word >> 16);
             if (at.t == 0) {
-                __half *par = static_cast<__half *>(p.pools.v_params) + chunk * 2 * NG * p.B + off;
-                par[at.group * p.B] = s;
-                par[(NG + at.group) * p.B] = m;
+                const int off = (int)r & ((1 << p.lb) - 1);
+                __half *par = static_cast<__half *>(p.pools.v_params) + (r - off) * 2 * NG + off;
+                par[at.group << p.lb] = s;
+                par[(NG + at.group) << p.lb] = m;
             }
         }
     }
@@ -155,51 +193,74 @@ __device__ __forceinline__ void store8(T *dst, const float (&x)[8]) {
     }
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) gather_q4_kernel(const StoreParams p) {
+template <int D, typename T, int ITER>
+__global__ void __launch_bounds__(kThreads) gather_q4_kernel(const __grid_constant__ StoreParams p) {
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
     const Place<D> at;
+    const Run<D, ITER> run(p);
     constexpr int NG = D / 32;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * at.kRows;
-    for (int64_t r = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * at.kRows + at.row;
-         r < p.rows; r += step) {
-        int64_t chunk;
-        int off;
-        locate(p, r, chunk, off, at.l == 0 && !at.is_v);
-        float x[8] = {};
-        if (chunk >= 0) {
-            const int64_t tr = chunk * p.B + off;
-            uint32_t word;
-            __half s, m;
-            if (!at.is_v) {
-                word = (static_cast<const uint32_t *>(p.pools.k_codes) + tr * (D / 8))[at.t * NG + at.group];
-                const __half *par = static_cast<const __half *>(p.pools.k_params) + tr * 2 * NG;
-                s = par[at.group];
-                m = par[NG + at.group];
-            } else {
-                const uint16_t *row = static_cast<const uint16_t *>(p.pools.v_codes) + tr * (D / 4);
-                word = row[2 * at.t * NG + at.group] |
-                       (uint32_t)row[(2 * at.t + 1) * NG + at.group] << 16;
-                const __half *par =
-                    static_cast<const __half *>(p.pools.v_params) + chunk * 2 * NG * p.B + off;
-                s = par[at.group * p.B];
-                m = par[(NG + at.group) * p.B];
-            }
-            const float sf = __half2float(s), mf = __half2float(m);
+    uint32_t word[ITER];
+    __half s[ITER], m[ITER];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = fmaf((float)((word >> (4 * i)) & 15u), sf, mf);
+    for (int i = 0; i < ITER; ++i) {
+        const int tok = run.token(at, i);
+        const int64_t slot = tok < p.T ? __ldg(p.slots + tok) : -1;
+        const int64_t r = locate(p, slot, run.g, at.l == 0 && !at.is_v && run.g == 0);
+        word[i] = 0;
+        s[i] = m[i] = __ushort_as_half(0);
+        if (r < 0) continue;
+        if (!at.is_v) {
+            word[i] = __ldg(static_cast<const uint32_t *>(p.pools.k_codes) + r * (D / 8) + at.t * NG + at.group);
+            const __half *par = static_cast<const __half *>(p.pools.k_params) + r * 2 * NG + at.group;
+            s[i] = __ldg(par);
+            m[i] = __ldg(par + NG);
+        } else {
+            const uint16_t *codes =
+                static_cast<const uint16_t *>(p.pools.v_codes) + r * (D / 4) + 2 * at.t * NG + at.group;
+            word[i] = __ldg(codes) | (uint32_t)__ldg(codes + NG) << 16;
+            const int off = (int)r & ((1 << p.lb) - 1);
+            const __half *par = static_cast<const __half *>(p.pools.v_params) + (r - off) * 2 * NG + off;
+            s[i] = __ldg(par + (at.group << p.lb));
+            m[i] = __ldg(par + ((NG + at.group) << p.lb));
         }
-        store8(static_cast<T *>(at.is_v ? p.v_out : p.k_out) + r * D + at.l * 8, x);
+    }
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int tok = run.token(at, i);
+        if (tok >= p.T) continue;
+        const float sf = __half2float(s[i]), mf = __half2float(m[i]);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((word[i] >> (4 * e)) & 15u), sf, mf);
+        store8(static_cast<T *>(at.is_v ? p.v_out : p.k_out) + ((int64_t)tok * p.Hk + run.g) * D + at.l * 8, x);
     }
 }
 
 bool misaligned(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
-dim3 grid_for(int64_t rows, int D) {
-    const int64_t per_cta = (kThreads / 32) * (D == 64 ? 2 : 1);
-    int64_t g = (rows + per_cta - 1) / per_cta;
-    return dim3((unsigned)(g > 16384 ? 16384 : g));
+// One row of a warp's at a time while that fills the GPU (152 SMs of 64 warps),
+// four from then on.
+constexpr int64_t kManyRows = 4 * 152 * 64;
+
+template <int D, int ITER>
+dim3 grid_for(const StoreParams &p) {
+    constexpr int per_cta = Run<D, ITER>::kTokens;
+    return dim3((unsigned)((int64_t)(p.T + per_cta - 1) / per_cta * p.Hk));
+}
+
+template <int D, typename T>
+cudaError_t launch_append(const StoreParams &p, cudaStream_t stream) {
+    return (int64_t)p.T * p.Hk >= kManyRows
+               ? launch_chained(append_q4_kernel<D, T, 4>, grid_for<D, 4>(p), kThreads, 0, stream, p)
+               : launch_chained(append_q4_kernel<D, T, 1>, grid_for<D, 1>(p), kThreads, 0, stream, p);
+}
+
+template <int D, typename T>
+cudaError_t launch_gather(const StoreParams &p, cudaStream_t stream) {
+    return (int64_t)p.T * p.Hk >= kManyRows
+               ? launch_chained(gather_q4_kernel<D, T, 4>, grid_for<D, 4>(p), kThreads, 0, stream, p)
+               : launch_chained(gather_q4_kernel<D, T, 1>, grid_for<D, 1>(p), kThreads, 0, stream, p);
 }
 
 pkv_status launch_failed(cudaError_t e, const char *what) {
@@ -248,11 +309,13 @@ pkv_status prepare(const pkv_q4cache_desc *cache, const pkv_q4cache_pools *pools
     if (misaligned(k) || misaligned(v) || reinterpret_cast<uintptr_t>(slots) % 8)
         return pkv::set_last_error(PKV_ERR_INVALID_ARG,
                                    "rows must be 16-byte aligned (slot_mapping 8)");
+    if ((int64_t)T * cache->num_kv_heads > INT32_MAX / 2)      // (their rows are over 100 GB)
+        return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_tokens * num_kv_heads too large for one launch");
     p->slots = slots;
-    p->rows = (int64_t)T * cache->num_kv_heads;
+    p->T = T;
     p->Hk = cache->num_kv_heads;
     p->NB = cache->num_blocks;
-    p->B = cache->block_size;
+    p->lb = cache->block_size == 8 ? 3 : cache->block_size == 16 ? 4 : 5;
     p->pools = *pools;
     return pkv::device_error_word(&p->err);
 }
@@ -273,10 +336,9 @@ pkv_status pkv_append_q4(const pkv_q4cache_desc *cache, const void *k_new, const
     p.k = k_new;
     p.v = v_new;
     const bool d64 = cache->head_dim == 64, h = cache->act_dtype == PKV_F16;
-    auto *kernel = d64 ? (h ? &append_q4_kernel<64, __half> : &append_q4_kernel<64, __nv_bfloat16>)
-                       : (h ? &append_q4_kernel<128, __half> : &append_q4_kernel<128, __nv_bfloat16>);
-    return launch_failed(launch_chained(kernel, grid_for(p.rows, cache->head_dim), kThreads, 0,
-                                        static_cast<cudaStream_t>(stream), p), "append_q4");
+    auto *go = d64 ? (h ? &launch_append<64, __half> : &launch_append<64, __nv_bfloat16>)
+                   : (h ? &launch_append<128, __half> : &launch_append<128, __nv_bfloat16>);
+    return launch_failed(go(p, static_cast<cudaStream_t>(stream)), "append_q4");
 }
 
 pkv_status pkv_gather_q4(const pkv_q4cache_desc *cache, const pkv_q4cache_pools *pools,
@@ -293,14 +355,11 @@ pkv_status pkv_gather_q4(const pkv_q4cache_desc *cache, const pkv_q4cache_pools 
     p.k_out = k_out;
     p.v_out = v_out;
     const bool d64 = cache->head_dim == 64;
-    auto *kernel = out_dtype == PKV_F32
-                       ? (d64 ? &gather_q4_kernel<64, float> : &gather_q4_kernel<128, float>)
-                   : out_dtype == PKV_F16
-                       ? (d64 ? &gather_q4_kernel<64, __half> : &gather_q4_kernel<128, __half>)
-                       : (d64 ? &gather_q4_kernel<64, __nv_bfloat16>
-                              : &gather_q4_kernel<128, __nv_bfloat16>);
-    return launch_failed(launch_chained(kernel, grid_for(p.rows, cache->head_dim), kThreads, 0,
-                                        static_cast<cudaStream_t>(stream), p), "gather_q4");
+    auto *go = out_dtype == PKV_F32   ? (d64 ? &launch_gather<64, float> : &launch_gather<128, float>)
+               : out_dtype == PKV_F16 ? (d64 ? &launch_gather<64, __half> : &launch_gather<128, __half>)
+                                      : (d64 ? &launch_gather<64, __nv_bfloat16>
+                                             : &launch_gather<128, __nv_bfloat16>);
+    return launch_failed(go(p, static_cast<cudaStream_t>(stream)), "gather_q4");
 }
 
 pkv_status pkv_block_copy_q4(const pkv_q4cache_desc *cache, const int64_t *src_dst_pairs,
