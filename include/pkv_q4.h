@@ -10,10 +10,11 @@
  * neighbouring elements. A group has a scale s >= 0 and a minimum m, both
  * fp16, and element d of group y = d / 32 has a code c in 0..15:
  *   value = s * c + m
- *   m = fp16(min), s = fp16((max - min) / 15), c = round((x - m) / s)
- * (differences, quotients and the rounding to the nearest code in fp32, ties
- * to even, clamped to 0..15; s = 0 gives code 0). min and (max - min) / 15 are
- * clamped to +-65504 before they are rounded. A group that holds an infinity
+ *   m = fp16(min), s = fp16((max - min) * r), c = round((x - m) / s)
+ * with r the fp32 number nearest 1 / 15 (differences, products, quotients and
+ * the rounding to the nearest code in fp32, ties to even, clamped to 0..15;
+ * s = 0 gives code 0). min and (max - min) * r are clamped to +-65504 before
+ * they are rounded. A group that holds an infinity
  * or a NaN gets s = m = NaN and zero codes, so that it is not hidden.
  *
  *   k_codes   [num_blocks][num_kv_heads][block_size][head_dim / 2] uint8

@@ -99,7 +99,7 @@ def q4_quantize(x):
     with np.errstate(all="ignore"):
         lo, hi = g.min(-1), g.max(-1)
         m = np.clip(lo, F32(-65504), F32(65504)).astype(np.float16)
-        s = np.minimum((hi - lo) / F32(15), F32(65504)).astype(np.float16)
+        s = np.minimum((hi - lo) * F32(1 / 15), F32(65504)).astype(np.float16)
         bad = ~np.isfinite(g).all(-1)
         m[bad] = s[bad] = np.nan
         c = np.clip(np.rint((g - m.astype(F32)[..., None]) / s.astype(F32)[..., None]), 0, 15)

@@ -9,8 +9,10 @@
 // are many, so that their loads are under way together.
 //
 // A code is the quotient (x - m) / s rounded to the nearest whole number. The
-// product with 1 / s, off by 2^-23 of it, decides all but quotients within
-// 1e-4 of a half (16 times 2^-23 is 2e-6); only those are divided.
+// product with 1 / s, off by 2^-22 of it, decides all but quotients within
+// 1e-4 of a half (16 times 2^-22 is 4e-6); only those are divided. Minima and
+// maxima are taken on pairs in the rows' own type, the code out of the low bits
+// of a sum: conversions to integers run at an eighth of the rate.
 //
 // What bounds it: HBM. A row of 128 elements is 256 bytes read and 80 written.
 #include <cuda_bf16.h>
@@ -18,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "device_utils.cuh"
 #include "launch_utils.h"
@@ -86,6 +90,35 @@ __device__ __forceinline__ int64_t locate(const StoreParams &p, int64_t slot, in
     return ((blk * p.Hk + g) << p.lb) + (slot & ((1 << p.lb) - 1));
 }
 
+constexpr uint32_t kSigns = 0x80008000u;
+
+// The larger of each of two pairs of T; a NaN is larger than anything.
+template <typename T>
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 r = __hmax2_nan(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        const __nv_bfloat162 r =
+            __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+}
+
+// Eight codes by division, for the few where the product leaves one open.
+template <typename T>
+__device__ __noinline__ uint32_t exact_word(uint4 raw, float mf, float sf) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float2 f = pkv::Elem<T>::unpack2(w[e / 2]);
+        word |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(f.x - mf, sf)), 0.f), 15.f) << (4 * e);
+        word |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(f.y - mf, sf)), 0.f), 15.f) << (4 * e + 4);
+    }
+    return word;
+}
+
 template <int D, typename T, int ITER>
 __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ StoreParams p) {
     pkv::grid_dependents_launch();
@@ -107,52 +140,47 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        float x[8], lo = INFINITY, hi = -INFINITY;
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const float2 f = pkv::Elem<T>::unpack2(w[e / 2]);
-            x[e] = f.x;
-            x[e + 1] = f.y;
-            lo = fminf(lo, fminf(f.x, f.y));
-            hi = fmaxf(hi, fmaxf(f.x, f.y));
-            bad |= !(fabsf(f.x) <= 3.402823466e38f) || !(fabsf(f.y) <= 3.402823466e38f);
-        }
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
-            bad |= __shfl_xor_sync(~0u, (int)bad, o) != 0;
-        }
+        // largest element and largest negated element of the group, as a pair
+        uint32_t ends = pair_max<T>(pair_max<T>(w[0], w[1]), pair_max<T>(w[2], w[3]));
+        uint32_t down = pair_max<T>(pair_max<T>(w[0] ^ kSigns, w[1] ^ kSigns),
+                                    pair_max<T>(w[2] ^ kSigns, w[3] ^ kSigns));
+        ends = pair_max<T>(__byte_perm(ends, down, 0x5410), __byte_perm(ends, down, 0x7632));
+        ends = pair_max<T>(ends, __shfl_xor_sync(~0u, ends, 1));
+        ends = pair_max<T>(ends, __shfl_xor_sync(~0u, ends, 2));
+        const float2 end = pkv::Elem<T>::unpack2(ends);
+        const float hi = end.x, lo = -end.y;
         __half m = __float2half_rn(fminf(fmaxf(lo, -kMaxHalf), kMaxHalf));
-        __half s = __float2half_rn(fminf(__fdiv_rn(hi - lo, 15.f), kMaxHalf));
-        if (bad) m = s = __ushort_as_half(0x7fff);
+        __half s = __float2half_rn(fminf((hi - lo) * (1.f / 15.f), kMaxHalf));
+        // a NaN is the largest of all; an infinity is one of the ends
+        if (!(fabsf(hi) <= 3.402823466e38f) || !(fabsf(lo) <= 3.402823466e38f)) m = s = __ushort_as_half(0x7fff);
         const float mf = __half2float(m), sf = __half2float(s);
         uint32_t word = 0;
         if (sf > 0.f) {                   // not 0, not NaN
-            const float inv = __frcp_rn(sf);
-            bool close = false;
-            float c[8];
+            float inv;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sf));
+            float q[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float2 f = pkv::Elem<T>::unpack2(w[e / 2]);
+                q[e] = (f.x - mf) * inv;
+                q[e + 1] = (f.y - mf) * inv;
+            }
+            // Quotients lie within 0.3 of [0, 15] and need no clamp where the
+            // minimum's rounding (2^-11 of it) is small beside the scale and
+            // the scale's own is relative (no subnormal, not the largest)
+            bool close = !(fabsf(mf) * 0x1p-9f < sf) || sf < 0x1p-13f || sf >= kMaxHalf;
+            // rounded by adding 1.5 * 2^23, whose low bits are then the code
+            uint32_t code[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float q = (x[e] - mf) * inv;
-                c[e] = rintf(q);
-                close |= fabsf(q - c[e]) > 0.4999f;
-            }
-            if (close) {
-#pragma unroll 1
-                for (int e = 0; e < 8; ++e) {
-                    // (indexed in registers: the loop is rare, its code small)
-                    float v = x[0];
-#pragma unroll
-                    for (int k = 1; k < 8; ++k) v = e == k ? x[k] : v;
-                    const float q = rintf(__fdiv_rn(v - mf, sf));
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) c[k] = e == k ? q : c[k];
-                }
+                const float c = q[e] + 12582912.f;
+                close |= fabsf(q[e] - (c - 12582912.f)) > 0.4999f;
+                code[e] = __float_as_uint(c);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) word |= (uint32_t)fminf(fmaxf(c[e], 0.f), 15.f) << (4 * e);
+            for (int e = 7; e >= 0; --e) word = word * 16 + code[e];
+            word -= 0x4b400000u * 0x11111111u;       // what all the codes' high bits come to
+            if (close) word = exact_word<T>(raw[i], mf, sf);
         }
         const int64_t r = row[i];
         if (r < 0) continue;

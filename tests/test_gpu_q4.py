@@ -40,7 +40,7 @@ def cache_arrays(c):
 # ------------------------------------------------------------------------------ store
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("T,Hk,D,B", [(1, 1, 64, 8), (1, 8, 128, 16), (67, 3, 64, 16), (300, 8, 128, 32),
-                                      (129, 5, 128, 8)])
+                                      (129, 5, 128, 8), (5000, 8, 128, 16), (9001, 5, 64, 32)])
 def test_append_bits_and_gather(T, Hk, D, B, dt):
     rng = np.random.default_rng([T, B])
     k, v = randn((T, Hk, D), dt, 0), randn((T, Hk, D), dt, 1, 3.0)
