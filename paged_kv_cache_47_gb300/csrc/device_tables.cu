@@ -3,9 +3,11 @@
 // One launch per call. Every CTA scans all requests (counts of tokens and
 // blocks, prefix sums over the threads), so each knows the totals, takes the
 // same all-or-nothing decision and can place any token by itself; the CTAs
-// share out the tokens (append) or returned blocks (release). Only the outputs
-// that may alias inputs (lengths, free count) have to wait until every CTA has
-// read them: the last CTA to arrive at a counter writes those. No CTA waits.
+// share out the tokens (append, four a thread in a large step) or returned
+// blocks (release). Lengths and the free count are written by one CTA, at once
+// where they have buffers of their own; where they are updated in place every
+// CTA has to have read them first, and the CTA that arrives last at a counter
+// writes them. No CTA waits.
 //
 // What bounds it: latency. A step of 64 requests is one CTA and a chain of
 // launch, two dependent loads, a scan, a table load and a store. A prompt wave
@@ -41,6 +43,7 @@ struct TablesParams {
     int32_t *positions;
     int max_tokens;
     int32_t *offsets;
+    bool in_place;             // lengths or free count are written over
     unsigned *arrived;         // zero between calls
     unsigned *err;
 };
@@ -85,8 +88,19 @@ __device__ __forceinline__ void warp_scan(long long &a, long long &b, int lane) 
     }
 }
 
+// Lengths and free count after the call.
 template <bool RELEASE>
-__global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) {
+__device__ __forceinline__ void write_state(const TablesParams &p, bool refused, int nf, long long blocks) {
+    for (int s = threadIdx.x; s < p.S; s += kThreads) {
+        const int len = p.lens[s];
+        p.lens_out[s] = refused ? len : RELEASE ? (p.released[s] ? 0 : len) : len + p.add[s];
+    }
+    if (threadIdx.x == 0) *p.num_free_out = refused ? nf : RELEASE ? nf + (int)blocks : nf - (int)blocks;
+}
+
+// PER: items a thread places at a time, neighbours.
+template <bool RELEASE, int PER>
+__global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ TablesParams p) {
     __shared__ long long first_item[kThreads + 1];   // items before thread t's requests
     __shared__ long long first_block[kThreads];
     __shared__ long long warp_items[kWarps], warp_blocks[kWarps];
@@ -139,58 +153,84 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
     first_item[tid] = item0;
     first_block[tid] = block0;
     if (tid == kThreads - 1) first_item[kThreads] = total;
-    if (blockIdx.x == 0 && tid == 0 && bad) atomicOr(p.err, bad);
+    const bool writer = blockIdx.x == gridDim.x - 1;     // the CTA with the fewest items
+    if (writer) {
+        if (tid == 0 && bad) atomicOr(p.err, bad);
+        if (!RELEASE) {
+            long long at = item0;
+            for (int s = s0; s < s1; ++s) {
+                p.offsets[s] = bad ? 0 : (int)at;
+                at += load_req<RELEASE>(p, s).items;
+            }
+            if (tid == 0) p.offsets[p.S] = (int)total;
+        }
+        if (!p.in_place) write_state<RELEASE>(p, bad != 0, nf, total_blocks);
+    }
     __syncthreads();
 
     const long long limit = RELEASE ? total : (long long)p.max_tokens;
-    for (long long i = (long long)blockIdx.x * kThreads + tid; i < limit;
-         i += (long long)gridDim.x * kThreads) {
-        if (i >= total) {            // append: a token buffer's unused end
-            p.slots[i] = -1;
-            p.positions[i] = 0;
-            continue;
-        }
-        // the last thread whose requests begin at or before item i holds it
-        int t = 0;
+    for (long long i0 = ((long long)blockIdx.x * kThreads + tid) * PER; i0 < limit;
+         i0 += (long long)gridDim.x * kThreads * PER) {
+        // the last thread whose requests begin at or before item i0 holds it
+        int t = 0, s = 0;
+        long long at = 0, blk = 0;
+        Req r = {};
+        if (i0 < total) {
 #pragma unroll
-        for (int step = kThreads / 2; step; step >>= 1)
-            if (first_item[t + step] <= i) t += step;
-        long long at = first_item[t], blk = first_block[t];
-        int s = t * K;
-        Req r = load_req<RELEASE>(p, s);
-        while (i >= at + r.items) {
-            at += r.items;
-            blk += r.blocks;
-            r = load_req<RELEASE>(p, ++s);
+            for (int step = kThreads / 2; step; step >>= 1)
+                if (first_item[t + step] <= i0) t += step;
+            at = first_item[t];
+            blk = first_block[t];
+            s = t * K;
+            r = load_req<RELEASE>(p, s);
         }
-        const int k = (int)(i - at);
-        if (RELEASE) {
-            const int id = p.tables[(int64_t)s * p.M + k];
-            if (id < 0 || id >= p.NB) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-            p.free_blocks[nf + i] = id;
+        int64_t slot[PER];
+        int position[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const long long i = i0 + q;
+            slot[q] = -1;                // past the last token: a buffer's unused end
+            position[q] = 0;
+            if (i >= total) continue;
+            while (i >= at + r.items) {
+                at += r.items;
+                blk += r.blocks;
+                r = load_req<RELEASE>(p, ++s);
+            }
+            const int k = (int)(i - at);
+            if (RELEASE) {
+                const int id = p.tables[(int64_t)s * p.M + k];
+                if (id < 0 || id >= p.NB) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+                p.free_blocks[nf + i] = id;
+            } else {
+                const int pos = r.len + k, j = pos >> p.lb, off = pos & (p.B - 1);
+                int32_t *entry = p.tables + (int64_t)s * p.M + j;
+                const int id = j < r.have ? *entry : p.free_blocks[nf - 1 - blk - (j - r.have)];
+                if (j >= r.have && off == 0) *entry = id;
+                const bool ok = id >= 0 && id < p.NB;
+                if (!ok) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+                if (ok) slot[q] = (int64_t)id * p.B + off;
+                position[q] = pos;
+            }
+        }
+        if (RELEASE) continue;
+        if (PER == 4 && i0 + PER <= limit) {     // (the buffers are 16-byte aligned then)
+            longlong2 *dst = reinterpret_cast<longlong2 *>(p.slots + i0);
+            dst[0] = make_longlong2(slot[0], slot[PER > 1]);
+            dst[1] = make_longlong2(slot[PER / 2], slot[PER - 1]);
+            *reinterpret_cast<int4 *>(p.positions + i0) =
+                make_int4(position[0], position[PER > 1], position[PER / 2], position[PER - 1]);
         } else {
-            const int pos = r.len + k, j = pos >> p.lb, off = pos & (p.B - 1);
-            int32_t *entry = p.tables + (int64_t)s * p.M + j;
-            const int id = j < r.have ? *entry : p.free_blocks[nf - 1 - blk - (j - r.have)];
-            if (j >= r.have && off == 0) *entry = id;
-            const bool ok = id >= 0 && id < p.NB;
-            if (!ok) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-            p.slots[i] = ok ? (int64_t)id * p.B + off : -1;
-            p.positions[i] = pos;
+            for (int q = 0; q < PER; ++q)
+                if (i0 + q < limit) {
+                    p.slots[i0 + q] = slot[q];
+                    p.positions[i0 + q] = position[q];
+                }
         }
     }
-    // token_offsets: read by nobody here, so shared out over the CTAs
-    if (!RELEASE && blockIdx.x == 0) {
-        long long at = item0;
-        for (int s = s0; s < s1; ++s) {
-            p.offsets[s] = bad ? 0 : (int)at;
-            at += load_req<RELEASE>(p, s).items;
-        }
-        if (tid == 0) p.offsets[p.S] = (int)total;
-    }
-    // lengths and free count may alias what other CTAs still read
+    if (!p.in_place) return;
+    __syncthreads();                     // this CTA's reads are done
     if (gridDim.x > 1) {
-        __syncthreads();             // this CTA's reads are done
         if (tid == 0) {
             __threadfence();
             is_last = atomicAdd(p.arrived, 1u) == gridDim.x - 1;
@@ -199,17 +239,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
         __syncthreads();
         if (!is_last) return;
         if (tid == 0) *p.arrived = 0;
-    } else {
-        __syncthreads();
     }
-    for (int s = tid; s < p.S; s += kThreads) {
-        const int len = p.lens[s];
-        int out = len;
-        if (!bad) out = RELEASE ? (p.released[s] ? 0 : len) : len + p.add[s];
-        p.lens_out[s] = out;
-    }
-    if (tid == 0)
-        *p.num_free_out = bad ? nf : RELEASE ? nf + (int)total_blocks : nf - (int)total_blocks;
+    write_state<RELEASE>(p, bad != 0, nf, total_blocks);
 }
 
 template <bool RELEASE>
@@ -218,10 +249,16 @@ pkv_status run(TablesParams &p, void *workspace, int64_t items, void *stream) {
     if (st != PKV_OK) return st;
     p.arrived = static_cast<unsigned *>(workspace);
     p.lb = p.B == 8 ? 3 : p.B == 16 ? 4 : 5;
+    p.in_place = p.lens_out == p.lens || p.num_free_out == p.num_free;
     int64_t ctas = (items + kItemsPerCta - 1) / kItemsPerCta;
     ctas = ctas < 1 ? 1 : ctas > kMaxCtas ? kMaxCtas : ctas;
-    const cudaError_t e = launch_chained(tables_kernel<RELEASE>, dim3((unsigned)ctas), kThreads, 0,
-                                         static_cast<cudaStream_t>(stream), p);
+    // four tokens a thread once there are several CTAs
+    const bool four = !RELEASE && ctas > 1 && reinterpret_cast<uintptr_t>(p.slots) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(p.positions) % 16 == 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        four ? launch_chained(tables_kernel<RELEASE, 4>, dim3((unsigned)ctas), kThreads, 0, s, p)
+             : launch_chained(tables_kernel<RELEASE, 1>, dim3((unsigned)ctas), kThreads, 0, s, p);
     if (e != cudaSuccess)
         return pkv::set_last_error(PKV_ERR_CUDA, "tables launch: %s", cudaGetErrorString(e));
     return PKV_OK;

@@ -75,6 +75,31 @@ def test_append_matches_oracle(S, hi, add_hi, B, in_place):
     check_append(st, add, int(add.sum()) + int(rng.integers(0, 70)), in_place)
 
 
+@pytest.mark.parametrize("shift", [0, 1])
+def test_append_many_ctas_and_unaligned_buffers(shift):
+    # token buffers that begin 8 (4) bytes past a 16-byte boundary
+    rng = np.random.default_rng(9)
+    S, B, M = 700, 16, 30
+    lens, add = rng.integers(0, 200, S), rng.integers(0, 60, S)
+    st = State(rng, S, M, B, lens, spare=4000)
+    T = int(add.sum()) + 7
+    tab, ln, free, nf = st.device()
+    slots = torch.full((T + 2,), 99, dtype=torch.int64, device="cuda")
+    pos = torch.full((T + 2,), 99, dtype=torch.int32, device="cuda")
+    offs = torch.empty(S + 1, dtype=torch.int32, device="cuda")
+    v = slice(shift, shift + T)
+    for _ in range(2):                               # twice in place: the second continues from the first
+        b.tables_append(tab, ln, dev(add.astype(np.int32)), free, nf, B, slots[v], pos[v], offs, b.alloc_tables_workspace())
+        assert b.get_error() == 0
+        st.tab, st.lens, st.nf, ws, wp, wo = O.tables_append(st.tab, st.lens, add.astype(np.int32), st.free, st.nf, B, T)
+        np.testing.assert_array_equal(slots[v].cpu().numpy(), ws)
+        np.testing.assert_array_equal(pos[v].cpu().numpy(), wp)
+        np.testing.assert_array_equal(offs.cpu().numpy(), wo)
+        np.testing.assert_array_equal(ln.cpu().numpy(), st.lens)
+        assert int(nf) == st.nf
+        assert (slots[:shift] == 99).all() and (slots[shift + T:] == 99).all() and (pos[shift + T:] == 99).all()
+
+
 def test_append_exact_fits():
     rng = np.random.default_rng(0)
     # every free block, every table entry and every token entry used
@@ -99,18 +124,18 @@ def test_append_refused_changes_nothing(what, bit, many):
     rng = np.random.default_rng(1)
     S = 200
     lens, add = rng.integers(0, 60, S), rng.integers(1, 30, S)
-    st = State(rng, S, 12, 8, lens, spare=2000)
-    T = int(add.sum()) + (9000 if many else 5)       # more tokens than one CTA's share: many CTAs
+    st = State(rng, S, 24, 8, lens, spare=2000)
+    if many:
+        add *= 4                                     # more tokens than one CTA's share: many CTAs
+    T = int(add.sum()) + 5
     if what == "blocks":
         st.nf = 3
     elif what == "tokens":
         T = int(add.sum()) - 1
-        if many:
-            pytest.skip("the buffer is what is too small")
     elif what == "negative":
         add[77] = -1
     elif what == "row":
-        add[77] = 97
+        add[77] = 193
     elif what == "length":
         st.lens[5] = -2
     else:
