@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     }
                     sum[y] += __shfl_xor_sync(~0u, sum[y], 1);
                     sum[y] += __shfl_xor_sync(~0u, sum[y], 2);
-                    sum[y] *= 0x1p-6f;               // at most 2^14
+                    sum[y] *= 0x1p-24f;              // at most 2^-4, in the codes' unit
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         qb[y][k][0] = as_u32(__floats2half2_rn(x[y][2 * k], x[y][4 + 2 * k]));
@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     }
                 }
                 // sums as fp16 pairs: k = 0..NG-1 the high parts, then the low ones
+                // (to 2^-25, 2^-21 of the largest sum a group of such q can have)
                 const bool upper = NG == 4 && (t & 1);
                 const float s0 = upper ? sum[NG - 2] : sum[0], s1 = upper ? sum[NG - 1] : sum[1];
                 __half2 hi = __floats2half2_rn(s0, s1);
@@ -514,8 +515,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 }
                 float x[4];
                 mma8_zero(x, m0, m1, qsum);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] *= 0x1p-18f;
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
                     float d[4];
@@ -640,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     }
                 }
                 {
-                    // minima as rows 0..NG-1, a row of ones as row 8
+                    // minima as rows 0..NG-1 (rows up to 7 repeat them, unused), a
+                    // row of ones as row 8
                     uint32_t m01, m23;
                     lds64(pv + vm_at + half * 32, m01, m23);
-                    if (g >= NG) m01 = m23 = 0;
                     mma16(accx, m01, one, m23, one, p01, p23);
                 }
 #pragma unroll
