@@ -123,10 +123,11 @@ __device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
 
-// cp.async of 16 bytes to dst + OFF.
-template <int OFF>
+// cp.async of 16 bytes from src + FROM to dst + OFF.
+template <int OFF, int FROM = 0>
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0+%2], [%1], 16;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;" ::"r"(dst), "l"(src), "n"(OFF), "n"(FROM)
+                 : "memory");
 }
 
 // The order of the 16-byte pieces of codes in a stage. Each 128-byte line has
@@ -210,8 +211,8 @@ struct Loader {
     int s, u, head, t0, left;
     int32_t window, next_window;     // table entries: lane holds entry `base + lane` of each
     int base;
-    uint32_t dst0, dst1;             // this lane's pieces of the codes in a stage
-    uint32_t dst_k, dst_v;           // and of the parameters
+    uint32_t dst0;                   // this lane's first piece of the codes in a stage
+    uint32_t dst_v;                  // and of the V parameters
     // The warp's place for one unit's q rows [GC][D]. A unit whose turn comes
     // while the last rows there have been taken up gets its own copied with its
     // first subtile; read from memory only when they are wanted, under the
@@ -223,8 +224,6 @@ struct Loader {
         : p(p_), len(len_), lane(lane_), cost(cost_), q_buf(q_buf_), q_unit(-1) {
         const int line = lane >> 3;
         dst0 = line * 128 + (((lane & 7) ^ line_xor<D>(line)) << 4);
-        dst1 = (line + 4) * 128 + (((lane & 7) ^ line_xor<D>(line + 4)) << 4);
-        dst_k = P::dst_k(lane);
         dst_v = P::dst_v(lane);
     }
 
@@ -277,14 +276,15 @@ struct Loader {
         fetch_q();
         return cost;
     }
-    // Piece J of the codes, K and V, from `src` on.
-    template <int J>
+    // Piece J of the codes, K and V, FROM bytes past `src` in their pools.
+    template <int J, int FROM>
     __device__ __forceinline__ void codes(uint32_t stage, uint64_t src) const {
-        // at D 128 a half has eight lines, two pieces' worth; at D 64 four
-        constexpr int OFF = D == 128 ? J / 2 * 1024 : J * 512;
-        const uint32_t dst = stage + (D == 128 && J % 2 ? dst1 : dst0);
-        copy16<OFF>(dst, p.kc + src);
-        copy16<OFF + C::kCodes>(dst, p.vc + src);
+        // at D 128 a half has eight lines, two pieces' worth (of the second one's
+        // lines the number's bit 2 is set); at D 64 four
+        constexpr int OFF = J * 512;
+        const uint32_t dst = stage + (D == 128 && J % 2 ? dst0 ^ 64u : dst0);
+        copy16<OFF, FROM>(dst, p.kc + src);
+        copy16<OFF + C::kCodes, FROM>(dst, p.vc + src);
     }
     __device__ __forceinline__ void issue(uint32_t stage) {
         const int at = (t0 >> LB) - base;
@@ -300,29 +300,30 @@ struct Loader {
             issue_ragged<D, LB>(p, stage, window, at, head, left, lane);
             return;
         }
-        // a chunk's codes lie in a row: lanes take neighbouring pieces
+        // a chunk's codes lie in a row: lanes take neighbouring pieces (chunks are
+        // 256 bytes or a multiple of 512, so lane offsets go into their low bits)
         const uint32_t piece = lane * 16;
         if constexpr (D == 128) {
             constexpr int PER = 1 << (LB - 3);           // 512-byte pieces of a chunk
-            codes<0>(stage, (uint64_t)chunk[0] * p.code_bytes + piece);
-            codes<1>(stage, (uint64_t)chunk[1 / PER] * p.code_bytes + (piece + 1 % PER * 512));
-            codes<2>(stage, (uint64_t)chunk[2 / PER] * p.code_bytes + (piece + 2 % PER * 512));
-            codes<3>(stage, (uint64_t)chunk[3 / PER] * p.code_bytes + (piece + 3 % PER * 512));
+            codes<0, 0>(stage, (uint64_t)chunk[0] * p.code_bytes | piece);
+            codes<1, 1 % PER * 512>(stage, (uint64_t)chunk[1 / PER] * p.code_bytes | piece);
+            codes<2, 2 % PER * 512>(stage, (uint64_t)chunk[2 / PER] * p.code_bytes | piece);
+            codes<3, 3 % PER * 512>(stage, (uint64_t)chunk[3 / PER] * p.code_bytes | piece);
         } else if constexpr (LB == 3) {
             const bool up = lane >= 16;                  // 256-byte chunks: two in a piece
             const uint32_t half = (lane & 15) * 16;
-            codes<0>(stage, (uint64_t)(up ? chunk[1] : chunk[0]) * p.code_bytes + half);
-            codes<1>(stage, (uint64_t)(up ? chunk[3] : chunk[2]) * p.code_bytes + half);
+            codes<0, 0>(stage, (uint64_t)(up ? chunk[1] : chunk[0]) * p.code_bytes | half);
+            codes<1, 0>(stage, (uint64_t)(up ? chunk[3] : chunk[2]) * p.code_bytes | half);
         } else {
             constexpr int PER = 1 << (LB - 4);
-            codes<0>(stage, (uint64_t)chunk[0] * p.code_bytes + piece);
-            codes<1>(stage, (uint64_t)chunk[1 / PER] * p.code_bytes + (piece + 1 % PER * 512));
+            codes<0, 0>(stage, (uint64_t)chunk[0] * p.code_bytes | piece);
+            codes<1, 1 % PER * 512>(stage, (uint64_t)chunk[1 / PER] * p.code_bytes | piece);
         }
         uint32_t c = chunk[0];
 #pragma unroll
         for (int k = 1; k < kBlocks; ++k) c = P::block(lane) == k ? chunk[k] : c;
-        const uint64_t src = (uint64_t)c * p.par_bytes + P::source(lane);
-        if (D == 128 || lane < 16) copy16<0>(stage + dst_k, reinterpret_cast<const uint8_t *>(p.kp) + src);
+        const uint64_t src = (uint64_t)c * p.par_bytes | P::source(lane);
+        if (D == 128 || lane < 16) copy16<2 * C::kCodes>(stage + P::index(lane) * 16, reinterpret_cast<const uint8_t *>(p.kp) + src);
         if (D == 128 || lane >= 16) copy16<0>(stage + dst_v, reinterpret_cast<const uint8_t *>(p.vp) + src);
     }
 };
