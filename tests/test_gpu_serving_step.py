@@ -2,6 +2,9 @@
 decode over the 16-bit cache, over the selected blocks of it, and over a 4-bit cache; captured into
 one CUDA graph and replayed step after step with no host decision in between."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -118,3 +121,45 @@ def test_graph_of_a_whole_serving_step():
             step_k = (kk.max(-1) - kk.min(-1)).max() / 15
             assert got.max() <= 0.5 * step_k + 2.0 ** -8 * np.abs(kk).max() + 16 * 2.0 ** -11 * np.abs(kk).max()
     assert max(len(h[0]) for h in hist) > 6 * B      # selections left blocks out
+
+
+FIRST_CALL = """
+import torch
+from paged_kv_cache_47_gb300 import binding as b
+i32 = dict(dtype=torch.int32, device="cuda")
+q, k = torch.randn(4, 8, 64, device="cuda").half(), torch.randn(4, 2, 64, device="cuda").half()
+pos, slots = torch.arange(4, **i32), torch.arange(4, device="cuda")
+kp, vp = (torch.zeros(8, 2, 16, 64, device="cuda").half() for _ in range(2))
+km = torch.zeros(8, 2, 64, device="cuda").half()
+tab, lens = torch.arange(4, **i32).view(4, 1), torch.full((4,), 1, **i32)
+free, nf, one = torch.arange(8, **i32), torch.tensor([4], **i32), torch.ones(4, **i32)
+sl, ps, of = torch.zeros(8, dtype=torch.int64, device="cuda"), torch.zeros(8, **i32), torch.zeros(5, **i32)
+c = b.Q4Cache.empty(8, 2, 16, 64, torch.float16)
+calls = [b.prepared_tables_release(tab, lens, torch.zeros(4, dtype=torch.bool, device="cuda"), free, nf, 16,
+                                   b.alloc_tables_workspace(), context_lens_out=one.clone(), num_free_out=nf.clone()),
+         b.prepared_tables_append(tab, lens, one, free, nf, 16, sl, ps, of, b.alloc_tables_workspace(),
+                                  context_lens_out=one.clone(), num_free_out=nf.clone()),
+         b.prepared_rope_append(q, k, k, pos, slots, b.RopePlan(64), kp, vp),
+         b.prepared_append_q4(k, k, slots, c), b.prepared_gather_q4(slots, c), b.prepared_block_means(slots, kp, km),
+         b.prepared_decode_attention_q4(q, c, tab, lens, 0.1),
+         b.prepared_decode_attention_sparse(q, kp, vp, km, tab, lens, 0.1, 1, 0, 1)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for call in calls:
+        call()
+g.replay()
+torch.cuda.synchronize()
+assert b.get_error() == 0
+a = [x.out.clone() for x in calls[6:]] + list(t.clone() for t in calls[4].out) + [sl.clone()]
+for call in calls:
+    call()
+assert all(torch.equal(x, y) for x, y in zip(a, [x.out for x in calls[6:]] + list(calls[4].out) + [sl]))
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "captured", r.stderr[-2000:]
