@@ -42,7 +42,7 @@ constexpr int kHeads = pkv::kWdHeads;
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSeqs = pkv::kWdMaxSeqs;
-constexpr int kUnitCost = 1;         // what a unit costs a warp besides its subtiles, in subtiles
+constexpr int kUnitCost = 2;         // what a unit costs a warp besides its subtiles, in subtiles
 constexpr float kNone = pkv::kWdNone;
 
 struct RowsParams {

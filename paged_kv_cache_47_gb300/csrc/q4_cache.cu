@@ -1,18 +1,20 @@
 // Storing rows in the 4-bit cache and reading them back (include/pkv_q4.h).
 //
-// One thread holds 8 neighbouring elements (one 16-byte load), four threads a
-// group of 32, so a group's minimum and maximum are two shuffles. The 8 codes
-// of a K row are exactly one of its 32-bit words, those of a V row two of its
-// half-words. Half the lanes of a warp hold K rows and half the V rows of the
-// same (token, kv head), so both go in one pass. A CTA takes one kv head of a
-// run of tokens, each warp every eighth of them, several at a time when there
-// are many, so that their loads are under way together.
+// One lane holds 32 elements of a row: the 16 bytes of codes that lie together,
+// which are 8 neighbouring elements of each group of 32 (D 64: 16 of each), so a
+// row is D / 32 lanes and four 16-byte loads a lane. The lanes of a row find the
+// groups' minima and maxima together, each lane ends up with one group's, makes
+// its scale and minimum and hands them round. The 8 codes of a K row are exactly
+// one of its 32-bit words, those of a V row two of its half-words. A warp takes
+// K or V rows of neighbouring tokens of one kv head.
 //
 // A code is the quotient (x - m) / s rounded to the nearest whole number. The
-// product with 1 / s, off by 2^-22 of it, decides all but quotients within
-// 1e-4 of a half (16 times 2^-22 is 4e-6); only those are divided. Minima and
-// maxima are taken on pairs in the rows' own type, the code out of the low bits
-// of a sum: conversions to integers run at an eighth of the rate.
+// product with 1 / s is taken into a sum whose last 16 bits are the quotient's
+// fraction and whose next 4 are the code: no conversion, and one comparison for
+// two elements tells whether the fraction is too near a half to be sure. The
+// sum is off by at most 0.75 of its last place (0.5 its own rounding, 16 * 2^-23
+// the reciprocal's, 16 * 2^-24 the quotient's by definition); quotients within
+// two places of a half are divided, one in 16000.
 //
 // What bounds it: HBM. A row of 128 elements is 256 bytes read and 80 written.
 #include <cuda_bf16.h>
@@ -44,39 +46,37 @@ struct StoreParams {
     unsigned *err;
 };
 
-// Lane's place: K or V, which row of the warp's, which 8 elements. A warp holds
-// 128 / D rows of K and of V at a time, of as many tokens.
+// Lane's place: which row of the warp's, which 32 elements of it.
 template <int D>
 struct Place {
-    static constexpr int kLanes = D / 8;              // lanes a row
-    static constexpr int kRows = 16 / kLanes;
+    static constexpr int kLanes = D / 32;             // lanes a row, groups a row
+    static constexpr int kRows = 32 / kLanes;         // rows of a warp
     __device__ Place() {
-        const int lane = threadIdx.x & 31;
-        is_v = lane >= 16;
-        row = (lane & 15) / kLanes;
-        l = lane % kLanes;
-        group = l / 4;
-        t = l % 4;
+        row = (threadIdx.x & 31) / kLanes;
+        l = threadIdx.x % kLanes;
     }
-    bool is_v;
-    int row, l, group, t;
+    // group of word j of a lane's four, and the word's first element in the row
+    static __device__ constexpr int group(int j) { return j % kLanes; }
+    __device__ __forceinline__ int element(int j) const {
+        return 32 * group(j) + 8 * (l * (4 / kLanes) + j / kLanes);
+    }
+    int row, l;
 };
 
-// The run of tokens and the kv head of a CTA: kv heads first, so that the rows
-// of a token, which lie side by side, are read together.
-template <int D, int ITER>
+// What a warp takes: K or V rows of a run of tokens, of the CTA's kv head (kv
+// heads first, so that the rows of a token, which lie side by side, are read
+// together).
+template <int D>
 struct Run {
-    static constexpr int kTokens = kThreads / 32 * Place<D>::kRows * ITER;
-    __device__ __forceinline__ Run(const StoreParams &p) {
-        const int tile = blockIdx.x / p.Hk;
+    static constexpr int kTokens = kThreads / 64 * Place<D>::kRows;      // of a CTA
+    __device__ __forceinline__ Run(const StoreParams &p, const Place<D> &at) {
+        const int tile = blockIdx.x / p.Hk, warp = threadIdx.x >> 5;
         g = blockIdx.x - tile * p.Hk;
-        first = tile * kTokens;
+        is_v = warp & 1;
+        tok = tile * kTokens + (warp >> 1) * Place<D>::kRows + at.row;
     }
-    int g, first;
-    // token of this lane's row in iteration i
-    __device__ __forceinline__ int token(const Place<D> &at, int i) const {
-        return first + (i * (kThreads / 32) + (threadIdx.x >> 5)) * at.kRows + at.row;
-    }
+    int g, tok;
+    bool is_v;
 };
 
 // A slot as row of the pools ((block * Hk + head) * B + offset); -1: none.
@@ -90,19 +90,39 @@ __device__ __forceinline__ int64_t locate(const StoreParams &p, int64_t slot, in
     return ((blk * p.Hk + g) << p.lb) + (slot & ((1 << p.lb) - 1));
 }
 
-constexpr uint32_t kSigns = 0x80008000u;
-
-// The larger of each of two pairs of T; a NaN is larger than anything.
+// The larger (smaller) of each of two pairs of T; a NaN wins over anything.
 template <typename T>
 __device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
-    if constexpr (std::is_same<T, __half>::value) {
-        const __half2 r = __hmax2_nan(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    } else {
-        const __nv_bfloat162 r =
-            __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    }
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value) asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A lane's words as a V row has them, by half-words with the groups side by
+// side, and back.
+template <int D>
+__device__ __forceinline__ uint4 v_order(const uint32_t (&w)[4]) {
+    if constexpr (D == 128)
+        return make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410),
+                          __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632));
+    return make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                      __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632));
+}
+template <int D>
+__device__ __forceinline__ uint4 words_of(uint4 v) {
+    if constexpr (D == 128)
+        return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                          __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+    return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                      __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
 }
 
 // Eight codes by division, for the few where the product leaves one open.
@@ -119,89 +139,117 @@ __device__ __noinline__ uint32_t exact_word(uint4 raw, float mf, float sf) {
     return word;
 }
 
-template <int D, typename T, int ITER>
+// 192 and a half, and two last places: a sum with a quotient in [-0.5, 15.5) has
+// the code in its bits 16..19 and the fraction's distance from a half, plus two,
+// below.
+constexpr float kCodeBase = 192.5f + 0x1p-15f;
+
+// The codes of eight elements; `unsure`: all by division.
+template <typename T>
+__device__ __forceinline__ uint32_t code_word(uint4 raw, float mf, float sf, float inv, bool unsure) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    const pkv::Pair minus = pkv::pair_of(-mf, -mf), inv2 = pkv::pair_of(inv, inv);
+    const pkv::Pair base = pkv::pair_of(kCodeBase, kCodeBase);
+    uint32_t c[8], near = ~0u;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float2 f = pkv::Elem<T>::unpack2(w[e / 2]);
+        float x, y;
+        pkv::unpair(pkv::fma2(pkv::add2(pkv::pair_of(f.x, f.y), minus), inv2, base), x, y);
+        c[e] = __float_as_uint(x);
+        c[e + 1] = __float_as_uint(y);
+        const uint32_t fractions = __byte_perm(c[e], c[e + 1], 0x5410);
+        asm("min.u16x2 %0, %0, %1;" : "+r"(near) : "r"(fractions));
+    }
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) word = word * 16 + __byte_perm(c[i], c[i + 4], 0x7632);
+    word -= 0x43404340u * 0x1111u;                   // what the sums' other bits come to
+    if ((near & 0xffffu) < 4 || near < 4u << 16 || unsure) word = exact_word<T>(raw, mf, sf);
+    return word;
+}
+
+template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ StoreParams p) {
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
-    const Place<D> at;
-    const Run<D, ITER> run(p);
     constexpr int NG = D / 32;
-    const T *from = static_cast<const T *>(at.is_v ? p.v : p.k) + 8 * at.l;
-    int64_t row[ITER];
-    uint4 raw[ITER];
+    const Place<D> at;
+    const Run<D> run(p, at);
+    const int64_t slot = run.tok < p.T ? __ldg(p.slots + run.tok) : -1;
+    uint4 raw[4] = {};
+    if (slot >= 0) {
+        const T *from = static_cast<const T *>(run.is_v ? p.v : p.k) + ((int64_t)run.tok * p.Hk + run.g) * D;
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int tok = run.token(at, i);
-        const int64_t slot = tok < p.T ? __ldg(p.slots + tok) : -1;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (slot >= 0) raw[i] = __ldg(reinterpret_cast<const uint4 *>(from + ((int64_t)tok * p.Hk + run.g) * D));
-        row[i] = locate(p, slot, run.g, at.l == 0 && !at.is_v && run.g == 0);
+        for (int j = 0; j < 4; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(from + at.element(j)));
     }
+    const int64_t r = locate(p, slot, run.g, at.l == 0 && !run.is_v && run.g == 0);
+    // of each group, among this lane's elements: (largest, smallest)
+    uint32_t ends[NG];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        // largest element and largest negated element of the group, as a pair
-        uint32_t ends = pair_max<T>(pair_max<T>(w[0], w[1]), pair_max<T>(w[2], w[3]));
-        uint32_t down = pair_max<T>(pair_max<T>(w[0] ^ kSigns, w[1] ^ kSigns),
-                                    pair_max<T>(w[2] ^ kSigns, w[3] ^ kSigns));
-        ends = pair_max<T>(__byte_perm(ends, down, 0x5410), __byte_perm(ends, down, 0x7632));
-        ends = pair_max<T>(ends, __shfl_xor_sync(~0u, ends, 1));
-        ends = pair_max<T>(ends, __shfl_xor_sync(~0u, ends, 2));
-        const float2 end = pkv::Elem<T>::unpack2(ends);
-        const float hi = end.x, lo = -end.y;
-        __half m = __float2half_rn(fminf(fmaxf(lo, -kMaxHalf), kMaxHalf));
-        __half s = __float2half_rn(fminf((hi - lo) * (1.f / 15.f), kMaxHalf));
-        // a NaN is the largest of all; an infinity is one of the ends
-        if (!(fabsf(hi) <= 3.402823466e38f) || !(fabsf(lo) <= 3.402823466e38f)) m = s = __ushort_as_half(0x7fff);
-        const float mf = __half2float(m), sf = __half2float(s);
-        uint32_t word = 0;
-        if (sf > 0.f) {                   // not 0, not NaN
-            float inv;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sf));
-            float q[8];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float2 f = pkv::Elem<T>::unpack2(w[e / 2]);
-                q[e] = (f.x - mf) * inv;
-                q[e + 1] = (f.y - mf) * inv;
-            }
-            // Quotients lie within 0.3 of [0, 15] and need no clamp where the
-            // minimum's rounding (2^-11 of it) is small beside the scale and
-            // the scale's own is relative (no subnormal, not the largest)
-            bool close = !(fabsf(mf) * 0x1p-9f < sf) || sf < 0x1p-13f || sf >= kMaxHalf;
-            // rounded by adding 1.5 * 2^23, whose low bits are then the code
-            uint32_t code[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float c = q[e] + 12582912.f;
-                close |= fabsf(q[e] - (c - 12582912.f)) > 0.4999f;
-                code[e] = __float_as_uint(c);
-            }
-#pragma unroll
-            for (int e = 7; e >= 0; --e) word = word * 16 + code[e];
-            word -= 0x4b400000u * 0x11111111u;       // what all the codes' high bits come to
-            if (close) word = exact_word<T>(raw[i], mf, sf);
+    for (int i = 0; i < NG; ++i) {
+        uint32_t hi = pair_max<T>(pair_max<T>(raw[i].x, raw[i].y), pair_max<T>(raw[i].z, raw[i].w));
+        uint32_t lo = pair_min<T>(pair_min<T>(raw[i].x, raw[i].y), pair_min<T>(raw[i].z, raw[i].w));
+        if constexpr (NG == 2) {
+            const uint4 b = raw[i + 2];
+            hi = pair_max<T>(hi, pair_max<T>(pair_max<T>(b.x, b.y), pair_max<T>(b.z, b.w)));
+            lo = pair_min<T>(lo, pair_min<T>(pair_min<T>(b.x, b.y), pair_min<T>(b.z, b.w)));
         }
-        const int64_t r = row[i];
-        if (r < 0) continue;
-        if (!at.is_v) {
-            static_cast<uint32_t *>(p.pools.k_codes)[r * (D / 8) + at.t * NG + at.group] = word;
-            if (at.t == 0) {
-                __half *par = static_cast<__half *>(p.pools.k_params) + r * 2 * NG + at.group;
-                par[0] = s;
-                par[NG] = m;
-            }
-        } else {
-            uint16_t *codes = static_cast<uint16_t *>(p.pools.v_codes) + r * (D / 4) + 2 * at.t * NG + at.group;
-            codes[0] = (uint16_t)word;
-            codes[NG] = (uint16_t)(word >> 16);
-            if (at.t == 0) {
-                const int off = (int)r & ((1 << p.lb) - 1);
-                __half *par = static_cast<__half *>(p.pools.v_params) + (r - off) * 2 * NG + off;
-                par[at.group << p.lb] = s;
-                par[(NG + at.group) << p.lb] = m;
-            }
+        // (the smallest negated: one maximum for both from here on)
+        lo ^= 0x80008000u;
+        ends[i] = pair_max<T>(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+    }
+    // lane l keeps group l: half the groups are handed on at each step
+#pragma unroll
+    for (int o = NG / 2; o > 0; o >>= 1) {
+        const bool upper = at.l & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const uint32_t give = upper ? ends[i] : ends[i + o];
+            ends[i] = pair_max<T>(upper ? ends[i + o] : ends[i], __shfl_xor_sync(~0u, give, o));
         }
+    }
+    const float2 end = pkv::Elem<T>::unpack2(ends[0]);
+    const float hi = end.x, lo = -end.y;
+    __half m = __float2half_rn(fminf(fmaxf(lo, -kMaxHalf), kMaxHalf));
+    __half s = __float2half_rn(fminf((hi - lo) * (1.f / 15.f), kMaxHalf));
+    // a NaN is the largest of all; an infinity is one of the ends
+    if (!(fabsf(hi) <= 3.402823466e38f) || !(fabsf(lo) <= 3.402823466e38f)) m = s = __ushort_as_half(0x7fff);
+    // Quotients lie within 0.3 of [0, 15] and need no clamp where the minimum's
+    // rounding (2^-11 of it) is small beside the scale and the scale's own is
+    // relative (no subnormal, not the largest)
+    const float own_m = fabsf(__half2float(m)), own_s = __half2float(s);
+    const unsigned unsure = __ballot_sync(~0u, !(own_m * 0x1p-9f < own_s) || own_s < 0x1p-13f || own_s >= kMaxHalf) >>
+                            (threadIdx.x & 31 & ~(NG - 1));
+    const uint32_t own = __half_as_ushort(s) | (uint32_t)__half_as_ushort(m) << 16;
+    uint32_t word[4];
+    float sf[NG], mf[NG], inv[NG];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+        const uint32_t v = __shfl_sync(~0u, own, i, NG);
+        sf[i] = __half2float(__ushort_as_half((unsigned short)v));
+        mf[i] = __half2float(__ushort_as_half((unsigned short)(v >> 16)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[i]) : "f"(sf[i]));
+    }
+    if (r < 0) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = Place<D>::group(j);
+        word[j] = 0;
+        // (a scale of 0 or NaN: codes 0)
+        if (sf[i] > 0.f) word[j] = code_word<T>(raw[j], mf[i], sf[i], inv[i], unsure >> i & 1);
+    }
+    if (!run.is_v) {
+        static_cast<uint4 *>(p.pools.k_codes)[r * (D / 32) + at.l] = make_uint4(word[0], word[1], word[2], word[3]);
+        __half *par = static_cast<__half *>(p.pools.k_params) + r * 2 * NG + at.l;
+        par[0] = s;
+        par[NG] = m;
+    } else {
+        static_cast<uint4 *>(p.pools.v_codes)[r * (D / 32) + at.l] = v_order<D>(word);
+        const int off = (int)r & ((1 << p.lb) - 1);
+        __half *par = static_cast<__half *>(p.pools.v_params) + (r - off) * 2 * NG + off;
+        par[at.l << p.lb] = s;
+        par[(NG + at.l) << p.lb] = m;
     }
 }
 
@@ -221,74 +269,77 @@ __device__ __forceinline__ void store8(T *dst, const float (&x)[8]) {
     }
 }
 
-template <int D, typename T, int ITER>
+// Codes stay where they are in the word: the bits of 2^23 with code e's four
+// bits in place are 2^23 + 16^e c, and the scale of the product has 16^-e.
+template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const __grid_constant__ StoreParams p) {
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
-    const Place<D> at;
-    const Run<D, ITER> run(p);
     constexpr int NG = D / 32;
-    uint32_t word[ITER];
-    __half s[ITER], m[ITER];
+    const Place<D> at;
+    const Run<D> run(p, at);
+    if (run.tok >= p.T) return;
+    const int64_t r = locate(p, __ldg(p.slots + run.tok), run.g, at.l == 0 && !run.is_v && run.g == 0);
+    uint4 codes = make_uint4(0, 0, 0, 0);
+    __half s[NG] = {}, m[NG] = {};
+    if (r >= 0) {
+        if (!run.is_v) {
+            codes = __ldg(static_cast<const uint4 *>(p.pools.k_codes) + r * (D / 32) + at.l);
+            const __half2 *par = reinterpret_cast<const __half2 *>(static_cast<const __half *>(p.pools.k_params) + r * 2 * NG);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int tok = run.token(at, i);
-        const int64_t slot = tok < p.T ? __ldg(p.slots + tok) : -1;
-        const int64_t r = locate(p, slot, run.g, at.l == 0 && !at.is_v && run.g == 0);
-        word[i] = 0;
-        s[i] = m[i] = __ushort_as_half(0);
-        if (r < 0) continue;
-        if (!at.is_v) {
-            word[i] = __ldg(static_cast<const uint32_t *>(p.pools.k_codes) + r * (D / 8) + at.t * NG + at.group);
-            const __half *par = static_cast<const __half *>(p.pools.k_params) + r * 2 * NG + at.group;
-            s[i] = __ldg(par);
-            m[i] = __ldg(par + NG);
+            for (int i = 0; i < NG; i += 2) {
+                const __half2 a = __ldg(par + i / 2), b = __ldg(par + (NG + i) / 2);
+                s[i] = __low2half(a), s[i + 1] = __high2half(a);
+                m[i] = __low2half(b), m[i + 1] = __high2half(b);
+            }
         } else {
-            const uint16_t *codes =
-                static_cast<const uint16_t *>(p.pools.v_codes) + r * (D / 4) + 2 * at.t * NG + at.group;
-            word[i] = __ldg(codes) | (uint32_t)__ldg(codes + NG) << 16;
+            codes = words_of<D>(__ldg(static_cast<const uint4 *>(p.pools.v_codes) + r * (D / 32) + at.l));
             const int off = (int)r & ((1 << p.lb) - 1);
             const __half *par = static_cast<const __half *>(p.pools.v_params) + (r - off) * 2 * NG + off;
-            s[i] = __ldg(par + (at.group << p.lb));
-            m[i] = __ldg(par + ((NG + at.group) << p.lb));
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                s[i] = __ldg(par + (i << p.lb));
+                m[i] = __ldg(par + ((NG + i) << p.lb));
+            }
         }
     }
+    T *to = static_cast<T *>(run.is_v ? p.v_out : p.k_out) + ((int64_t)run.tok * p.Hk + run.g) * D;
+    const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
+    const pkv::Pair back = pkv::pair_of(-8388608.f, -8388608.f);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int tok = run.token(at, i);
-        if (tok >= p.T) continue;
+    for (int j = 0; j < 4; ++j) {
+        const int i = Place<D>::group(j);
         const float sf = __half2float(s[i]), mf = __half2float(m[i]);
+        const pkv::Pair minimum = pkv::pair_of(mf, mf);
+        const pkv::Pair scale[2] = {pkv::pair_of(sf, sf * 0x1p-4f), pkv::pair_of(sf * 0x1p-8f, sf * 0x1p-12f)};
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((word[i] >> (4 * e)) & 15u), sf, mf);
-        store8(static_cast<T *>(at.is_v ? p.v_out : p.k_out) + ((int64_t)tok * p.Hk + run.g) * D + at.l * 8, x);
+        for (int e = 0; e < 8; e += 2) {
+            const uint32_t w = e < 4 ? word[j] : word[j] >> 16;
+            const pkv::Pair c = pkv::pair_of(__uint_as_float((w & (15u << (4 * (e & 3)))) | 0x4b000000u),
+                                             __uint_as_float((w & (15u << (4 * (e & 3) + 4))) | 0x4b000000u));
+            pkv::unpair(pkv::fma2(pkv::add2(c, back), scale[(e & 3) / 2], minimum), x[e], x[e + 1]);
+        }
+        store8(to + at.element(j), x);
     }
 }
 
 bool misaligned(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
-// One row of a warp's at a time while that fills the GPU (152 SMs of 64 warps),
-// four from then on.
-constexpr int64_t kManyRows = 4 * 152 * 64;
-
-template <int D, int ITER>
+template <int D>
 dim3 grid_for(const StoreParams &p) {
-    constexpr int per_cta = Run<D, ITER>::kTokens;
+    constexpr int per_cta = Run<D>::kTokens;
     return dim3((unsigned)((int64_t)(p.T + per_cta - 1) / per_cta * p.Hk));
 }
 
 template <int D, typename T>
 cudaError_t launch_append(const StoreParams &p, cudaStream_t stream) {
-    return (int64_t)p.T * p.Hk >= kManyRows
-               ? launch_chained(append_q4_kernel<D, T, 4>, grid_for<D, 4>(p), kThreads, 0, stream, p)
-               : launch_chained(append_q4_kernel<D, T, 1>, grid_for<D, 1>(p), kThreads, 0, stream, p);
+    return launch_chained(append_q4_kernel<D, T>, grid_for<D>(p), kThreads, 0, stream, p);
 }
 
 template <int D, typename T>
 cudaError_t launch_gather(const StoreParams &p, cudaStream_t stream) {
-    return (int64_t)p.T * p.Hk >= kManyRows
-               ? launch_chained(gather_q4_kernel<D, T, 4>, grid_for<D, 4>(p), kThreads, 0, stream, p)
-               : launch_chained(gather_q4_kernel<D, T, 1>, grid_for<D, 1>(p), kThreads, 0, stream, p);
+    return launch_chained(gather_q4_kernel<D, T>, grid_for<D>(p), kThreads, 0, stream, p);
 }
 
 pkv_status launch_failed(cudaError_t e, const char *what) {

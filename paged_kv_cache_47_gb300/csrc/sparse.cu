@@ -43,7 +43,13 @@
 
 namespace {
 
+using pkv::add2;
+using pkv::fma2;
 using pkv::launch_chained;
+using pkv::mul2;
+using pkv::Pair;
+using pkv::pair_of;
+using pkv::unpair;
 
 constexpr int kRowThreads = 128;     // a CTA that scores and selects one row: four fit on an SM
 constexpr int kScoreThreads = 256;
@@ -138,32 +144,6 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     if (x != x) x = INFINITY;
     const uint32_t b = __float_as_uint(x + 0.f);     // -0 becomes +0
     return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-
-// Two fp32 values in one register pair.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair_of(float lo, float hi) {
-    Pair r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpair(Pair x, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-    Pair r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 
 // The neighbouring 8 elements of a row, as fp32.
