@@ -34,7 +34,7 @@ namespace {
 
 using pkv::launch_chained;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr float kMaxHalf = 65504.f;
 
 struct StoreParams {
