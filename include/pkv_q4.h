@@ -83,8 +83,9 @@ size_t pkv_decode_q4_workspace_bytes(const pkv_q4cache_desc *cache, int32_t num_
 /*
  * pkv_decode_attention_q4 — pkv_decode_attention_ex over a 4-bit cache:
  * out[s][h] = softmax(scale * q K^T) V with K and V the cached values. q:
- * [num_seqs][num_q_heads][head_dim] in act_dtype. Tables, lengths, out, the
- * workspace (zero-filled before first use, left zero) and errors as there. A
+ * [num_seqs][num_q_heads][head_dim] in act_dtype. Tables, lengths, out
+ * (aligned to four of its elements), the workspace (zero-filled before first
+ * use, not shared by calls that may overlap) and errors as there. A
  * row that holds NaN parameters gives NaN where it is attended to; rows past a
  * context's length are not used, whatever they hold. options: num_ctas,
  * tables_ready, lse_out and timing_events apply; pending_tail is accepted and

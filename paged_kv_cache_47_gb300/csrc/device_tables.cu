@@ -10,8 +10,12 @@
 // writes them. No CTA waits.
 //
 // What bounds it: latency. A step of 64 requests is one CTA and a chain of
-// launch, two dependent loads, a scan, a table load and a store. A prompt wave
-// writes 12 bytes a token, which the CTAs stream out in order.
+// launch, two dependent loads, a scan, a table load and a store; append and
+// release together take 7.0 us, the host's time for two calls (10.0 with the
+// lengths always written behind the counter). A prompt wave writes 12 bytes a
+// token, which the CTAs stream out in order: 997 requests, a fifth of them
+// released and replaced by prompts of up to 2000 tokens, 13.6 us for both calls
+// (16.2 at one token a thread).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

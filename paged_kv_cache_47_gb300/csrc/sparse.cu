@@ -1,7 +1,8 @@
 // Block means, scores and selection for sparse decode (include/pkv_sparse.h).
 //
 // block_means: a warp per (token, kv head) whose token filled its block; a
-// lane adds 4 (fp32: 2 x 2) neighbouring elements over the block's rows.
+// lane adds D / 32 neighbouring elements over the block's rows, eight rows'
+// loads at a time. Latency: 2.5 us for a step.
 //
 // Scores. A warp takes one kv head and a run of a sequence's blocks. Lanes hold
 // 8 neighbouring elements of a mean each, so a row is 16 lanes (D 128) and a
@@ -11,8 +12,12 @@
 // fp32 caches use the two steps. The sums over lanes halve the heads a lane
 // carries at each step, which leaves the order of the additions as defined:
 // neighbours first. What is kept of a score is its key: its bits made
-// monotonic, a NaN as +infinity, -0 as +0. Bound by HBM on long contexts (each
-// mean is read once), by the multiply-adds from 8 heads a group on.
+// monotonic, a NaN as +infinity, -0 as +0. Bound by instructions: at 8 heads a
+// group 100 of a warp for each 512 bytes of means (32 of them the paired
+// multiply-adds), 0.5 a cycle with the 16 warps that q's registers leave room
+// for. 94 MB of means (8 contexts of up to 131072 tokens) take 31 us, 3 TB/s;
+// 67 us without pairs and with loads held in registers. Half the heads at a time
+// with 24 warps reads means twice: 45 us.
 //
 // Selection. The candidates taken are those above the top-th largest key and
 // the first of its equals. One warp finds that key bit by bit, counting keys in
@@ -25,8 +30,11 @@
 //
 // Rows (sequence, kv head) enough for every SM: one kernel, a CTA a row, keys
 // in shared memory; up to 256 candidates one warp selects alone, with no
-// barrier. Fewer rows: a first kernel scores even runs of blocks all over the
-// GPU, a second one selects, a CTA a row.
+// barrier: 15 us for 512 rows of 27 to 251 candidates, a chain of latencies
+// (lengths, tables, means, scores, 20 bits, tables again). Fewer rows: a first
+// kernel scores even runs of blocks all over the GPU, a second one selects, a
+// CTA a row: 11 us for 64 rows of up to 8192 candidates (16 bit by bit; CTAs of
+// 1024 threads 17).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

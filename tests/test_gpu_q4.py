@@ -103,6 +103,57 @@ def test_append_extremes(dt):
     assert np.isnan(got[2]).sum() == 6 and b.get_error() == 0
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("low", [0.0, -8.0, 512.0, 1000.0])
+def test_append_halves(dt, low):
+    """Quotients on a half, and one step of the rows' type to either side of it."""
+    t = low + 2.0 * torch.arange(16, dtype=torch.float64)
+    halves = (t[:15] + 1).to(DT[dt])
+    step = torch.tensor([torch.finfo(DT[dt]).eps]).to(torch.float64) * halves.double().abs()
+    rows = []
+    for d in (0, -1, 1, -0.5, 0.5):
+        x = torch.zeros(32, dtype=torch.float64)
+        x[:16], x[16:31], x[31] = t, halves.double() + d * step, low
+        rows.append(x.to(DT[dt]))
+    k = torch.stack(rows * 8)[:, None, :].repeat(1, 3, 4)
+    c = b.Q4Cache.empty(6, 3, 8, 128, DT[dt])
+    slots = np.random.default_rng(0).permutation(48)[: len(k)]
+    want = O.q4_append(k.float().numpy(), -k.float().numpy(), slots, *cache_arrays(c))
+    b.append_q4(k.cuda(), -k.cuda(), dev(slots), c)
+    assert b.get_error() == 0
+    for g, w in zip(cache_arrays(c), want):
+        np.testing.assert_array_equal(g.view(np.uint8), w.view(np.uint8))
+    if low == 0 or dt == "f16":                      # (the type holds every one of these halves)
+        assert (want[2][slots[0] // 8, 0, slots[0] % 8, :4] == 2).all()
+        codes = O.q4_unpack(want[0][slots[0] // 8, 0, slots[0] % 8], True).reshape(4, 32)[0]
+        assert codes[:16].tolist() == list(range(16))
+        assert codes[16:31].tolist() == [2 * ((i + 1) // 2) for i in range(15)]
+
+
+def test_pool_past_32_bits():
+    """Codes and parameters whose byte offsets pass 2^32: both ends of the pool."""
+    Hk, B, D, NB = 8, 32, 128, 270000                # codes 4.4 GB each, element offsets past 2^32
+    assert NB * Hk * B * (D // 2) > 1 << 32
+    c = b.Q4Cache.empty(NB, Hk, B, D, torch.bfloat16)
+    ids = np.array([NB - 1, 0, NB - 2, 1, NB // 2], np.int32)
+    L = 5 * B - 3
+    k, v = randn((L, Hk, D), "bf16", 0), randn((L, Hk, D), "bf16", 1)
+    pos = np.arange(L)
+    slots = ids[pos // B].astype(np.int64) * B + pos % B
+    small = b.Q4Cache.empty(5, Hk, B, D, torch.bfloat16)
+    for cache, at in ((c, slots), (small, pos)):
+        b.append_q4(k.cuda(), v.cuda(), dev(at), cache)
+    q = randn((1, 32, D), "bf16", 2).cuda()
+    lens = dev(np.array([L], np.int32))
+    out = b.decode_attention_q4(q, c, dev(ids[None]), lens, 0.09)
+    assert torch.equal(out, b.decode_attention_q4(q, small, dev(np.arange(5, dtype=np.int32)[None]), lens, 0.09))
+    for x, y in zip(b.gather_q4(dev(slots), c), b.gather_q4(dev(pos), small)):
+        assert torch.equal(x, y)
+    b.block_copy_q4([[NB - 1, 2]], c)
+    ids[0] = 2
+    assert torch.equal(out, b.decode_attention_q4(q, c, dev(ids[None]), lens, 0.09))
+    assert b.get_error() == 0
+
 def test_bad_slots_are_flagged_and_skipped():
     c = b.Q4Cache.empty(2, 2, 8, 64, torch.float16)
     x = randn((3, 2, 64), "f16", 0).cuda()
@@ -368,3 +419,23 @@ def test_decode_over_a_selection_of_one_head_blocks():
             rows = np.concatenate([np.arange(16), np.arange(16) + 16 * (2 + h), np.arange(16) + 80])
             want, _, _ = O.attend(q[s, 2 * h: 2 * h + 2].double().numpy(), k[h: h + 1, rows], v[h: h + 1, rows], 0.1)
             assert np.abs(out[s, 2 * h: 2 * h + 2].numpy() - want).max() <= 2.0 ** -10 * np.abs(v).max()
+
+
+def test_decode_two_streams_at_once():
+    t, u = Batch(23, [4000, 900, 45], 2, 128, 16), Batch(24, [7000, 31], 2, 128, 16)
+    runs = []
+    for x in (t, u):
+        q = randn((len(x.lens), 8, 128), x.dt, 5).cuda()
+        want = b.decode_attention_q4(q, x.cache, dev(x.tab), dev(x.lens), 0.09)
+        outs = [torch.zeros_like(q) for _ in range(20)]
+        ws = b.alloc_q4_workspace(x.cache, 8)        # one for each stream
+        runs.append((torch.cuda.Stream(), want, outs, [b.prepared_decode_attention_q4(
+            q, x.cache, dev(x.tab), dev(x.lens), 0.09, out=o, workspace=ws) for o in outs]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for st, _, _, calls in runs:
+            calls[i](st)
+    torch.cuda.synchronize()
+    for _, want, outs, _ in runs:
+        for o in outs:
+            assert torch.equal(o, want)

@@ -184,3 +184,53 @@ def test_sparse_graph_and_other_stream():
     q.neg_()
     g.replay()
     assert torch.equal(out, b.decode_attention_sparse(q, kp, vp, km, dev(t.tab), dev(t.lens), 0.09, 6, 1, 2))
+
+
+def test_sparse_two_streams_at_once():
+    runs = []
+    for seed, lens, Hk in ((7, [16 * 700, 16 * 250 + 3], 2), (8, list(range(16, 16 * 90, 70)), 8)):
+        t = Batch(seed, lens, Hk, 128, 16, "bf16")
+        q = randn((len(lens), 4 * Hk, 128), "bf16", 0).cuda()
+        pools = (t.k.cuda(), t.v.cuda(), t.means.cuda())
+        args = (q, *pools, dev(t.tab), dev(t.lens), 0.09, 6, 1, 2)
+        want = b.decode_attention_sparse(*args)
+        outs = [torch.zeros_like(q) for _ in range(20)]
+        ws = b.alloc_sparse_workspace(pools[0], len(lens), 4 * Hk, t.tab.shape[1])
+        runs.append((torch.cuda.Stream(), want, outs,
+                     [b.prepared_decode_attention_sparse(*args, out=o, workspace=ws) for o in outs]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for st, _, _, calls in runs:
+            calls[i](st)
+    torch.cuda.synchronize()
+    for _, want, outs, _ in runs:
+        for o in outs:
+            assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("S", [18, 20])
+def test_sparse_pool_past_32_bits(S):
+    """Chunks and means at both ends of a pool of more than 2^32 bytes; 18 sequences of 8 heads are
+    fewer rows than SMs, 20 more: the selection's two forms."""
+    Hk, B, D, NB, n = 8, 32, 128, 70000, 13
+    assert NB * Hk * B * D * 2 > 1 << 32
+    t = Batch(9, [B * n - 5] * S, Hk, D, B, "bf16")
+    args = (1 / math.sqrt(D), 4, 1, 2)
+    q = randn((S, 4 * Hk, D), "bf16", 3).cuda()
+    small = [x.cuda() for x in (t.k, t.v, t.means)]
+    lens = dev(t.lens)
+    want = b.decode_attention_sparse(q, *small, dev(t.tab), lens, *args)
+    place = np.arange(len(t.k)) * 3
+    place = np.where(np.arange(len(t.k)) % 2 == 0, place, NB - 1 - place)
+    at = torch.from_numpy(place).cuda()
+    big = [torch.empty(NB, *x.shape[1:], dtype=x.dtype, device="cuda") for x in small]
+    for x, y in zip(big, small):
+        x[at] = y
+    tab = np.where(t.tab >= 0, place[t.tab], -1).astype(np.int32)
+    assert torch.equal(want, b.decode_attention_sparse(q, *big, dev(tab), lens, *args))
+    # the means of the same blocks, from their slots
+    full = place[t.tab[:, : n - 1].ravel()].astype(np.int64)
+    big[2].zero_()
+    b.block_means(dev(full * B + B - 1), big[0], big[2])
+    assert torch.equal(big[2][torch.from_numpy(full).cuda()], small[2][torch.from_numpy(t.tab[:, : n - 1].ravel().astype(np.int64)).cuda()])
+    assert b.get_error() == 0
