@@ -63,7 +63,7 @@ constexpr int kSub = 32;             // tokens of a subtile: two halves of 16, t
 constexpr int kHeads = pkv::kWdHeads;
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxSeqs = pkv::kWdMaxSeqs;
+constexpr int kMaxSeqs = 1024;       // of one launch
 // What a warp spends on a unit besides its subtiles (q to operands, the piece
 // it leaves), in subtiles: 3.1 us against 2.07 us a subtile on the Llama-shaped
 // batch. Counting units as 2 subtiles evened the warps' ends out (loops of 29.6
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
     using C = Cfg<D>;
     constexpr int NG = C::NG;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ pkv::WdListShared<kWarps> list;
+    __shared__ pkv::WdListShared<kWarps, kMaxSeqs> list;
     __shared__ pkv::WdJoinShared<kWarps> join;
     uint8_t *ring_all = smem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -44,7 +44,9 @@ constexpr int kSub = 16;             // tokens of a subtile
 constexpr int kHeads = pkv::kWdHeads;
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxSeqs = pkv::kWdMaxSeqs;
+// Contexts of one launch. The longer list costs its scan and the L1 that it
+// takes, 0.6 us, and is taken where it saves a second launch.
+constexpr int kFewSeqs = 1024, kMaxSeqs = pkv::kRowsMaxSeqs;
 constexpr int kUnitCost = 2;         // what a unit costs a warp besides its subtiles, in subtiles
 constexpr float kNone = pkv::kWdNone;
 
@@ -176,13 +178,13 @@ struct Loader {
     }
 };
 
-template <typename T, int D, int LB>
+template <typename T, int D, int LB, int N>
 __global__ void __launch_bounds__(kThreads, 1) decode_rows_kernel(const __grid_constant__ RowsParams p) {
     using C = Cfg<D>;
     using E = pkv::Elem<T>;
     using Mma = pkv::MmaOp<T>;
     extern __shared__ __align__(1024) uint8_t rings[];
-    __shared__ pkv::WdListShared<kWarps> list;
+    __shared__ pkv::WdListShared<kWarps, N> list;
     __shared__ pkv::WdJoinShared<kWarps> join;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *heads_o = p.ws_pieces + (size_t)blockIdx.x * kWarps * p.o.GC * D;
@@ -341,8 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_rows_kernel(const __grid_c
     pkv::wd_join<kWarps, D>(p.o, share, join, heads_o, reinterpret_cast<const float *>(rings), C::kRing / 4);
 }
 
-template <typename T, int D, int LB>
-cudaError_t launch(const RowsParams &p, cudaStream_t stream) {
+template <typename T, int D, int LB, int N>
+cudaError_t launch_list(const RowsParams &p, cudaStream_t stream) {
     // the attribute is per device and idempotent; set once for each
     static std::atomic<uint64_t> ready{0};
     constexpr int smem = kWarps * Cfg<D>::kRing;
@@ -351,11 +353,16 @@ cudaError_t launch(const RowsParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(decode_rows_kernel<T, D, LB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(decode_rows_kernel<T, D, LB, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_chained(decode_rows_kernel<T, D, LB>, dim3((unsigned)p.C), kThreads, smem, stream, p);
+    return launch_chained(decode_rows_kernel<T, D, LB, N>, dim3((unsigned)p.C), kThreads, smem, stream, p);
+}
+
+template <typename T, int D, int LB>
+cudaError_t launch(const RowsParams &p, cudaStream_t stream) {
+    return p.list.S <= kFewSeqs ? launch_list<T, D, LB, kFewSeqs>(p, stream) : launch_list<T, D, LB, kMaxSeqs>(p, stream);
 }
 
 template <typename T>

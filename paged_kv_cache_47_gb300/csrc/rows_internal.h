@@ -9,6 +9,8 @@
 
 namespace pkv {
 
+constexpr int kRowsMaxSeqs = 2048;       // contexts of one launch: 256 sequences of 8 kv heads
+
 // Workspace bytes for `heads` q heads a kv head (0: no device).
 size_t rows_workspace_bytes(int heads, int head_dim);
 

@@ -28,13 +28,13 @@
 // neighbouring candidates, so two scans over them give each its place in
 // ascending order.
 //
-// Rows (sequence, kv head) enough for every SM: one kernel, a CTA a row, keys
-// in shared memory; up to 256 candidates one warp selects alone, with no
-// barrier: 15 us for 512 rows of 27 to 251 candidates, a chain of latencies
-// (lengths, tables, means, scores, 20 bits, tables again). Fewer rows: a first
-// kernel scores even runs of blocks all over the GPU, a second one selects, a
-// CTA a row: 11 us for 64 rows of up to 8192 candidates (16 bit by bit; CTAs of
-// 1024 threads 17).
+// Short rows, or enough of them to fill the GPU: one kernel, a CTA for each
+// (sequence, kv head), keys in shared memory; up to 256 candidates one warp
+// selects alone, with no barrier: 12 us for 512 rows of 27 to 251 candidates, a
+// chain of latencies (lengths, tables, means, scores, 20 bits, tables again).
+// Few long rows: a first kernel scores even runs of blocks all over the GPU, a
+// second one selects, a CTA a row: 11 us for 64 rows of up to 8192 candidates
+// (16 bit by bit; CTAs of 1024 threads 17).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,6 +42,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/pkv_sparse.h"
 #include "device_utils.cuh"
@@ -59,7 +60,7 @@ using pkv::Pair;
 using pkv::pair_of;
 using pkv::unpair;
 
-constexpr int kRowThreads = 128;     // a CTA that scores and selects one row: four fit on an SM
+constexpr int kRowMost = 512;        // threads of a CTA that scores and selects one row: 128, 256 or 512
 constexpr int kScoreThreads = 256;
 constexpr int kSelThreads = 512;
 constexpr int kPerThread = 16;       // keys a thread holds
@@ -639,13 +640,14 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectP
 
 // Scores and selects one row.
 template <typename T, int D, int GP>
-__global__ void __launch_bounds__(kRowThreads, 4) block_rows_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kRowMost, 1) block_rows_kernel(const SelectParams p) {
     extern __shared__ __align__(128) uint8_t rings[];       // then the row's keys
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
-    constexpr int kWarps = kRowThreads / 32;
-    uint32_t *row_keys = reinterpret_cast<uint32_t *>(rings + kWarps * kRingBytes);
-    static_assert(sizeof(SelectShared<kRowThreads>) <= kWarps * kRingBytes, "it takes the rings' place");
+    const int warps = blockDim.x / 32;
+    uint32_t *row_keys = reinterpret_cast<uint32_t *>(rings + warps * kRingBytes);
+    static_assert(sizeof(SelectShared<128>) <= 4 * kRingBytes && sizeof(SelectShared<kRowMost>) <= 8 * kRingBytes,
+                  "it takes the rings' place");
     const int s = blockIdx.x / p.Hk, g = blockIdx.x - s * p.Hk, warp = threadIdx.x >> 5;
     const int L = clamp_len(p, s, g == 0 && threadIdx.x == 0);
     const int n = (L + p.B - 1) / p.B, cand = n - p.last - p.first;
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) block_rows_kernel(const Select
         return;
     }
     // even shares, in whole loads
-    const int share = ((cand + kWarps - 1) / kWarps + 3) & ~3;
+    const int share = ((cand + warps - 1) / warps + 3) & ~3;
     const int lo = p.first + min(cand, warp * share), hi = p.first + min(cand, (warp + 1) * share);
     if (lo < hi) score_blocks<T, D, GP>(p, s, g, lo, hi, row_keys, pkv::smem_u32(rings) + warp * kRingBytes);
     __syncthreads();
@@ -667,8 +669,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) block_rows_kernel(const Select
     } else {
         write_rest(p, blockIdx.x, L, n, false, row, g, 0);
         // (the rings are used up: the selection's histogram takes their place)
-        block_select<kRowThreads>(p, row_keys, cand, row, g, out,
-                                  *reinterpret_cast<SelectShared<kRowThreads> *>(rings));
+        auto select = [&](auto threads) {
+            constexpr int T = decltype(threads)::value;
+            block_select<T>(p, row_keys, cand, row, g, out, *reinterpret_cast<SelectShared<T> *>(rings));
+        };
+        if (warps == 4) select(std::integral_constant<int, 128>());
+        else if (warps == 8) select(std::integral_constant<int, 256>());
+        else select(std::integral_constant<int, kRowMost>());
     }
 }
 
@@ -678,7 +685,22 @@ bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 // Keys of a row, padded to whole 16-byte loads.
 int key_pitch(int64_t M) { return (int)((M + 3) / 4 * 4); }
 
-constexpr size_t kRowKeyBytes = 64 << 10;        // keys of a row in shared memory, at most
+constexpr int kRowShort = 1024;                  // table columns up to which a CTA a row is always taken
+constexpr size_t kRowKeyBytes = 64 << 10;        // keys of a row in shared memory, at most (128 threads)
+
+// A CTA for each (sequence, kv head): its threads, or 0 for the two kernels that
+// spread a row over the GPU. One SM against many: 144 rows of 512 to 1024 blocks
+// take 15.5 us by rows and 20.7 spread, 24 rows 13.2 and 13.8, 8 rows 12.4 and
+// 11.1, but 64 rows of 2048 to 4096 blocks 30 and 21; with rows for twice the
+// SMs the spread form's second kernel and keys in memory cost more (800 rows of
+// 512 to 1024: 49 and 62). Threads: an SM holds 512, in up to four CTAs (144 rows
+// of 128 to 256 blocks: 9.9, 8.2 and 6.9 us with 128, 256 and 512; 480 rows:
+// 12.7, 14.8 and 21.4), and short rows do not fill many warps (144 rows of 32
+// to 64: 5.1, 5.4 and 5.5).
+int row_threads(int64_t rows, int M, int pitch, int sms) {
+    if (M > kRowShort && (rows < 2 * sms || (size_t)pitch * 4 > kRowKeyBytes)) return 0;
+    return rows <= sms && M > 128 && M <= kRowShort ? 512 : rows <= 2 * sms && M > 64 && M <= kRowShort ? 256 : 128;
+}
 
 // Shared memory above the default 48 KB: an attribute of each kernel on each
 // device, set once (`ready`: devices done).
@@ -696,13 +718,14 @@ cudaError_t allow_smem(K *kernel, size_t bytes, std::atomic<uint64_t> &ready) {
 
 template <typename T, int D, int GP>
 struct Launch {
-    static cudaError_t rows(const SelectParams &p, cudaStream_t stream) {
+    static cudaError_t rows(const SelectParams &p, int threads, cudaStream_t stream) {
         static std::atomic<uint64_t> ready{0};
-        constexpr size_t ring = (size_t)kRowThreads / 32 * kRingBytes;
-        const cudaError_t e = allow_smem(block_rows_kernel<T, D, GP>, ring + kRowKeyBytes, ready);
+        constexpr size_t most = kRowMost / 32 * (size_t)kRingBytes + kRowShort * 4;
+        static_assert(4 * kRingBytes + kRowKeyBytes <= most, "four warps and the longest row");
+        const cudaError_t e = allow_smem(block_rows_kernel<T, D, GP>, most, ready);
         if (e != cudaSuccess) return e;
-        return launch_chained(block_rows_kernel<T, D, GP>, dim3((unsigned)(p.S * p.Hk)), kRowThreads,
-                              ring + (size_t)p.pitch * 4, stream, p);
+        return launch_chained(block_rows_kernel<T, D, GP>, dim3((unsigned)(p.S * p.Hk)), threads,
+                              threads / 32 * (size_t)kRingBytes + (size_t)p.pitch * 4, stream, p);
     }
     static cudaError_t runs(const SelectParams &p, int sms, cudaStream_t stream) {
         static std::atomic<uint64_t> ready{0};
@@ -716,23 +739,23 @@ struct Launch {
 };
 
 template <typename T, int D, int GP>
-cudaError_t launch_select(const SelectParams &p, bool rows, int sms, cudaStream_t stream) {
-    return rows ? Launch<T, D, GP>::rows(p, stream) : Launch<T, D, GP>::runs(p, sms, stream);
+cudaError_t launch_select(const SelectParams &p, int threads, int sms, cudaStream_t stream) {
+    return threads ? Launch<T, D, GP>::rows(p, threads, stream) : Launch<T, D, GP>::runs(p, sms, stream);
 }
 
 template <typename T, int D>
-cudaError_t launch_select_d(const SelectParams &p, bool rows, int sms, cudaStream_t stream) {
+cudaError_t launch_select_d(const SelectParams &p, int threads, int sms, cudaStream_t stream) {
     // heads at a time: the registers of q are 8 a head
     auto *go = p.G == 1   ? &launch_select<T, D, 1>
                : p.G == 2 ? &launch_select<T, D, 2>
                : p.G <= 4 ? &launch_select<T, D, 4>
                           : &launch_select<T, D, 8>;
-    return go(p, rows, sms, stream);
+    return go(p, threads, sms, stream);
 }
 
 template <typename T>
-cudaError_t launch_select_t(int D, const SelectParams &p, bool rows, int sms, cudaStream_t stream) {
-    return D == 64 ? launch_select_d<T, 64>(p, rows, sms, stream) : launch_select_d<T, 128>(p, rows, sms, stream);
+cudaError_t launch_select_t(int D, const SelectParams &p, int threads, int sms, cudaStream_t stream) {
+    return D == 64 ? launch_select_d<T, 64>(p, threads, sms, stream) : launch_select_d<T, 128>(p, threads, sms, stream);
 }
 
 size_t score_bytes(const pkv_cache_desc *c, int64_t S, int64_t M) {
@@ -861,12 +884,11 @@ pkv_status pkv_select_blocks(const pkv_cache_desc *cache, const void *q, int32_t
     p.sel_lens = sel_lens;
     int sms = 0;
     if ((st = pkv::device_sm_count(&sms)) != PKV_OK) return st;
-    // a CTA a row where the rows fill the GPU
-    const bool rows = (int64_t)num_seqs * p.Hk >= sms && (size_t)p.pitch * 4 <= kRowKeyBytes;
+    const int threads = row_threads((int64_t)num_seqs * p.Hk, max_blocks_per_seq, p.pitch, sms);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = cache->dtype == PKV_F32   ? launch_select_t<float>(cache->head_dim, p, rows, sms, s)
-                          : cache->dtype == PKV_F16 ? launch_select_t<__half>(cache->head_dim, p, rows, sms, s)
-                                                    : launch_select_t<__nv_bfloat16>(cache->head_dim, p, rows, sms, s);
+    const cudaError_t e = cache->dtype == PKV_F32   ? launch_select_t<float>(cache->head_dim, p, threads, sms, s)
+                          : cache->dtype == PKV_F16 ? launch_select_t<__half>(cache->head_dim, p, threads, sms, s)
+                                                    : launch_select_t<__nv_bfloat16>(cache->head_dim, p, threads, sms, s);
     if (e != cudaSuccess)
         return pkv::set_last_error(PKV_ERR_CUDA, "block selection launch: %s", cudaGetErrorString(e));
     return PKV_OK;
@@ -906,10 +928,10 @@ pkv_status pkv_decode_attention_sparse(const pkv_cache_desc *cache, const void *
                                    workspace ? workspace_bytes : (size_t)0);
     if (misaligned(workspace, 16))
         return pkv::set_last_error(PKV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-    // what one launch of the decode holds: 1024 (sequence, kv head) contexts of W blocks
+    // what one launch of the decode holds: so many (sequence, kv head) contexts of W blocks
     const int64_t heads = num_q_heads / cache->num_kv_heads;
     const int64_t blocks = select ? (int64_t)select->top_blocks + select->first_blocks + select->last_blocks : 0;
-    if (1024 * ((heads + 7) / 8) * (blocks * cache->block_size / 16 + 2) >= INT32_MAX)
+    if (pkv::kRowsMaxSeqs * ((heads + 7) / 8) * (blocks * cache->block_size / 16 + 3) >= INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "selection too large for one launch");
     // [decode workspace][scores]: the decode's counters lie first, as it wants them
     const size_t dec = selection_decode_bytes(cache, num_q_heads);

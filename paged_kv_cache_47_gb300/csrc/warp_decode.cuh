@@ -17,7 +17,6 @@
 namespace pkv {
 
 constexpr int kWdHeads = 8;              // q heads of a unit (the n, or half the m, of the mma)
-constexpr int kWdMaxSeqs = 1024;         // sequences of one launch
 constexpr float kWdNone = 2e-38f;        // reference exponent of a head before its first finite
                                          // score: 0 to any score, and no score's own
 
@@ -50,11 +49,11 @@ __device__ __forceinline__ float wd_ex2(float x) {
 }
 
 // ---------------------------------------------------------------- the list
-template <int W>
+template <int W, int N>                  // N: sequences of one launch, at most
 struct WdListShared {
-    int prefix[kWdMaxSeqs + 1];          // places before a sequence, for one unit a sequence
-    int len[kWdMaxSeqs];
-    uint16_t nonempty[kWdMaxSeqs + 2];   // sequences with tokens before a sequence
+    int prefix[N + 1];                   // places before a sequence, for one unit a sequence
+    int len[N];
+    uint16_t nonempty[N + 2];            // sequences with tokens before a sequence
     int scan[3][W];
 };
 
@@ -72,16 +71,16 @@ struct WdPlace {
 // Lengths, their prefixes, zeros for empty contexts, and this warp's share (a
 // CTA without work gets an empty one: CT <= its index). SUB tokens a subtile.
 // All threads of the CTA; waits for the preceding kernel.
-template <int W, int SUB>
+template <int W, int SUB, int N>
 __device__ __forceinline__ WdShare wd_share(const WdList &p, const WdOut &o, int D, int unit_cost,
-                                            WdListShared<W> &sh) {
+                                            WdListShared<W, N> &sh) {
     constexpr int T = 32 * W;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (!p.tables_ready) grid_dependency_wait();
     int longest = 0;
     WdShare r;
     {
-        constexpr int K = (kWdMaxSeqs + T - 1) / T;
+        constexpr int K = (N + T - 1) / T;
         int n[K], sum = 0, some = 0;                 // subtiles; sequences that have any
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -91,7 +90,7 @@ __device__ __forceinline__ WdShare wd_share(const WdList &p, const WdOut &o, int
                 if (blockIdx.x == 0) atomicOr(p.err, PKV_DEVERR_CONTEXT);
                 L = L < 0 ? 0 : p.M << p.lb;
             }
-            if (s < kWdMaxSeqs) sh.len[s] = L;
+            if (s < N) sh.len[s] = L;
             n[k] = (L + SUB - 1) / SUB;
             sum += n[k];
             some += L > 0;
@@ -127,7 +126,7 @@ __device__ __forceinline__ WdShare wd_share(const WdList &p, const WdOut &o, int
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int s = tid * K + k;
-            if (s < kWdMaxSeqs) {
+            if (s < N) {
                 sh.prefix[s] = before + r.cost * before1;
                 sh.nonempty[s] = (uint16_t)before1;
             }
@@ -135,8 +134,8 @@ __device__ __forceinline__ WdShare wd_share(const WdList &p, const WdOut &o, int
             before1 += n[k] > 0;
         }
         if (tid == T - 1) {
-            sh.prefix[kWdMaxSeqs] = before + r.cost * before1;
-            sh.nonempty[kWdMaxSeqs] = (uint16_t)before1;
+            sh.prefix[N] = before + r.cost * before1;
+            sh.nonempty[N] = (uint16_t)before1;
         }
         __syncthreads();
     }
@@ -151,8 +150,8 @@ __device__ __forceinline__ WdShare wd_share(const WdList &p, const WdOut &o, int
                 for (int h = tid; h < o.Hq; h += T) o.lse_out[(size_t)s * o.Hq + h] = -INFINITY;
         }
 
-    const int cta = blockIdx.x, units = sh.nonempty[kWdMaxSeqs] * p.U;
-    r.NV = sh.prefix[kWdMaxSeqs] * p.U;
+    const int cta = blockIdx.x, units = sh.nonempty[N] * p.U;
+    r.NV = sh.prefix[N] * p.U;
     r.A = r.Z = r.a = r.z = 0;
     if (r.cost == 0 && units <= (int)gridDim.x && longest <= split_one_cta(W)) {
         // a unit for each CTA
@@ -180,8 +179,8 @@ __device__ __forceinline__ WdShare wd_share(const WdList &p, const WdOut &o, int
 }
 
 // The first subtile at or after place a.
-template <int W>
-__device__ __forceinline__ WdPlace wd_place(const WdList &p, const WdListShared<W> &sh, int a, int cost) {
+template <int W, int N>
+__device__ __forceinline__ WdPlace wd_place(const WdList &p, const WdListShared<W, N> &sh, int a, int cost) {
     // the last sequence whose units begin at or before it (of equal prefixes,
     // the empty sequences come first)
     int lo = 0, hi = p.S - 1;
@@ -201,8 +200,8 @@ __device__ __forceinline__ WdPlace wd_place(const WdList &p, const WdListShared<
 }
 
 // The next unit, if its first subtile lies before place z.
-template <int W>
-__device__ __forceinline__ bool wd_next_unit(const WdList &p, const WdListShared<W> &sh, WdPlace &w, int z) {
+template <int W, int N>
+__device__ __forceinline__ bool wd_next_unit(const WdList &p, const WdListShared<W, N> &sh, WdPlace &w, int z) {
     w.i = 0;
     w.tu += w.nv;
     if (w.tu >= z) return false;

@@ -138,6 +138,26 @@ def test_long_selections(dt):
     Batch(3, [8 * 20011], 1, 64, 8, dt, ties=True).check(1, 9999, 0, 1, attention=False)
 
 
+@pytest.mark.parametrize("S,Hk,hi", [(1, 2, 60), (19, 8, 60), (3, 2, 300), (38, 8, 300), (1, 1, 1023), (2, 1, 1024),
+                                     (39, 8, 300), (305, 1, 1100), (5, 1, 1100), (160, 1, 1100)])
+def test_selection_forms(S, Hk, hi):
+    """Rows for less and more than one, two and four CTAs an SM, short and long; more than 256
+    candidates and fewer."""
+    rng = np.random.default_rng(S)
+    lens = rng.integers(1, 8 * (hi - 1), S)
+    lens[0] = 8 * (hi - 1)                           # table columns: hi
+    Batch(40, lens, Hk, 64, 8, "bf16").check(2, 30, attention=False)
+    if S == 38:
+        Batch(41, lens, Hk, 64, 8, "bf16", ties=True).check(2, 30, attention=False)
+
+
+@pytest.mark.parametrize("S", [256, 257, 300])
+def test_sparse_many_rows(S):
+    """2048 rows are one launch of the decode, more are several."""
+    lens = np.random.default_rng(0).integers(0, 60, S)
+    Batch(42, lens, 8, 64, 8, "f16").check(3, 2)
+
+
 def test_nan_infinite_and_zero_means():
     t = Batch(4, [16 * 30], 1, 64, 16, "bf16")
     for j, x in ((3, math.nan), (9, math.inf), (10, -math.inf), (20, 0.0), (21, -0.0)):
