@@ -229,6 +229,16 @@ __device__ __forceinline__ void wd_add_scaled(float (&o)[E], const float *src, f
     }
 }
 template <int E>
+__device__ __forceinline__ void wd_load(float (&o)[E], const float *src) {
+    if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
+        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+    } else {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        o[0] = v.x, o[1] = v.y;
+    }
+}
+template <int E>
 __device__ __forceinline__ void wd_load_cg(float (&o)[E], const float *src) {
     if constexpr (E == 4) {
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
@@ -320,9 +330,20 @@ __device__ __forceinline__ void wd_join(const WdOut &p, const WdShare &share, Wd
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
             float o[E] = {};
-            for (int q = 0; q <= more; ++q) {
-                const float *src = q == 0 && sl ? slot1 + w * pitch : slot0 + (size_t)(w + q) * p.GC * D;
-                wd_add_scaled(o, src + h * D + lane * E, __shfl_sync(~0u, f, q));
+            for (int q0 = 0; q0 <= more; q0 += 4) {
+                float x[4][E];                       // four loads under way at once
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int q = min(q0 + i, more);
+                    const float *src = q == 0 && sl ? slot1 + w * pitch : slot0 + (size_t)(w + q) * p.GC * D;
+                    wd_load(x[i], src + h * D + lane * E);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float fq = __shfl_sync(~0u, f, q0 + i);    // (0 past the last)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] = q0 + i <= more ? fmaf(x[i][e], fq, o[e]) : o[e];
+                }
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
