@@ -16,11 +16,14 @@
 // Softmax in base 2 in fp32, with a reference exponent that moves only when a
 // score passes it by more than 8.
 //
-// What bounds it: HBM, 4 D bytes a token. 12 warps keep two subtiles each in
-// flight or in use, 192 KB an SM. 512 contexts of 592 tokens (155 MB) take 38 us
-// and 64 of 4096 with 8 heads each (135 MB) 35; the copies themselves run at
-// near 6 TB/s, but the list, the first table entries and the joins are 10 us of
-// either. A unit counted as two subtiles evens the warps' ends out by 0.6 us.
+// What bounds it: HBM, 4 D bytes a token. 10 warps keep two subtiles each in
+// flight or in use, 160 KB an SM, and the pieces that they leave fit beside the
+// rings: 12 warps whose pieces went through memory took 5 us more, as a join
+// waits for such loads twice. 512 contexts of 592 tokens (155 MB) take 33 us and
+// 64 of 4096 with 8 heads each (135 MB) 31; from the first copy to the last the
+// stream runs at the memory's rate, the list and the first table entries before
+// it (4 us) and the joins after it (5) are what is left. A unit counted as two
+// subtiles evens the warps' ends out by 0.6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,7 +45,7 @@ using pkv::wd_ex2;
 
 constexpr int kSub = 16;             // tokens of a subtile
 constexpr int kHeads = pkv::kWdHeads;
-constexpr int kWarps = 12;
+constexpr int kWarps = 10;
 constexpr int kThreads = 32 * kWarps;
 // Contexts of one launch. The longer list costs its scan and the L1 that it
 // takes, 0.6 us, and is taken where it saves a second launch.
@@ -58,7 +61,6 @@ struct RowsParams {
     int Hk, NB;
     uint32_t chunk_bytes;            // of one (block, kv head) chunk, K or V
     float scale_log2;
-    float *ws_pieces;                // [C][warps][GC][D]: pieces of units that began before a warp's share
     int C;
 };
 
@@ -187,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_rows_kernel(const __grid_c
     __shared__ pkv::WdListShared<kWarps, N> list;
     __shared__ pkv::WdJoinShared<kWarps> join;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *heads_o = p.ws_pieces + (size_t)blockIdx.x * kWarps * p.o.GC * D;
+    // pieces of units that began before a warp's share: [warps][GC][D] behind the rings
+    float *heads_o = reinterpret_cast<float *>(rings + kWarps * Cfg<D>::kRing);
     pkv::grid_dependents_launch();
     pkv::wd_join_init(join);
     const pkv::WdShare share = pkv::wd_share<kWarps, kSub>(p.list, p.o, D, kUnitCost, list);
@@ -347,17 +350,17 @@ template <typename T, int D, int LB, int N>
 cudaError_t launch_list(const RowsParams &p, cudaStream_t stream) {
     // the attribute is per device and idempotent; set once for each
     static std::atomic<uint64_t> ready{0};
-    constexpr int smem = kWarps * Cfg<D>::kRing;
+    constexpr int ring = kWarps * Cfg<D>::kRing, most = ring + kWarps * kHeads * D * 4;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(decode_rows_kernel<T, D, LB, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(decode_rows_kernel<T, D, LB, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_chained(decode_rows_kernel<T, D, LB, N>, dim3((unsigned)p.C), kThreads, smem, stream, p);
+    return launch_chained(decode_rows_kernel<T, D, LB, N>, dim3((unsigned)p.C), kThreads, ring + kWarps * p.o.GC * D * 4, stream, p);
 }
 
 template <typename T, int D, int LB>
@@ -374,8 +377,8 @@ cudaError_t launch_for(int D, const RowsParams &p, cudaStream_t stream) {
 }
 
 // workspace: [PKV_MAX_DECODE_CTAS] arrival counters (a fixed region, whatever
-// the launch), then [C][2][GC][D] outputs, [C][warps][GC][D] pieces, [C][2][GC]
-// log2 denominators
+// the launch), then [C][2][GC][D] outputs and [C][2][GC] log2 denominators of
+// units cut between CTAs
 constexpr size_t kCounterBytes = PKV_MAX_DECODE_CTAS * sizeof(unsigned);
 
 }  // namespace
@@ -386,7 +389,7 @@ size_t rows_workspace_bytes(int heads, int D) {
     int C = 0;
     if (device_sm_count(&C) != PKV_OK) return 0;
     const int GC = heads < kHeads ? heads : kHeads;
-    return kCounterBytes + (size_t)C * GC * ((2 + kWarps) * D + 2) * sizeof(float);
+    return kCounterBytes + (size_t)C * GC * (2 * D + 2) * sizeof(float);
 }
 
 pkv_status decode_rows(const pkv_cache_desc *cache, const void *q, int S, int Hq, const void *k_pool,
@@ -412,8 +415,7 @@ pkv_status decode_rows(const pkv_cache_desc *cache, const void *q, int S, int Hq
     p.o.GC = GC;
     p.o.cnt = static_cast<unsigned *>(ws);
     p.o.ws_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kCounterBytes);
-    p.ws_pieces = p.o.ws_o + (size_t)p.C * 2 * GC * D;
-    p.o.ws_lse = p.ws_pieces + (size_t)p.C * kWarps * GC * D;
+    p.o.ws_lse = p.o.ws_o + (size_t)p.C * 2 * GC * D;
     p.k = static_cast<const uint8_t *>(k_pool);
     p.v = static_cast<const uint8_t *>(v_pool);
     p.Hk = Hk;

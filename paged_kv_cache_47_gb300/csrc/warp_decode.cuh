@@ -16,6 +16,7 @@
 
 namespace pkv {
 
+constexpr int kWdFewParts = 4;           // parts of a unit that one warp joins at once
 constexpr int kWdHeads = 8;              // q heads of a unit (the n, or half the m, of the mma)
 constexpr float kWdNone = 2e-38f;        // reference exponent of a head before its first finite
                                          // score: 0 to any score, and no score's own
@@ -385,9 +386,45 @@ __device__ __forceinline__ void wd_join(const WdOut &p, const WdShare &share, Wd
         fence_acq_rel_gpu();
     }
     __syncthreads();
+    // few parts: a warp for each head of either unit, a lane for each part's denominator
+    for (int task = warp; task < 2 * kWdHeads; task += W) {
+        const int side = task & 1, h = task >> 1, n = sh.join_n[side];
+        if (n == 0 || n > kWdFewParts || h >= p.heads(sh.cut_u[side])) continue;
+        // the first CTA's part is its side 1, the others' their side 0
+        const size_t at0 = (size_t)2 * sh.join_first[side] * p.GC + h;
+        const size_t pitch_parts = 2 * (size_t)p.GC;
+        float x[kWdFewParts][E], l = -INFINITY;
+        if (lane < n) l = __ldcg(p.ws_lse + at0 + lane * pitch_parts + (lane ? 0 : p.GC));
+#pragma unroll
+        for (int k = 0; k < kWdFewParts; ++k) {
+            const int part = min(k, n - 1);
+            wd_load_cg(x[k], p.ws_o + (at0 + part * pitch_parts + (part ? 0 : p.GC)) * D + lane * E);
+        }
+        float mx = l;
+#pragma unroll
+        for (int d = kWdFewParts / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+        mx = __shfl_sync(~0u, mx, 0);
+        if (mx == -INFINITY) mx = 0.f;
+        const float f = wd_ex2(l - mx);              // (0 past the last)
+        float sum = f;
+#pragma unroll
+        for (int d = kWdFewParts / 2; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        sum = __shfl_sync(~0u, sum, 0);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        float o[E] = {};
+#pragma unroll
+        for (int k = 0; k < kWdFewParts; ++k) {
+            const float fk = __shfl_sync(~0u, f, k) * inv;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = k < n ? fmaf(x[k][e], fk, o[e]) : o[e];
+        }
+        const size_t at = (size_t)sh.cut_s[side] * p.Hq + p.first_head(sh.cut_u[side]) + h;
+        wd_store_row<E>(p, at * D + lane * E, o);
+        if (p.lse_out && lane == 0) p.lse_out[at] = mx + log2f(sum);
+    }
     for (int side = 0; side < 2; ++side) {
         const int n = sh.join_n[side], first = sh.join_first[side];
-        if (n == 0) continue;
+        if (n <= kWdFewParts) continue;
         const int u = sh.cut_u[side], gca = p.heads(u);
         // the warps of a head take every ways-th part; they meet in slot0
         const int ways = W / gca, h = warp % gca, sub = warp / gca;
@@ -395,7 +432,6 @@ __device__ __forceinline__ void wd_join(const WdOut &p, const WdShare &share, Wd
         if (sub < ways) {
 #pragma unroll 4
             for (int k = sub; k < n; k += ways) {
-                // the first CTA's part is its side 1, the others' their side 0
                 const size_t at = (size_t)(2 * (first + k) + (k == 0)) * p.GC + h;
                 const float l = __ldcg(p.ws_lse + at);
                 float x[E];
