@@ -184,11 +184,13 @@ template <int W, int N>
 __device__ __forceinline__ WdPlace wd_place(const WdList &p, const WdListShared<W, N> &sh, int a, int cost) {
     // the last sequence whose units begin at or before it (of equal prefixes,
     // the empty sequences come first)
-    int lo = 0, hi = p.S - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (sh.prefix[mid] * p.U <= a) lo = mid;
-        else hi = mid - 1;
+    int lo = 0;
+    for (int n = p.S; n > 1;) {          // 32 ways at a time
+        const int step = (n + 31) / 32, lane = threadIdx.x & 31;
+        const bool at_or_before = lane * step < n && sh.prefix[lo + lane * step] * p.U <= a;
+        const int skip = (__popc(__ballot_sync(~0u, at_or_before)) - 1) * step;
+        lo += skip;
+        n = min(step, n - skip);
     }
     WdPlace w;
     w.nv = sh.prefix[lo + 1] - sh.prefix[lo];
@@ -378,12 +380,12 @@ __device__ __forceinline__ void wd_join(const WdOut &p, const WdShare &share, Wd
         const int side = threadIdx.x;
         const int first = split_owner(sh.cut_tu[side], share.NV, share.CT);
         const int n = split_owner(sh.cut_tu[side] + sh.cut_nu[side] - 1, share.NV, share.CT) - first + 1;
-        fence_acq_rel_gpu();
-        const bool last = atomicAdd(p.cnt + first, 1u) == (unsigned)n - 1;
+        // the parts' stores come before it for whoever counts later, and theirs
+        // before the reads below
+        const bool last = atomic_add_acq_rel_gpu(p.cnt + first, 1u) == (unsigned)n - 1;
         if (last) p.cnt[first] = 0;
         sh.join_n[side] = last ? n : 0;
         sh.join_first[side] = first;
-        fence_acq_rel_gpu();
     }
     __syncthreads();
     // few parts: a warp for each head of either unit, a lane for each part's denominator
