@@ -30,7 +30,7 @@
 // 32768 to 131072 tokens and 8 kv heads (0.84 GB) 132 to 148 us, 5.7 to 6.3.
 // A step of 64 sequences of 512 to 4096 tokens and 8 kv heads (190 MB) takes
 // 47 us: 30 in the loops (6.3 TB/s), the rest is the list (1.6 us), tables and
-// first copies (2), the joins within the CTA (2) and between CTAs (4). Sixteen warps in a CTA against
+// first copies (2), the joins within the CTA and between CTAs (5), the launch. Sixteen warps in a CTA against
 // two CTAs of eight: 52 and 54 us (that step), 359 and 383, 133 and 144.
 //
 // Softmax in base 2 with a reference exponent that moves only when a score
