@@ -48,7 +48,7 @@ constexpr int kHeads = pkv::kWdHeads;
 constexpr int kWarps = 10;
 constexpr int kThreads = 32 * kWarps;
 // Contexts of one launch. The longer list costs its scan and the L1 that it
-// takes, 0.6 us, and is taken where it saves a second launch.
+// takes, half a microsecond, and is taken where it saves a second launch.
 constexpr int kFewSeqs = 1024, kMaxSeqs = pkv::kRowsMaxSeqs;
 constexpr int kUnitCost = 2;         // what a unit costs a warp besides its subtiles, in subtiles
 constexpr float kNone = pkv::kWdNone;

@@ -117,7 +117,7 @@ int main() {
         for (int &n : units) n = pick(1, most);
         const int C = i % 3 == 0 ? pick(1, 4) : i % 3 == 1 ? 152 : pick(1, 600);
         bool ok = true;
-        for (int W : {8, 12, 16})
+        for (int W : {8, 10, 12, 16})
             for (int cost : {0, 1, 2}) ok = ok && run(units, C, W, cost);
         if (!ok) {
             std::printf("FAIL at %d\n", i);
