@@ -181,9 +181,10 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
     constexpr int NG = D / 32;
     const Place<D> at;
     const Run<D> run(p, at);
-    const int64_t slot = run.tok < p.T ? __ldg(p.slots + run.tok) : -1;
+    int64_t slot = -1;
     uint4 raw[4] = {};
-    if (slot >= 0) {
+    if (run.tok < p.T) {                 // (a row without a slot is read too: nothing waits for the slot)
+        slot = __ldg(p.slots + run.tok);
         const T *from = static_cast<const T *>(run.is_v ? p.v : p.k) + ((int64_t)run.tok * p.Hk + run.g) * D;
 #pragma unroll
         for (int j = 0; j < 4; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(from + at.element(j)));
