@@ -284,38 +284,37 @@ __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const __grid_consta
     constexpr int NG = D / 32;
     const Place<D> at;
     const Run<D> run(p, at);
-    if (run.tok >= p.T) return;
-    const int64_t r = locate(p, __ldg(p.slots + run.tok), run.g, at.l == 0 && !run.is_v && run.g == 0);
+    const int64_t slot = run.tok < p.T ? __ldg(p.slots + run.tok) : -1;
+    const int64_t r = locate(p, slot, run.g, at.l == 0 && !run.is_v && run.g == 0);
     uint4 codes = make_uint4(0, 0, 0, 0);
-    __half s[NG] = {}, m[NG] = {};
+    uint32_t own = 0;                    // group l's scale and minimum
     if (r >= 0) {
+        const __half *par;
+        int to_min;
         if (!run.is_v) {
             codes = __ldg(static_cast<const uint4 *>(p.pools.k_codes) + r * (D / 32) + at.l);
-            const __half2 *par = reinterpret_cast<const __half2 *>(static_cast<const __half *>(p.pools.k_params) + r * 2 * NG);
-#pragma unroll
-            for (int i = 0; i < NG; i += 2) {
-                const __half2 a = __ldg(par + i / 2), b = __ldg(par + (NG + i) / 2);
-                s[i] = __low2half(a), s[i + 1] = __high2half(a);
-                m[i] = __low2half(b), m[i + 1] = __high2half(b);
-            }
+            par = static_cast<const __half *>(p.pools.k_params) + r * 2 * NG + at.l;
+            to_min = NG;
         } else {
             codes = words_of<D>(__ldg(static_cast<const uint4 *>(p.pools.v_codes) + r * (D / 32) + at.l));
             const int off = (int)r & ((1 << p.lb) - 1);
-            const __half *par = static_cast<const __half *>(p.pools.v_params) + (r - off) * 2 * NG + off;
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                s[i] = __ldg(par + (i << p.lb));
-                m[i] = __ldg(par + ((NG + i) << p.lb));
-            }
+            par = static_cast<const __half *>(p.pools.v_params) + (r - off) * 2 * NG + off + (at.l << p.lb);
+            to_min = NG << p.lb;
         }
+        own = __half_as_ushort(__ldg(par)) | (uint32_t)__half_as_ushort(__ldg(par + to_min)) << 16;
     }
+    uint32_t params[NG];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) params[i] = __shfl_sync(~0u, own, i, NG);
+    if (run.tok >= p.T) return;
     T *to = static_cast<T *>(run.is_v ? p.v_out : p.k_out) + ((int64_t)run.tok * p.Hk + run.g) * D;
     const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
     const pkv::Pair back = pkv::pair_of(-8388608.f, -8388608.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int i = Place<D>::group(j);
-        const float sf = __half2float(s[i]), mf = __half2float(m[i]);
+        const float sf = __half2float(__ushort_as_half((unsigned short)params[i]));
+        const float mf = __half2float(__ushort_as_half((unsigned short)(params[i] >> 16)));
         const pkv::Pair minimum = pkv::pair_of(mf, mf);
         const pkv::Pair scale[2] = {pkv::pair_of(sf, sf * 0x1p-4f), pkv::pair_of(sf * 0x1p-8f, sf * 0x1p-12f)};
         float x[8];
