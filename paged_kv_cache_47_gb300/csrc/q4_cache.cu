@@ -18,10 +18,11 @@
 //
 // What bounds it: HBM, and close to it the instructions. A row of 128 elements
 // is 256 bytes read and 80 written: 103 instructions of a warp for a K and a V
-// row (232 with 8 elements a lane, each lane its group's scale). 16383 tokens of
-// 8 heads of 128 appended and read back take 38.3 us, 4.6 TB/s of what the two
-// calls must read and write (60.6 us with 8 elements a lane; CTAs of 256 and of
-// 64 threads 39.2 and 40.7).
+// row (232 with 8 elements a lane, each lane its group's scale), 67 to read them
+// back. 16383 tokens of 8 heads of 128 appended and read back take 36.0 us, 4.9
+// TB/s of what the two calls must read and write (60.6 us with 8 elements a lane;
+// CTAs of 256 and of 64 threads 1.1 and 2.6 more; rows read after their slots
+// 1.5 more).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
