@@ -139,16 +139,24 @@ def test_long_selections(dt):
 
 
 @pytest.mark.parametrize("S,Hk,hi", [(1, 2, 60), (19, 8, 60), (3, 2, 300), (38, 8, 300), (1, 1, 1023), (2, 1, 1024),
-                                     (39, 8, 300), (305, 1, 1100), (5, 1, 1100), (160, 1, 1100)])
+                                     (39, 8, 300), (305, 1, 1100), (5, 1, 1100), (160, 1, 1100), (305, 1, 16384), (305, 1, 16385)])
 def test_selection_forms(S, Hk, hi):
     """Rows for less and more than one, two and four CTAs an SM, short and long; more than 256
     candidates and fewer."""
     rng = np.random.default_rng(S)
-    lens = rng.integers(1, 8 * (hi - 1), S)
+    lens = rng.integers(1, 8 * (min(hi, 1100) - 1), S)
     lens[0] = 8 * (hi - 1)                           # table columns: hi
     Batch(40, lens, Hk, 64, 8, "bf16").check(2, 30, attention=False)
     if S == 38:
         Batch(41, lens, Hk, 64, 8, "bf16", ties=True).check(2, 30, attention=False)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hk,G", [(1, 1), (3, 2), (2, 4), (1, 5), (2, 8), (1, 12)])
+def test_spread_selections(Hk, G, D, dt):
+    """Long rows, few of them: scores from all over the GPU."""
+    Batch(43, [8 * 1500 - 3, 0, 8 * 1030, 5, 8 * 70 + 1], Hk, D, 8, dt).check(G, 25, 2, 3)
 
 
 @pytest.mark.parametrize("S", [256, 257, 300])
