@@ -222,11 +222,13 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
     __half s = __float2half_rn(fminf((hi - lo) * (1.f / 15.f), kMaxHalf));
     // a NaN is the largest of all; an infinity is one of the ends
     if (!(fabsf(hi) <= 3.402823466e38f) || !(fabsf(lo) <= 3.402823466e38f)) m = s = __ushort_as_half(0x7fff);
-    // Quotients lie within 0.3 of [0, 15] and need no clamp where the minimum's
-    // rounding (2^-11 of it) is small beside the scale and the scale's own is
-    // relative (no subnormal, not the largest)
+    // Quotients lie within 0.3 of [0, 15] and need no clamp where the minimum is
+    // the group's own but for its rounding (2^-11 of it), that is small beside
+    // the scale, and the scale's rounding is relative (no subnormal, not the
+    // largest)
     const float own_m = fabsf(__half2float(m)), own_s = __half2float(s);
-    const unsigned unsure = __ballot_sync(~0u, !(own_m * 0x1p-9f < own_s) || own_s < 0x1p-13f || own_s >= kMaxHalf) >>
+    const unsigned unsure = __ballot_sync(~0u, !(fabsf(lo) <= kMaxHalf) || !(own_m * 0x1p-9f < own_s) ||
+                                                   own_s < 0x1p-13f || own_s >= kMaxHalf) >>
                             (threadIdx.x & 31 & ~(NG - 1));
     const uint32_t own = __half_as_ushort(s) | (uint32_t)__half_as_ushort(m) << 16;
     uint32_t word[4];
