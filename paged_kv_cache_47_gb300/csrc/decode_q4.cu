@@ -6,13 +6,16 @@
 // so codes meet the matrix instructions as they are and the parameters enter
 // per token and group, not per element.
 //
-// Codes as operands. A 4-bit code at bits 0..3 (or 4..7) of an fp16 whose other
-// bits are zero is the subnormal number c 2^-24 (or c 2^-20), exactly: one AND
-// makes two operands, with no bias to take off again and no conversion. Codes
-// at bits 4..7 count 16 fold; q carries the 1/16 on the K side, the epilogue
-// on the V side. mma.sync takes subnormals at full rate. (tcgen05 has no form
-// that reads these rows: its 4-bit kinds want the contracted index along the
-// row for both operands, and a V row holds one token.)
+// Codes as operands. A 4-bit code in an fp16 whose other bits are zero is a
+// subnormal number, exactly: one AND makes two operands, with no bias to take
+// off again and no conversion. mma.sync takes subnormals at full rate, but aligns
+// products by their operands' exponent fields before it adds them: leading zeros
+// of a subnormal are bits that the sum loses. On K's side codes are shifted to
+// bits 4..7 (c 2^-20), which keeps a sum to 2^-17 of the largest |q| for a code's
+// unit (2^-12.6 at bits 0..3, measured; normal numbers 2^-18). On V's side codes
+// at bits 4..7 count 16 fold, which the epilogue takes off. (tcgen05 has no form
+// that reads these rows: its 4-bit kinds want the contracted index along the row
+// for both operands, and a V row holds one token.)
 //
 // Work. The batch's (sequence, kv head, up to 8 q heads) units, cut into
 // subtiles of 32 tokens (two halves of 16, the m of the scores' product and the
@@ -69,6 +72,12 @@ constexpr int kMaxSeqs = 1024;       // of one launch
 // batch. Counting units as 2 subtiles evened the warps' ends out (loops of 29.6
 // and 29.8 us with one and two units, 31.7 and 35.3 us uncounted).
 constexpr int kUnitCost = 2;
+constexpr float kCodeUnit = 0x1p-20f;    // of a K code as operand
+// Sums of q over a group, 2^20 at most, as operands: in this unit they end below
+// the largest fp16 number. (In the codes' own they would end near 1 and lose
+// what lies below 2^-25, a part of the head's largest element that is more than
+// another group's sum: a few large channels are the usual case.)
+constexpr float kSumUnit = 0x1p-5f;
 constexpr float kNone = pkv::kWdNone;
 
 struct Q4Params {
@@ -451,16 +460,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     }
                     sum[y] += __shfl_xor_sync(~0u, sum[y], 1);
                     sum[y] += __shfl_xor_sync(~0u, sum[y], 2);
-                    sum[y] *= 0x1p-24f;              // at most 2^-4, in the codes' unit
+                    sum[y] *= kSumUnit;              // at most 2^15
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         qb[y][k][0] = as_u32(__floats2half2_rn(x[y][2 * k], x[y][4 + 2 * k]));
-                        qb[y][k][1] = as_u32(__floats2half2_rn(x[y][2 * k + 1] * 0.0625f,
-                                                               x[y][4 + 2 * k + 1] * 0.0625f));
+                        qb[y][k][1] = as_u32(__floats2half2_rn(x[y][2 * k + 1], x[y][4 + 2 * k + 1]));
                     }
                 }
                 // sums as fp16 pairs: k = 0..NG-1 the high parts, then the low ones
-                // (to 2^-25, 2^-21 of the largest sum a group of such q can have)
+                // (to 2^-22 of the sum, at least to 2^-34 of the head's largest
+                // element: a head with a few large channels keeps the sums of its
+                // other groups)
                 const bool upper = NG == 4 && (t & 1);
                 const float s0 = upper ? sum[NG - 2] : sum[0], s1 = upper ? sum[NG - 1] : sum[1];
                 __half2 hi = __floats2half2_rn(s0, s1);
@@ -469,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     hi = __floats2half2_rn(s0 - f.x, s1 - f.y);
                 }
                 qsum = NG == 2 && t >= 2 ? 0u : as_u32(hi);
-                const float zq = p.scale_log2 * 0x1p24f * down;
+                const float zq = p.scale_log2 / kCodeUnit * down;
                 zs0 = __shfl_sync(~0u, zq, 8 * t);
                 zs1 = __shfl_sync(~0u, zq, 8 * t + 4);
             }
@@ -528,15 +538,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 float x[4];
                 mma8_zero(x, m0, m1, qsum);
 #pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] *= kCodeUnit / kSumUnit;    // to the codes' unit
+#pragma unroll
                 for (int y = 0; y < NG; ++y) {
                     float d[4];
-                    uint32_t wa = w[0][y], wb = w[1][y];
-                    mma16_zero(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
-                               qb[y][0][0], qb[y][0][1]);
-                    wa >>= 8;
-                    wb >>= 8;
-                    mma16(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
-                          qb[y][1][0], qb[y][1][1]);
+                    const uint32_t wa = w[0][y], wb = w[1][y], code = 0x00f000f0u;
+                    mma16_zero(d, wa << 4 & code, wb << 4 & code, wa & code, wb & code, qb[y][0][0], qb[y][0][1]);
+                    mma16(d, wa >> 4 & code, wb >> 4 & code, wa >> 8 & code, wb >> 8 & code, qb[y][1][0], qb[y][1][1]);
                     x[0] = fmaf(d[0], s0[y], x[0]);
                     x[1] = fmaf(d[1], s0[y], x[1]);
                     x[2] = fmaf(d[2], s1[y], x[2]);

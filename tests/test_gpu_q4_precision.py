@@ -1,0 +1,109 @@
+"""How near the 4-bit decode comes to 64 bits where operands of fewer bits would show: queries with a
+few large channels, weights far below the largest, V scales from 1e-7 to thousands side by side.
+
+Tolerances. A score is off by
+  - the sums of D exact products and NG scaled partial sums in fp32, below (D / 8 + 8) 2^-23 of
+    A = |scale| sum |q| (|s c| + |m|) for any order within the matrix instructions;
+  - the operands: an element of q by at most 2^-35 of the head's largest, a group's sum of q (a pair
+    of fp16) by 2^-22 of itself, which the first term's constant covers, and 2^-34 of the largest
+    element: 2^-33 |scale| max|q| sum (|s c| + |m|) for both.
+A weight's exponent is the score z in log2 units times a constant rounded twice, less the reference,
+at most three roundings more: 2^-21 |z|, and the exponential 2^-21. The joins' weights have the
+same from the denominators' logarithms. A weight is kept to 2^-22, at least to 2^-25 where
+the largest is at 2^10 or above: 2^-35 of the largest. A weight times a V scale is kept to 2^-20, at
+least to 2^-24 of the unit that the group's largest scale S (in half or more of it) has:
+2 S 2^-34 of the largest weight, 15 times that for a code; scales of less than 2^-14 S to 2^-24 S.
+Sums over tokens: a warp adds its own, two products for 16 of them, and up to 64 additions join the
+warps' pieces: (n / 8 + 64) 2^-23 of sum p (|s c| + |m|) for n tokens a warp, for the denominator the
+same of itself. Then half a step of the output's type."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import step_ops as O
+from paged_kv_cache_47_gb300 import binding as b
+from test_gpu_q4 import Batch, DT, dev, randn
+
+pytestmark = pytest.mark.gpu
+
+
+def sizes(t, s):
+    """|s c| + |m| of sequence s's K and V elements at most, and the V scales' largest: [Hk][L][D] twice, [Hk][D]."""
+    NG, L = t.D // 32, int(t.lens[s])
+    blk = t.tab[s, : -(-L // t.B)].astype(np.int64)
+    size, top = [], None
+    for par in (t.kp[blk], t.vp[blk].swapaxes(2, 3)):
+        par = par.transpose(1, 0, 2, 3).reshape(t.Hk, -1, 2 * NG)[:, :L].astype(np.float64)
+        size.append(np.repeat(15 * np.abs(par[..., :NG]) + np.abs(par[..., NG:]), 32, -1))
+        top = np.repeat(np.abs(par[..., :NG]).max(1), 32, -1)
+    return size[0], size[1], top
+
+
+def score_error(t, q, size, scale):
+    """Of one sequence, [Hq][L]; q [Hq][D] in 64 bits."""
+    size = np.repeat(size, q.shape[0] // t.Hk, 0)
+    a = np.einsum("hd,hld->hl", np.abs(q), size) * (t.D / 8 + 8) * 2.0 ** -23
+    return abs(scale) * (a + size.sum(-1) * np.abs(q).max(-1)[:, None] * 2.0 ** -33)
+
+
+def check(t, q, scale, **kw):
+    """q [S][Hq][D], CPU. Output in fp32 and denominators within the tolerances above."""
+    S, Hq, _ = q.shape
+    G = Hq // t.Hk
+    lse = torch.full((S, Hq), 7.0, device="cuda")
+    out = b.decode_attention_q4(q.cuda(), t.cache, dev(t.tab), dev(t.lens), scale, out_dtype=torch.float32, lse_out=lse, **kw)
+    assert b.get_error() == 0
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    # tokens a warp has of one context: an even share of all subtiles of 32, a unit's start counted as two
+    warps = 16 * (kw.get("num_ctas") or torch.cuda.get_device_properties(0).multi_processor_count)
+    units = t.Hk * -(-G // 8)
+    share = 32 * (-(-int(sum(-(-int(n) // 32) + 2 for n in t.lens)) * units // warps) + 1)
+    if kw.get("num_ctas", 0) == 0:
+        share = max(share, 4 * 32)                   # few short units: a CTA each
+    for s in range(S):
+        L = int(t.lens[s])
+        k, v = O.q4_rows(t.tab[s], L, t.kc, t.vc, t.kp, t.vp)
+        qs = q[s].double().numpy()
+        want, wl, p = O.attend(qs, k, v, scale)
+        ks, vs, top = sizes(t, s)
+        z = np.abs(wl)[:, None] + np.abs(np.log2(np.maximum(p, 1e-300)))    # |log2 units| of a score, at most
+        weight = score_error(t, qs, ks, scale) + (z + 1) * 2.0 ** -21 + 2.0 ** -22
+        sums = (min(L, share) / 8 + 64) * 2.0 ** -23
+        vs, top, v = (np.repeat(x, G, 0) for x in (vs, top, v))
+        tol = np.zeros_like(want)
+        for h in range(Hq):
+            move = np.abs(v[h] - want[h])
+            tol[h] = 2 * (p[h] * weight[h]) @ move + (p[h] @ vs[h]) * (2 * sums + 2.0 ** -20)
+            tol[h] += L * 2.0 ** -35 * p[h].max() * move.max(0)
+            tol[h] += 15 * top[h] * (L * 2.0 ** -33 * p[h].max() + 2.0 ** -24)
+        tol += np.abs(want) * 2.0 ** -24
+        err = np.abs(out[s] - want)
+        assert (err <= tol).all(), (s, float((err / tol).max()), float(err.max()))
+        lt = 1.5 * ((p * weight).sum(-1) + sums + L * 2.0 ** -35 * p.max(-1)) + np.abs(wl) * 2.0 ** -22 + 2.0 ** -20
+        assert (np.abs(lse[s] - wl) <= lt).all(), (s, float((np.abs(lse[s] - wl) / lt).max()))
+
+
+def with_channels(S, Hq, D, dt, peak, seed=0):
+    """Normal queries with one element of each head at `peak`, in turn of either sign."""
+    q = randn((S, Hq, D), dt, seed)
+    rng = np.random.default_rng(seed)
+    for s in range(S):
+        for h in range(Hq):
+            q[s, h, rng.integers(D)] = peak * (-1) ** h
+    return q
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("peak", [30.0, 100.0, 300.0, 3000.0])
+def test_queries_with_a_large_channel(peak, D, dt):
+    # one token: the denominator's logarithm is the score itself
+    t = Batch([int(peak), D], [1] * 24, 2, D, 16, dt)
+    check(t, with_channels(24, 8, D, dt, peak), 1 / math.sqrt(D))
+    # minima far from zero
+    t = Batch([int(peak), D], [1] * 24, 2, D, 16, dt)
+    t.kp[..., t.D // 32:] += np.float16(20)
+    t.cache = b.Q4Cache(dev(t.kc), dev(t.vc), dev(t.kp), dev(t.vp), DT[dt])
+    check(t, with_channels(24, 8, D, dt, peak), 1 / math.sqrt(D))
