@@ -10,12 +10,11 @@
 // subnormal number, exactly: one AND makes two operands, with no bias to take
 // off again and no conversion. mma.sync takes subnormals at full rate, but aligns
 // products by their operands' exponent fields before it adds them: leading zeros
-// of a subnormal are bits that the sum loses. On K's side codes are shifted to
-// bits 4..7 (c 2^-20), which keeps a sum to 2^-17 of the largest |q| for a code's
-// unit (2^-12.6 at bits 0..3, measured; normal numbers 2^-18). On V's side codes
-// at bits 4..7 count 16 fold, which the epilogue takes off. (tcgen05 has no form
-// that reads these rows: its 4-bit kinds want the contracted index along the row
-// for both operands, and a V row holds one token.)
+// of a subnormal are bits that the sum loses. Codes are shifted to
+// bits 4..7 (c 2^-20), which keeps a sum to 2^-17 of the largest |q|, or weight
+// times scale, for a code's unit (2^-12.6 at bits 0..3, measured; normal numbers
+// 2^-18). (tcgen05 has no form that reads these rows: its 4-bit kinds want the
+// contracted index along the row for both operands, and a V row holds one token.)
 //
 // Work. The batch's (sequence, kv head, up to 8 q heads) units, cut into
 // subtiles of 32 tokens (two halves of 16, the m of the scores' product and the
@@ -40,10 +39,9 @@
 // passes it by more than the fp16 weights can hold, or a V scale grows past
 // its bound: most subtiles need one vote instead of a reduction over lanes and
 // a rescale of the accumulators. The denominator is summed by the same product
-// that weighs the minima (a row of ones), over the rounded weights, so a
-// weight's rounding moves the average, not its normalisation. Weight times V
-// scale is kept as an fp16 pair (22 bits): codes are positive, so an error
-// there would not cancel against the minimum's share.
+// that weighs the minima (a row of ones). Weights, and weights times V scales,
+// are pairs of fp16 (22 bits): codes are positive, so an error of the products
+// would not cancel against the minimum's share.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -72,7 +70,7 @@ constexpr int kMaxSeqs = 1024;       // of one launch
 // batch. Counting units as 2 subtiles evened the warps' ends out (loops of 29.6
 // and 29.8 us with one and two units, 31.7 and 35.3 us uncounted).
 constexpr int kUnitCost = 2;
-constexpr float kCodeUnit = 0x1p-20f;    // of a K code as operand
+constexpr float kCodeUnit = 0x1p-20f;    // of a code as operand
 // Sums of q over a group, 2^20 at most, as operands: in this unit they end below
 // the largest fp16 number. (In the codes' own they would end near 1 and lose
 // what lies below 2^-25, a part of the head's largest element that is more than
@@ -631,11 +629,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                // ---- weights, transposed: lane (g, t) has head g, tokens 4t .. 4t + 3
-                const uint32_t p01 =
-                    transpose8(as_u32(__floats2half2_rn(wd_ex2(sc[half][0]), wd_ex2(sc[half][1]))));
-                const uint32_t p23 =
-                    transpose8(as_u32(__floats2half2_rn(wd_ex2(sc[half][2]), wd_ex2(sc[half][3]))));
+                // ---- weights as pairs, transposed: lane (g, t) has head g, tokens 4t .. 4t + 3
+                uint32_t ph[2], pl[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float w0 = wd_ex2(sc[half][2 * i]), w1 = wd_ex2(sc[half][2 * i + 1]);
+                    const __half2 hi = __floats2half2_rn(w0, w1);
+                    const float2 f = __half22float2(hi);
+                    ph[i] = transpose8(as_u32(hi));
+                    pl[i] = transpose8(as_u32(__floats2half2_rn(w0 - f.x, w1 - f.y)));
+                }
                 // ---- V: rows of the product are d, its contracted index the tokens
                 uint32_t v01[NG], v23[NG];
                 {
@@ -663,21 +666,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     // row of ones as row 8
                     uint32_t m01, m23;
                     lds64(pv + vm_at + half * 32, m01, m23);
-                    mma16(accx, m01, one, m23, one, p01, p23);
+                    mma16(accx, m01, one, m23, one, ph[0], ph[1]);
+                    mma16(accx, m01, one, m23, one, pl[0], pl[1]);
                 }
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
                     uint32_t vs0, vs1;
                     lds64(pv + y * (2 * kSub) + half * 32 + t * 8, vs0, vs1);
                     const __half2 s01 = as_h2(vs0), s23 = as_h2(vs1);
-                    const __half2 h01 = __hmul2(as_h2(p01), s01), h23 = __hmul2(as_h2(p23), s23);
-                    const uint32_t l01 = as_u32(__hfma2(as_h2(p01), s01, __hneg2(h01)));
-                    const uint32_t l23 = as_u32(__hfma2(as_h2(p23), s23, __hneg2(h23)));
+                    const __half2 h01 = __hmul2(as_h2(ph[0]), s01), h23 = __hmul2(as_h2(ph[1]), s23);
+                    const uint32_t l01 = as_u32(__hfma2(as_h2(pl[0]), s01, __hfma2(as_h2(ph[0]), s01, __hneg2(h01))));
+                    const uint32_t l23 = as_u32(__hfma2(as_h2(pl[1]), s23, __hfma2(as_h2(ph[1]), s23, __hneg2(h23))));
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint32_t wa = v01[y] >> (8 * k), wb = v23[y] >> (8 * k);
-                        const uint32_t a0 = wa & 0x000f000fu, a1 = wa & 0x00f000f0u;
-                        const uint32_t a2 = wb & 0x000f000fu, a3 = wb & 0x00f000f0u;
+                        const uint32_t wa = v01[y], wb = v23[y], code = 0x00f000f0u;
+                        const uint32_t a0 = (k ? wa >> 4 : wa << 4) & code, a1 = (k ? wa >> 8 : wa) & code;
+                        const uint32_t a2 = (k ? wb >> 4 : wb << 4) & code, a3 = (k ? wb >> 8 : wb) & code;
                         mma16(acc[y][k], a0, a1, a2, a3, as_u32(h01), as_u32(h23));
                         mma16(acc[y][k], a0, a1, a2, a3, l01, l23);
                     }
@@ -713,12 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     const int h = 2 * t + e;
                     if (h >= gca) continue;
                     const float m = e ? x1 : x0, inv = e ? inv1 : inv0;
-                    const float o0 = fmaf(acc[y][0][e], 0x1p24f, m) * inv;
-                    const float o1 = fmaf(acc[y][0][2 + e], 0x1p20f, m) * inv;
-                    const float o2 = fmaf(acc[y][1][e], 0x1p24f, m) * inv;
-                    const float o3 = fmaf(acc[y][1][2 + e], 0x1p20f, m) * inv;
                     const int d = 32 * y + 4 * g;
-                    const float o4[4] = {o0, o1, o2, o3};
+                    float o4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o4[i] = fmaf(acc[y][i / 2][2 * (i & 1) + e], 1 / kCodeUnit, m) * inv;
                     if (whole) {
                         pkv::wd_store_row<4>(p.o, ((size_t)at.s * p.o.Hq + h0 + h) * D + d, o4);
                     } else {

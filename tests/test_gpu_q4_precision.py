@@ -107,3 +107,19 @@ def test_queries_with_a_large_channel(peak, D, dt):
     t.kp[..., t.D // 32:] += np.float16(20)
     t.cache = b.Q4Cache(dev(t.kc), dev(t.vc), dev(t.kp), dev(t.vp), DT[dt])
     check(t, with_channels(24, 8, D, dt, peak), 1 / math.sqrt(D))
+# ------------------------------------------------------------------------------ weights
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("Hk,G,D,B", [(1, 1, 64, 8), (2, 4, 128, 16), (1, 8, 128, 32), (2, 3, 64, 32), (1, 12, 128, 16)])
+@pytest.mark.parametrize("std", [0.01, 1.0])
+def test_weights_keep_their_bits(std, Hk, G, D, B, dt):
+    # nearly equal weights: their own rounding is what an output would show
+    t = Batch([G, D, B], [20, 33, 1, 700, 5], Hk, D, B, dt)
+    for num_ctas in (0, 3):
+        check(t, randn((5, Hk * G, D), dt, 1, std), 1 / math.sqrt(D), num_ctas=num_ctas)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("peak", [30.0, 300.0])
+def test_contexts_of_queries_with_a_large_channel(peak, D):
+    t = Batch([int(peak), D], [700, 33, 64], 2, D, 16)
+    check(t, with_channels(3, 8, D, t.dt, peak), 0.01)
