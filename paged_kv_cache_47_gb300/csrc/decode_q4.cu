@@ -36,12 +36,15 @@
 // two CTAs of eight: 52 and 54 us (that step), 359 and 383, 133 and 144.
 //
 // Softmax in base 2 with a reference exponent that moves only when a score
-// passes it by more than the fp16 weights can hold, or a V scale grows past
-// its bound: most subtiles need one vote instead of a reduction over lanes and
-// a rescale of the accumulators. The denominator is summed by the same product
-// that weighs the minima (a row of ones). Weights, and weights times V scales,
-// are pairs of fp16 (22 bits): codes are positive, so an error of the products
-// would not cancel against the minimum's share.
+// passes it by more than the fp16 weights can hold, or a V scale grows past its
+// group's bound: most subtiles need one vote instead of a reduction over lanes
+// and a rescale of the accumulators. V scales are brought to at most 1 by a
+// power of two for each group, so that neither a large scale pushes light tokens,
+// other heads or other groups below fp16's range nor tiny scales lose bits. The
+// denominator is summed by the same product that weighs the minima (a row of
+// ones). Weights, and weights times V scales, are pairs of fp16 (22 bits): codes
+// are positive, so an error of the products would not cancel against the
+// minimum's share.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -76,6 +79,10 @@ constexpr float kCodeUnit = 0x1p-20f;    // of a code as operand
 // what lies below 2^-25, a part of the head's largest element that is more than
 // another group's sum: a few large channels are the usual case.)
 constexpr float kSumUnit = 0x1p-5f;
+// Exponent that a reference gives the top score: up to 2^15 needs no new one, and
+// what a pair of fp16 cannot hold of a light token is 2^-35 of the largest.
+constexpr float kTop = 10.f;
+constexpr uint32_t kMostUp = 0x78007800u;    // 2^15 twice
 constexpr float kNone = pkv::kWdNone;
 
 struct Q4Params {
@@ -393,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             v_at = t * 128 + (((g >> 2) ^ line_xor<D>(t)) << 4) + 4 * (g & 3);
         }
         m_at = 2 * NG + (NG == 4 ? 4 * (t & 1) : 0);                 // minima of two groups in a K row
+        const uint32_t vs_at = (g & (NG - 1)) * (2 * kSub) + (g / NG & 1) * 32 + t * 8;      // scales of a group, V
         const uint32_t vm_at = (NG + (g & (NG - 1))) * (2 * kSub) + t * 8;   // minima of a group, V
         const uint32_t one = g == 0 ? 0x3c003c00u : 0u;
 
@@ -483,7 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             }
             float mu0 = kNone, mu1 = kNone;      // reference exponents
             float room = -INFINITY;              // largest score above them that needs no new ones
-            uint32_t sbound = 0x3c003c00u;       // V scales so far stay at or below it (1)
+            // V scales are multiplied, group by group, by a power of two that
+            // brings the largest so far to [1/2, 1): of the groups in pairs, and
+            // of the one that this lane watches
+            uint32_t vm[NG / 2], vm_own = kMostUp;
+#pragma unroll
+            for (int i = 0; i < NG / 2; ++i) vm[i] = kMostUp;
             float acc[NG][2][4], accx[4];
 #pragma unroll
             for (int y = 0; y < NG; ++y)
@@ -563,46 +576,42 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             }
             left -= kSub;
 
-            // ---- V scales of tokens 4t .. 4t + 3, and the reference exponent
-            // (the scales are read again where they are used: held, they would spill)
-            __half2 big = __float2half2_rn(0.f);
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int y = 0; y < NG; ++y) {
-                    uint32_t v0, v1;
-                    lds64(pv + y * (2 * kSub) + half * 32 + t * 8, v0, v1);
-                    big = __hmax2(big, __hmax2(as_h2(v0), as_h2(v1)));
-                }
+            // ---- V scales' bounds, and the reference exponent. Lane (g, t) looks at
+            // four tokens' scales of one group
+            uint32_t v0, v1;
+            lds64(pv + vs_at, v0, v1);
+            const __half2 big = __hmax2(as_h2(v0), as_h2(v1));
             const float over = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
                                      fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
-            if (__any_sync(~0u, over > room || !__hble2(big, as_h2(sbound)))) {
-                // raise the bound on V scales to this subtile's largest, the
-                // reference to 7 (less where scales are large) below the top score
+            if (__any_sync(~0u, over > room || !__hble2(__hmul2(big, as_h2(vm_own)), __float2half2_rn(1.f)))) {
+                // the factors for this subtile's largest scales, the reference
+                // to 10 below the top score
                 float bs = fmaxf(__low2float(big), __high2float(big));
                 float t0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2])) + mu0;
                 float t1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3])) + mu1;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    bs = fmaxf(bs, __shfl_xor_sync(~0u, bs, o));
+                    if (o < 4 || o >= 4 * NG) bs = fmaxf(bs, __shfl_xor_sync(~0u, bs, o));
                     if (o >= 4) {
                         t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, o));
                         t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, o));
                     }
                 }
-                bs = fminf(fmaxf(bs, __low2float(as_h2(sbound))), 65504.f);
-                sbound = as_u32(__float2half2_rn(bs));
-                // scales up to 2^e, e >= 1: weights up to 2^(15 - e)
-                const float e = (float)((int)(__float_as_uint(bs) >> 23) - 126);
+                // a largest scale of 2^(k - 1) to 2^k: 2^-k, 2^15 at most
+                const float was = __low2float(as_h2(vm_own));
+                const uint32_t top = __float_as_uint(fminf(fmaxf(bs, 0x1p-15f), 65504.f)) >> 23;
+                const float now = fminf(was, __uint_as_float((253 - top) << 23));
+                const float down = __uint_as_float(__float_as_uint(now) - __float_as_uint(was) + 0x3f800000u);
+                vm_own = as_u32(__float2half2_rn(now));
                 float u0 = mu0, u1 = mu1;
                 const bool none0 = mu0 == kNone, none1 = mu1 == kNone;
-                if (t0 > -INFINITY) u0 = none0 ? t0 - 7.f + e : fmaxf(mu0, t0 - 7.f + e);
-                if (t1 > -INFINITY) u1 = none1 ? t1 - 7.f + e : fmaxf(mu1, t1 - 7.f + e);
+                if (t0 > -INFINITY) u0 = none0 ? t0 - kTop : fmaxf(mu0, t0 - kTop);
+                if (t1 > -INFINITY) u1 = none1 ? t1 - kTop : fmaxf(mu1, t1 - kTop);
                 // (before the first score there is nothing to rescale)
                 const float f0 = none0 ? 1.f : wd_ex2(mu0 - u0), f1 = none1 ? 1.f : wd_ex2(mu1 - u1);
                 // a head that has had no score but -infinity keeps none, and
                 // the next subtile asks again
-                room = __any_sync(~0u, u0 == kNone || u1 == kNone) ? -INFINITY : 15.f - e;
+                room = __any_sync(~0u, u0 == kNone || u1 == kNone) ? -INFINITY : 15.f;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     sc[half][0] = sc[half][0] + mu0 - u0;
@@ -613,14 +622,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 mu0 = u0;
                 mu1 = u1;
 #pragma unroll
-                for (int y = 0; y < NG; ++y)
+                for (int y = 0; y < NG; ++y) {
+                    const float d = __shfl_sync(~0u, down, 4 * y), g0 = f0 * d, g1 = f1 * d;
+                    if (y % 2 == 0) vm[y / 2] = __byte_perm(__shfl_sync(~0u, vm_own, 4 * y), __shfl_sync(~0u, vm_own, 4 * y + 4), 0x5410);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        acc[y][k][0] *= f0;
-                        acc[y][k][1] *= f1;
-                        acc[y][k][2] *= f0;
-                        acc[y][k][3] *= f1;
+                        acc[y][k][0] *= g0;
+                        acc[y][k][1] *= g1;
+                        acc[y][k][2] *= g0;
+                        acc[y][k][3] *= g1;
                     }
+                }
                 accx[0] *= f0;
                 accx[1] *= f1;
                 accx[2] *= f0;
@@ -673,7 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 for (int y = 0; y < NG; ++y) {
                     uint32_t vs0, vs1;
                     lds64(pv + y * (2 * kSub) + half * 32 + t * 8, vs0, vs1);
-                    const __half2 s01 = as_h2(vs0), s23 = as_h2(vs1);
+                    const __half2 m2 = y & 1 ? __high2half2(as_h2(vm[y / 2])) : __low2half2(as_h2(vm[y / 2]));
+                    const __half2 s01 = __hmul2(as_h2(vs0), m2), s23 = __hmul2(as_h2(vs1), m2);
                     const __half2 h01 = __hmul2(as_h2(ph[0]), s01), h23 = __hmul2(as_h2(ph[1]), s23);
                     const uint32_t l01 = as_u32(__hfma2(as_h2(pl[0]), s01, __hfma2(as_h2(ph[0]), s01, __hneg2(h01))));
                     const uint32_t l23 = as_u32(__hfma2(as_h2(pl[1]), s23, __hfma2(as_h2(ph[1]), s23, __hneg2(h23))));
@@ -712,6 +725,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             for (int y = 0; y < NG; ++y) {
                 const float x0 = __shfl_sync(~0u, accx[0], 4 * y + t);
                 const float x1 = __shfl_sync(~0u, accx[1], 4 * y + t);
+                // one over the group's power of two, in the codes' unit
+                const float m2 = y & 1 ? __high2float(as_h2(vm[y / 2])) : __low2float(as_h2(vm[y / 2]));
+                const float up = __uint_as_float(0x7f000000u - __float_as_uint(m2)) / kCodeUnit;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {            // head 2t + e
                     const int h = 2 * t + e;
@@ -720,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     const int d = 32 * y + 4 * g;
                     float o4[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o4[i] = fmaf(acc[y][i / 2][2 * (i & 1) + e], 1 / kCodeUnit, m) * inv;
+                    for (int i = 0; i < 4; ++i) o4[i] = fmaf(acc[y][i / 2][2 * (i & 1) + e], up, m) * inv;
                     if (whole) {
                         pkv::wd_store_row<4>(p.o, ((size_t)at.s * p.o.Hq + h0 + h) * D + d, o4);
                     } else {

@@ -123,3 +123,44 @@ def test_weights_keep_their_bits(std, Hk, G, D, B, dt):
 def test_contexts_of_queries_with_a_large_channel(peak, D):
     t = Batch([int(peak), D], [700, 33, 64], 2, D, 16)
     check(t, with_channels(3, 8, D, t.dt, peak), 0.01)
+# ---------------------------------------------------------------------------- V scales
+@pytest.mark.parametrize("num_ctas", [0, 1])
+@pytest.mark.parametrize("D,top", [(64, 0.3), (64, 5000.0), (128, 300.0), (128, 60000.0)])
+def test_light_tokens_beside_a_large_scale(D, top, num_ctas):
+    # one token 2^18 to 2^22 above 131071 others, which hold about a tenth of the softmax together
+    L, NG = 131072, D // 32
+    t = Batch([D, int(top)], [L], 1, D, 32)
+    rng = np.random.default_rng(1)
+    t.kp[..., :NG] = 0
+    x = -rng.uniform(18, 22, L) * math.log(2) / (D * 0.125)
+    x[200] = 0                                        # (of the first warp where there are 16)
+    t.kp[t.tab[0, : L // 32], 0, :, NG:] = x.reshape(-1, 32, 1).astype(np.float16)
+    t.vp[t.tab[0, 3], 0, 0, 5] = top                  # a V scale of group 0, token 101
+    t.cache = b.Q4Cache(dev(t.kc), dev(t.vc), dev(t.kp), dev(t.vp), DT[t.dt])
+    check(t, torch.ones(1, 2, D, dtype=DT[t.dt]), 0.125, num_ctas=num_ctas)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scales", [(1e-6, 1e-6), (1e-4, 1e-4), (1e-4, 1000.0), (1000.0, 1e-4), (60000.0, 1e-6)])
+def test_tiny_and_mixed_scales(scales, D):
+    # even and odd groups of different orders, with minima of their own order
+    NG = D // 32
+    t = Batch(3, [300, 17], 2, D, 16)
+    rng = np.random.default_rng(2)
+    for g in range(NG):
+        s = rng.uniform(0.3, 1.0, t.vp[:, :, g].shape) * scales[g % 2]
+        live = ~np.isnan(t.vp[:, :, g])
+        t.vp[:, :, g][live] = s[live].astype(np.float16)
+        t.vp[:, :, NG + g][live] = (-7.5 * np.minimum(s, 8000))[live].astype(np.float16)
+    t.cache = b.Q4Cache(dev(t.kc), dev(t.vc), dev(t.kp), dev(t.vp), DT[t.dt])
+    for std in (0.01, 1.0):
+        check(t, randn((2, 8, D), t.dt, 4, std), 1 / math.sqrt(D))
+
+
+def test_scales_that_grow_from_tiny_to_large():
+    t = Batch(7, [640], 1, 64, 16)
+    for i, blk in enumerate(t.tab[0, :40]):
+        t.vp[blk] = (t.vp[blk].astype(np.float64) * 2.0 ** (i - 22)).clip(-60000, 60000).astype(np.float16)
+    t.cache = b.Q4Cache(dev(t.kc), dev(t.vc), dev(t.kp), dev(t.vp), DT[t.dt])
+    for c in (1, 3):
+        check(t, randn((1, 3, 64), t.dt, 0, 2.0), 0.125, num_ctas=c)
