@@ -353,7 +353,9 @@ struct Loader {
     }
 };
 
-template <int D, int LB>
+// WIDE: units of more than 4 heads. Narrower ones have half of the product's
+// columns free: columns 4..7 carry the same heads' low parts.
+template <int D, int LB, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_constant__ Q4Params p) {
     using C = Cfg<D>;
     constexpr int NG = C::NG;
@@ -374,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 
     const uint32_t ring = pkv::smem_u32(ring_all) + warp * C::kRing;
     const int g = lane >> 2, t = lane & 3;
+    const int hd = WIDE ? g : g & 3;         // head of the unit whose column this is
 
     if (a < z) {
         pkv::WdPlace at = pkv::wd_place(p.list, list, a, cost);
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             uint32_t qsum;                       // sums of q over the groups, as a B operand
             float zs0, zs1;                      // scores to log2 units, heads 2t and 2t + 1
             {
-                // lane (g, t) holds elements 32 y + 8 t .. + 7 of head g
+                // lane (g, t) holds elements 32 y + 8 t .. + 7 of its head
                 float x[NG][8], top = 0.f;
                 const bool here = ld.q_unit == at.s * p.list.U + at.u;
                 if (here) {
@@ -426,13 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
                     uint4 raw = make_uint4(0, 0, 0, 0);
-                    if (g < gca) {
+                    if (hd < gca) {
                         if (here)
-                            pkv::lds_u32x4(ld.q_buf + g * (D * 2) + 64 * y + 16 * t, raw.x, raw.y, raw.z, raw.w);
+                            pkv::lds_u32x4(ld.q_buf + hd * (D * 2) + 64 * y + 16 * t, raw.x, raw.y, raw.z, raw.w);
                         else
                             raw = __ldg(reinterpret_cast<const uint4 *>(
                                 static_cast<const uint16_t *>(p.q) +
-                                ((size_t)at.s * p.o.Hq + h0 + g) * D + 32 * y + 8 * t));
+                                ((size_t)at.s * p.o.Hq + h0 + hd) * D + 32 * y + 8 * t));
                     }
                     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                // ---- weights as pairs, transposed: lane (g, t) has head g, tokens 4t .. 4t + 3
+                // ---- weights as pairs, transposed: lane (g, t) has its head, tokens 4t .. 4t + 3
                 uint32_t ph[2], pl[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -651,6 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     ph[i] = transpose8(as_u32(hi));
                     pl[i] = transpose8(as_u32(__floats2half2_rn(w0 - f.x, w1 - f.y)));
                 }
+                // narrow units: a column has the high parts or the low ones
+                const uint32_t low = WIDE || g >= 4 ? ~0u : 0u;
+                const uint32_t pc[2] = {WIDE || g < 4 ? ph[0] : pl[0], WIDE || g < 4 ? ph[1] : pl[1]};
+                const uint32_t pm[2] = {ph[0] & low, ph[1] & low};
+                pl[0] &= low, pl[1] &= low;
                 // ---- V: rows of the product are d, its contracted index the tokens
                 uint32_t v01[NG], v23[NG];
                 {
@@ -678,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     // row of ones as row 8
                     uint32_t m01, m23;
                     lds64(pv + vm_at + half * 32, m01, m23);
-                    mma16(accx, m01, one, m23, one, ph[0], ph[1]);
-                    mma16(accx, m01, one, m23, one, pl[0], pl[1]);
+                    mma16(accx, m01, one, m23, one, pc[0], pc[1]);
+                    if (WIDE) mma16(accx, m01, one, m23, one, pl[0], pl[1]);
                 }
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
@@ -687,7 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     lds64(pv + y * (2 * kSub) + half * 32 + t * 8, vs0, vs1);
                     const __half2 m2 = y & 1 ? __high2half2(as_h2(vm[y / 2])) : __low2half2(as_h2(vm[y / 2]));
                     const __half2 s01 = __hmul2(as_h2(vs0), m2), s23 = __hmul2(as_h2(vs1), m2);
-                    const __half2 h01 = __hmul2(as_h2(ph[0]), s01), h23 = __hmul2(as_h2(ph[1]), s23);
+                    // high parts of the products, then what they leave (narrow units:
+                    // in a column of high parts nothing is taken off or added)
+                    const __half2 h01 = __hmul2(as_h2(pm[0]), s01), h23 = __hmul2(as_h2(pm[1]), s23);
                     const uint32_t l01 = as_u32(__hfma2(as_h2(pl[0]), s01, __hfma2(as_h2(ph[0]), s01, __hneg2(h01))));
                     const uint32_t l23 = as_u32(__hfma2(as_h2(pl[1]), s23, __hfma2(as_h2(ph[1]), s23, __hneg2(h23))));
 #pragma unroll
@@ -695,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                         const uint32_t wa = v01[y], wb = v23[y], code = 0x00f000f0u;
                         const uint32_t a0 = (k ? wa >> 4 : wa << 4) & code, a1 = (k ? wa >> 8 : wa) & code;
                         const uint32_t a2 = (k ? wb >> 4 : wb << 4) & code, a3 = (k ? wb >> 8 : wb) & code;
-                        mma16(acc[y][k], a0, a1, a2, a3, as_u32(h01), as_u32(h23));
+                        if (WIDE) mma16(acc[y][k], a0, a1, a2, a3, as_u32(h01), as_u32(h23));
                         mma16(acc[y][k], a0, a1, a2, a3, l01, l23);
                     }
                 }
@@ -714,6 +724,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             // ---- the unit's output, or a piece of it
             const bool whole = at.i == 0 && count == n;
             const int slot = at.i ? 0 : 1;       // i > 0: it began before this warp's part
+            if (!WIDE) {                         // high and low parts
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    accx[i] += __shfl_xor_sync(~0u, accx[i], 2);
+#pragma unroll
+                    for (int y = 0; y < NG; ++y)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) acc[y][k][i] += __shfl_xor_sync(~0u, acc[y][k][i], 2);
+                }
+            }
             const float l0 = __shfl_sync(~0u, accx[2], t), l1 = __shfl_sync(~0u, accx[3], t);
             const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
             // a piece of a unit that goes on in the next warp lies in this
@@ -771,8 +791,8 @@ size_t smem_bytes(int GC) {
     return (size_t)kWarps * (Cfg<D>::kRing + GC * D * 2 + (pieces_on_chip(GC, D) ? GC * D * sizeof(float) : 0));
 }
 
-template <int D, int LB>
-cudaError_t launch(const Q4Params &p, cudaStream_t stream) {
+template <int D, int LB, bool WIDE>
+cudaError_t launch_width(const Q4Params &p, cudaStream_t stream) {
     // the attribute is per device and idempotent; set once for each
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
@@ -780,12 +800,17 @@ cudaError_t launch(const Q4Params &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        const size_t most = smem_bytes<D>(4) > smem_bytes<D>(kHeads) ? smem_bytes<D>(4) : smem_bytes<D>(kHeads);
-        e = cudaFuncSetAttribute(decode_q4_kernel<D, LB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        e = cudaFuncSetAttribute(decode_q4_kernel<D, LB, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem_bytes<D>(WIDE ? kHeads : 4));
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_chained(decode_q4_kernel<D, LB>, dim3((unsigned)p.C), kThreads, smem_bytes<D>(p.o.GC), stream, p);
+    return launch_chained(decode_q4_kernel<D, LB, WIDE>, dim3((unsigned)p.C), kThreads, smem_bytes<D>(p.o.GC), stream, p);
+}
+
+template <int D, int LB>
+cudaError_t launch(const Q4Params &p, cudaStream_t stream) {
+    return p.o.GC > 4 ? launch_width<D, LB, true>(p, stream) : launch_width<D, LB, false>(p, stream);
 }
 
 bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
