@@ -12,9 +12,12 @@
 // Products. S = Q K^T with the unit's (up to 8) q heads as rows 0..7 of the
 // m16n8k16's m: then a lane's scores are already where the next product wants
 // its weights, and rows 8..15 carry the weights' low parts: O = [P_hi; P_lo] V
-// costs nothing more than P_hi V, and weights keep 16 (bf16) or 22 (fp16) bits.
-// Softmax in base 2 in fp32, with a reference exponent that moves only when a
-// score passes it by more than 8.
+// costs nothing more than P_hi V, and weights keep 16 (bf16, half a step 2^-17: a
+// third part would be another product) or 22 (fp16) bits. Softmax in base 2 in
+// fp32, with a reference exponent that moves only when a score passes what the
+// type holds: fp16 weights stand as high as they can, the top one at 2^10 to
+// 2^15, so that a light token keeps its bits down to 2^-35 of the top. The
+// denominator sums the weights as they enter the product.
 //
 // What bounds it: HBM, 4 D bytes a token. 10 warps keep two subtiles each in
 // flight or in use, 160 KB an SM, and the pieces that they leave fit beside the
@@ -52,6 +55,11 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kFewSeqs = 1024, kMaxSeqs = pkv::kRowsMaxSeqs;
 constexpr int kUnitCost = 2;         // what a unit costs a warp besides its subtiles, in subtiles
 constexpr float kNone = pkv::kWdNone;
+// Exponent that a reference gives the top score, and the largest that needs no new one.
+template <typename T> constexpr float kTop = 0.f;
+template <> constexpr float kTop<__half> = 10.f;
+template <typename T> constexpr float kRoom = 8.f;
+template <> constexpr float kRoom<__half> = 15.f;
 
 struct RowsParams {
     pkv::WdList list;
@@ -274,11 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_rows_kernel(const __grid_c
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                     const bool none = mu == kNone;
                     float nm = mu;
-                    if (top > -INFINITY) nm = none ? top : fmaxf(mu, top);
+                    if (top > -INFINITY) nm = none ? top - kTop<T> : fmaxf(mu, top - kTop<T>);
                     const float f = none ? 1.f : wd_ex2(mu - nm);
                     // a head that has had no score but -infinity keeps none,
                     // and the next subtile asks again
-                    room = __any_sync(~0u, nm == kNone) ? -INFINITY : 8.f;
+                    room = __any_sync(~0u, nm == kNone) ? -INFINITY : kRoom<T>;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = e[i] + mu - nm;
                     mu = nm;
@@ -289,12 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_rows_kernel(const __grid_c
                         for (int i = 0; i < 4; ++i) acc[j][i] *= f;
                 }
                 // ---- weights: high parts in rows 0..7, low parts in rows 8..15
-                float w[4], r0, r1, r2, r3, x, y;
+                float w[4], r0, r1, r2, r3, x0, x1, x2, x3;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = wd_ex2(e[i]);
-                l += (w[0] + w[1]) + (w[2] + w[3]);
                 const uint32_t a0 = E::pack2(w[0], w[1], r0, r1), a2 = E::pack2(w[2], w[3], r2, r3);
-                const uint32_t a1 = E::pack2(w[0] - r0, w[1] - r1, x, y), a3 = E::pack2(w[2] - r2, w[3] - r3, x, y);
+                const uint32_t a1 = E::pack2(w[0] - r0, w[1] - r1, x0, x1), a3 = E::pack2(w[2] - r2, w[3] - r3, x2, x3);
+                l += ((r0 + x0) + (r1 + x1)) + ((r2 + x2) + (r3 + x3));
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     uint32_t b0, b1, b2, b3;
