@@ -28,8 +28,8 @@
  * The angle of a far position would lose its low bits in fp32, so the plan
  * holds each w_i as a fraction of a turn in 64-bit fixed point: position times
  * fraction modulo 2^64 is the angle modulo one turn, without rounding. The
- * fraction itself is off by at most 2^-53 of its value (it is computed in
- * double), 2^-32 turns at position 2^21.
+ * fraction itself is off by a few roundings of 2^-53 of its value (it is
+ * computed in double) and 2^-65, below 2^-30 turns at position 2^21.
  */
 #ifndef PKV_ROPE_H
 #define PKV_ROPE_H

@@ -307,7 +307,7 @@ pkv_status pkv_rope_plan_init(const pkv_rope_desc *d, pkv_rope_plan *plan) {
         // a fraction of a turn; whole turns (factors below 1) drop out
         double turns = w / kTwoPi;
         turns -= floor(turns);
-        plan->turns[i] = (uint64_t)ldexp(turns, 63) << 1;
+        plan->turns[i] = (uint64_t)rint(ldexp(turns, 64));      // (turns < 1: below 2^64)
     }
     return PKV_OK;
 }
