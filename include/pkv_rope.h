@@ -23,7 +23,7 @@
  *                    lo = max(floor d(beta_fast), 0), hi = min(ceil d(beta_slow),
  *                    rotary_dim - 1), u = clamp((i - lo) / max(hi - lo, 0.001), 0, 1):
  *                    (1 - u) w_i + u w_i / f; amplitude attention_factor, or
- *                    0.1 ln(f) + 1 where that is 0
+ *                    0.1 ln(f) + 1 where that is 0 (1 for f <= 1)
  *
  * The angle of a far position would lose its low bits in fp32, so the plan
  * holds each w_i as a fraction of a turn in 64-bit fixed point: position times

@@ -74,7 +74,7 @@ def rope_frequencies(rotary_dim, base, scaling="none", factor=1.0, original_len=
             u = min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001)))
             w = (1 - u) * w + u * w / factor
         out.append(w)
-    amp = (attention_factor or 0.1 * math.log(factor) + 1) if scaling == "yarn" else 1.0
+    amp = (attention_factor or 0.1 * math.log(max(1.0, factor)) + 1) if scaling == "yarn" else 1.0
     return np.array(out), amp
 
 

@@ -286,7 +286,7 @@ pkv_status pkv_rope_plan_init(const pkv_rope_desc *d, pkv_rope_plan *plan) {
     plan->layout = d->layout;
     plan->amplitude = 1.f;
     if (sc == PKV_ROPE_YARN)
-        plan->amplitude = (float)(d->attention_factor != 0 ? d->attention_factor : 0.1 * log(f) + 1);
+        plan->amplitude = (float)(d->attention_factor != 0 ? d->attention_factor : f > 1 ? 0.1 * log(f) + 1 : 1);
     for (int i = 0; i < rd / 2; ++i) {
         double w = pow(base, -2.0 * i / rd), t;
         switch (sc) {

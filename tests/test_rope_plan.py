@@ -26,3 +26,11 @@ def test_turns_are_rounded(base, rd):
         odd += p.turns[i] & 1
     if base >= 1e15:
         assert odd                                   # the last bit is in use
+
+
+@pytest.mark.parametrize("factor,amplitude", [(0.25, 1.0), (1.0, 1.0), (math.e ** 2, 1.2), (16.0, 0.1 * math.log(16) + 1)])
+def test_yarn_amplitude(factor, amplitude):
+    # only a longer context raises it
+    kw = dict(scaling="yarn", factor=factor, original_len=4096)
+    assert b.RopePlan(64, **kw).c.amplitude == pytest.approx(amplitude, rel=2.0 ** -23)
+    assert b.RopePlan(64, attention_factor=0.7, **kw).c.amplitude == pytest.approx(0.7, rel=2.0 ** -23)
