@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 bool misaligned(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
 template <typename T>
-cudaError_t launch(RopeParams &p, cudaStream_t stream) {
+cudaError_t launch(RopeParams &p, int sms, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const int rd = p.plan.rotary_dim;
     const bool vectors = rd % (2 * V) == 0 || (p.plan.layout == PKV_ROPE_INTERLEAVED && rd % V == 0);
@@ -189,7 +189,7 @@ cudaError_t launch(RopeParams &p, cudaStream_t stream) {
     const int items = heads * (vectors ? p.D * (int)sizeof(T) / 32 : p.D / 2);
     // few tokens: several CTAs a token, one item a thread
     int parts = (items + kThreads - 1) / kThreads;
-    const int wanted = 2 * 152 / (p.T < 2 * 152 ? p.T : 2 * 152);
+    const int wanted = 2 * sms / (p.T < 2 * sms ? p.T : 2 * sms);
     if (parts > wanted) parts = wanted;
     p.parts = parts;
     const dim3 grid((unsigned)(p.T * parts));
@@ -199,9 +199,12 @@ cudaError_t launch(RopeParams &p, cudaStream_t stream) {
 
 pkv_status run(int dtype, RopeParams &p, void *stream) {
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == PKV_F32   ? launch<float>(p, s)
-                          : dtype == PKV_F16 ? launch<__half>(p, s)
-                                             : launch<__nv_bfloat16>(p, s);
+    int sms = 0;
+    const pkv_status st = pkv::device_sm_count(&sms);
+    if (st != PKV_OK) return st;
+    const cudaError_t e = dtype == PKV_F32   ? launch<float>(p, sms, s)
+                          : dtype == PKV_F16 ? launch<__half>(p, sms, s)
+                                             : launch<__nv_bfloat16>(p, sms, s);
     if (e != cudaSuccess)
         return pkv::set_last_error(PKV_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
     return PKV_OK;
