@@ -63,11 +63,7 @@ struct WdShare {
     int cost, NV, CT, A, Z, a, z;
 };
 
-// A subtile's place: sequence, unit, subtile of the unit; places of a unit of
-// the sequence; place of the unit's first subtile.
-struct WdPlace {
-    int s, u, i, nv, tu;
-};
+using WdPlace = SplitPlace;
 
 // Lengths, their prefixes, zeros for empty contexts, and this warp's share (a
 // CTA without work gets an empty one: CT <= its index). SUB tokens a subtile.
@@ -154,20 +150,11 @@ __device__ __forceinline__ WdShare wd_share(const WdList &p, const WdOut &o, int
     const int cta = blockIdx.x, units = sh.nonempty[N] * p.U;
     r.NV = sh.prefix[N] * p.U;
     r.A = r.Z = r.a = r.z = 0;
-    if (r.cost == 0 && units <= (int)gridDim.x && longest <= split_one_cta(W)) {
+    if (split_units_alone(r.cost, units, longest, (int)gridDim.x, W)) {
         // a unit for each CTA
         r.CT = units;
         if (cta >= r.CT) return r;
-        int lo = 0, hi = p.S - 1;                    // the last sequence with at most k before it
-        const int k = cta / p.U;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (sh.nonempty[mid] <= k) lo = mid;
-            else hi = mid - 1;
-        }
-        const int n = sh.prefix[lo + 1] - sh.prefix[lo];
-        r.A = sh.prefix[lo] * p.U + (cta - k * p.U) * n;
-        r.Z = r.A + n;
+        split_unit_share(sh.prefix, split_unit_sequence(sh.nonempty, p.S, p.U, cta), p.U, cta, r.A, r.Z);
     } else {
         r.CT = split_active_ctas(r.NV, (int)gridDim.x, W, r.cost);
         if (cta >= r.CT) return r;
@@ -182,38 +169,17 @@ __device__ __forceinline__ WdShare wd_share(const WdList &p, const WdOut &o, int
 // The first subtile at or after place a.
 template <int W, int N>
 __device__ __forceinline__ WdPlace wd_place(const WdList &p, const WdListShared<W, N> &sh, int a, int cost) {
-    // the last sequence whose units begin at or before it (of equal prefixes,
-    // the empty sequences come first)
-    int lo = 0;
-    for (int n = p.S; n > 1;) {          // 32 ways at a time
-        const int step = (n + 31) / 32, lane = threadIdx.x & 31;
-        const bool at_or_before = lane * step < n && sh.prefix[lo + lane * step] * p.U <= a;
-        const int skip = (__popc(__ballot_sync(~0u, at_or_before)) - 1) * step;
-        lo += skip;
-        n = min(step, n - skip);
-    }
-    WdPlace w;
-    w.nv = sh.prefix[lo + 1] - sh.prefix[lo];
-    const int r = a - sh.prefix[lo] * p.U;
-    w.s = lo;
-    w.u = r / w.nv;
-    w.tu = a - (r - w.u * w.nv) + cost;
-    w.i = max(0, a - w.tu);
-    return w;
+    const int lane = threadIdx.x & 31;
+    const int s = split_sequence(p.S, [&](int lo, int n, int step) {
+        return __popc(__ballot_sync(~0u, lane * step < n && sh.prefix[lo + lane * step] * p.U <= a));
+    });
+    return split_place(sh.prefix, s, p.U, a, cost);
 }
 
 // The next unit, if its first subtile lies before place z.
 template <int W, int N>
 __device__ __forceinline__ bool wd_next_unit(const WdList &p, const WdListShared<W, N> &sh, WdPlace &w, int z) {
-    w.i = 0;
-    w.tu += w.nv;
-    if (w.tu >= z) return false;
-    if (++w.u == p.U) {
-        w.u = 0;
-        do ++w.s; while (sh.len[w.s] == 0);          // (there is one: the list goes on)
-        w.nv = sh.prefix[w.s + 1] - sh.prefix[w.s];
-    }
-    return true;
+    return split_next_unit(sh.prefix, sh.len, p.U, w, z);
 }
 
 // ---------------------------------------------------------------- rows of E = D / 32 elements a lane
