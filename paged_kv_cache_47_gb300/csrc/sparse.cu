@@ -100,12 +100,13 @@ __global__ void __launch_bounds__(kMeanThreads) block_means_kernel(const MeansPa
         const int64_t tok = r / p.Hk;
         const int g = (int)(r - tok * p.Hk);
         const int64_t slot = p.slots[tok];
-        if (slot < 0 || slot % p.B != p.B - 1) continue;
+        if (slot < 0) continue;
         const int64_t blk = slot / p.B;
         if (blk >= p.NB) {
             if (lane == 0 && g == 0) atomicOr(p.err, PKV_DEVERR_SLOT);
             continue;
         }
+        if (slot - blk * p.B != p.B - 1) continue;
         const int64_t chunk = blk * p.Hk + g;
         const Part *src = reinterpret_cast<const Part *>(static_cast<const T *>(p.k) + chunk * p.B * D) + lane;
         float sum[E];
