@@ -6,6 +6,7 @@ these functions raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -993,7 +994,8 @@ class PreparedCall:
     """A call whose arguments are checked and marshalled once, for repeated steps on stable
     buffers (the usual serving loop, and CUDA-graph capture): each call only passes the stream
     (None: the current one) and returns `out`. The buffers are kept alive by this object and
-    rewritten in place by the caller between steps."""
+    rewritten in place by the caller between steps. Outputs and workspaces that the caller did
+    not give are made on the stream that was current at construction."""
 
     def __init__(self, name: str, args, keep, out=None, after=()):
         self._fn = getattr(_ops_lib(), name)
@@ -1020,6 +1022,16 @@ class PreparedCall:
             if status:
                 _check(status)
         return self.out
+
+
+def _on(stream, device):
+    """For one-shot calls: what they allocate (outputs, zero-filled workspaces) is made on the stream
+    that the call runs on, so that it is filled before and not handed on before the call is done."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    return torch.cuda.stream(stream)
 
 
 def _raw_stream(device: int) -> int:
@@ -1191,7 +1203,8 @@ def rope(q, k, positions, plan: RopePlan, q_out: Optional[torch.Tensor] = None,
          k_out: Optional[torch.Tensor] = None, stream=None):
     """q [T][Hq][D] and k [T][Hk][D] (token-strided views allowed) turned to their positions
     (int32 [T]); into new tensors unless q_out / k_out are given (q and k themselves allowed)."""
-    return prepared_rope(q, k, positions, plan, q_out, k_out)(stream)
+    with _on(stream, q.device):
+        return prepared_rope(q, k, positions, plan, q_out, k_out)(stream)
 
 
 def prepared_rope_append(q, k_new, v_new, positions, slot_mapping, plan: RopePlan, k_pool, v_pool,
@@ -1220,8 +1233,9 @@ def rope_append(q, k_new, v_new, positions, slot_mapping, plan: RopePlan, k_pool
                 q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rope and append in one launch (pkv_rope_append): returns the turned q; the turned k and
     v go to slot_mapping [T] (int64). q, k_new, v_new: [T][heads][D], token-strided views allowed."""
-    return prepared_rope_append(q, k_new, v_new, positions, slot_mapping, plan, k_pool, v_pool,
-                                q_out)(stream)
+    with _on(stream, q.device):
+        return prepared_rope_append(q, k_new, v_new, positions, slot_mapping, plan, k_pool, v_pool,
+                                    q_out)(stream)
 
 
 # --------------------------------------------------------------------- 4-bit KV cache
@@ -1312,7 +1326,8 @@ def prepared_gather_q4(slot_mapping, cache: Q4Cache, k_out: Optional[torch.Tenso
 def gather_q4(slot_mapping, cache: Q4Cache, k_out: Optional[torch.Tensor] = None,
               v_out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, stream=None):
     """The cached rows at slot_mapping [T] as values: (k, v) [T][Hk][D]."""
-    return prepared_gather_q4(slot_mapping, cache, k_out, v_out, out_dtype)(stream)
+    with _on(stream, slot_mapping.device):
+        return prepared_gather_q4(slot_mapping, cache, k_out, v_out, out_dtype)(stream)
 
 
 def q4_workspace_bytes(cache: Q4Cache, num_q_heads: int, num_ctas: int = 0) -> int:
@@ -1367,8 +1382,9 @@ def decode_attention_q4(q, cache: Q4Cache, block_tables, context_lens, scale: fl
                         lse_out: Optional[torch.Tensor] = None, tables_ready: bool = False,
                         timing_events: Optional[Sequence] = None) -> torch.Tensor:
     """decode_attention over a 4-bit cache; q [S][Hq][D] in the cache's activation dtype."""
-    return prepared_decode_attention_q4(q, cache, block_tables, context_lens, scale, out, out_dtype,
-                                        workspace, num_ctas, lse_out, tables_ready, timing_events)(stream)
+    with _on(stream, q.device):
+        return prepared_decode_attention_q4(q, cache, block_tables, context_lens, scale, out, out_dtype,
+                                            workspace, num_ctas, lse_out, tables_ready, timing_events)(stream)
 
 
 def block_copy_q4(pairs, cache: Q4Cache, stream=None) -> None:
@@ -1452,8 +1468,9 @@ def select_blocks(q, k_pool, k_means, block_tables, context_lens, top_blocks: in
     """(sel_tables [S][Hk][W], sel_lens [S][Hk]): the blocks each kv head of each sequence reads
     (pkv_select_blocks), as tables over the pool viewed as [NB * Hk][1][B][D]. k_pool gives the
     shape only."""
-    return prepared_select_blocks(q, k_pool, k_means, block_tables, context_lens, top_blocks,
-                                  first_blocks, last_blocks, sel_tables, sel_lens, workspace)(stream)
+    with _on(stream, q.device):
+        return prepared_select_blocks(q, k_pool, k_means, block_tables, context_lens, top_blocks,
+                                      first_blocks, last_blocks, sel_tables, sel_lens, workspace)(stream)
 
 
 def alloc_sparse_workspace(k_pool, num_seqs: int, num_q_heads: int, max_blocks_per_seq: int) -> torch.Tensor:
@@ -1499,6 +1516,7 @@ def decode_attention_sparse(q, k_pool, v_pool, k_means, block_tables, context_le
                             workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Decode attention over the blocks that the block means select for each (sequence, kv head):
     the top_blocks best, the first_blocks first and the last_blocks last (pkv_sparse.h)."""
-    return prepared_decode_attention_sparse(q, k_pool, v_pool, k_means, block_tables, context_lens,
-                                            scale, top_blocks, first_blocks, last_blocks, out,
-                                            out_dtype, sel_tables, sel_lens, workspace)(stream)
+    with _on(stream, q.device):
+        return prepared_decode_attention_sparse(q, k_pool, v_pool, k_means, block_tables, context_lens,
+                                                scale, top_blocks, first_blocks, last_blocks, out,
+                                                out_dtype, sel_tables, sel_lens, workspace)(stream)
