@@ -999,13 +999,7 @@ class PreparedCall:
 
     def __init__(self, name: str, args, keep, out=None, after=()):
         self._fn = getattr(_ops_lib(), name)
-        devices = {t.device for t in keep if isinstance(t, torch.Tensor)}
-        for c in keep:
-            if isinstance(c, Q4Cache):
-                devices |= {t.device for t in (c.k_codes, c.v_codes, c.k_params, c.v_params)}
-        if len(devices) != 1 or next(iter(devices)).type != "cuda":
-            raise ValueError(f"{name}: the tensors are not on one GPU ({sorted(map(str, devices))})")
-        self._device = next(iter(devices)).index
+        self._device = _one_gpu(name, keep)
         # plain numbers become ctypes objects once, not at each call
         kinds = self._fn.argtypes
         self._args = tuple(k(a) if a is None or isinstance(a, (int, float)) else a
@@ -1022,6 +1016,17 @@ class PreparedCall:
             if status:
                 _check(status)
         return self.out
+
+
+def _one_gpu(name: str, keep) -> int:
+    """The GPU that all tensors and caches of a call lie on."""
+    devices = {t.device for t in keep if isinstance(t, torch.Tensor)}
+    for c in keep:
+        if isinstance(c, Q4Cache):
+            devices |= {t.device for t in (c.k_codes, c.v_codes, c.k_params, c.v_params)}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError(f"{name}: the tensors are not on one GPU ({sorted(map(str, devices))})")
+    return next(iter(devices)).index
 
 
 def _on(stream, device):
@@ -1391,8 +1396,9 @@ def block_copy_q4(pairs, cache: Q4Cache, stream=None) -> None:
     """Copy whole blocks src -> dst of a 4-bit cache; pairs is host data [n][2]."""
     p = torch.as_tensor(pairs, dtype=torch.int64).reshape(-1, 2).contiguous()
     assert p.device.type == "cpu", "block-copy pairs are host memory"
-    _check(_ops_lib().pkv_block_copy_q4(ctypes.byref(cache.desc), _ptr(p), p.shape[0],
-                                        ctypes.byref(cache.pools), _stream(stream)))
+    with torch.cuda.device(_one_gpu("pkv_block_copy_q4", (cache,))):
+        _check(_ops_lib().pkv_block_copy_q4(ctypes.byref(cache.desc), _ptr(p), p.shape[0],
+                                            ctypes.byref(cache.pools), _stream(stream)))
 
 
 # ---------------------------------------------------------------- block-sparse decode
