@@ -771,19 +771,25 @@ size_t selection_decode_bytes(const pkv_cache_desc *c, int Hq) {
     return (n + 15) / 16 * 16;
 }
 
-pkv_status check_select(const pkv_cache_desc *c, int32_t S, int32_t Hq, int32_t M) {
+pkv_status check_batch(const pkv_cache_desc *c, int32_t S, int32_t M) {
     pkv_status st = pkv::check_cache_desc(c);
     if (st != PKV_OK) return st;
     if (S < 0) return pkv::set_last_error(PKV_ERR_INVALID_ARG, "num_seqs %d", S);
-    if (Hq < 1 || Hq % c->num_kv_heads)
-        return pkv::set_last_error(PKV_ERR_INVALID_ARG,
-                                   "num_q_heads %d is not a positive multiple of num_kv_heads %d", Hq,
-                                   c->num_kv_heads);
     if (M < 1) return pkv::set_last_error(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d", M);
     if ((int64_t)c->num_blocks * c->num_kv_heads > INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");
     if ((int64_t)M * c->block_size > INT32_MAX || (int64_t)S * c->num_kv_heads > INT32_MAX / 64)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
+    return PKV_OK;
+}
+
+pkv_status check_select(const pkv_cache_desc *c, int32_t S, int32_t Hq, int32_t M) {
+    const pkv_status st = check_batch(c, S, M);
+    if (st != PKV_OK) return st;
+    if (Hq < 1 || Hq % c->num_kv_heads)
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG,
+                                   "num_q_heads %d is not a positive multiple of num_kv_heads %d", Hq,
+                                   c->num_kv_heads);
     return PKV_OK;
 }
 
@@ -829,7 +835,7 @@ pkv_status pkv_block_means(const pkv_cache_desc *cache, const int64_t *slot_mapp
 
 size_t pkv_select_workspace_bytes(const pkv_cache_desc *cache, int32_t num_seqs,
                                   int32_t max_blocks_per_seq) {
-    if (pkv::check_cache_desc(cache) != PKV_OK || num_seqs < 0 || max_blocks_per_seq < 1) return 0;
+    if (check_batch(cache, num_seqs, max_blocks_per_seq) != PKV_OK) return 0;
     const size_t n = score_bytes(cache, num_seqs, max_blocks_per_seq);
     return n ? n : 16;
 }
