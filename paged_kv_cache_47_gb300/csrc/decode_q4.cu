@@ -144,6 +144,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 
+// Two codes as operands, of bits 0..3 and of bits 4..7 of a word's halves: the
+// former multiplied by 16, where a shift would wait for the pipe of the ANDs.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
+    return as_u32(__hmul2(as_h2(w & 0x000f000fu), __float2half2_rn(16.f)));
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return w & 0x00f000f0u; }
+
 __device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
@@ -556,9 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
                     float d[4];
-                    const uint32_t wa = w[0][y], wb = w[1][y], code = 0x00f000f0u;
-                    mma16_zero(d, wa << 4 & code, wb << 4 & code, wa & code, wb & code, qb[y][0][0], qb[y][0][1]);
-                    mma16(d, wa >> 4 & code, wb >> 4 & code, wa >> 8 & code, wb >> 8 & code, qb[y][1][0], qb[y][1][1]);
+                    uint32_t wa = w[0][y], wb = w[1][y];
+                    mma16_zero(d, low_codes(wa), low_codes(wb), high_codes(wa), high_codes(wb), qb[y][0][0], qb[y][0][1]);
+                    wa >>= 8;
+                    wb >>= 8;
+                    mma16(d, low_codes(wa), low_codes(wb), high_codes(wa), high_codes(wb), qb[y][1][0], qb[y][1][1]);
                     x[0] = fmaf(d[0], s0[y], x[0]);
                     x[1] = fmaf(d[1], s0[y], x[1]);
                     x[2] = fmaf(d[2], s1[y], x[2]);
@@ -702,9 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     const uint32_t l23 = as_u32(__hfma2(as_h2(pl[1]), s23, __hfma2(as_h2(ph[1]), s23, __hneg2(h23))));
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint32_t wa = v01[y], wb = v23[y], code = 0x00f000f0u;
-                        const uint32_t a0 = (k ? wa >> 4 : wa << 4) & code, a1 = (k ? wa >> 8 : wa) & code;
-                        const uint32_t a2 = (k ? wb >> 4 : wb << 4) & code, a3 = (k ? wb >> 8 : wb) & code;
+                        const uint32_t wa = v01[y] >> (8 * k), wb = v23[y] >> (8 * k);
+                        const uint32_t a0 = low_codes(wa), a1 = high_codes(wa), a2 = low_codes(wb), a3 = high_codes(wb);
                         if (WIDE) mma16(acc[y][k], a0, a1, a2, a3, as_u32(h01), as_u32(h23));
                         mma16(acc[y][k], a0, a1, a2, a3, l01, l23);
                     }
