@@ -88,9 +88,14 @@ size_t pkv_decode_q4_workspace_bytes(const pkv_q4cache_desc *cache, int32_t num_
  * use, not shared by calls that may overlap) and errors as there. A
  * row that holds NaN parameters gives NaN where it is attended to; rows past a
  * context's length are not used, whatever they hold. options: num_ctas,
- * tables_ready, lse_out and timing_events apply; pending_tail is accepted and
- * every other read waits for the preceding kernel; consumer 1 (CUDA-core math)
- * is PKV_ERR_UNSUPPORTED.
+ * tables_ready (not with tables that pkv_tables_append wrote on the stream),
+ * lse_out and timing_events apply; pending_tail is accepted and every other read
+ * waits for the preceding kernel; consumer 1 (CUDA-core math) is
+ * PKV_ERR_UNSUPPORTED.
+ *
+ * Sums are in fp32. Operands of fewer bits: weights, weights times V scales and
+ * the sums of q that meet the minima are pairs of fp16 (22 bits); q times a power
+ * of two is one fp16, exact for elements down to 2^-28 of the head's largest.
  */
 pkv_status pkv_decode_attention_q4(const pkv_q4cache_desc *cache, const void *q, int32_t num_seqs,
                                    int32_t num_q_heads, const pkv_q4cache_pools *pools,

@@ -16,7 +16,9 @@
  * ties going to the lower j, a NaN counting as +infinity. Scores are computed
  * in fp32 in one stated order, so that equal inputs select equal blocks:
  * products of eight neighbouring elements are added one after another, then
- * neighbouring sums in pairs, again and again.
+ * neighbouring sums in pairs, again and again. (16-bit types: product and
+ * addition are one fused step, which is the same wherever a product is a normal
+ * fp32 number; fp32: two steps.)
  *
  * The selection is written as a block table of its own: sel_tables[s][g]
  * lists, in ascending j, tab[s][j] * num_kv_heads + g, then -1 up to
@@ -67,8 +69,8 @@ size_t pkv_select_workspace_bytes(const pkv_cache_desc *cache, int32_t num_seqs,
  * q: [num_seqs][num_q_heads][head_dim] in the cache's dtype. sel_tables: int32
  * [num_seqs][num_kv_heads][W]; sel_lens: int32 [num_seqs][num_kv_heads]. A
  * context length out of range is clamped and sets PKV_DEVERR_CONTEXT; a block
- * id out of range scores 0, is listed as -1 if selected and sets
- * PKV_DEVERR_BLOCK_ID. num_blocks * num_kv_heads must stay below 2^31.
+ * id out of range scores as a mean of zeros does, is listed as -1 if selected
+ * and sets PKV_DEVERR_BLOCK_ID. num_blocks * num_kv_heads must stay below 2^31.
  */
 pkv_status pkv_select_blocks(const pkv_cache_desc *cache, const void *q, int32_t num_seqs,
                              int32_t num_q_heads, const void *k_means,

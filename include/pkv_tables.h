@@ -37,6 +37,12 @@
  * is (release).
  *
  * Calls on one state are ordered by the caller (one stream, or events).
+ *
+ * The tables, lengths and slots that these calls write are never "ready" in the
+ * sense of pkv_decode_options.tables_ready or pkv_append_options.inputs_ready
+ * for a call that follows on the stream, even with other calls in between: each
+ * kernel lets the next one start before it has itself waited, so a chain of
+ * them may run at once. A step made of them leaves both options 0.
  */
 #ifndef PKV_TABLES_H
 #define PKV_TABLES_H
