@@ -40,11 +40,20 @@
 // group's bound: most subtiles need one vote instead of a reduction over lanes
 // and a rescale of the accumulators. V scales are brought to at most 1 by a
 // power of two for each group, so that neither a large scale pushes light tokens,
-// other heads or other groups below fp16's range nor tiny scales lose bits. The
-// denominator is summed by the same product that weighs the minima (a row of
-// ones). Weights, and weights times V scales, are pairs of fp16 (22 bits): codes
-// are positive, so an error of the products would not cancel against the
-// minimum's share.
+// other heads or other groups below fp16's range nor tiny scales lose bits.
+// Weights, and weights times V scales, are pairs of fp16 (22 bits): codes are
+// positive, so an error of the products would not cancel against the minimum's
+// share.
+//
+// Sums over a long context. The matrix instruction cuts its sum towards zero:
+// half a last place, 4e-8, a step, always the same way, and the codes' sum and
+// the minima's cancel in the output (2000 tokens a warp: 2e-5 of either, where
+// outputs are 5e-3). So codes are added up around zero: the second half of a
+// subtile enters as 15 - c with its weights negated (an inverted mask and sign,
+// no instruction more), and 15 times its weights times scales are added at the
+// end. Minima, these and the denominator (rows of scales and of ones beside the
+// minima) are small enough to be summed for each half alone and added in fp32,
+// which rounds to nearest.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -411,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
         }
         m_at = 2 * NG + (NG == 4 ? 4 * (t & 1) : 0);                 // minima of two groups in a K row
         const uint32_t vs_at = (g & (NG - 1)) * (2 * kSub) + (g / NG & 1) * 32 + t * 8;      // scales of a group, V
-        const uint32_t vm_at = (NG + (g & (NG - 1))) * (2 * kSub) + t * 8;   // minima of a group, V
+        const uint32_t vm_at = ((g & (2 * NG - 1)) ^ NG) * (2 * kSub) + t * 8;       // minima, then scales of a group, V
+        const uint32_t minima = g & NG ? 0u : ~0u;
         const uint32_t one = g == 0 ? 0x3c003c00u : 0u;
 
         while (true) {
@@ -691,18 +701,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     }
                 }
                 {
-                    // minima as rows 0..NG-1 (rows up to 7 repeat them, unused), a
-                    // row of ones as row 8
+                    // minima as rows 0..NG-1, scales of the second half as rows
+                    // NG..2NG-1 (rows up to 7 repeat them, unused), a row of ones
+                    // as row 8
                     uint32_t m01, m23;
+                    float sums[4];
                     lds64(pv + vm_at + half * 32, m01, m23);
-                    mma16(accx, m01, one, m23, one, pc[0], pc[1]);
-                    if (WIDE) mma16(accx, m01, one, m23, one, pl[0], pl[1]);
+                    if (half == 0) m01 &= minima, m23 &= minima;
+                    mma16_zero(sums, m01, one, m23, one, pc[0], pc[1]);
+                    if (WIDE) mma16(sums, m01, one, m23, one, pl[0], pl[1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) accx[i] += sums[i];
                 }
 #pragma unroll
                 for (int y = 0; y < NG; ++y) {
                     uint32_t vs0, vs1;
                     lds64(pv + y * (2 * kSub) + half * 32 + t * 8, vs0, vs1);
-                    const __half2 m2 = y & 1 ? __high2half2(as_h2(vm[y / 2])) : __low2half2(as_h2(vm[y / 2]));
+                    __half2 m2 = y & 1 ? __high2half2(as_h2(vm[y / 2])) : __low2half2(as_h2(vm[y / 2]));
+                    if (half) m2 = __hneg2(m2);
                     const __half2 s01 = __hmul2(as_h2(vs0), m2), s23 = __hmul2(as_h2(vs1), m2);
                     // high parts of the products, then what they leave (narrow units:
                     // in a column of high parts nothing is taken off or added)
@@ -711,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                     const uint32_t l23 = as_u32(__hfma2(as_h2(pl[1]), s23, __hfma2(as_h2(ph[1]), s23, __hneg2(h23))));
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint32_t wa = v01[y] >> (8 * k), wb = v23[y] >> (8 * k);
+                        uint32_t wa = v01[y] >> (8 * k), wb = v23[y] >> (8 * k);
+                        if (half) wa = ~wa, wb = ~wb;
                         const uint32_t a0 = low_codes(wa), a1 = high_codes(wa), a2 = low_codes(wb), a3 = high_codes(wb);
                         if (WIDE) mma16(acc[y][k], a0, a1, a2, a3, as_u32(h01), as_u32(h23));
                         mma16(acc[y][k], a0, a1, a2, a3, l01, l23);
@@ -751,8 +768,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
             if (slot && !whole) __syncwarp();
 #pragma unroll
             for (int y = 0; y < NG; ++y) {
-                const float x0 = __shfl_sync(~0u, accx[0], 4 * y + t);
-                const float x1 = __shfl_sync(~0u, accx[1], 4 * y + t);
+                const float x0 = fmaf(__shfl_sync(~0u, accx[0], 4 * (NG + y) + t), 15.f, __shfl_sync(~0u, accx[0], 4 * y + t));
+                const float x1 = fmaf(__shfl_sync(~0u, accx[1], 4 * (NG + y) + t), 15.f, __shfl_sync(~0u, accx[1], 4 * y + t));
                 // one over the group's power of two, in the codes' unit
                 const float m2 = y & 1 ? __high2float(as_h2(vm[y / 2])) : __low2float(as_h2(vm[y / 2]));
                 const float up = __uint_as_float(0x7f000000u - __float_as_uint(m2)) / kCodeUnit;

@@ -164,3 +164,32 @@ def test_scales_that_grow_from_tiny_to_large():
     t.cache = b.Q4Cache(dev(t.kc), dev(t.vc), dev(t.kp), dev(t.vp), DT[t.dt])
     for c in (1, 3):
         check(t, randn((1, 3, 64), t.dt, 0, 2.0), 0.125, num_ctas=c)
+
+
+# -------------------------------------------------------------------------- long sums
+@pytest.mark.parametrize("G", [1, 5])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_sums_are_not_cut_to_one_side(D, G):
+    """Nearly equal weights over n = 8192 tokens a warp: the codes' share of an output and the minima's
+    are some 2 and cancel, so a sum that is cut towards zero at each step would show (7e-5 here). The
+    tolerance, in units u = 2^-23 of the mean |m| or scale s:
+      - sums of minima, scales and weights in fp32, two additions a subtile to nearest, N = n / 16 each:
+        errors of either sign with a deviation of u / sqrt(12) of the sum so far, sqrt(N / 3) u / sqrt(12)
+        in all; three sums, 16 warps, six deviations: 0.44 sqrt(N) u
+      - their products within a half, cut at most four times: 4 u
+      - codes around zero: n steps of up to 7.5 s, 4.7 s rms of either sign, wander to 6 times
+        4.7 s sqrt(n), of which each of n / 8 cuts takes up to u: (n / 8) 28 s / sqrt(n) u of the mean."""
+    L, NG = 131072, D // 32
+    n = L // 16
+    t = Batch(5, [L], 1, D, 32)
+    q = randn((1, G, D), t.dt, 3, 0.01)
+    k, v = O.q4_rows(t.tab[0], L, t.kc, t.vc, t.kp, t.vp)
+    want, _, _ = O.attend(q[0].double().numpy(), k, v, 0.09)
+    par = np.abs(t.vp[t.tab[0, : L // 32]].astype(np.float64)).mean((0, 1, 3))
+    s, m = np.repeat(par[:NG], 32), np.repeat(par[NG:], 32)
+    u = 2.0 ** -23
+    tol = u * ((0.44 * math.sqrt(n / 16) + 4) * m + n / 8 * 28 * s / math.sqrt(n)) + np.abs(want) * 2.0 ** -19
+    out = b.decode_attention_q4(q.cuda(), t.cache, dev(t.tab), dev(t.lens), 0.09, out_dtype=torch.float32, num_ctas=1)
+    err = np.abs(out[0].double().cpu().numpy() - want)
+    assert b.get_error() == 0
+    assert (err <= tol).all(), (float((err / tol).max()), float(err.max()))
