@@ -9,6 +9,8 @@
  *
  *   k_means [num_blocks][num_kv_heads][head_dim], the cache's dtype: the mean
  *   of a full block's keys (pkv_block_means). Only full blocks' means are read.
+ *   They are made from a pool of that dtype: a cache of codes that is to be read
+ *   through a selection needs the keys of its last blocks in such a pool too.
  *
  * For sequence s of n = ceil(L / B) blocks and kv head g, blocks j < first and
  * j >= n - last are read always, and of the others the top ones by

@@ -10,11 +10,12 @@
 // subnormal number, exactly: one AND makes two operands, with no bias to take
 // off again and no conversion. mma.sync takes subnormals at full rate, but aligns
 // products by their operands' exponent fields before it adds them: leading zeros
-// of a subnormal are bits that the sum loses. Codes are shifted to
-// bits 4..7 (c 2^-20), which keeps a sum to 2^-17 of the largest |q|, or weight
-// times scale, for a code's unit (2^-12.6 at bits 0..3, measured; normal numbers
-// 2^-18). (tcgen05 has no form that reads these rows: its 4-bit kinds want the
-// contracted index along the row for both operands, and a V row holds one token.)
+// of a subnormal are bits that the sum loses. All codes are brought to bits 4..7
+// (c 2^-20), which keeps a sum of 16 to 2^-16.6 of the largest |q|, or weight
+// times scale, for a code's unit (2^-12.6 with codes at bits 0..3, measured;
+// normal numbers 2^-18); it takes 2 to 3 % of the time. (tcgen05 has no form that
+// reads these rows: its 4-bit kinds want the contracted index along the row for
+// both operands, and a V row holds one token.)
 //
 // Work. The batch's (sequence, kv head, up to 8 q heads) units, cut into
 // subtiles of 32 tokens (two halves of 16, the m of the scores' product and the
@@ -25,15 +26,18 @@
 // unit cut between warps are joined in shared memory, between CTAs through the
 // workspace by the CTA that arrives last (nobody waits).
 //
-// What bounds it: HBM, D + D / 4 bytes a token and kv head for K and V, and
-// close behind it the instructions: 620 to 720 of a warp a subtile (D 128),
-// half an instruction a cycle. Large batches run at the memory: 256 sequences
-// of 128 to 2048 tokens and 40 heads (1.79 GB) take 300 us, 6.0 TB/s; 8 of
-// 32768 to 131072 tokens and 8 kv heads (0.84 GB) 132 to 148 us, 5.7 to 6.3.
-// A step of 64 sequences of 512 to 4096 tokens and 8 kv heads (190 MB) takes
-// 47 us: 30 in the loops (6.3 TB/s), the rest is the list (1.6 us), tables and
-// first copies (2), the joins within the CTA and between CTAs (5), the launch. Sixteen warps in a CTA against
-// two CTAs of eight: 52 and 54 us (that step), 359 and 383, 133 and 144.
+// What bounds it: HBM, D + D / 4 bytes a token and kv head for K and V, and the
+// instructions beside it: 700 to 730 of a warp a subtile (D 128), 0.62 to 0.71 a
+// cycle, the ANDs' pipe half busy. 256 sequences of 128 to 2048 tokens and 40
+// heads (1.79 GB) take 305 to 312 us, 5.8 TB/s; 8 of 32768 to 131072 tokens and
+// 8 kv heads of 8 q heads (0.84 GB) 150 to 171 us, 4.9 to 5.6: units of more
+// than 4 heads have no free columns for the weights' low parts, and their
+// instructions bound them. A step of 64 sequences of 512 to 4096 tokens and 8 kv
+// heads (190 MB) takes 46 us: 30 in the loops (6.3 TB/s), the rest is the list
+// (1.6 us), tables and first copies (2), the joins within the CTA and between
+// CTAs (5), the launch. Single weights, and codes where they lie, took 46.5, 303
+// and 152 us in the same process. Sixteen warps in a CTA against two CTAs of
+// eight, with those: 52 and 54 us (the step), 359 and 383, 133 and 144.
 //
 // Softmax in base 2 with a reference exponent that moves only when a score
 // passes it by more than the fp16 weights can hold, or a V scale grows past its

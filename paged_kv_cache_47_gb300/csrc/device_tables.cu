@@ -9,13 +9,13 @@
 // CTA has to have read them first, and the CTA that arrives last at a counter
 // writes them. No CTA waits.
 //
-// What bounds it: latency. A step of 64 requests is one CTA and a chain of
-// launch, two dependent loads, a scan, a table load and a store; append and
-// release together take 7.0 us, the host's time for two calls (10.0 with the
-// lengths always written behind the counter). A prompt wave writes 12 bytes a
-// token, which the CTAs stream out in order: 997 requests, a fifth of them
-// released and replaced by prompts of up to 2000 tokens, 13.6 us for both calls
-// (16.2 at one token a thread).
+// What bounds it: latency. A step of 64 requests is one CTA (release: two) and a
+// chain of launch, two dependent loads, a scan, a table load and a store; append
+// and release together take 7.2 us, the host's time for two calls, and 5.2
+// replayed as a graph (with the state updated in place 7.4 and 6.5: the counter).
+// A prompt wave writes 12 bytes a token, which the CTAs stream out in order: 997
+// requests, a fifth of them released and replaced by prompts of up to 2000
+// tokens, 13.3 us for both calls, 11.4 as a graph (16.2 at one token a thread).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

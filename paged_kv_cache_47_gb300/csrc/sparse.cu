@@ -2,7 +2,8 @@
 //
 // block_means: a warp per (token, kv head) whose token filled its block; a
 // lane adds D / 32 neighbouring elements over the block's rows, eight rows'
-// loads at a time. Latency: 2.5 us for a step.
+// loads at a time. Latency: 2.5 us for a step. A wave of prompts has a warp for
+// every token though one in B has work: 16384 tokens of 8 heads (34 MB) 19 us.
 //
 // Scores. A warp takes one kv head and a run of a sequence's blocks. Lanes hold
 // 8 neighbouring elements of a mean each, so a row is 16 lanes (D 128) and a
@@ -697,7 +698,11 @@ constexpr size_t kRowKeyBytes = 64 << 10;        // keys of a row in shared memo
 // 512 to 1024: 49 and 62). Threads: an SM holds 512, in up to four CTAs (144 rows
 // of 128 to 256 blocks: 9.9, 8.2 and 6.9 us with 128, 256 and 512; 480 rows:
 // 12.7, 14.8 and 21.4), and short rows do not fill many warps (144 rows of 32
-// to 64: 5.1, 5.4 and 5.5).
+// to 64: 5.1, 5.4 and 5.5). These are rows of tables about as wide as the longest
+// context. The lengths are on the device, so a wider table chooses by its width:
+// 512 rows of 32 to 256 blocks take 10.5 us up to 2048 columns and 13.3 with 8192
+// (keys in shared memory for all columns), 64 such rows 5.8 up to 1024 columns
+// and 13.4 past them (the spread form).
 int row_threads(int64_t rows, int M, int pitch, int sms) {
     if (M > kRowShort && (rows < 2 * sms || (size_t)pitch * 4 > kRowKeyBytes)) return 0;
     return rows <= sms && M > 128 && M <= kRowShort ? 512 : rows <= 2 * sms && M > 64 && M <= kRowShort ? 256 : 128;
