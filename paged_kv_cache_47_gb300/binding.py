@@ -1108,7 +1108,8 @@ def tables_append(block_tables, context_lens, new_tokens, free_blocks, num_free,
     slot_mapping / positions [max_tokens] and token_offsets [S + 1], writes the new blocks
     into block_tables [S][M], and updates the lengths and the free count (in place unless
     the *_out tensors are given). free_blocks [num_blocks] is the stack of free blocks.
-    Returns the three outputs."""
+    What it writes is never ready in the sense of tables_ready or inputs_ready for calls that
+    follow on the stream (pkv_tables.h). Returns the three outputs."""
     return prepared_tables_append(block_tables, context_lens, new_tokens, free_blocks, num_free,
                                   block_size, slot_mapping, positions, token_offsets, workspace,
                                   context_lens_out, num_free_out)(stream)

@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const __grid_con
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                 // a power of two that brings the head's largest element to
-                // [2^14, 2^15): exact, and fp16 then holds q to 2^-25 of it
+                // [2^14, 2^15): exact, and fp16 then holds q exactly down to
+                // 2^-28 of it
                 const int ef = max((int)(__float_as_uint(top) >> 23), 15);
                 const float up = __uint_as_float((uint32_t)(268 - ef) << 23);
                 const float down = __uint_as_float((uint32_t)(ef - 14) << 23);
