@@ -264,7 +264,8 @@ def _calls(st):
              b.prepared_tree_commit(path, count, st["offs"], st["lens"], st["tables"], st["k_pool"], st["v_pool"],
                                     max_tree=st["max_tree"]),
              b.prepared_tables_truncate(st["tables"], st["lens"], lens, st["free"], st["num_free"], case["B"],
-                                        workspace=b.alloc_tables_workspace(), num_free_out=left))
+                                        workspace=b.alloc_tables_workspace(), context_lens_out=i32(S),
+                                        num_free_out=left))
     return calls, {"path": path, "counts": count, "next": last, "lens": lens, "free": st["free"], "num_free": left,
                    "k_pool": st["k_pool"], "v_pool": st["v_pool"]}
 
