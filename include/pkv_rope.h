@@ -111,6 +111,62 @@ pkv_status pkv_rope_append(const pkv_cache_desc *cache, const pkv_rope_plan *pla
                            const void *k_new, int64_t k_stride, const void *v_new,
                            int64_t v_stride, void *k_pool, void *v_pool, void *stream);
 
+/*
+ * Positions of several axes (time, height, width of pictures and video; text
+ * has one position on all of them): pair i turns by its axis's position,
+ *   angle = positions[axis_i][token] * w_i
+ * sections[a] pairs belong to axis a, sum of sections = rotary_dim / 2:
+ *   PKV_ROPE_SECTIONS  the first sections[0] pairs are axis 0's, the next
+ *                      sections[1] axis 1's, and so on
+ *   PKV_ROPE_CYCLED    dealt out in turn, one pair an axis, by the axes that
+ *                      have pairs left
+ * and the frequencies are
+ *   PKV_ROPE_SHARED    w_i of the whole rotary_dim, whatever the axis
+ *   PKV_ROPE_OWN       each axis's own: its j-th pair has the frequency j of a
+ *                      rotary embedding of 2 * sections[a] elements, with the
+ *                      description's scaling
+ */
+#define PKV_ROPE_MAX_AXES 4
+typedef enum { PKV_ROPE_SECTIONS = 0, PKV_ROPE_CYCLED = 1 } pkv_rope_order;
+typedef enum { PKV_ROPE_SHARED = 0, PKV_ROPE_OWN = 1 } pkv_rope_frequencies;
+
+typedef struct {
+    pkv_rope_desc rope;                      /* rotary_dim = 2 * sum of sections */
+    int32_t num_axes;                        /* 1..PKV_ROPE_MAX_AXES             */
+    int32_t sections[PKV_ROPE_MAX_AXES];     /* each at least 1                  */
+    int32_t order;                           /* pkv_rope_order                   */
+    int32_t frequencies;                     /* pkv_rope_frequencies             */
+} pkv_rope_axes_desc;
+
+typedef struct {
+    pkv_rope_plan plan;
+    int32_t num_axes;
+    int32_t reserved;
+    uint8_t axis[PKV_ROPE_MAX_PAIRS];        /* of each pair */
+} pkv_rope_axes_plan;
+
+/* Fill *plan from *desc (host only; no device is needed). */
+pkv_status pkv_rope_axes_plan_init(const pkv_rope_axes_desc *desc, pkv_rope_axes_plan *plan);
+
+/*
+ * pkv_rope_axes, pkv_rope_axes_append — pkv_rope and pkv_rope_append with a
+ * position on each axis: positions is device int32 [num_axes][..], axis a's
+ * num_tokens positions from positions + a * positions_stride on (in elements,
+ * not negative; 0: one position on all axes). Everything else as there.
+ */
+pkv_status pkv_rope_axes(int32_t dtype, int32_t head_dim, const pkv_rope_axes_plan *plan,
+                         const int32_t *positions, int64_t positions_stride, int32_t num_tokens,
+                         const void *q, int64_t q_stride, int32_t num_q_heads, void *q_out,
+                         int64_t q_out_stride, const void *k, int64_t k_stride,
+                         int32_t num_kv_heads, void *k_out, int64_t k_out_stride, void *stream);
+pkv_status pkv_rope_axes_append(const pkv_cache_desc *cache, const pkv_rope_axes_plan *plan,
+                                const int32_t *positions, int64_t positions_stride,
+                                const int64_t *slot_mapping, int32_t num_tokens, const void *q,
+                                int64_t q_stride, int32_t num_q_heads, void *q_out,
+                                int64_t q_out_stride, const void *k_new, int64_t k_stride,
+                                const void *v_new, int64_t v_stride, void *k_pool, void *v_pool,
+                                void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,14 +27,14 @@
  *
  * A call whose request cannot be met changes nothing (all or nothing) and sets
  * a bit of the device error word (pkv_get_error):
- *   PKV_DEVERR_NO_BLOCKS  more blocks needed than free, or (release) more
- *                         returned than the pool holds
+ *   PKV_DEVERR_NO_BLOCKS  more blocks needed than free, or (release,
+ *                         truncate) more returned than the pool holds
  *   PKV_DEVERR_TOKENS     a negative token count, or more new tokens than
  *                         max_tokens
  *   PKV_DEVERR_CONTEXT    a length < 0 or past max_blocks_per_seq * B
  * A block id outside [0, num_blocks) among the entries used sets
  * PKV_DEVERR_BLOCK_ID: its tokens get slot -1 (append), or it is pushed as it
- * is (release).
+ * is (release, truncate).
  *
  * Calls on one state are ordered by the caller (one stream, or events).
  *
@@ -97,6 +97,24 @@ pkv_status pkv_tables_release(int32_t num_blocks, int32_t block_size, int32_t nu
                               int32_t *context_lens_out, int32_t *free_blocks,
                               const int32_t *num_free, int32_t *num_free_out, void *workspace,
                               void *stream);
+
+/*
+ * pkv_tables_truncate — shorten requests and give the blocks behind them back.
+ *
+ * Request s keeps its first kept_lens[s] tokens, 0 <= kept_lens[s] <= L_s
+ * (what pkv_tree_accept leaves of the drafted ones, say): blocks
+ * ceil(kept / B) .. ceil(L_s / B) - 1 of its row are pushed in table order,
+ * request after request, and context_lens_out[s] = kept_lens[s]. Table rows
+ * stay as they are. A kept length outside its range refuses the call
+ * (PKV_DEVERR_CONTEXT). The aliases of pkv_tables_append are allowed;
+ * kept_lens overlaps no output.
+ */
+pkv_status pkv_tables_truncate(int32_t num_blocks, int32_t block_size, int32_t num_seqs,
+                               const int32_t *kept_lens, const int32_t *block_tables,
+                               int32_t max_blocks_per_seq, const int32_t *context_lens,
+                               int32_t *context_lens_out, int32_t *free_blocks,
+                               const int32_t *num_free, int32_t *num_free_out, void *workspace,
+                               void *stream);
 
 #ifdef __cplusplus
 }

@@ -78,11 +78,33 @@ def rope_frequencies(rotary_dim, base, scaling="none", factor=1.0, original_len=
     return np.array(out), amp
 
 
+def axes_frequencies(sections, order, frequencies, base, **scaling):
+    """(axis of each pair, radians a position of each pair, amplitude) of a rotary embedding over several axes."""
+    axis, left = [], list(sections)
+    a = 0
+    while sum(left):
+        while left[a] == 0:
+            a = (a + 1) % len(left)
+        axis.append(a)
+        left[a] -= 1
+        if order == "cycled":
+            a = (a + 1) % len(left)
+    w, amp = rope_frequencies(2 * len(axis), base, **scaling)
+    if frequencies == "own":
+        own = [rope_frequencies(2 * n, base, **scaling)[0] for n in sections]
+        used = [0] * len(sections)
+        for i, a in enumerate(axis):
+            w[i] = own[a][used[a]]
+            used[a] += 1
+    return np.array(axis), w, amp
+
+
 def rope(x, positions, w, amp, layout):
     """x [T][H][D] float64, turned; and, element by element, |x_a| + |x_b| of its pair."""
     y, size = x.copy(), np.abs(x)
     n = len(w)
-    ang = positions.astype(np.float64)[:, None] * w
+    pos = positions.astype(np.float64)
+    ang = (pos if pos.ndim == 2 else pos[:, None]) * w           # 2-D: a position for each pair
     c, s = (np.cos(ang) * amp)[:, None], (np.sin(ang) * amp)[:, None]
     a, b = ((slice(0, n), slice(n, 2 * n)) if layout == "half" else
             (slice(0, 2 * n, 2), slice(1, 2 * n, 2)))

@@ -23,7 +23,7 @@ CODE_DTYPE = {v: k for k, v in DTYPE_CODE.items()}
 STATUS = {0: "PKV_OK", -1: "PKV_ERR_INVALID_ARG", -2: "PKV_ERR_UNSUPPORTED", -3: "PKV_ERR_CUDA",
           -4: "PKV_ERR_OUT_OF_RANGE", -5: "PKV_ERR_TIMEOUT", -6: "PKV_ERR_WORKSPACE"}
 DEVERR_BLOCK_ID, DEVERR_CONTEXT, DEVERR_TIMEOUT, DEVERR_SLOT = 0x1, 0x2, 0x4, 0x8
-DEVERR_NO_BLOCKS, DEVERR_TOKENS = 0x10, 0x20
+DEVERR_NO_BLOCKS, DEVERR_TOKENS, DEVERR_TREE = 0x10, 0x20, 0x40
 
 
 class CacheDesc(ctypes.Structure):
@@ -951,7 +951,7 @@ TABLES_WORKSPACE_BYTES = 64
 
 
 def _ops_lib():
-    """libpkv with the signatures of pkv_tables.h, pkv_rope.h, pkv_q4.h and pkv_sparse.h."""
+    """libpkv with the signatures of pkv_tables.h, pkv_rope.h, pkv_q4.h, pkv_sparse.h and pkv_tree.h."""
     L = lib()
     if not getattr(L, "_ops_ready", False):
         vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
@@ -959,6 +959,7 @@ def _ops_lib():
         dp, q4, pools = (ctypes.POINTER(CacheDesc), ctypes.POINTER(Q4CacheDesc),
                          ctypes.POINTER(Q4Pools))
         plan, sel = ctypes.POINTER(_RopePlan), ctypes.POINTER(SparseSelect)
+        axes = ctypes.POINTER(_RopeAxesPlan)
         for name, args in {
             "pkv_tables_append": [i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp,
                                   vp, vp],
@@ -967,6 +968,16 @@ def _ops_lib():
             "pkv_rope": [i32, i32, plan, vp, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp],
             "pkv_rope_append": [dp, plan, vp, vp, i32, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp,
                                 vp, vp],
+            "pkv_tables_truncate": [i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp],
+            "pkv_rope_axes_plan_init": [ctypes.POINTER(RopeAxesDesc), axes],
+            "pkv_rope_axes": [i32, i32, axes, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp],
+            "pkv_rope_axes_append": [dp, axes, vp, i64, vp, i32, vp, i64, i32, vp, i64, vp, i64, vp, i64,
+                                     vp, vp, vp],
+            "pkv_tree_plan": [i32, i32, vp, vp, vp, vp, vp, i32, vp, i32, vp],
+            "pkv_tree_accept": [i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
+            "pkv_tree_commit": [dp, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp],
+            "pkv_decode_attention_tree": [dp, vp, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, i32, i32,
+                                          f32, vp, i32, vp, sz, vp, ctypes.POINTER(TreeOptions)],
             "pkv_append_q4": [q4, vp, vp, vp, i32, pools, vp],
             "pkv_gather_q4": [q4, pools, vp, i32, vp, vp, i32, vp],
             "pkv_decode_attention_q4": [q4, vp, i32, i32, pools, vp, i32, vp, f32, vp, i32, vp, sz,
@@ -983,6 +994,7 @@ def _ops_lib():
             "pkv_decode_q4_workspace_bytes": [q4, i32, i32],
             "pkv_select_workspace_bytes": [dp, i32, i32],
             "pkv_decode_sparse_workspace_bytes": [dp, i32, i32, i32],
+            "pkv_decode_tree_workspace_bytes": [dp, i32, i32, i32],
         }.items():
             getattr(L, name).argtypes = args
             getattr(L, name).restype = sz
@@ -1141,6 +1153,32 @@ def tables_release(block_tables, context_lens, released, free_blocks, num_free, 
                                    block_size, workspace, context_lens_out, num_free_out)(stream)
 
 
+def prepared_tables_truncate(block_tables, context_lens, kept_lens, free_blocks, num_free,
+                             block_size: int, workspace,
+                             context_lens_out: Optional[torch.Tensor] = None,
+                             num_free_out: Optional[torch.Tensor] = None) -> PreparedCall:
+    """tables_truncate as a PreparedCall."""
+    S, M, NB, lens_out, free_out = _tables_state(block_tables, context_lens, free_blocks, num_free,
+                                                 context_lens_out, num_free_out)
+    _need(kept_lens, "kept_lens", torch.int32, (S,))
+    if workspace.numel() * workspace.element_size() < TABLES_WORKSPACE_BYTES:
+        raise ValueError("workspace is too small")
+    return PreparedCall("pkv_tables_truncate", (
+        NB, block_size, S, _ptr(kept_lens), _ptr(block_tables), M, _ptr(context_lens), _ptr(lens_out),
+        _ptr(free_blocks), _ptr(num_free), _ptr(free_out), _ptr(workspace)),
+        keep=(block_tables, context_lens, kept_lens, free_blocks, num_free, lens_out, free_out, workspace),
+        out=None)
+
+
+def tables_truncate(block_tables, context_lens, kept_lens, free_blocks, num_free, block_size: int,
+                    workspace, context_lens_out: Optional[torch.Tensor] = None,
+                    num_free_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Shorten each request to its first kept_lens[s] tokens (int32 [S], at most its length) and push
+    the blocks behind them onto the stack of free blocks (pkv_tables_truncate)."""
+    return prepared_tables_truncate(block_tables, context_lens, kept_lens, free_blocks, num_free,
+                                    block_size, workspace, context_lens_out, num_free_out)(stream)
+
+
 # ------------------------------------------------------------------ rotary positions
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4}
@@ -1242,6 +1280,269 @@ def rope_append(q, k_new, v_new, positions, slot_mapping, plan: RopePlan, k_pool
     with _on(stream, q.device):
         return prepared_rope_append(q, k_new, v_new, positions, slot_mapping, plan, k_pool, v_pool,
                                     q_out)(stream)
+
+
+ROPE_ORDERS = {"sections": 0, "cycled": 1}
+ROPE_FREQUENCIES = {"shared": 0, "own": 1}
+
+
+class RopeAxesDesc(ctypes.Structure):
+    _fields_ = [("rope", RopeDesc), ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("order", ctypes.c_int32), ("frequencies", ctypes.c_int32)]
+
+
+class _RopeAxesPlan(ctypes.Structure):
+    _fields_ = [("plan", _RopePlan), ("num_axes", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 64)]
+
+
+class RopeAxesPlan:
+    """A rotary embedding whose pairs turn by the positions of several axes (pkv_rope_axes_plan_init):
+    sections[a] pairs for axis a, "sections" (one axis's pairs after another's) or "cycled" (dealt out in
+    turn); frequencies "shared" (of the whole embedding) or "own" (each axis's own). The rest as RopePlan;
+    the rotated part of a head is twice the sum of the sections."""
+
+    def __init__(self, sections, order: str = "sections", frequencies: str = "shared", base: float = 10000.0,
+                 layout: str = "half", scaling: str = "none", factor: float = 1.0, original_len: int = 0,
+                 low_freq_factor: float = 1.0, high_freq_factor: float = 4.0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, attention_factor: float = 0.0):
+        sections = [int(n) for n in sections]
+        if not 1 <= len(sections) <= 4:
+            raise ValueError(f"{len(sections)} axes (1 to 4)")
+        rope = RopeDesc(2 * sum(sections), ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], original_len, base,
+                        factor, low_freq_factor, high_freq_factor, beta_fast, beta_slow, attention_factor)
+        desc = RopeAxesDesc(rope, len(sections), (ctypes.c_int32 * 4)(*sections), ROPE_ORDERS[order],
+                            ROPE_FREQUENCIES[frequencies])
+        self.c = _RopeAxesPlan()
+        _check(_ops_lib().pkv_rope_axes_plan_init(ctypes.byref(desc), ctypes.byref(self.c)))
+
+
+def _axes_positions(positions, plan: RopeAxesPlan, T: int) -> int:
+    """The stride from one axis's positions to the next's."""
+    if positions.dtype != torch.int32 or positions.dim() != 2 or tuple(positions.shape) != (plan.c.num_axes, T):
+        raise ValueError(f"positions must be int32 [{plan.c.num_axes}][{T}]")
+    if T > 1 and positions.stride(1) != 1:
+        raise ValueError("positions: each axis's must be contiguous")
+    return positions.stride(0)
+
+
+def prepared_rope_axes(q, k, positions, plan: RopeAxesPlan, q_out: Optional[torch.Tensor] = None,
+                       k_out: Optional[torch.Tensor] = None) -> PreparedCall:
+    """rope_axes as a PreparedCall."""
+    T, _, D = q.shape
+    (Hq, qs), (Hk, ks) = _heads(q, "q"), _heads(k, "k", q.dtype, T)
+    if k.shape[2] != D:
+        raise ValueError("q and k differ in head_dim")
+    q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(T, Hk, D, dtype=q.dtype, device=q.device) if k_out is None else k_out
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out have the shapes of q and k")
+    (_, qos), (_, kos) = _heads(q_out, "q_out", q.dtype, T), _heads(k_out, "k_out", q.dtype, T)
+    ps = _axes_positions(positions, plan, T)
+    return PreparedCall("pkv_rope_axes", (
+        DTYPE_CODE[q.dtype], D, ctypes.byref(plan.c), _ptr(positions), ps, T, _ptr(q), qs, Hq, _ptr(q_out), qos,
+        _ptr(k), ks, Hk, _ptr(k_out), kos),
+        keep=(q, k, positions, plan, q_out, k_out), out=(q_out, k_out))
+
+
+def rope_axes(q, k, positions, plan: RopeAxesPlan, q_out: Optional[torch.Tensor] = None,
+              k_out: Optional[torch.Tensor] = None, stream=None):
+    """rope with a position on each axis: positions int32 [axes][T] (pkv_rope_axes)."""
+    with _on(stream, q.device):
+        return prepared_rope_axes(q, k, positions, plan, q_out, k_out)(stream)
+
+
+def prepared_rope_axes_append(q, k_new, v_new, positions, slot_mapping, plan: RopeAxesPlan, k_pool, v_pool,
+                              q_out: Optional[torch.Tensor] = None) -> PreparedCall:
+    """rope_axes_append as a PreparedCall."""
+    desc = _pools(k_pool, v_pool)
+    T, _, D = q.shape
+    dt = k_pool.dtype
+    (Hq, qs), (Hk, ks), (Hv, vs) = _heads(q, "q", dt), _heads(k_new, "k_new", dt, T), _heads(v_new, "v_new", dt, T)
+    if Hk != desc.num_kv_heads or Hv != Hk or not D == k_new.shape[2] == v_new.shape[2] == desc.head_dim:
+        raise ValueError("q, k_new or v_new do not fit the pools")
+    q_out = torch.empty(T, Hq, D, dtype=dt, device=q.device) if q_out is None else q_out
+    if q_out.shape != q.shape:
+        raise ValueError("q_out has the shape of q")
+    _, qos = _heads(q_out, "q_out", dt, T)
+    ps = _axes_positions(positions, plan, T)
+    _need(slot_mapping, "slot_mapping", torch.int64, (T,))
+    return PreparedCall("pkv_rope_axes_append", (
+        ctypes.byref(desc), ctypes.byref(plan.c), _ptr(positions), ps, _ptr(slot_mapping), T, _ptr(q), qs, Hq,
+        _ptr(q_out), qos, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(k_pool), _ptr(v_pool)),
+        keep=(q, k_new, v_new, positions, slot_mapping, plan, k_pool, v_pool, q_out, desc), out=q_out)
+
+
+def rope_axes_append(q, k_new, v_new, positions, slot_mapping, plan: RopeAxesPlan, k_pool, v_pool,
+                     q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """rope_append with a position on each axis: positions int32 [axes][T] (pkv_rope_axes_append)."""
+    with _on(stream, q.device):
+        return prepared_rope_axes_append(q, k_new, v_new, positions, slot_mapping, plan, k_pool, v_pool,
+                                         q_out)(stream)
+
+
+# ---------------------------------------------------------------------- drafted tokens
+TREE_MAX_TOKENS = 256
+
+
+class TreeOptions(ctypes.Structure):
+    _fields_ = [("num_ctas", ctypes.c_int32), ("reserved", ctypes.c_int32), ("lse_out", ctypes.c_void_p)]
+
+
+def _tree_batch(parents, token_offsets, context_lens, T: int) -> int:
+    S = context_lens.shape[0]
+    if parents is not None:
+        _need(parents, "parents", torch.int32, (T,))
+    _need(token_offsets, "token_offsets", torch.int32, (S + 1,))
+    _need(context_lens, "context_lens", torch.int32, (S,))
+    return S
+
+
+def _mask_words(masks, T: int) -> int:
+    if masks.dim() != 2 or not 1 <= masks.shape[1] <= 4:
+        raise ValueError("masks must be int64 [tokens][1 to 4 words]")
+    _need(masks, "masks", torch.int64, (T, masks.shape[1]))
+    return masks.shape[1]
+
+
+def prepared_tree_plan(parents, token_offsets, context_lens, masks=None, positions=None,
+                       position_deltas: Optional[torch.Tensor] = None, mask_words: int = 4) -> PreparedCall:
+    """tree_plan as a PreparedCall."""
+    if masks is None and positions is None:
+        raise ValueError("neither masks nor positions to write")
+    T = masks.shape[0] if masks is not None else positions.shape[-1]
+    S = _tree_batch(parents, token_offsets, context_lens, T)
+    words = mask_words if masks is None else _mask_words(masks, T)
+    axes = 1
+    if positions is not None:
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        _need(positions, "positions", torch.int32, (axes, T) if positions.dim() == 2 else (T,))
+    if position_deltas is not None:
+        _need(position_deltas, "position_deltas", torch.int32, (S,))
+    return PreparedCall("pkv_tree_plan", (
+        S, T, _ptr(parents), _ptr(token_offsets), _ptr(context_lens), _ptr(position_deltas), _ptr(masks), words,
+        _ptr(positions), axes),
+        keep=(parents, token_offsets, context_lens, position_deltas, masks, positions), out=(masks, positions))
+
+
+def tree_plan(parents, token_offsets, context_lens, masks=None, positions=None,
+              position_deltas: Optional[torch.Tensor] = None, mask_words: int = 4, stream=None):
+    """Masks (int64 [T][words]) and positions (int32 [T] or [axes][T]) of drafted tokens from their
+    parents (int32 [T], None: chains); either output may be None (pkv_tree_plan). Returns both."""
+    return prepared_tree_plan(parents, token_offsets, context_lens, masks, positions, position_deltas,
+                              mask_words)(stream)
+
+
+def tree_workspace_bytes(k_pool, num_q_heads: int, max_tree: int, num_ctas: int = 0) -> int:
+    with torch.cuda.device(k_pool.device):
+        return int(_ops_lib().pkv_decode_tree_workspace_bytes(ctypes.byref(cache_desc(k_pool)), num_q_heads, max_tree,
+                                                              num_ctas))
+
+
+def alloc_tree_workspace(k_pool, num_q_heads: int, max_tree: int, num_ctas: int = 0) -> torch.Tensor:
+    """Workspace of decode_attention_tree; one for calls that may overlap."""
+    n = tree_workspace_bytes(k_pool, num_q_heads, max_tree, num_ctas)
+    if n == 0:
+        raise PkvError(-1, lib().pkv_last_error_message().decode())
+    return torch.empty(n, dtype=torch.uint8, device=k_pool.device)
+
+
+def prepared_decode_attention_tree(q, k_pool, v_pool, block_tables, context_lens, token_offsets, masks,
+                                   scale: float, max_tree: int, out: Optional[torch.Tensor] = None,
+                                   out_dtype: Optional[torch.dtype] = None,
+                                   workspace: Optional[torch.Tensor] = None, num_ctas: int = 0,
+                                   lse_out: Optional[torch.Tensor] = None) -> PreparedCall:
+    """decode_attention_tree as a PreparedCall."""
+    desc = _pools(k_pool, v_pool)
+    T, Hq, D = q.shape
+    _need(q, "q", k_pool.dtype, (T, Hq, desc.head_dim))
+    S = _tree_batch(None, token_offsets, context_lens, T)
+    _need(block_tables, "block_tables", torch.int32, (S, block_tables.shape[-1]))
+    words = 0 if masks is None else _mask_words(masks, T)
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=out_dtype or q.dtype, device=q.device)
+    _need(out, "out", out.dtype, q.shape)
+    if workspace is None:
+        workspace = alloc_tree_workspace(k_pool, Hq, max_tree, num_ctas)
+    opts = TreeOptions(num_ctas, 0, None)
+    if lse_out is not None:
+        opts.lse_out = _need(lse_out, "lse_out", torch.float32, (T, Hq)).data_ptr()
+    return PreparedCall("pkv_decode_attention_tree", (
+        ctypes.byref(desc), _ptr(q), T, Hq, _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), S, block_tables.shape[1],
+        _ptr(context_lens), _ptr(token_offsets), _ptr(masks), words, max_tree, float(scale), _ptr(out),
+        DTYPE_CODE[out.dtype], _ptr(workspace), workspace.numel() * workspace.element_size()),
+        keep=(q, k_pool, v_pool, block_tables, context_lens, token_offsets, masks, out, workspace, lse_out, opts,
+              desc),
+        out=out, after=(ctypes.byref(opts),))
+
+
+def decode_attention_tree(q, k_pool, v_pool, block_tables, context_lens, token_offsets, masks, scale: float,
+                          max_tree: int, out: Optional[torch.Tensor] = None,
+                          out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None,
+                          num_ctas: int = 0, lse_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of all drafted tokens over the cache, whose last tokens they are: q [T][Hq][D], one
+    sequence's tokens after another's (token_offsets int32 [S + 1]), each sees the context before them
+    and the drafted tokens of its mask (int64 [T][words]; None: chains). max_tree: tokens a sequence at
+    most (pkv_decode_attention_tree)."""
+    with _on(stream, q.device):
+        return prepared_decode_attention_tree(q, k_pool, v_pool, block_tables, context_lens, token_offsets, masks,
+                                              scale, max_tree, out, out_dtype, workspace, num_ctas,
+                                              lse_out)(stream)
+
+
+def prepared_tree_accept(parents, tokens, targets, token_offsets, context_lens, path, counts, next_tokens,
+                         context_lens_out, max_tree: int) -> PreparedCall:
+    """tree_accept as a PreparedCall."""
+    T = tokens.shape[0]
+    S = _tree_batch(parents, token_offsets, context_lens, T)
+    for name, t, n in (("tokens", tokens, T), ("targets", targets, T), ("path", path, T), ("counts", counts, S),
+                       ("next_tokens", next_tokens, S), ("context_lens_out", context_lens_out, S)):
+        _need(t, name, torch.int32, (n,))
+    return PreparedCall("pkv_tree_accept", (
+        S, T, max_tree, _ptr(parents), _ptr(tokens), _ptr(targets), _ptr(token_offsets), _ptr(context_lens),
+        _ptr(path), _ptr(counts), _ptr(next_tokens), _ptr(context_lens_out)),
+        keep=(parents, tokens, targets, token_offsets, context_lens, path, counts, next_tokens, context_lens_out),
+        out=(path, counts, next_tokens, context_lens_out))
+
+
+def tree_accept(parents, tokens, targets, token_offsets, context_lens, max_tree: int,
+                path: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                next_tokens: Optional[torch.Tensor] = None, context_lens_out: Optional[torch.Tensor] = None,
+                stream=None):
+    """The branch of each sequence's drafted tokens (int32 [T]) that the model's answers (targets) confirm
+    (pkv_tree_accept): (path [T], counts [S], next_tokens [S], context_lens_out [S]), new tensors unless
+    given. A new path is -1 past the last sequence's rows too."""
+    with _on(stream, tokens.device):
+        i32 = dict(dtype=torch.int32, device=tokens.device)
+        S = context_lens.shape[0]
+        path = torch.full(tokens.shape, -1, **i32) if path is None else path
+        counts, next_tokens, context_lens_out = (torch.empty(S, **i32) if t is None else t
+                                                 for t in (counts, next_tokens, context_lens_out))
+        return prepared_tree_accept(parents, tokens, targets, token_offsets, context_lens, path, counts, next_tokens,
+                                    context_lens_out, max_tree)(stream)
+
+
+def prepared_tree_commit(path, counts, token_offsets, context_lens, block_tables, k_pool, v_pool,
+                         max_tree: int) -> PreparedCall:
+    """tree_commit as a PreparedCall."""
+    desc = _pools(k_pool, v_pool)
+    T = path.shape[0]
+    S = _tree_batch(None, token_offsets, context_lens, T)
+    _need(path, "path", torch.int32, (T,))
+    _need(counts, "counts", torch.int32, (S,))
+    _need(block_tables, "block_tables", torch.int32, (S, block_tables.shape[-1]))
+    return PreparedCall("pkv_tree_commit", (
+        ctypes.byref(desc), S, T, max_tree, _ptr(path), _ptr(counts), _ptr(token_offsets), _ptr(context_lens),
+        _ptr(block_tables), block_tables.shape[1], _ptr(k_pool), _ptr(v_pool)),
+        keep=(path, counts, token_offsets, context_lens, block_tables, k_pool, v_pool, desc), out=None)
+
+
+def tree_commit(path, counts, token_offsets, context_lens, block_tables, k_pool, v_pool, max_tree: int,
+                stream=None) -> None:
+    """Move the accepted drafted rows of each sequence together in the cache, behind its context
+    (pkv_tree_commit). context_lens: the lengths that count all drafted tokens."""
+    return prepared_tree_commit(path, counts, token_offsets, context_lens, block_tables, k_pool, v_pool,
+                                max_tree)(stream)
 
 
 # --------------------------------------------------------------------- 4-bit KV cache

@@ -33,10 +33,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kItemsPerCta = 2048;   // tokens (or blocks) one CTA is launched for
 constexpr int kMaxCtas = 592;        // beyond, CTAs take several strides
 
+enum { APPEND, RELEASE, TRUNCATE };
+
 struct TablesParams {
     int NB, B, lb, S, M;       // B = 1 << lb
-    const int32_t *add;        // append: new tokens; release: unused
-    const uint8_t *released;   // release: flags; append: unused
+    const int32_t *add;        // append: new tokens; truncate: lengths kept
+    const uint8_t *released;   // release: flags
     int32_t *tables;
     const int32_t *lens;
     int32_t *lens_out;
@@ -52,14 +54,14 @@ struct TablesParams {
     unsigned *err;
 };
 
-// Request s as the scan sees it. items: tokens (append) or blocks (release)
-// to place; blocks: blocks taken or returned.
+// Request s as the scan sees it. items: tokens (append) or blocks (release,
+// truncate) to place; blocks: blocks taken or returned.
 struct Req {
     int len, items, have, blocks;
     unsigned bad;              // PKV_DEVERR_* bits
 };
 
-template <bool RELEASE>
+template <int MODE>
 __device__ __forceinline__ Req load_req(const TablesParams &p, int s) {
     Req r;
     r.len = p.lens[s];
@@ -67,8 +69,13 @@ __device__ __forceinline__ Req load_req(const TablesParams &p, int s) {
     const int64_t cap = (int64_t)p.M * p.B;
     if (r.len < 0 || r.len > cap) r.bad = PKV_DEVERR_CONTEXT;
     r.have = r.bad ? 0 : (int)(((unsigned)r.len + p.B - 1) >> p.lb);
-    if (RELEASE) {
+    if (MODE == RELEASE) {
         r.blocks = p.released[s] ? r.have : 0;
+        r.items = r.blocks;
+    } else if (MODE == TRUNCATE) {
+        const int kept = p.add[s];
+        if (kept < 0 || kept > r.len) r.bad |= PKV_DEVERR_CONTEXT;
+        r.blocks = r.bad ? 0 : r.have - (int)(((unsigned)kept + p.B - 1) >> p.lb);
         r.items = r.blocks;
     } else {
         const int a = p.add[s];
@@ -93,17 +100,20 @@ __device__ __forceinline__ void warp_scan(long long &a, long long &b, int lane) 
 }
 
 // Lengths and free count after the call.
-template <bool RELEASE>
+template <int MODE>
 __device__ __forceinline__ void write_state(const TablesParams &p, bool refused, int nf, long long blocks) {
     for (int s = threadIdx.x; s < p.S; s += kThreads) {
         const int len = p.lens[s];
-        p.lens_out[s] = refused ? len : RELEASE ? (p.released[s] ? 0 : len) : len + p.add[s];
+        p.lens_out[s] = refused           ? len
+                        : MODE == RELEASE ? (p.released[s] ? 0 : len)
+                        : MODE == TRUNCATE ? p.add[s]
+                                           : len + p.add[s];
     }
-    if (threadIdx.x == 0) *p.num_free_out = refused ? nf : RELEASE ? nf + (int)blocks : nf - (int)blocks;
+    if (threadIdx.x == 0) *p.num_free_out = refused ? nf : MODE != APPEND ? nf + (int)blocks : nf - (int)blocks;
 }
 
 // PER: items a thread places at a time, neighbours.
-template <bool RELEASE, int PER>
+template <int MODE, int PER>
 __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ TablesParams p) {
     __shared__ long long first_item[kThreads + 1];   // items before thread t's requests
     __shared__ long long first_block[kThreads];
@@ -119,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     long long items = 0, blocks = 0;
     unsigned bad = 0;
     for (int s = s0; s < s1; ++s) {
-        const Req r = load_req<RELEASE>(p, s);
+        const Req r = load_req<MODE>(p, s);
         items += r.items;
         blocks += r.blocks;
         bad |= r.bad;
@@ -147,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
         bad |= warp_bad[w];
     }
     if (nf < 0 || nf > p.NB) bad |= PKV_DEVERR_NO_BLOCKS;
-    if (RELEASE) {
+    if (MODE != APPEND) {
         if (nf + total_blocks > p.NB) bad |= PKV_DEVERR_NO_BLOCKS;
     } else {
         if (total_blocks > nf) bad |= PKV_DEVERR_NO_BLOCKS;
@@ -160,19 +170,19 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     const bool writer = blockIdx.x == gridDim.x - 1;     // the CTA with the fewest items
     if (writer) {
         if (tid == 0 && bad) atomicOr(p.err, bad);
-        if (!RELEASE) {
+        if (MODE == APPEND) {
             long long at = item0;
             for (int s = s0; s < s1; ++s) {
                 p.offsets[s] = bad ? 0 : (int)at;
-                at += load_req<RELEASE>(p, s).items;
+                at += load_req<MODE>(p, s).items;
             }
             if (tid == 0) p.offsets[p.S] = (int)total;
         }
-        if (!p.in_place) write_state<RELEASE>(p, bad != 0, nf, total_blocks);
+        if (!p.in_place) write_state<MODE>(p, bad != 0, nf, total_blocks);
     }
     __syncthreads();
 
-    const long long limit = RELEASE ? total : (long long)p.max_tokens;
+    const long long limit = MODE != APPEND ? total : (long long)p.max_tokens;
     for (long long i0 = ((long long)blockIdx.x * kThreads + tid) * PER; i0 < limit;
          i0 += (long long)gridDim.x * kThreads * PER) {
         // the last thread whose requests begin at or before item i0 holds it
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
             at = first_item[t];
             blk = first_block[t];
             s = t * K;
-            r = load_req<RELEASE>(p, s);
+            r = load_req<MODE>(p, s);
         }
         int64_t slot[PER];
         int position[PER];
@@ -199,11 +209,11 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
             while (i >= at + r.items) {
                 at += r.items;
                 blk += r.blocks;
-                r = load_req<RELEASE>(p, ++s);
+                r = load_req<MODE>(p, ++s);
             }
             const int k = (int)(i - at);
-            if (RELEASE) {
-                const int id = p.tables[(int64_t)s * p.M + k];
+            if (MODE != APPEND) {
+                const int id = p.tables[(int64_t)s * p.M + r.have - r.blocks + k];
                 if (id < 0 || id >= p.NB) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
                 p.free_blocks[nf + i] = id;
             } else {
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
                 position[q] = pos;
             }
         }
-        if (RELEASE) continue;
+        if (MODE != APPEND) continue;
         if (PER == 4 && i0 + PER <= limit) {     // (the buffers are 16-byte aligned then)
             longlong2 *dst = reinterpret_cast<longlong2 *>(p.slots + i0);
             dst[0] = make_longlong2(slot[0], slot[PER > 1]);
@@ -244,10 +254,10 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
         if (!is_last) return;
         if (tid == 0) *p.arrived = 0;
     }
-    write_state<RELEASE>(p, bad != 0, nf, total_blocks);
+    write_state<MODE>(p, bad != 0, nf, total_blocks);
 }
 
-template <bool RELEASE>
+template <int MODE>
 pkv_status run(TablesParams &p, void *workspace, int64_t items, void *stream) {
     pkv_status st = pkv::device_error_word(&p.err);
     if (st != PKV_OK) return st;
@@ -257,12 +267,12 @@ pkv_status run(TablesParams &p, void *workspace, int64_t items, void *stream) {
     int64_t ctas = (items + kItemsPerCta - 1) / kItemsPerCta;
     ctas = ctas < 1 ? 1 : ctas > kMaxCtas ? kMaxCtas : ctas;
     // four tokens a thread once there are several CTAs
-    const bool four = !RELEASE && ctas > 1 && reinterpret_cast<uintptr_t>(p.slots) % 16 == 0 &&
+    const bool four = MODE == APPEND && ctas > 1 && reinterpret_cast<uintptr_t>(p.slots) % 16 == 0 &&
                       reinterpret_cast<uintptr_t>(p.positions) % 16 == 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
-        four ? launch_chained(tables_kernel<RELEASE, 4>, dim3((unsigned)ctas), kThreads, 0, s, p)
-             : launch_chained(tables_kernel<RELEASE, 1>, dim3((unsigned)ctas), kThreads, 0, s, p);
+        four ? launch_chained(tables_kernel<MODE, 4>, dim3((unsigned)ctas), kThreads, 0, s, p)
+             : launch_chained(tables_kernel<MODE, 1>, dim3((unsigned)ctas), kThreads, 0, s, p);
     if (e != cudaSuccess)
         return pkv::set_last_error(PKV_ERR_CUDA, "tables launch: %s", cudaGetErrorString(e));
     return PKV_OK;
@@ -321,7 +331,7 @@ pkv_status pkv_tables_append(int32_t num_blocks, int32_t block_size, int32_t num
     p.positions = positions;
     p.max_tokens = max_tokens;
     p.offsets = token_offsets;
-    return run<false>(p, workspace, max_tokens, stream);
+    return run<APPEND>(p, workspace, max_tokens, stream);
 }
 
 pkv_status pkv_tables_release(int32_t num_blocks, int32_t block_size, int32_t num_seqs,
@@ -356,7 +366,43 @@ pkv_status pkv_tables_release(int32_t num_blocks, int32_t block_size, int32_t nu
     // step, so the launch is sized for a quarter of the table and strides
     int64_t most = (int64_t)num_seqs * max_blocks_per_seq / 4;
     if (most > num_blocks) most = num_blocks;
-    return run<true>(p, workspace, most, stream);
+    return run<RELEASE>(p, workspace, most, stream);
+}
+
+pkv_status pkv_tables_truncate(int32_t num_blocks, int32_t block_size, int32_t num_seqs,
+                               const int32_t *kept_lens, const int32_t *block_tables,
+                               int32_t max_blocks_per_seq, const int32_t *context_lens,
+                               int32_t *context_lens_out, int32_t *free_blocks,
+                               const int32_t *num_free, int32_t *num_free_out, void *workspace,
+                               void *stream) {
+    pkv_status st = check(num_blocks, block_size, num_seqs, max_blocks_per_seq);
+    if (st != PKV_OK) return st;
+    if ((num_seqs > 0 && (!kept_lens || !block_tables || !context_lens || !context_lens_out)) ||
+        !free_blocks || !num_free || !num_free_out)
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "a pointer argument is NULL");
+    if (!workspace) return pkv::set_last_error(PKV_ERR_WORKSPACE, "workspace is NULL");
+    if (misaligned(kept_lens, 4) || misaligned(block_tables, 4) || misaligned(context_lens, 4) ||
+        misaligned(context_lens_out, 4) || misaligned(free_blocks, 4) || misaligned(num_free, 4) ||
+        misaligned(num_free_out, 4) || misaligned(workspace, 4))
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+    if (num_seqs > 0 && kept_lens == context_lens_out)
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "kept_lens is also an output");
+    TablesParams p = {};
+    p.NB = num_blocks;
+    p.B = block_size;
+    p.S = num_seqs;
+    p.M = max_blocks_per_seq;
+    p.add = kept_lens;
+    p.tables = const_cast<int32_t *>(block_tables);       // read only when truncating
+    p.lens = context_lens;
+    p.lens_out = context_lens_out;
+    p.free_blocks = free_blocks;
+    p.num_free = num_free;
+    p.num_free_out = num_free_out;
+    // a few blocks a request come back
+    int64_t most = 4 * (int64_t)num_seqs;
+    if (most > num_blocks) most = num_blocks;
+    return run<TRUNCATE>(p, workspace, most, stream);
 }
 
 }  // extern "C"

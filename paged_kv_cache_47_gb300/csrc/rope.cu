@@ -37,6 +37,7 @@ constexpr int kThreads = 256;
 
 struct RopeParams {
     const int32_t *pos;
+    int64_t pos_st;              // several axes: from one axis's positions to the next's
     const int64_t *slots;        // with the append; else NULL
     const void *q, *k, *v;       // v: with the append only
     void *q_out, *k_out, *v_out; // k_out, v_out: the pools with the append
@@ -46,6 +47,7 @@ struct RopeParams {
     int parts;                   // CTAs a token
     unsigned *err;
     pkv_rope_plan plan;
+    uint8_t axis[PKV_ROPE_MAX_PAIRS];         // several axes: of each pair
 };
 
 template <typename T>
@@ -120,7 +122,7 @@ __device__ __forceinline__ void do_pair(const T *src, T *dst, int j, bool rotate
     dst[b] = y;
 }
 
-template <typename T, bool VECTORS>
+template <typename T, bool VECTORS, bool AXES>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 cs[PKV_ROPE_MAX_PAIRS];
     pkv::grid_dependents_launch();
@@ -128,8 +130,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int tok = blockIdx.x / p.parts, part = blockIdx.x - tok * p.parts;
     const int rd = p.plan.rotary_dim;
     if (threadIdx.x < rd / 2) {
-        const unsigned long long u = (unsigned long long)(long long)p.pos[tok] *
-                                     p.plan.turns[threadIdx.x];
+        const int32_t pos = AXES ? p.pos[p.axis[threadIdx.x] * p.pos_st + tok] : p.pos[tok];
+        const unsigned long long u = (unsigned long long)(long long)pos * p.plan.turns[threadIdx.x];
         // signed: half a turn either way, in units of pi
         float s, c;
         sincospif(__ll2float_rn((long long)u) * 0x1p-63f, &s, &c);
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 bool misaligned(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
-template <typename T>
+template <typename T, bool AXES>
 cudaError_t launch(RopeParams &p, int sms, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const int rd = p.plan.rotary_dim;
@@ -193,18 +195,19 @@ cudaError_t launch(RopeParams &p, int sms, cudaStream_t stream) {
     if (parts > wanted) parts = wanted;
     p.parts = parts;
     const dim3 grid((unsigned)(p.T * parts));
-    return vectors ? launch_chained(rope_kernel<T, true>, grid, kThreads, 0, stream, p)
-                   : launch_chained(rope_kernel<T, false>, grid, kThreads, 0, stream, p);
+    return vectors ? launch_chained(rope_kernel<T, true, AXES>, grid, kThreads, 0, stream, p)
+                   : launch_chained(rope_kernel<T, false, AXES>, grid, kThreads, 0, stream, p);
 }
 
+template <bool AXES>
 pkv_status run(int dtype, RopeParams &p, void *stream) {
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms = 0;
     const pkv_status st = pkv::device_sm_count(&sms);
     if (st != PKV_OK) return st;
-    const cudaError_t e = dtype == PKV_F32   ? launch<float>(p, sms, s)
-                          : dtype == PKV_F16 ? launch<__half>(p, sms, s)
-                                             : launch<__nv_bfloat16>(p, sms, s);
+    const cudaError_t e = dtype == PKV_F32   ? launch<float, AXES>(p, sms, s)
+                          : dtype == PKV_F16 ? launch<__half, AXES>(p, sms, s)
+                                             : launch<__nv_bfloat16, AXES>(p, sms, s);
     if (e != cudaSuccess)
         return pkv::set_last_error(PKV_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
     return PKV_OK;
@@ -240,6 +243,122 @@ pkv_status check_heads(int T, int Hq, int Hk) {
     if (Hq < 0 || Hk < 0 || Hq > 65536 || Hk > 65536)
         return pkv::set_last_error(PKV_ERR_INVALID_ARG, "head counts %d, %d", Hq, Hk);
     return PKV_OK;
+}
+
+// The plan's checks; axes: NULL, or the plan's axes.
+pkv_status check_axes(const pkv_rope_plan *plan, int D, const pkv_rope_axes_plan *axes, int64_t stride) {
+    const pkv_status st = check_plan(plan, D);
+    if (st != PKV_OK || !axes) return st;
+    if (axes->num_axes < 1 || axes->num_axes > PKV_ROPE_MAX_AXES)
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "not a plan of pkv_rope_axes_plan_init");
+    for (int i = 0; i < plan->rotary_dim / 2; ++i)
+        if (axes->axis[i] >= axes->num_axes)
+            return pkv::set_last_error(PKV_ERR_INVALID_ARG, "not a plan of pkv_rope_axes_plan_init");
+    if (stride < 0) return pkv::set_last_error(PKV_ERR_INVALID_ARG, "positions_stride %lld", (long long)stride);
+    return PKV_OK;
+}
+
+pkv_status run_axes(int dtype, RopeParams &p, const pkv_rope_axes_plan *axes, int64_t stride, void *stream) {
+    if (!axes) return run<false>(dtype, p, stream);
+    p.pos_st = stride;
+    memcpy(p.axis, axes->axis, sizeof(p.axis));
+    return run<true>(dtype, p, stream);
+}
+
+pkv_status rotate(int32_t dtype, int32_t head_dim, const pkv_rope_plan *plan, const pkv_rope_axes_plan *axes,
+                  const int32_t *positions, int64_t positions_stride, int32_t num_tokens, const void *q,
+                  int64_t q_stride, int32_t num_q_heads, void *q_out, int64_t q_out_stride, const void *k,
+                  int64_t k_stride, int32_t num_kv_heads, void *k_out, int64_t k_out_stride, void *stream) {
+    if (dtype != PKV_F32 && dtype != PKV_F16 && dtype != PKV_BF16)
+        return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "dtype %d", dtype);
+    if (head_dim != 64 && head_dim != 128)
+        return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
+    pkv_status st = check_axes(plan, head_dim, axes, positions_stride);
+    if (st != PKV_OK) return st;
+    if ((st = check_heads(num_tokens, num_q_heads, num_kv_heads)) != PKV_OK) return st;
+    if (num_tokens == 0 || num_q_heads + num_kv_heads == 0) return PKV_OK;
+    const int es = dtype == PKV_F32 ? 4 : 2;
+    if (!positions) return pkv::set_last_error(PKV_ERR_INVALID_ARG, "positions is NULL");
+    if (reinterpret_cast<uintptr_t>(positions) % 4)
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+    if (num_q_heads) {
+        if ((st = check_rows("q", q, q_stride, num_q_heads, head_dim, es)) != PKV_OK) return st;
+        if ((st = check_rows("q_out", q_out, q_out_stride, num_q_heads, head_dim, es)) != PKV_OK)
+            return st;
+    }
+    if (num_kv_heads) {
+        if ((st = check_rows("k", k, k_stride, num_kv_heads, head_dim, es)) != PKV_OK) return st;
+        if ((st = check_rows("k_out", k_out, k_out_stride, num_kv_heads, head_dim, es)) != PKV_OK)
+            return st;
+    }
+    if ((num_q_heads && q == q_out && q_stride != q_out_stride) ||
+        (num_kv_heads && k == k_out && k_stride != k_out_stride))
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "in place needs equal strides");
+    RopeParams p = {};
+    p.pos = positions;
+    p.q = q;
+    p.k = k;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.q_st = q_stride;
+    p.k_st = k_stride;
+    p.qo_st = q_out_stride;
+    p.ko_st = k_out_stride;
+    p.T = num_tokens;
+    p.Hq = num_q_heads;
+    p.Hk = num_kv_heads;
+    p.D = head_dim;
+    p.plan = *plan;
+    return run_axes(dtype, p, axes, positions_stride, stream);
+}
+
+pkv_status rotate_append(const pkv_cache_desc *cache, const pkv_rope_plan *plan, const pkv_rope_axes_plan *axes,
+                         const int32_t *positions, int64_t positions_stride, const int64_t *slot_mapping,
+                         int32_t num_tokens, const void *q, int64_t q_stride, int32_t num_q_heads, void *q_out,
+                         int64_t q_out_stride, const void *k_new, int64_t k_stride, const void *v_new,
+                         int64_t v_stride, void *k_pool, void *v_pool, void *stream) {
+    pkv_status st = pkv::check_cache_desc(cache);
+    if (st != PKV_OK) return st;
+    if ((st = check_axes(plan, cache->head_dim, axes, positions_stride)) != PKV_OK) return st;
+    const int D = cache->head_dim, Hk = cache->num_kv_heads, es = cache->dtype == PKV_F32 ? 4 : 2;
+    if ((st = check_heads(num_tokens, num_q_heads, Hk)) != PKV_OK) return st;
+    if (num_tokens == 0) return PKV_OK;
+    if (!positions || !slot_mapping || !k_pool || !v_pool)
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "a pointer argument is NULL");
+    if (reinterpret_cast<uintptr_t>(positions) % 4 || reinterpret_cast<uintptr_t>(slot_mapping) % 8 ||
+        misaligned(k_pool) || misaligned(v_pool))
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG,
+                                   "pools must be 16-byte aligned (slot_mapping 8, positions 4)");
+    if (num_q_heads) {
+        if ((st = check_rows("q", q, q_stride, num_q_heads, D, es)) != PKV_OK) return st;
+        if ((st = check_rows("q_out", q_out, q_out_stride, num_q_heads, D, es)) != PKV_OK) return st;
+        if (q == q_out && q_stride != q_out_stride)
+            return pkv::set_last_error(PKV_ERR_INVALID_ARG, "in place needs equal strides");
+    }
+    if ((st = check_rows("k_new", k_new, k_stride, Hk, D, es)) != PKV_OK) return st;
+    if ((st = check_rows("v_new", v_new, v_stride, Hk, D, es)) != PKV_OK) return st;
+    RopeParams p = {};
+    if ((st = pkv::device_error_word(&p.err)) != PKV_OK) return st;
+    p.pos = positions;
+    p.slots = slot_mapping;
+    p.q = q;
+    p.k = k_new;
+    p.v = v_new;
+    p.q_out = q_out;
+    p.k_out = k_pool;
+    p.v_out = v_pool;
+    p.q_st = q_stride;
+    p.k_st = k_stride;
+    p.v_st = v_stride;
+    p.qo_st = q_out_stride;
+    p.T = num_tokens;
+    p.Hq = num_q_heads;
+    p.Hk = Hk;
+    p.D = D;
+    p.NB = cache->num_blocks;
+    p.B = cache->block_size;
+    p.plan = *plan;
+    return run_axes(cache->dtype, p, axes, positions_stride, stream);
 }
 
 }  // namespace
@@ -320,47 +439,8 @@ pkv_status pkv_rope(int32_t dtype, int32_t head_dim, const pkv_rope_plan *plan,
                     int32_t num_q_heads, void *q_out, int64_t q_out_stride, const void *k,
                     int64_t k_stride, int32_t num_kv_heads, void *k_out, int64_t k_out_stride,
                     void *stream) {
-    if (dtype != PKV_F32 && dtype != PKV_F16 && dtype != PKV_BF16)
-        return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "dtype %d", dtype);
-    if (head_dim != 64 && head_dim != 128)
-        return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
-    pkv_status st = check_plan(plan, head_dim);
-    if (st != PKV_OK) return st;
-    if ((st = check_heads(num_tokens, num_q_heads, num_kv_heads)) != PKV_OK) return st;
-    if (num_tokens == 0 || num_q_heads + num_kv_heads == 0) return PKV_OK;
-    const int es = dtype == PKV_F32 ? 4 : 2;
-    if (!positions) return pkv::set_last_error(PKV_ERR_INVALID_ARG, "positions is NULL");
-    if (reinterpret_cast<uintptr_t>(positions) % 4)
-        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "positions must be 4-byte aligned");
-    if (num_q_heads) {
-        if ((st = check_rows("q", q, q_stride, num_q_heads, head_dim, es)) != PKV_OK) return st;
-        if ((st = check_rows("q_out", q_out, q_out_stride, num_q_heads, head_dim, es)) != PKV_OK)
-            return st;
-    }
-    if (num_kv_heads) {
-        if ((st = check_rows("k", k, k_stride, num_kv_heads, head_dim, es)) != PKV_OK) return st;
-        if ((st = check_rows("k_out", k_out, k_out_stride, num_kv_heads, head_dim, es)) != PKV_OK)
-            return st;
-    }
-    if ((num_q_heads && q == q_out && q_stride != q_out_stride) ||
-        (num_kv_heads && k == k_out && k_stride != k_out_stride))
-        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "in place needs equal strides");
-    RopeParams p = {};
-    p.pos = positions;
-    p.q = q;
-    p.k = k;
-    p.q_out = q_out;
-    p.k_out = k_out;
-    p.q_st = q_stride;
-    p.k_st = k_stride;
-    p.qo_st = q_out_stride;
-    p.ko_st = k_out_stride;
-    p.T = num_tokens;
-    p.Hq = num_q_heads;
-    p.Hk = num_kv_heads;
-    p.D = head_dim;
-    p.plan = *plan;
-    return run(dtype, p, stream);
+    return rotate(dtype, head_dim, plan, nullptr, positions, 0, num_tokens, q, q_stride, num_q_heads, q_out,
+                  q_out_stride, k, k_stride, num_kv_heads, k_out, k_out_stride, stream);
 }
 
 pkv_status pkv_rope_append(const pkv_cache_desc *cache, const pkv_rope_plan *plan,
@@ -369,48 +449,68 @@ pkv_status pkv_rope_append(const pkv_cache_desc *cache, const pkv_rope_plan *pla
                            int32_t num_q_heads, void *q_out, int64_t q_out_stride,
                            const void *k_new, int64_t k_stride, const void *v_new,
                            int64_t v_stride, void *k_pool, void *v_pool, void *stream) {
-    pkv_status st = pkv::check_cache_desc(cache);
-    if (st != PKV_OK) return st;
-    if ((st = check_plan(plan, cache->head_dim)) != PKV_OK) return st;
-    const int D = cache->head_dim, Hk = cache->num_kv_heads, es = cache->dtype == PKV_F32 ? 4 : 2;
-    if ((st = check_heads(num_tokens, num_q_heads, Hk)) != PKV_OK) return st;
-    if (num_tokens == 0) return PKV_OK;
-    if (!positions || !slot_mapping || !k_pool || !v_pool)
-        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "a pointer argument is NULL");
-    if (reinterpret_cast<uintptr_t>(positions) % 4 || reinterpret_cast<uintptr_t>(slot_mapping) % 8 ||
-        misaligned(k_pool) || misaligned(v_pool))
-        return pkv::set_last_error(PKV_ERR_INVALID_ARG,
-                                   "pools must be 16-byte aligned (slot_mapping 8, positions 4)");
-    if (num_q_heads) {
-        if ((st = check_rows("q", q, q_stride, num_q_heads, D, es)) != PKV_OK) return st;
-        if ((st = check_rows("q_out", q_out, q_out_stride, num_q_heads, D, es)) != PKV_OK) return st;
-        if (q == q_out && q_stride != q_out_stride)
-            return pkv::set_last_error(PKV_ERR_INVALID_ARG, "in place needs equal strides");
+    return rotate_append(cache, plan, nullptr, positions, 0, slot_mapping, num_tokens, q, q_stride, num_q_heads,
+                         q_out, q_out_stride, k_new, k_stride, v_new, v_stride, k_pool, v_pool, stream);
+}
+
+pkv_status pkv_rope_axes_plan_init(const pkv_rope_axes_desc *d, pkv_rope_axes_plan *plan) {
+    if (!d || !plan) return pkv::set_last_error(PKV_ERR_INVALID_ARG, "a pointer argument is NULL");
+    if (d->num_axes < 1 || d->num_axes > PKV_ROPE_MAX_AXES)
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "num_axes %d (1..%d)", d->num_axes, PKV_ROPE_MAX_AXES);
+    if ((d->order != PKV_ROPE_SECTIONS && d->order != PKV_ROPE_CYCLED) ||
+        (d->frequencies != PKV_ROPE_SHARED && d->frequencies != PKV_ROPE_OWN))
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "order %d, frequencies %d", d->order, d->frequencies);
+    int64_t pairs = 0;
+    for (int a = 0; a < d->num_axes; ++a) {
+        if (d->sections[a] < 1)
+            return pkv::set_last_error(PKV_ERR_INVALID_ARG, "sections[%d] is %d", a, d->sections[a]);
+        pairs += d->sections[a];
     }
-    if ((st = check_rows("k_new", k_new, k_stride, Hk, D, es)) != PKV_OK) return st;
-    if ((st = check_rows("v_new", v_new, v_stride, Hk, D, es)) != PKV_OK) return st;
-    RopeParams p = {};
-    if ((st = pkv::device_error_word(&p.err)) != PKV_OK) return st;
-    p.pos = positions;
-    p.slots = slot_mapping;
-    p.q = q;
-    p.k = k_new;
-    p.v = v_new;
-    p.q_out = q_out;
-    p.k_out = k_pool;
-    p.v_out = v_pool;
-    p.q_st = q_stride;
-    p.k_st = k_stride;
-    p.v_st = v_stride;
-    p.qo_st = q_out_stride;
-    p.T = num_tokens;
-    p.Hq = num_q_heads;
-    p.Hk = Hk;
-    p.D = D;
-    p.NB = cache->num_blocks;
-    p.B = cache->block_size;
-    p.plan = *plan;
-    return run(cache->dtype, p, stream);
+    if (2 * pairs != d->rope.rotary_dim)
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "sections hold %lld pairs, rotary_dim %d has %d",
+                                   (long long)pairs, d->rope.rotary_dim, d->rope.rotary_dim / 2);
+    pkv_rope_axes_plan r = {};
+    pkv_status st = pkv_rope_plan_init(&d->rope, &r.plan);
+    if (st != PKV_OK) return st;
+    r.num_axes = d->num_axes;
+    pkv_rope_plan own[PKV_ROPE_MAX_AXES];
+    for (int a = 0; a < d->num_axes && d->frequencies == PKV_ROPE_OWN; ++a) {
+        pkv_rope_desc one = d->rope;
+        one.rotary_dim = 2 * d->sections[a];
+        if ((st = pkv_rope_plan_init(&one, &own[a])) != PKV_OK) return st;
+    }
+    int used[PKV_ROPE_MAX_AXES] = {}, a = 0;
+    for (int i = 0; i < (int)pairs; ++i) {
+        if (d->order == PKV_ROPE_CYCLED && i) a = (a + 1) % d->num_axes;
+        while (used[a] == d->sections[a]) a = (a + 1) % d->num_axes;
+        r.axis[i] = (uint8_t)a;
+        if (d->frequencies == PKV_ROPE_OWN) r.plan.turns[i] = own[a].turns[used[a]];
+        ++used[a];
+    }
+    *plan = r;
+    return PKV_OK;
+}
+
+pkv_status pkv_rope_axes(int32_t dtype, int32_t head_dim, const pkv_rope_axes_plan *plan,
+                         const int32_t *positions, int64_t positions_stride, int32_t num_tokens,
+                         const void *q, int64_t q_stride, int32_t num_q_heads, void *q_out,
+                         int64_t q_out_stride, const void *k, int64_t k_stride,
+                         int32_t num_kv_heads, void *k_out, int64_t k_out_stride, void *stream) {
+    return rotate(dtype, head_dim, plan ? &plan->plan : nullptr, plan, positions, positions_stride, num_tokens, q,
+                  q_stride, num_q_heads, q_out, q_out_stride, k, k_stride, num_kv_heads, k_out, k_out_stride,
+                  stream);
+}
+
+pkv_status pkv_rope_axes_append(const pkv_cache_desc *cache, const pkv_rope_axes_plan *plan,
+                                const int32_t *positions, int64_t positions_stride,
+                                const int64_t *slot_mapping, int32_t num_tokens, const void *q,
+                                int64_t q_stride, int32_t num_q_heads, void *q_out,
+                                int64_t q_out_stride, const void *k_new, int64_t k_stride,
+                                const void *v_new, int64_t v_stride, void *k_pool, void *v_pool,
+                                void *stream) {
+    return rotate_append(cache, plan ? &plan->plan : nullptr, plan, positions, positions_stride, slot_mapping,
+                         num_tokens, q, q_stride, num_q_heads, q_out, q_out_stride, k_new, k_stride, v_new,
+                         v_stride, k_pool, v_pool, stream);
 }
 
 }  // extern "C"
