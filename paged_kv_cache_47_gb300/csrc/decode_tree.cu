@@ -205,16 +205,13 @@ cudaError_t launch(int dtype, const TreeParams &p, cudaStream_t stream) {
 struct Shape {
     int rows, tile, ctas;
 };
-pkv_status shape_of(const pkv_cache_desc *c, int Hq, int max_tree, int ctas, Shape *s) {
-    s->rows = kRows;
-    s->tile = kTile;
-    s->ctas = ctas;
-    if (ctas == 0) {
-        const pkv_status st = pkv::device_sm_count(&s->ctas);
-        if (st != PKV_OK) return st;
-        s->ctas *= kCtasPerSm;
-    }
-    return PKV_OK;
+Shape shape_of(const pkv_cache_desc *c, int Hq, int max_tree) { return {kRows, kTile, 0}; }
+pkv_status ctas_of(int asked, Shape *s) {
+    s->ctas = asked;
+    if (asked) return PKV_OK;
+    const pkv_status st = pkv::device_sm_count(&s->ctas);
+    s->ctas *= kCtasPerSm;
+    return st;
 }
 
 size_t workspace_for(const Shape &s, int D) {
@@ -244,10 +241,9 @@ extern "C" {
 
 size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc *cache, int32_t num_q_heads,
                                        int32_t max_tree, int32_t num_ctas) {
-    Shape s;
-    if (check_shape(cache, num_q_heads, max_tree, num_ctas) != PKV_OK ||
-        shape_of(cache, num_q_heads, max_tree, num_ctas, &s) != PKV_OK)
-        return 0;
+    if (check_shape(cache, num_q_heads, max_tree, num_ctas) != PKV_OK) return 0;
+    Shape s = shape_of(cache, num_q_heads, max_tree);
+    if (ctas_of(num_ctas, &s) != PKV_OK) return 0;
     return workspace_for(s, cache->head_dim);
 }
 
@@ -283,8 +279,7 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
         return pkv::set_last_error(PKV_ERR_INVALID_ARG,
                                    "q and the pools must be 16-byte aligned, out to four of its elements, the others "
                                    "to their elements");
-    Shape shape;
-    if ((st = shape_of(cache, num_q_heads, max_tree, asked, &shape)) != PKV_OK) return st;
+    Shape shape = shape_of(cache, num_q_heads, max_tree);
     const int G = num_q_heads / Hk, RC = shape.rows;
     // the list's places fit 32 bits
     const int64_t capacity = (int64_t)M * cache->block_size, seqs = num_seqs < pkv::kTreeMaxSeqs ? num_seqs : pkv::kTreeMaxSeqs;
@@ -293,6 +288,7 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
     if ((int64_t)cache->num_blocks * Hk > INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");
+    if ((st = ctas_of(asked, &shape)) != PKV_OK) return st;
     const size_t need = workspace_for(shape, D);
     if (!workspace || workspace_bytes < need)
         return pkv::set_last_error(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
