@@ -38,16 +38,9 @@ struct Shared {
     int scan[kThreads / 32];
 };
 
-// Four elements as fp32.
 __device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-    const float2 a = pkv::Elem<T>::unpack2(w.x), b = pkv::Elem<T>::unpack2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared<D> &sh = *reinterpret_cast<Shared<D> *>(raw);
@@ -58,7 +51,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     TreePlace at;
     const TreeShare share = pkv::tree_share<kTile, kThreads>(p, sh.prefix, sh.scan, at);
     if (tid == 0) p.cuts[blockIdx.x].parts = 0;
-    const T *kp = static_cast<const T *>(p.k), *vp = static_cast<const T *>(p.v), *qp = static_cast<const T *>(p.q);
+    const float *kp = static_cast<const float *>(p.k), *vp = static_cast<const float *>(p.v), *qp = static_cast<const float *>(p.q);
     const int B = 1 << p.b.lb;
     for (int left = share.Z - share.A, done = 0; left > 0;) {
         const int count = min(at.tiles - at.i, left), i0 = at.i, P = at.q.L - at.q.n;
@@ -175,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simt(const TreeParams &p, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
@@ -183,18 +176,16 @@ cudaError_t launch_simt(const TreeParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(tree_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared<D>));
+        e = cudaFuncSetAttribute(tree_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared<D>));
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_chained(tree_simt_kernel<T, D>, dim3((unsigned)p.C), kThreads, sizeof(Shared<D>), stream, p);
+    return launch_chained(tree_simt_kernel<D>, dim3((unsigned)p.C), kThreads, sizeof(Shared<D>), stream, p);
 }
 
 template <int D>
 cudaError_t launch(int dtype, const TreeParams &p, cudaStream_t stream) {
-    cudaError_t e = dtype == PKV_F32   ? launch_simt<float, D>(p, stream)
-                    : dtype == PKV_F16 ? launch_simt<__half, D>(p, stream)
-                                       : launch_simt<__nv_bfloat16, D>(p, stream);
+    cudaError_t e = dtype == PKV_F32 ? launch_simt<D>(p, stream) : pkv::launch_tree_mma(dtype, D, p, stream);
     if (e != cudaSuccess) return e;
     int y = (p.RC + pkv::kTreeJoinWarps - 1) / pkv::kTreeJoinWarps;
     if (y > 8) y = 8;
@@ -205,12 +196,18 @@ cudaError_t launch(int dtype, const TreeParams &p, cudaStream_t stream) {
 struct Shape {
     int rows, tile, ctas;
 };
-Shape shape_of(const pkv_cache_desc *c, int Hq, int max_tree) { return {kRows, kTile, 0}; }
-pkv_status ctas_of(int asked, Shape *s) {
+Shape shape_of(const pkv_cache_desc *c, int Hq, int max_tree) {
+    if (c->dtype == PKV_F32) return {kRows, kTile, 0};
+    // what the largest tree needs, up to two row tiles: they share each tile of K
+    // and V, which more rows would read again
+    const int64_t rows = (int64_t)max_tree * (Hq / c->num_kv_heads), most = 2 * pkv::kTreeMmaTile;
+    return {(int)(rows < most ? rows : most), pkv::kTreeMmaTile, 0};
+}
+pkv_status ctas_of(const pkv_cache_desc *c, int asked, Shape *s) {
     s->ctas = asked;
     if (asked) return PKV_OK;
     const pkv_status st = pkv::device_sm_count(&s->ctas);
-    s->ctas *= kCtasPerSm;
+    if (c->dtype == PKV_F32) s->ctas *= kCtasPerSm;
     return st;
 }
 
@@ -243,7 +240,7 @@ size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc *cache, int32_t num_
                                        int32_t max_tree, int32_t num_ctas) {
     if (check_shape(cache, num_q_heads, max_tree, num_ctas) != PKV_OK) return 0;
     Shape s = shape_of(cache, num_q_heads, max_tree);
-    if (ctas_of(num_ctas, &s) != PKV_OK) return 0;
+    if (ctas_of(cache, num_ctas, &s) != PKV_OK) return 0;
     return workspace_for(s, cache->head_dim);
 }
 
@@ -272,13 +269,12 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
     if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
     if (!q || !k_pool || !v_pool || !block_tables || !context_lens || !token_offsets || !out)
         return pkv::set_last_error(PKV_ERR_INVALID_ARG, "a pointer argument is NULL");
-    const int D = cache->head_dim, Hk = cache->num_kv_heads, oes = out_dtype == PKV_F32 ? 4 : 2;
-    if (misaligned(q, 16) || misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(out, 4 * oes) ||
+    const int D = cache->head_dim, Hk = cache->num_kv_heads;
+    if (misaligned(q, 16) || misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(out, 16) ||
         misaligned(block_tables, 4) || misaligned(context_lens, 4) || misaligned(token_offsets, 4) ||
         misaligned(masks, 8) || (options && misaligned(options->lse_out, 4)))
         return pkv::set_last_error(PKV_ERR_INVALID_ARG,
-                                   "q and the pools must be 16-byte aligned, out to four of its elements, the others "
-                                   "to their elements");
+                                   "q, the pools and out must be 16-byte aligned, the others to their elements");
     Shape shape = shape_of(cache, num_q_heads, max_tree);
     const int G = num_q_heads / Hk, RC = shape.rows;
     // the list's places fit 32 bits
@@ -288,7 +284,7 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
     if ((int64_t)cache->num_blocks * Hk > INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");
-    if ((st = ctas_of(asked, &shape)) != PKV_OK) return st;
+    if ((st = ctas_of(cache, asked, &shape)) != PKV_OK) return st;
     const size_t need = workspace_for(shape, D);
     if (!workspace || workspace_bytes < need)
         return pkv::set_last_error(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
@@ -297,8 +293,7 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
         return pkv::set_last_error(PKV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
     TreeParams p = {};
     if ((st = pkv::device_error_word(&p.b.err)) != PKV_OK) return st;
-    int drop;
-    pkv::next_wait_fault(&p.wait_ns, &drop);
+    if (cache->dtype != PKV_F32) pkv::next_wait_fault(&p.wait_ns, &p.drop_arrival);
     p.b.T = num_tokens;
     p.b.N = max_tree;
     p.b.M = M;

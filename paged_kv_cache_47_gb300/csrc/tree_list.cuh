@@ -25,6 +25,7 @@ namespace pkv {
 
 constexpr int kTreeMaxSeqs = 1024;       // sequences of one launch
 constexpr int kTreeJoinWarps = 8;
+constexpr int kTreeMmaTile = 128;        // tokens of a tile, and rows of a row tile, on the tensor cores
 
 // What the CTA in which a cut unit begins writes down for the join.
 struct TreeCut {
@@ -46,8 +47,12 @@ struct TreeParams {
     float scale_log2;
     float *ws_o, *ws_lse;                // [C][2][RC][D], [C][2][RC]
     TreeCut *cuts;                       // [C]
-    unsigned long long wait_ns;
+    unsigned long long wait_ns;          // bounded waits, as in DecodeParams
+    int drop_arrival;
 };
+
+// 16-bit caches (decode_tree_mma.cu).
+cudaError_t launch_tree_mma(int dtype, int D, const TreeParams &p, cudaStream_t s);
 
 __device__ __forceinline__ int tree_units(const TreeParams &p, int n) {
     return p.Hk * ((n * p.G + p.RC - 1) / p.RC);
@@ -167,17 +172,19 @@ __device__ __forceinline__ void tree_store(const TreeParams &p, size_t at, const
         return;
     }
     float a, b;
+    uint32_t w[E / 2];
 #pragma unroll
-    for (int i = 0; i < E; i += 4) {
-        uint2 w;
-        if (p.out_dtype == PKV_F16) {
-            w.x = Elem<__half>::pack2(o[i], o[i + 1], a, b);
-            w.y = Elem<__half>::pack2(o[i + 2], o[i + 3], a, b);
-        } else {
-            w.x = Elem<__nv_bfloat16>::pack2(o[i], o[i + 1], a, b);
-            w.y = Elem<__nv_bfloat16>::pack2(o[i + 2], o[i + 3], a, b);
-        }
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at + i) = w;
+    for (int i = 0; i < E; i += 2)
+        w[i / 2] = p.out_dtype == PKV_F16 ? Elem<__half>::pack2(o[i], o[i + 1], a, b)
+                                          : Elem<__nv_bfloat16>::pack2(o[i], o[i + 1], a, b);
+    uint16_t *dst = static_cast<uint16_t *>(p.out) + at;
+    if constexpr (E % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < E; i += 8)
+            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) *reinterpret_cast<uint2 *>(dst + i) = make_uint2(w[i / 2], w[i / 2 + 1]);
     }
 }
 
