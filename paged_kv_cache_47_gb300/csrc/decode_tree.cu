@@ -185,7 +185,9 @@ cudaError_t launch_simt(const TreeParams &p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch(int dtype, const TreeParams &p, cudaStream_t stream) {
-    cudaError_t e = dtype == PKV_F32 ? launch_simt<D>(p, stream) : pkv::launch_tree_mma(dtype, D, p, stream);
+    cudaError_t e = dtype == PKV_F32   ? launch_simt<D>(p, stream)
+                    : dtype == PKV_F16 ? pkv::launch_tree_f16(D, p, stream)
+                                       : pkv::launch_tree_bf16(D, p, stream);
     if (e != cudaSuccess) return e;
     int y = (p.RC + pkv::kTreeJoinWarps - 1) / pkv::kTreeJoinWarps;
     if (y > 8) y = 8;

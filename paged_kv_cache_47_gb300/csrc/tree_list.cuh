@@ -51,8 +51,9 @@ struct TreeParams {
     int drop_arrival;
 };
 
-// 16-bit caches (decode_tree_mma.cu).
-cudaError_t launch_tree_mma(int dtype, int D, const TreeParams &p, cudaStream_t s);
+// 16-bit caches (tree_mma.cuh).
+cudaError_t launch_tree_bf16(int D, const TreeParams &p, cudaStream_t s);
+cudaError_t launch_tree_f16(int D, const TreeParams &p, cudaStream_t s);
 
 __device__ __forceinline__ int tree_units(const TreeParams &p, int n) {
     return p.Hk * ((n * p.G + p.RC - 1) / p.RC);

@@ -1,0 +1,909 @@
+// Tree attention over 16-bit caches on the 5th-generation tensor cores.
+//
+// Products. A unit's rows (a q head of a drafted token each) are the M of
+// tcgen05.mma, 128 at a time: S[128 rows][128 tokens] = Q K^T, Q and K from
+// shared memory as they were copied, and O[128 rows][D] += P V, P from tensor
+// memory, V from shared memory read along its tokens. A thread owns a row: the
+// softmax's maximum and sum need no other thread. K and V are read once for
+// all rows of a kv head, so up to 128 rows (or 256, in two tiles that share
+// each K and V) cost the memory what one row does.
+//
+// P enters as two parts, hi = the type's nearest and lo = the rest's, so
+// weights keep 16 (bf16) or 22 (fp16) bits: with hi alone a bf16 output's error
+// against 64 bits grows by half (weights are rounded like the parts lie where their scores lay: 16 scores become 8 words of hi and 8 of lo.
+//
+// Roles. Four warps copy K, V (tiles of 128 tokens, a ring of half-tiles) and q
+// rows through cp.async, whose 16-byte pieces serve blocks of 8 to 32 tokens
+// as well as long runs. Two groups of four warps each take a tile through both
+// products; a group's chain (product, softmax, product) is long, so units of up
+// to 128 rows give their tiles to the groups in turn and join the two states,
+// which lie in the same lanes of tensor memory, at the end. Units of more rows
+// give each group its own 128 rows, and every tile.
+//
+// The softmax's reference exponent moves only when a score passes what the type
+// holds; only then are the outputs rescaled, by one read and write of them.
+//
+// What a row does not see has weight zero; as zero times infinity is not zero,
+// tiles with drafted tokens are looked through for V that are not finite, and
+// such a tile's second product is done on the CUDA cores, over what has weight.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "device_utils.cuh"
+#include "launch_utils.h"
+#include "pkv_internal.h"
+#include "tree_list.cuh"
+
+namespace {
+
+using pkv::launch_chained;
+using pkv::TreeParams;
+using pkv::TreePlace;
+using pkv::TreeShare;
+
+constexpr int kTile = pkv::kTreeMmaTile;       // 128 tokens
+constexpr int kSub = 64;                       // tokens of a product
+constexpr int kGroups = 2, kGroupThreads = 128, kGroupWarps = 4;
+constexpr int kKWarps = 2, kVWarps = 2;        // that copy K, and V
+constexpr int kSoftmaxThreads = kGroups * kGroupThreads;
+constexpr int kThreads = kSoftmaxThreads + 32 * (kGroups + kKWarps + kVWarps + 1);
+constexpr int kMetas = 16;                     // more than the tiles a ring holds
+constexpr uint32_t kColumns = 512;             // tensor memory: each group twice kSub of S, then O
+constexpr float kNone = 2e-38f;                // reference exponent before a row's first finite score
+
+// Exponent that a reference gives the top score, and the largest that needs no new one.
+template <typename T> constexpr float kTop = 0.f;
+template <> constexpr float kTop<__half> = 10.f;
+template <typename T> constexpr float kRoom = 8.f;
+template <> constexpr float kRoom<__half> = 15.f;
+
+// A tile as its groups see it.
+struct Tile {
+    int o, n, L, g;          // first q row, drafted tokens, context, kv head
+    int r0, nr;              // the unit's first row and rows
+    int t0;                  // first token
+    int at, left;            // tiles of the segment before and after it
+    int seg;                 // the CTA's segments before it
+    int whole, slot;         // whole unit, or slot of the piece
+};
+
+// Rows of a unit at most: 64 and 128 take one row tile, 256 two.
+template <int D, int ROWS>
+struct Cfg {
+    static constexpr int kTwo = ROWS > kTile;                // each group its own rows
+    static constexpr int kPlanes = D / 64;                   // of 64 elements, 128 bytes a row
+    static constexpr int kPlane = kTile * 128;
+    static constexpr int kSlot = kPlanes * kPlane;           // K or V of a tile
+    static constexpr int kQPlane = (kTwo ? kTile : ROWS) * 128;
+    static constexpr int kQTile = kPlanes * kQPlane;         // q of a row tile
+    static constexpr int kQBufs = ROWS == 64 ? 2 : 1;
+    static constexpr int kQ = (kTwo ? 2 : 1) * kQTile;       // q of a unit
+    // Rings of K and of V, with q 224 KB (D 64: less). Where the groups take turns
+    // the rings' sizes are even: a slot's last tile was then this group's own, so
+    // that a barrier's parity names one phase for it. (Copies of a later tile may
+    // land before those of an earlier one.)
+    static constexpr int kSlots = (kTwo ? 5 : 6) * (128 / D);
+    static constexpr int kK = kTwo ? kSlots / 2 : D == 128 ? 2 : 6, kV = kSlots - kK;
+    static_assert(kTwo || (kK % 2 == 0 && kV % 2 == 0), "");
+    static constexpr int kBytes = kQBufs * kQ + kSlots * kSlot;
+};
+
+struct Control {
+    uint64_t full_k[6], free_k[6], full_v[6], free_v[6], free_q[2];
+    uint64_t s[kGroups][2], p[kGroups][2], o[kGroups][2], meet[kGroups], state[kGroups], taken[kGroups];
+    Tile tiles[kMetas];
+    int odd[kGroups][2];             // product (+ 1) last found to have V that are not finite, by turns
+    int skip[kGroups][2];            // by buffer: the weights are used up already
+    int which[kGroups][2];           // by buffer: twice the tile, and the product of it; -1: no more
+    float2 told[kTile];              // a state's reference and sum, for the other group
+    uint32_t tmem;
+};
+
+template <typename T>
+constexpr uint32_t idesc(int N, bool b_mn, bool negate) {
+    constexpr uint32_t f = sizeof(T) == 2 && !std::is_same<T, __half>::value ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((negate ? 1u : 0u) << 13) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"(accumulate)
+        : "memory");
+}
+// A from tensor memory: lane = row, 8 columns = 16 elements along K.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"(accumulate)
+        : "memory");
+}
+
+#define PKV_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define PKV_M8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+#define PKV_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// 32 columns of this thread's lane; valid after tm_wait on them.
+__device__ __forceinline__ void tm_load(uint32_t at, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
+        "%23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : PKV_R8(r, 0), PKV_R8(r, 8), PKV_R8(r, 16), PKV_R8(r, 24)
+        : "r"(at));
+}
+__device__ __forceinline__ void tm_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_M8(r, 0), PKV_M8(r, 8), PKV_M8(r, 16), PKV_M8(r, 24) : : "memory");
+}
+__device__ __forceinline__ void tm_store(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
+        "%23, %24, %25, %26, %27, %28, %29, %30, %31};" ::PKV_W8(r, 0),
+        PKV_W8(r, 8), PKV_W8(r, 16), PKV_W8(r, 24), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::PKV_W8(r, 0),
+        PKV_W8(r, 8), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float f32(uint32_t x) { return __uint_as_float(x); }
+
+// ---------------------------------------------------------------- copies
+__device__ __forceinline__ bool warp_wait(const TreeParams &p, uint64_t &bar, uint32_t parity) {
+    return __all_sync(~0u, pkv::mbar_wait(pkv::smem_u32(&bar), parity & 1, p.b.err, p.wait_ns));
+}
+
+// A segment: the tiles of one unit that lie in this CTA's share.
+struct Segment {
+    int n, i0, g, r0, nr;
+    bool whole;
+};
+__device__ __forceinline__ Segment segment(const TreeParams &p, const TreePlace &at, int left) {
+    Segment x;
+    x.n = min(at.tiles - at.i, left);
+    x.i0 = at.i;
+    const int chunks = at.units / p.Hk;
+    x.g = at.u / chunks;
+    x.r0 = (at.u - x.g * chunks) * p.RC;
+    x.nr = min(p.RC, at.q.n * p.G - x.r0);
+    x.whole = x.n == at.tiles;
+    return x;
+}
+
+// Copies of K, or of V, into a ring of its own; a tile's tokens shared out to its warps.
+template <int D, int ROWS, int LB, bool V>
+struct Producer {
+    using C = Cfg<D, ROWS>;
+    static constexpr int kRows = kTile / (V ? kVWarps : kKWarps);
+    static constexpr int E = kRows >> LB;                    // blocks of a warp's tokens of a tile
+    static constexpr int kAhead = 32 / E;                    // tiles whose entries a warp holds
+    static constexpr int kPieces = kRows * C::kPlanes * 8 / 32;    // 16-byte pieces a lane copies of a tile
+    static constexpr int kRing = V ? C::kV : C::kK;
+    const TreeParams &p;
+    Control *ctl;
+    uint32_t base;                                           // the ring
+    int lane, pw;
+    int32_t window, next_window;
+    int from;                                                // tile that the window begins at
+
+    __device__ __forceinline__ int32_t entries(int s, int tile) const {
+        const int e = (tile + lane / E) * (kTile >> LB) + pw * E + lane % E;
+        return e < p.b.M ? __ldg(p.tables + (int64_t)s * p.b.M + e) : -1;
+    }
+
+    // Lane's destination of its piece j of the warp's rows, of which piece 0's is
+    // at lane_at: rows are 128 bytes and their pieces exclusive-ored by the row
+    // modulo 8, so later pieces differ by a constant and a constant's bits.
+    static __device__ __forceinline__ uint32_t lane_at(int pw, int lane) {
+        if (D == 128) return pw * kRows * 128 + (lane >> 3 & 1) * C::kPlane + (lane >> 4) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
+        return pw * kRows * 128 + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+    }
+    static __device__ __forceinline__ uint32_t piece(uint32_t at, int j) {
+        return D == 128 ? (at ^ ((2 * j & 6) << 4)) + j * 256 : (at ^ ((4 * j & 4) << 4)) + j * 512;
+    }
+
+    // A context's last tile, or one with a block id outside the pool (its rows
+    // become zeros). Scores of rows past the context are not looked at, so those
+    // of K may hold anything; V's are zeros up to the product's last 16 tokens.
+    static __device__ __noinline__ void ragged(const TreeParams &p, const uint8_t *pool, uint32_t slot, int32_t ids, int at, int g,
+                                               int left, int pw) {
+        const int lane = threadIdx.x & 31;
+        constexpr int R = C::kPlanes * 8;                    // pieces of a row
+        const int rows = max(0, min(kRows, (V ? (left + 15) & ~15 : left) - pw * kRows));
+        const uint32_t to = slot + lane_at(pw, lane);
+#pragma unroll 4
+        for (int j = 0; j < (rows * R + 31) / 32; ++j) {
+            const int r = (lane + 32 * j) / R, w = (lane + 32 * j) % R;
+            const int id = __shfl_sync(~0u, ids, at + (r >> LB));
+            const bool in = pw * kRows + r < left, ok = (unsigned)id < (unsigned)p.NB;
+            if (in && !ok && !V) atomicOr(p.b.err, PKV_DEVERR_BLOCK_ID);
+            const size_t src = ((((size_t)(ok ? id : 0) * p.Hk + g) << LB) + (r & ((1 << LB) - 1))) * (2 * D) + w * 16;
+            pkv::cp_async_16(piece(to, j), pool + src, in && ok);
+        }
+    }
+
+    __device__ __forceinline__ void copy(uint32_t slot, int32_t ids, int at, int g, int left) const {
+        const uint8_t *src = static_cast<const uint8_t *>(V ? p.v : p.k);
+        const int32_t mine = __shfl_sync(~0u, ids, at + lane % E);
+        if (left < kTile || __any_sync(~0u, (unsigned)mine >= (unsigned)p.NB)) {
+            ragged(p, src, slot, ids, at, g, left, pw);
+            return;
+        }
+        constexpr int PB = kPieces / E;                      // pieces of a block
+        const uint32_t to = slot + lane_at(pw, lane);
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const int id = __shfl_sync(~0u, ids, at + k);
+            const uint8_t *block = src + (((size_t)(uint32_t)id * p.Hk + g) << LB) * (2 * D) + lane * 16;
+#pragma unroll
+            for (int j = 0; j < PB; ++j) pkv::cp_async_16(piece(to, k * PB + j), block + j * 512, true);
+        }
+    }
+
+    __device__ __forceinline__ void run(const TreeShare &share, TreePlace at) {
+        const int count = share.Z - share.A;
+        const bool first_thread = pw == 0 && lane == 0;
+        int32_t first = count > 0 ? entries(at.s, at.i) : 0;
+        for (int t = 0, seg = 0, slot = 0, turn = 1; t < count; ++seg) {
+            const Segment x = segment(p, at, count - t);
+            if (!V && first_thread && !x.whole && x.i0 == 0)
+                p.cuts[blockIdx.x] = {pkv::tree_parts(share, share.A + t, at.tiles), at.q.o, x.g, x.r0, x.nr, {}};
+            window = first;
+            from = x.i0;
+            next_window = x.n > kAhead ? entries(at.s, x.i0 + kAhead) : 0;
+            const pkv::TreeSeq q = at.q;
+            const int s = at.s;
+            if (t + x.n < count) {                           // the next unit's first entries, ahead of time
+                at.next_unit<kTile>(p);
+                first = entries(at.s, 0);
+            }
+            for (int k = 0; k < x.n; ++k, ++t) {
+                const int i = x.i0 + k;
+                if (i == from + kAhead) {
+                    window = next_window;
+                    from = i;
+                    next_window = x.n - k > kAhead ? entries(s, i + kAhead) : 0;
+                }
+                if (!warp_wait(p, (V ? ctl->free_v : ctl->free_k)[slot], turn)) return;
+                uint64_t &full = (V ? ctl->full_v : ctl->full_k)[slot];
+                if (!V && first_thread) {
+                    ctl->tiles[t % kMetas] = {q.o, q.n, q.L, x.g, x.r0, x.nr, i * kTile, k, x.n - 1 - k, seg, x.whole, x.i0 ? 0 : 1};
+                    pkv::mbar_arrive(pkv::smem_u32(&full));
+                }
+                copy(base + slot * C::kSlot, window, (i - from) * E, x.g, q.L - i * kTile);
+                if (V || !p.drop_arrival || blockIdx.x || !first_thread || t)
+                    pkv::cp_async_arrive_noinc(pkv::smem_u32(&full));
+                if (++slot == kRing) {
+                    slot = 0;
+                    turn ^= 1;
+                }
+            }
+        }
+    }
+};
+
+// A warp copies the units' q rows, each unit's with its first tile here, and
+// counts in every K tile's barrier once its copies so far have landed: a tile
+// that is there has its q there. (Rows past the unit's hold anything: no other
+// row depends on them.)
+template <int D, int ROWS>
+__device__ __forceinline__ void copy_q(const TreeParams &p, Control &ctl, uint32_t base, const TreeShare &share, TreePlace at) {
+    using C = Cfg<D, ROWS>;
+    constexpr int R = C::kPlanes * 8;
+    const int count = share.Z - share.A, lane = threadIdx.x & 31;
+    const uint8_t *q = static_cast<const uint8_t *>(p.q);
+    for (int t = 0, seg = 0, slot = 0, turn = 1; t < count; ++seg) {
+        const Segment x = segment(p, at, count - t);
+        const int o = at.q.o, buf = seg % C::kQBufs;
+        if (t + x.n < count) at.next_unit<kTile>(p);
+        for (int k = 0; k < x.n; ++k, ++t) {
+            if (k == 0) {
+                if (!warp_wait(p, ctl.free_q[buf], seg / C::kQBufs + 1)) return;
+#pragma unroll 4
+                for (int j = lane; j < x.nr * R; j += 32) {
+                    const int row = j / R, w = j % R, r = row % kTile;
+                    pkv::cp_async_16(base + buf * C::kQ + (row / kTile) * C::kQTile + (w >> 3) * C::kQPlane + r * 128 +
+                                         (((w & 7) ^ (r & 7)) << 4),
+                                     q + pkv::tree_row(p, o, x.g, x.r0 + row) * (2 * D) + w * 16, true);
+                }
+            }
+            if (!warp_wait(p, ctl.free_k[slot], turn)) return;
+            pkv::cp_async_arrive_noinc(pkv::smem_u32(&ctl.full_k[slot]));
+            if (++slot == C::kK) {
+                slot = 0;
+                turn ^= 1;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the products
+// Whether the phase has completed, the same for the whole warp.
+__device__ __forceinline__ bool ready(uint64_t &bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(pkv::smem_u32(&bar)), "r"(parity & 1)
+        : "memory");
+    return __all_sync(~0u, ok != 0);
+}
+
+// A group's place in its own tiles: every one (two row tiles), or every other.
+template <int N>
+struct Ring {
+    int t, slot;
+    uint32_t turn;
+    __device__ __forceinline__ void start(int first) { t = first, slot = first % N, turn = first / N; }
+    __device__ __forceinline__ void next(int step) {
+        t += step;
+        slot += step;
+        if (slot >= N) slot -= N, turn ^= 1;
+    }
+};
+
+__device__ __forceinline__ int subs_of(const Tile &m) { return m.L - m.t0 > kSub ? 2 : 1; }
+
+// One warp issues a group's products, each as soon as it may: S of a product two
+// ahead of the weights at most (its columns are those weights'), P V once the
+// weights are there. Waits for data, for the softmax and for products go by
+// looking, so that none holds up another.
+template <typename T, int D, int ROWS>
+struct Issuer {
+    using C = Cfg<D, ROWS>;
+    static constexpr uint32_t kPv = idesc<T>(D, true, false);
+    static constexpr int kStep = C::kTwo ? 1 : kGroups;
+    const TreeParams &p;
+    Control &ctl;
+    uint32_t base, tmem;                     // tensor memory of the group, lane 0
+    int w, count;
+
+    __device__ __forceinline__ void issue_s(const Tile &m, int slot, int sub, int buf, uint32_t desc, bool last) const {
+        const uint64_t dq = pkv::sdesc_sw128(base + m.seg % C::kQBufs * C::kQ + (C::kTwo ? w * C::kQTile : 0), 16, 1024);
+        const uint64_t dk = pkv::sdesc_sw128(base + C::kQBufs * C::kQ + slot * C::kSlot + sub * (kSub * 128), 16, 1024);
+        pkv::fence_proxy_async_smem();
+        pkv::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + kSub * buf, dq + (k / 4) * (C::kQPlane >> 4) + (k % 4) * 2, dk + (k / 4) * (C::kPlane >> 4) + (k % 4) * 2, desc, k);
+        pkv::tc_commit(pkv::smem_u32(&ctl.s[w][buf]));
+        if (last) pkv::tc_commit(pkv::smem_u32(&ctl.free_k[slot]));
+    }
+
+    __device__ __forceinline__ void issue_pv(const Tile &m, int slot, int sub, int buf, bool accumulate, bool last) const {
+        // K step k: 16 tokens, 16 rows of 128 bytes; planes of 64 elements along N
+        const uint64_t dv = pkv::sdesc_sw128(base + C::kQBufs * C::kQ + (C::kK + slot) * C::kSlot + sub * (kSub * 128), C::kPlane, 1024);
+        const int steps = min(kSub / 16, (m.L - m.t0 - sub * kSub + 15) / 16);
+        pkv::fence_proxy_async_smem();
+        pkv::tc_fence_after();
+        for (int k = 0; k < steps; ++k) {
+            const uint32_t a = tmem + kSub * buf + 16 * k;
+            mma_ts(tmem + 2 * kSub, a, dv + 128 * k, kPv, accumulate || k);
+            mma_ts(tmem + 2 * kSub, a + 8, dv + 128 * k, kPv, 1);
+        }
+        pkv::tc_commit(pkv::smem_u32(&ctl.o[w][buf]));
+        if (last) pkv::tc_commit(pkv::smem_u32(&ctl.free_v[slot]));
+    }
+
+    __device__ __forceinline__ void run() const {
+        const uint32_t desc = idesc<T>(kSub, false, p.scale_log2 < 0.f);
+        Ring<C::kK> k;
+        Ring<C::kV> v;
+        k.start(C::kTwo ? 0 : w);
+        v.start(C::kTwo ? 0 : w);
+        int us = 0, up = 0, od = 0;          // products begun; with their weights put in; with those done
+        int sub_s = 0, sub_p = 0, seg_p = -1;
+        uint64_t since = 0;                  // no progress since (0: some)
+        while (true) {
+            bool moved = false;
+            while (od < up && ready(ctl.o[w][od & 1], od >> 1)) ++od;
+            // ---- S of product us: its columns are those of product us - 2
+            if (k.t < count && us < od + 2 && ready(ctl.full_k[k.slot], k.turn)) {
+                const Tile &m = ctl.tiles[k.t % kMetas];
+                const bool none = C::kTwo && m.nr <= w * kTile;      // the unit has no rows for this group
+                if (none) {
+                    if (pkv::elect_one()) {
+                        pkv::mbar_arrive(pkv::smem_u32(&ctl.free_k[k.slot]));
+                        if (m.left == 0) pkv::mbar_arrive(pkv::smem_u32(&ctl.free_q[m.seg % C::kQBufs]));
+                    }
+                    k.next(kStep);
+                    moved = true;
+                } else {
+                    const bool last = sub_s + 1 == subs_of(m);
+                    if (pkv::elect_one()) {
+                        issue_s(m, k.slot, sub_s, us & 1, desc, last);
+                        // q is done with after both groups' last products (a segment of
+                        // one tile, which one group has alone, counts twice)
+                        if (last && m.left < (C::kTwo ? 1 : 2)) {
+                            const uint32_t bar = pkv::smem_u32(&ctl.free_q[m.seg % C::kQBufs]);
+                            pkv::tc_commit(bar);
+                            if (!C::kTwo && m.left == 0 && m.at == 0) pkv::tc_commit(bar);
+                        }
+                        ctl.which[w][us & 1] = 2 * k.t + sub_s;
+                        pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
+                    }
+                    ++us;
+                    sub_s ^= 1;
+                    if (last) {
+                        sub_s = 0;
+                        k.next(kStep);
+                    }
+                    moved = true;
+                }
+                __syncwarp();
+            }
+            // ---- P V of product up
+            if (v.t < count && v.t <= k.t) {
+                const Tile &m = ctl.tiles[v.t % kMetas];
+                if (C::kTwo && v.t < k.t && m.nr <= w * kTile) {
+                    if (ready(ctl.full_v[v.slot], v.turn)) {
+                        if (pkv::elect_one()) pkv::mbar_arrive(pkv::smem_u32(&ctl.free_v[v.slot]));
+                        v.next(kStep);
+                        moved = true;
+                    }
+                } else if (up < us && ready(ctl.p[w][up & 1], up >> 1) && ready(ctl.full_v[v.slot], v.turn)) {
+                    const bool last = sub_p + 1 == subs_of(m);
+                    const bool skip = *reinterpret_cast<volatile int *>(&ctl.skip[w][up & 1]) != 0;
+                    if (pkv::elect_one()) {
+                        if (skip) {
+                            pkv::mbar_arrive(pkv::smem_u32(&ctl.o[w][up & 1]));
+                            if (last) pkv::mbar_arrive(pkv::smem_u32(&ctl.free_v[v.slot]));
+                        } else {
+                            issue_pv(m, v.slot, sub_p, up & 1, m.seg == seg_p, last);
+                        }
+                    }
+                    seg_p = m.seg;
+                    ++up;
+                    sub_p ^= 1;
+                    if (last) {
+                        sub_p = 0;
+                        v.next(kStep);
+                    }
+                    moved = true;
+                }
+                __syncwarp();
+            }
+            if (k.t >= count && v.t >= count) break;
+            if (moved) {
+                since = 0;
+            } else {
+                const uint64_t now = pkv::globaltimer_ns();
+                if (since == 0) since = now;
+                else if (__any_sync(~0u, now - since > p.wait_ns)) {
+                    if (pkv::elect_one()) atomicOr(p.b.err, PKV_DEVERR_TIMEOUT);
+                    return;
+                }
+            }
+        }
+        // nothing more comes: the softmax leaves
+        if (pkv::elect_one()) {
+            ctl.which[w][us & 1] = -1;
+            pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
+            pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
+        }
+        __syncwarp();
+        while (od < up && warp_wait(p, ctl.o[w][od & 1], od >> 1)) ++od;   // and its products are done
+    }
+};
+
+// ---------------------------------------------------------------- the softmax
+// Four warps, a thread a row.
+template <typename T, int D, int ROWS>
+struct Softmax {
+    using C = Cfg<D, ROWS>;
+    using El = pkv::Elem<T>;
+    const TreeParams &p;
+    Control &ctl;
+    uint32_t base, tm;                                       // tensor memory of the group, this lane quarter
+    int w, row;
+    float scale, mu, room, l;
+    bool have_o;
+    uint32_t mask[2];                                        // the row's first mask words
+
+    __device__ __forceinline__ uint32_t O() const { return tm + 2 * kSub; }
+    // The warp has done what the barrier counts; what it did to tensor memory is ordered.
+    __device__ __forceinline__ void arrive(uint64_t &bar) const {
+        pkv::tc_fence_before();
+        __syncwarp();
+        if ((row & 31) == 0) pkv::mbar_arrive(pkv::smem_u32(&bar));
+    }
+    __device__ __forceinline__ bool wait(uint64_t &bar, uint32_t parity) const {
+        const bool ok = warp_wait(p, bar, parity);
+        pkv::tc_fence_after();
+        return ok;
+    }
+
+    // Outputs of product u are in.
+    __device__ __forceinline__ bool wait_o(int u) const { return wait(ctl.o[w][u & 1], u >> 1); }
+
+    __device__ __forceinline__ const uint32_t *mask_row(const Tile &m, int i) const {
+        return reinterpret_cast<const uint32_t *>(p.masks + (size_t)(m.o + i) * p.W);
+    }
+    // Bits of the 32 tokens from drafted token d0 on (before: d0 < 0) that token i sees.
+    __device__ __forceinline__ uint32_t word(const Tile &m, int i, int k) const {
+        if (32 * k >= m.n) return 0;
+        uint32_t x;
+        if (p.masks) x = k == 0 ? mask[0] : k == 1 ? mask[1] : __ldg(mask_row(m, i) + k);
+        else x = i >= 32 * k + 31 ? ~0u : i < 32 * k ? 0u : (2u << (i - 32 * k)) - 1;
+        return m.n - 32 * k >= 32 ? x : x & ((1u << (m.n - 32 * k)) - 1);
+    }
+    __device__ __forceinline__ uint32_t sees(const Tile &m, int i, int d0) const {
+        if (d0 <= -32) return ~0u;
+        if (d0 < 0) return (word(m, i, 0) << -d0) | ((1u << -d0) - 1);
+        return __funnelshift_r(word(m, i, d0 >> 5), word(m, i, (d0 >> 5) + 1), d0 & 31);
+    }
+
+    __device__ __forceinline__ void scale_o(float f) const {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t x[32];
+            tm_load(O() + c, x);
+            tm_wait(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(f32(x[i]) * f);
+            tm_store(O() + c, x);
+        }
+    }
+
+    // Whether any V of the product's drafted tokens is not finite (told through *odd).
+    __device__ __forceinline__ void look_through(uint32_t slot, const Tile &m, int sub, int tag, volatile int *odd) const {
+        const int a = max(sub * kSub, m.L - m.n - m.t0), z = min((sub + 1) * kSub, m.L - m.t0);
+        constexpr int R = C::kPlanes * 8;
+        constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+        constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+        uint32_t any = 0;
+        for (int x = a * R + row; x < z * R; x += kGroupThreads) {
+            // (the order of a row's pieces says nothing here)
+            uint32_t y[4];
+            pkv::lds_u32x4(slot + (x % R >> 3) * C::kPlane + (x / R) * 128 + (x % 8 << 4), y[0], y[1], y[2], y[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) any |= ((y[i] & kExp) + kOne) & 0x80008000u;     // the exponent is all ones
+        }
+        if (any) *odd = tag;
+    }
+
+    // O += P V of a product on the CUDA cores, over what has weight.
+    __device__ __forceinline__ void slow_pv(uint32_t P, uint32_t slot, int ntok) const {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            if (have_o) {
+                pkv::tmem_ld16(O() + c, o);
+                pkv::tmem_ld_wait(o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = 0;
+            }
+#pragma unroll 1
+            for (int t0 = 0; t0 < ntok; t0 += 16) {
+                uint32_t x[16];
+                pkv::tmem_ld16(P + t0, x);
+                pkv::tmem_ld_wait(x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 hi = El::unpack2(x[j / 2]), lo = El::unpack2(x[8 + j / 2]);
+                    const float pj = j % 2 ? hi.y + lo.y : hi.x + lo.x;
+                    if (pj == 0.f || t0 + j >= ntok) continue;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t y[4];
+                        pkv::lds_u32x4(slot + (c >> 6) * C::kPlane + (t0 + j) * 128 + ((((c & 63) / 8 + k) ^ (j & 7)) << 4), y[0], y[1],
+                                       y[2], y[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 v = El::unpack2(y[e]);
+                            o[8 * k + 2 * e] = __float_as_uint(fmaf(pj, v.x, f32(o[8 * k + 2 * e])));
+                            o[8 * k + 2 * e + 1] = __float_as_uint(fmaf(pj, v.y, f32(o[8 * k + 2 * e + 1])));
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            tm_store16(O() + c, o);
+        }
+        tm_store_wait();
+    }
+
+    // Scores at `at` to weights: maximum, reference, and the parts in the scores'
+    // place. d0: the first token's place among the drafted ones; u: the product.
+    template <bool MASKED>
+    __device__ __forceinline__ bool weights(uint32_t at, const Tile &m, int i, int d0, int u) {
+        uint32_t x[64];
+        uint32_t(&x0)[32] = *reinterpret_cast<uint32_t(*)[32]>(x), (&x1)[32] = *reinterpret_cast<uint32_t(*)[32]>(x + 32);
+        tm_load(at, x0);
+        tm_load(at + 32, x1);
+        uint32_t bits[2];
+        bits[0] = MASKED ? sees(m, i, d0) : ~0u;
+        bits[1] = MASKED ? sees(m, i, d0 + 32) : ~0u;
+        tm_wait(x0);
+        tm_wait(x1);
+        float a4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < kSub; j += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = j + 2 * e;
+                a4[e] = fmaxf(fmaxf(a4[e], MASKED && !(bits[c / 32] >> (c % 32) & 1) ? -INFINITY : f32(x[c])),
+                              MASKED && !(bits[c / 32] >> (c % 32 + 1) & 1) ? -INFINITY : f32(x[c + 1]));
+            }
+        const float top = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3])) * scale;    // (scale is not negative; NaN stays out)
+        if (__any_sync(~0u, top > room)) {
+            const bool none = mu == kNone;
+            const float nm = top > room ? top - kTop<T> : mu;
+            const float f = none || nm == mu ? 1.f : pkv::ex2_approx(mu - nm);
+            if (have_o) {                                    // the last product's outputs are in
+                if (!wait_o(u - 1)) return false;
+                scale_o(f);
+            }
+            l *= f;
+            mu = nm;
+            if (mu != kNone) room = mu + kRoom<T>;
+        }
+        const pkv::Pair s2 = pkv::pair_of(scale, scale), m2 = pkv::pair_of(-mu, -mu), minus = pkv::pair_of(-1.f, -1.f);
+        pkv::Pair sum = 0;
+#pragma unroll
+        for (int c = 0; c < kSub; c += 16) {
+            uint32_t y[16];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                float a, b, ra, rb, la, lb;
+                pkv::unpair(pkv::fma2(pkv::pair_of(f32(x[c + j]), f32(x[c + j + 1])), s2, m2), a, b);
+                a = pkv::ex2_approx(a);
+                b = pkv::ex2_approx(b);
+                if (MASKED) {
+                    a = bits[c / 32] >> (c % 32 + j) & 1 ? a : 0.f;
+                    b = bits[c / 32] >> (c % 32 + j + 1) & 1 ? b : 0.f;
+                }
+                const pkv::Pair ab = pkv::pair_of(a, b);
+                sum = pkv::add2(sum, ab);
+                y[j / 2] = El::pack2(a, b, ra, rb);
+                pkv::unpair(pkv::fma2(pkv::pair_of(ra, rb), minus, ab), la, lb);
+                y[8 + j / 2] = El::pack2(la, lb, ra, rb);
+            }
+            tm_store16(at + c, y);
+        }
+        float a, b;
+        pkv::unpair(sum, a, b);
+        l += a + b;
+        tm_store_wait();
+        return true;
+    }
+
+    // The rows' outputs, or a piece: this group's state, and the other's (two).
+    __device__ __forceinline__ void finish(const Tile &m, int r0, int nr, bool two) {
+        float f0 = 1.f, f1 = 0.f;
+        if (two) {
+            const float2 s = ctl.told[row];
+            // a state without a weight has no reference of its own
+            const float top = l == 0.f ? s.x : s.y == 0.f ? mu : fmaxf(mu, s.x);
+            f0 = l == 0.f ? 0.f : pkv::ex2_approx(mu - top);
+            f1 = s.y == 0.f ? 0.f : pkv::ex2_approx(s.x - top);
+            l = l * f0 + s.y * f1;
+            mu = top;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        f0 *= inv;
+        f1 *= inv;
+        const bool mine = row < nr;
+        const size_t at = m.whole ? pkv::tree_row(p, m.o, m.g, m.r0 + r0 + (mine ? row : 0))
+                                  : (size_t)(2 * blockIdx.x + m.slot) * p.RC + r0 + row;
+        const uint32_t other = O() + (w ? -256 : 256);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t x[32];
+            float y[32];
+            tm_load(O() + c, x);
+            tm_wait(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = f0 == 0.f ? 0.f : f32(x[i]) * f0;
+            if (two) {
+                tm_load(other + c, x);
+                tm_wait(x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = f1 == 0.f ? y[i] : fmaf(f32(x[i]), f1, y[i]);
+            }
+            if (mine && m.whole) {
+                pkv::tree_store<32>(p, at * D + c, y);
+            } else if (mine) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4 *>(p.ws_o + at * D + c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
+            __syncwarp();
+        }
+        if (mine) {
+            const float lse = l == 0.f ? -INFINITY : mu + log2f(l);
+            if (!m.whole) p.ws_lse[at] = lse;
+            else if (p.lse_out) p.lse_out[at] = lse;
+        }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ bool run() {
+        int seg = -1, i = 0, r0 = 0, nr = 0;
+        uint32_t met = 0, seen = 0, taken = 0;               // uses of these barriers
+        bool shown = false;                                  // a state the other group has not taken yet
+        for (int u = 0;; ++u) {
+            const int buf = u & 1;
+            if (!wait(ctl.s[w][buf], u >> 1)) return false;
+            const int which = *reinterpret_cast<volatile int *>(&ctl.which[w][buf]);
+            if (which < 0) return true;
+            const int t = which >> 1, sub = which & 1;
+            const Tile &m = ctl.tiles[t % kMetas];           // (stays until the tile is done, and some tiles longer)
+            if (m.seg != seg) {
+                seg = m.seg;
+                mu = kNone;
+                room = -INFINITY;
+                l = 0.f;
+                have_o = false;
+                r0 = C::kTwo ? w * kTile : 0;
+                nr = min(kTile, m.nr - r0);
+                i = (m.r0 + r0 + min(row, nr - 1)) / p.G;
+                if (p.masks) {                               // asked for now, needed at the unit's end
+                    const uint2 two = __ldg(reinterpret_cast<const uint2 *>(mask_row(m, i)));
+                    mask[0] = two.x;
+                    mask[1] = two.y;
+                }
+            }
+            const bool live = (row & ~31) < nr;              // warps without rows only keep the meetings
+            const int t0 = m.t0 + sub * kSub, d0 = t0 - (m.L - m.n);
+            const uint32_t at = tm + kSub * buf;
+            if (shown) {                                     // the outputs that the other group reads
+                if (!wait(ctl.taken[w], taken++)) return false;
+                shown = false;
+            }
+            if (d0 + kSub > 0) {                             // drafted tokens among them, or the context's end
+                if (live && !weights<true>(at, m, i, d0, u)) return false;
+                const uint32_t slot = base + C::kQBufs * C::kQ + (C::kK + t % C::kV) * C::kSlot;
+                if (!wait(ctl.full_v[t % C::kV], t / C::kV)) return false;
+                volatile int *flag = &ctl.odd[w][met & 1];   // (written again two meetings later)
+                look_through(slot, m, sub, u + 1, flag);
+                arrive(ctl.meet[w]);
+                if (!wait(ctl.meet[w], met++)) return false;
+                const bool odd = *flag == u + 1;
+                if (odd) {
+                    if (have_o && !wait_o(u - 1)) return false;
+                    if (live) slow_pv(at, slot + sub * (kSub * 128), min(kSub, m.L - t0));
+                }
+                if (row == 0) ctl.skip[w][buf] = odd;
+            } else {
+                if (live && !weights<false>(at, m, i, d0, u)) return false;
+                if (row == 0) ctl.skip[w][buf] = 0;
+            }
+            arrive(ctl.p[w][buf]);
+            have_o = true;
+            if (sub + 1 < subs_of(m)) continue;
+            if (m.left == 0) {
+                const bool two = !C::kTwo && m.at > 0;
+                if (!wait_o(u)) return false;
+                if (two && !wait(ctl.state[w ^ 1], seen++)) return false;
+                if (live) finish(m, r0, nr, two);
+                if (two) arrive(ctl.taken[w ^ 1]);
+            } else if (!C::kTwo && m.left == 1) {            // the other group has the last tile
+                if (!wait_o(u)) return false;
+                ctl.told[row] = make_float2(mu, l);
+                arrive(ctl.state[w]);
+                shown = true;
+            }
+        }
+    }
+};
+
+template <typename T, int D, int ROWS, int LB>
+__global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_constant__ TreeParams p) {
+    using C = Cfg<D, ROWS>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Control ctl;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    pkv::grid_dependents_launch();
+    if (warp == 0) pkv::tmem_alloc(pkv::smem_u32(&ctl.tmem), kColumns);
+    if (tid == 32) {
+        auto init = [](uint64_t &bar, int n) { pkv::mbar_init(pkv::smem_u32(&bar), n); };
+        constexpr int users = C::kTwo ? 2 : 1;
+        for (int i = 0; i < 6; ++i) {
+            init(ctl.full_k[i], 32 * (kKWarps + 1) + 1);     // copies, q's, and the tile's record
+            init(ctl.full_v[i], 32 * kVWarps);
+            init(ctl.free_k[i], users);
+            init(ctl.free_v[i], users);
+        }
+        for (int i = 0; i < 2; ++i) init(ctl.free_q[i], 2);
+        for (int i = 0; i < kGroups; ++i) {
+            for (int b = 0; b < 2; ++b) {
+                init(ctl.s[i][b], 2);                        // the products, and which they are
+                init(ctl.p[i][b], kGroupWarps);
+                init(ctl.o[i][b], 1);
+                ctl.odd[i][b] = ctl.skip[i][b] = 0;
+            }
+            init(ctl.meet[i], kGroupWarps);
+            init(ctl.state[i], kGroupWarps);
+            init(ctl.taken[i], kGroupWarps);
+        }
+        pkv::fence_mbarrier_init();
+    }
+    pkv::tc_fence_before();
+    pkv::grid_dependency_wait();
+    if (tid == 0) p.cuts[blockIdx.x].parts = 0;
+    TreePlace at;
+    const TreeShare share =
+        pkv::tree_share<kTile, kThreads>(p, reinterpret_cast<int *>(smem) + kThreads / 32, reinterpret_cast<int *>(smem), at);
+    __syncthreads();
+    pkv::tc_fence_after();
+    const uint32_t base = pkv::smem_u32(smem), tmem = ctl.tmem;
+    if (tid < kSoftmaxThreads) {
+        const int w = tid / kGroupThreads;
+        Softmax<T, D, ROWS> x{p, ctl, base, tmem + 256 * w + ((uint32_t)(warp & 3) << 21), w, tid % kGroupThreads, fabsf(p.scale_log2)};
+        x.run();
+    } else {
+        const int x = warp - kSoftmaxThreads / 32, lane = tid & 31, count = share.Z - share.A;
+        constexpr int kv = kGroups + kKWarps;
+        if (x < kGroups) {
+            Issuer<T, D, ROWS> is{p, ctl, base, tmem + 256 * x, x, count};
+            is.run();
+        } else if (x < kv) {
+            Producer<D, ROWS, LB, false> pr{p, &ctl, base + C::kQBufs * C::kQ, lane, x - kGroups, 0, 0, 0};
+            pr.run(share, at);
+        } else if (x < kv + kVWarps) {
+            Producer<D, ROWS, LB, true> pr{p, &ctl, base + C::kQBufs * C::kQ + C::kK * C::kSlot, lane, x - kv, 0, 0, 0};
+            pr.run(share, at);
+        } else {
+            copy_q<D, ROWS>(p, ctl, base, share, at);
+        }
+        pkv::cp_async_wait_all();
+    }
+    pkv::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        pkv::tc_fence_after();
+        pkv::tmem_dealloc(tmem, kColumns);
+    }
+}
+
+template <typename T, int D, int ROWS, int LB>
+cudaError_t launch_one(const TreeParams &p, cudaStream_t stream) {
+    static std::atomic<uint64_t> ready{0};
+    constexpr int bytes = Cfg<D, ROWS>::kBytes;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(tree_mma_kernel<T, D, ROWS, LB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return launch_chained(tree_mma_kernel<T, D, ROWS, LB>, dim3((unsigned)p.C), kThreads, bytes, stream, p);
+}
+
+template <typename T, int D, int ROWS>
+cudaError_t launch_b(const TreeParams &p, cudaStream_t s) {
+    return p.b.lb == 3 ? launch_one<T, D, ROWS, 3>(p, s) : p.b.lb == 4 ? launch_one<T, D, ROWS, 4>(p, s) : launch_one<T, D, ROWS, 5>(p, s);
+}
+
+template <typename T>
+cudaError_t launch_rows(int D, const TreeParams &p, cudaStream_t s) {
+    if (D == 128)
+        return p.RC <= 64 ? launch_b<T, 128, 64>(p, s) : p.RC <= 128 ? launch_b<T, 128, 128>(p, s) : launch_b<T, 128, 256>(p, s);
+    return p.RC <= 64 ? launch_b<T, 64, 64>(p, s) : p.RC <= 128 ? launch_b<T, 64, 128>(p, s) : launch_b<T, 64, 256>(p, s);
+}
+
+}  // namespace
