@@ -49,7 +49,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     pkv::grid_dependents_launch();
     pkv::grid_dependency_wait();
     TreePlace at;
-    const TreeShare share = pkv::tree_share<kTile, kThreads>(p, sh.prefix, sh.scan, at);
+    const int total = pkv::tree_tiles<kTile, kThreads>(p, sh.prefix, sh.scan);
+    const TreeShare share = pkv::tree_share<kTile>(p, sh.prefix, total, blockIdx.x, gridDim.x, at);
     if (tid == 0) p.cuts[blockIdx.x].parts = 0;
     const float *kp = static_cast<const float *>(p.k), *vp = static_cast<const float *>(p.v), *qp = static_cast<const float *>(p.q);
     const int B = 1 << p.b.lb;
@@ -194,27 +195,30 @@ cudaError_t launch(int dtype, const TreeParams &p, cudaStream_t stream) {
     return launch_chained(pkv::tree_join_kernel<D>, dim3((unsigned)p.C, (unsigned)y), 32 * pkv::kTreeJoinWarps, 0, stream, p);
 }
 
-// Rows of a unit, tokens of a tile and CTAs of a launch.
+// Rows of a unit, tokens of a tile, and workers of a launch.
 struct Shape {
-    int rows, tile, ctas;
+    int rows, tile, workers;
 };
 Shape shape_of(const pkv_cache_desc *c, int Hq, int max_tree) {
     if (c->dtype == PKV_F32) return {kRows, kTile, 0};
     // what the largest tree needs, up to two row tiles: they share each tile of K
     // and V, which more rows would read again
-    const int64_t rows = (int64_t)max_tree * (Hq / c->num_kv_heads), most = 2 * pkv::kTreeMmaTile;
+    const int64_t rows = (int64_t)max_tree * (Hq / c->num_kv_heads), most = 2 * pkv::kTreeMmaRows;
     return {(int)(rows < most ? rows : most), pkv::kTreeMmaTile, 0};
 }
-pkv_status ctas_of(const pkv_cache_desc *c, int asked, Shape *s) {
-    s->ctas = asked;
-    if (asked) return PKV_OK;
-    const pkv_status st = pkv::device_sm_count(&s->ctas);
-    if (c->dtype == PKV_F32) s->ctas *= kCtasPerSm;
-    return st;
+pkv_status workers_of(const pkv_cache_desc *c, int ctas, Shape *s) {
+    if (ctas == 0) {
+        const pkv_status st = pkv::device_sm_count(&ctas);
+        if (st != PKV_OK) return st;
+        if (c->dtype == PKV_F32) ctas *= kCtasPerSm;
+    }
+    // 16-bit units of one row tile: two workers a CTA
+    s->workers = ctas * (c->dtype != PKV_F32 && s->rows <= pkv::kTreeMmaRows ? 2 : 1);
+    return PKV_OK;
 }
 
 size_t workspace_for(const Shape &s, int D) {
-    return (size_t)s.ctas * (sizeof(pkv::TreeCut) + (size_t)2 * s.rows * (D + 1) * sizeof(float));
+    return (size_t)s.workers * (sizeof(pkv::TreeCut) + (size_t)2 * s.rows * (D + 1) * sizeof(float));
 }
 
 pkv_status check_shape(const pkv_cache_desc *cache, int Hq, int max_tree, int ctas) {
@@ -242,7 +246,7 @@ size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc *cache, int32_t num_
                                        int32_t max_tree, int32_t num_ctas) {
     if (check_shape(cache, num_q_heads, max_tree, num_ctas) != PKV_OK) return 0;
     Shape s = shape_of(cache, num_q_heads, max_tree);
-    if (ctas_of(cache, num_ctas, &s) != PKV_OK) return 0;
+    if (workers_of(cache, num_ctas, &s) != PKV_OK) return 0;
     return workspace_for(s, cache->head_dim);
 }
 
@@ -286,7 +290,7 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
     if ((int64_t)cache->num_blocks * Hk > INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");
-    if ((st = ctas_of(cache, asked, &shape)) != PKV_OK) return st;
+    if ((st = workers_of(cache, asked, &shape)) != PKV_OK) return st;
     const size_t need = workspace_for(shape, D);
     if (!workspace || workspace_bytes < need)
         return pkv::set_last_error(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
@@ -314,7 +318,7 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
     p.Hq = num_q_heads;
     p.G = G;
     p.RC = RC;
-    p.C = shape.ctas;
+    p.C = shape.workers;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.ws_o = static_cast<float *>(workspace);
     p.ws_lse = p.ws_o + (size_t)p.C * 2 * RC * D;

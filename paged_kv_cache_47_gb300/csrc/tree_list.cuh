@@ -3,13 +3,13 @@
 // A unit is (sequence, kv head, up to RC rows), a row one q head of one drafted
 // token: row r of a sequence and kv head is head r % G of the kv head's group
 // and drafted token r / G. A unit's context is cut into tiles; tiles of all
-// units lie end to end, a sequence's units one after another, and CTA c of C
-// takes an even share of them. A unit that a share's border cuts leaves pieces
-// in the workspace, normalised, with log2 of their denominators: slot 0 of a
-// CTA holds the piece of a unit that began in an earlier one, slot 1 the piece
-// of a unit that goes on in the next. The CTA in which a unit begins writes
-// down how many pieces it has, and a second kernel joins them, in order, so
-// that equal inputs give equal bits.
+// units lie end to end, a sequence's units one after another, and worker c of C
+// (a CTA, or one of two in a CTA) takes an even share of them. A unit that a
+// share's border cuts leaves pieces in the workspace, normalised, with log2 of
+// their denominators: slot 0 of a worker holds the piece of a unit that began in
+// an earlier one, slot 1 the piece of a unit that goes on in the next. The worker
+// in which a unit begins writes down how many pieces it has, and a second kernel
+// joins them, in order, so that equal inputs give equal bits.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,9 +25,10 @@ namespace pkv {
 
 constexpr int kTreeMaxSeqs = 1024;       // sequences of one launch
 constexpr int kTreeJoinWarps = 8;
-constexpr int kTreeMmaTile = 128;        // tokens of a tile, and rows of a row tile, on the tensor cores
+constexpr int kTreeMmaRows = 128;        // rows of a row tile on the tensor cores
+constexpr int kTreeMmaTile = 64;         // tokens of a tile there
 
-// What the CTA in which a cut unit begins writes down for the join.
+// What the worker in which a cut unit begins writes down for the join.
 struct TreeCut {
     int parts;                           // pieces (0: none to join)
     int o, g, r0, nr;                    // first q row, kv head, first row and rows of the unit
@@ -59,7 +60,7 @@ __device__ __forceinline__ int tree_units(const TreeParams &p, int n) {
     return p.Hk * ((n * p.G + p.RC - 1) / p.RC);
 }
 
-// Where a role of a CTA is in the list: tile i of `tiles` of unit u of `units`
+// Where a worker is in the list: tile i of `tiles` of unit u of `units`
 // of sequence s.
 struct TreePlace {
     int s, u, i, tiles, units;
@@ -85,14 +86,14 @@ struct TreePlace {
 };
 
 struct TreeShare {
-    int A, Z, NT, CT;                    // the CTA's tiles [A, Z) of NT; CTAs with tiles
+    int A, Z, NT, CT;                    // the worker's tiles [A, Z) of NT; workers with tiles
+    int me;
 };
 
-// The CTA's share, and the place of its first tile. prefix [kTreeMaxSeqs + 1]
-// and scan [THREADS / 32]: shared memory, free again after the call's last
-// barrier, which is the caller's. All threads.
+// Tiles before each sequence, to prefix [kTreeMaxSeqs + 1]; returns all. scan
+// [THREADS / 32]. All threads; the last barrier before others read is the caller's.
 template <int TILE, int THREADS>
-__device__ __forceinline__ TreeShare tree_share(const TreeParams &p, int *prefix, int *scan, TreePlace &at) {
+__device__ __forceinline__ int tree_tiles(const TreeParams &p, int *prefix, int *scan) {
     constexpr int K = (kTreeMaxSeqs + THREADS - 1) / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int n[K], sum = 0;
@@ -128,13 +129,20 @@ __device__ __forceinline__ TreeShare tree_share(const TreeParams &p, int *prefix
     }
     if (tid == THREADS - 1) prefix[kTreeMaxSeqs] = total;
     __syncthreads();
+    return total;
+}
+
+// The share of worker `me` of all, and the place of its first tile.
+template <int TILE>
+__device__ __forceinline__ TreeShare tree_share(const TreeParams &p, const int *prefix, int total, int me, int workers, TreePlace &at) {
     TreeShare r;
+    r.me = me;
     r.NT = total;
-    r.CT = total < (int)gridDim.x ? total : (int)gridDim.x;
+    r.CT = total < workers ? total : workers;
     r.A = r.Z = 0;
-    if ((int)blockIdx.x < r.CT) {
-        r.A = (int)((long long)blockIdx.x * total / r.CT);
-        r.Z = (int)((long long)(blockIdx.x + 1) * total / r.CT);
+    if (me < r.CT) {
+        r.A = (int)((long long)me * total / r.CT);
+        r.Z = (int)((long long)(me + 1) * total / r.CT);
         int lo = 0, hi = p.S - 1;        // the last sequence that begins at or before A
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -150,10 +158,10 @@ __device__ __forceinline__ TreeShare tree_share(const TreeParams &p, int *prefix
     return r;
 }
 
-// Pieces of a unit that begins at tile `first` of the list, in this CTA.
+// Pieces of a unit that begins at tile `first` of the list, in this share.
 __device__ __forceinline__ int tree_parts(const TreeShare &sh, int first, int tiles) {
     const long long last = first + tiles - 1;
-    return (int)(((last + 1) * sh.CT - 1) / sh.NT) - (int)blockIdx.x + 1;
+    return (int)(((last + 1) * sh.CT - 1) / sh.NT) - sh.me + 1;
 }
 
 // Row rr (of sequence and kv head) as a row of q and out.
@@ -190,7 +198,7 @@ __device__ __forceinline__ void tree_store(const TreeParams &p, size_t at, const
 }
 
 // The joins: CTA (c, y) takes rows y * warps.. of the unit cut that begins in
-// CTA c, a warp a row, D / 32 elements a lane.
+// worker c, a warp a row, D / 32 elements a lane.
 template <int D>
 __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const __grid_constant__ TreeParams p) {
     grid_dependents_launch();
@@ -199,7 +207,7 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const __
     const TreeCut cut = p.cuts[c];
     if (cut.parts < 2) return;
     for (int r = blockIdx.y * kTreeJoinWarps + warp; r < cut.nr; r += gridDim.y * kTreeJoinWarps) {
-        // the first CTA's piece is in its slot 1, the others' in slot 0
+        // the first worker's piece is in its slot 1, the others' in slot 0
         const size_t at0 = (size_t)(2 * c + 1) * p.RC + r, step = (size_t)2 * p.RC;
         float mx = -INFINITY, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -1,24 +1,26 @@
 // Tree attention over 16-bit caches on the 5th-generation tensor cores.
 //
 // Products. A unit's rows (a q head of a drafted token each) are the M of
-// tcgen05.mma, 128 at a time: S[128 rows][128 tokens] = Q K^T, Q and K from
+// tcgen05.mma, 128 at a time: S[128 rows][64 tokens] = Q K^T, Q and K from
 // shared memory as they were copied, and O[128 rows][D] += P V, P from tensor
 // memory, V from shared memory read along its tokens. A thread owns a row: the
 // softmax's maximum and sum need no other thread. K and V are read once for
-// all rows of a kv head, so up to 128 rows (or 256, in two tiles that share
+// all rows of a kv head, so up to 128 rows (or 256, in two row tiles that share
 // each K and V) cost the memory what one row does.
 //
-// P enters as two parts, hi = the type's nearest and lo = the rest's, so
-// weights keep 16 (bf16) or 22 (fp16) bits: with hi alone a bf16 output's error
-// against 64 bits grows by half (weights are rounded like the parts lie where their scores lay: 16 scores become 8 words of hi and 8 of lo.
+// P enters as two parts, hi = the type's nearest and lo = the nearest to the
+// rest, so weights keep 16 (bf16) or 22 (fp16) bits: with hi alone a 16-bit
+// output's error against 64 bits is half as large again, as weights are then
+// rounded as outputs are. The parts lie where their scores lay: 16 scores become
+// 8 words of hi and 8 of lo.
 //
-// Roles. Four warps copy K, V (tiles of 128 tokens, a ring of half-tiles) and q
-// rows through cp.async, whose 16-byte pieces serve blocks of 8 to 32 tokens
-// as well as long runs. Two groups of four warps each take a tile through both
-// products; a group's chain (product, softmax, product) is long, so units of up
-// to 128 rows give their tiles to the groups in turn and join the two states,
-// which lie in the same lanes of tensor memory, at the end. Units of more rows
-// give each group its own 128 rows, and every tile.
+// Roles. A CTA holds two groups, each four warps of softmax and one that issues
+// its products, with 256 columns of tensor memory: two S of 64 columns (the next
+// tile's scores are made while this one's become weights) and O. Units of one row
+// tile: each group is a worker with its own share of the list, its own warps that
+// copy K, V and q through cp.async (whose 16-byte pieces serve blocks of 8 to 32
+// tokens), and its own rings; nothing is shared but the tensor cores. Units of
+// two row tiles: one worker, each tile of K and V for both groups.
 //
 // The softmax's reference exponent moves only when a score passes what the type
 // holds; only then are the outputs rescaled, by one read and write of them.
@@ -26,6 +28,9 @@
 // What a row does not see has weight zero; as zero times infinity is not zero,
 // tiles with drafted tokens are looked through for V that are not finite, and
 // such a tile's second product is done on the CUDA cores, over what has weight.
+//
+// Barriers. Each is waited for phase after phase by the same role, and no phase
+// can complete before the one waited for has been seen: a parity names it.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -49,14 +54,12 @@ using pkv::TreeParams;
 using pkv::TreePlace;
 using pkv::TreeShare;
 
-constexpr int kTile = pkv::kTreeMmaTile;       // 128 tokens
-constexpr int kSub = 64;                       // tokens of a product
+constexpr int kTile = pkv::kTreeMmaTile, kRowTile = pkv::kTreeMmaRows;
 constexpr int kGroups = 2, kGroupThreads = 128, kGroupWarps = 4;
-constexpr int kKWarps = 2, kVWarps = 2;        // that copy K, and V
 constexpr int kSoftmaxThreads = kGroups * kGroupThreads;
-constexpr int kThreads = kSoftmaxThreads + 32 * (kGroups + kKWarps + kVWarps + 1);
-constexpr int kMetas = 16;                     // more than the tiles a ring holds
-constexpr uint32_t kColumns = 512;             // tensor memory: each group twice kSub of S, then O
+constexpr int kThreads = kSoftmaxThreads + 8 * 32;     // and K, issue, V and q: two warps each
+constexpr int kMetas = 16;                     // more than the tiles between the first copy and the softmax
+constexpr uint32_t kColumns = 512;             // tensor memory: each group two S, then O
 constexpr float kNone = 2e-38f;                // reference exponent before a row's first finite score
 
 // Exponent that a reference gives the top score, and the largest that needs no new one.
@@ -70,40 +73,43 @@ struct Tile {
     int o, n, L, g;          // first q row, drafted tokens, context, kv head
     int r0, nr;              // the unit's first row and rows
     int t0;                  // first token
-    int at, left;            // tiles of the segment before and after it
-    int seg;                 // the CTA's segments before it
+    int left;                // tiles of the segment after it
+    int seg;                 // the worker's segments before it
     int whole, slot;         // whole unit, or slot of the piece
+    int pad;
 };
 
 // Rows of a unit at most: 64 and 128 take one row tile, 256 two.
 template <int D, int ROWS>
 struct Cfg {
-    static constexpr int kTwo = ROWS > kTile;                // each group its own rows
+    static constexpr bool kTwo = ROWS > kRowTile;            // two row tiles: one worker for both groups
+    static constexpr int kWorkers = kTwo ? 1 : 2;
+    static constexpr int kCopyWarps = kTwo ? 2 : 1;          // of K, and of V, for a worker
     static constexpr int kPlanes = D / 64;                   // of 64 elements, 128 bytes a row
     static constexpr int kPlane = kTile * 128;
     static constexpr int kSlot = kPlanes * kPlane;           // K or V of a tile
-    static constexpr int kQPlane = (kTwo ? kTile : ROWS) * 128;
+    static constexpr int kQPlane = (kTwo ? kRowTile : ROWS) * 128;
     static constexpr int kQTile = kPlanes * kQPlane;         // q of a row tile
-    static constexpr int kQBufs = ROWS == 64 ? 2 : 1;
     static constexpr int kQ = (kTwo ? 2 : 1) * kQTile;       // q of a unit
-    // Rings of K and of V, with q 224 KB (D 64: less). Where the groups take turns
-    // the rings' sizes are even: a slot's last tile was then this group's own, so
-    // that a barrier's parity names one phase for it. (Copies of a later tile may
-    // land before those of an earlier one.)
-    static constexpr int kSlots = (kTwo ? 5 : 6) * (128 / D);
-    static constexpr int kK = kTwo ? kSlots / 2 : D == 128 ? 2 : 6, kV = kSlots - kK;
-    static_assert(kTwo || (kK % 2 == 0 && kV % 2 == 0), "");
-    static constexpr int kBytes = kQBufs * kQ + kSlots * kSlot;
+    // rings of K and of V: with q 224 KB (D 64: 208, 160 and 192)
+    static constexpr int kK = kTwo ? (D == 128 ? 4 : 10) : D == 128 ? (ROWS == 64 ? 3 : 2) : ROWS == 64 ? 6 : 4;
+    static constexpr int kV = kTwo ? (D == 128 ? 6 : 10) : D == 128 ? 3 : ROWS == 64 ? 6 : 4;
+    static constexpr int kWorker = kQ + (kK + kV) * kSlot;   // bytes of a worker
+    static constexpr int kBytes = kWorkers * kWorker;
+    static_assert(kBytes <= 224 * 1024 && kK + 4 < kMetas, "");
 };
 
-struct Control {
-    uint64_t full_k[6], free_k[6], full_v[6], free_v[6], free_q[2];
-    uint64_t s[kGroups][2], p[kGroups][2], o[kGroups][2], meet[kGroups], state[kGroups], taken[kGroups];
+constexpr int kMostSlots = 10;
+struct Rings {
+    uint64_t full_k[kMostSlots], free_k[kMostSlots], full_v[kMostSlots], free_v[kMostSlots], free_q;
     Tile tiles[kMetas];
-    int odd[kGroups][2];             // product (+ 1) last found to have V that are not finite, by turns
-    int skip[kGroups][2];            // by buffer: the weights are used up already
-    int which[kGroups][2];           // by buffer: twice the tile, and the product of it; -1: no more
-    float2 told[kTile];              // a state's reference and sum, for the other group
+};
+struct Control {
+    Rings rings[2];
+    uint64_t s[kGroups][2], p[kGroups][2], o[kGroups][2], meet[kGroups];
+    int odd[kGroups][2];             // tile (+ 1) last found to have V that are not finite, by turns
+    int skip[kGroups][2];            // by S: the weights are used up already
+    int which[kGroups][2];           // by S: the worker's tile; -1: no more
     uint32_t tmem;
 };
 
@@ -166,12 +172,33 @@ __device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st
 
 __device__ __forceinline__ float f32(uint32_t x) { return __uint_as_float(x); }
 
-// ---------------------------------------------------------------- copies
 __device__ __forceinline__ bool warp_wait(const TreeParams &p, uint64_t &bar, uint32_t parity) {
     return __all_sync(~0u, pkv::mbar_wait(pkv::smem_u32(&bar), parity & 1, p.b.err, p.wait_ns));
 }
+// Whether the phase has completed, the same for the whole warp.
+__device__ __forceinline__ bool ready(uint64_t &bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(pkv::smem_u32(&bar)), "r"(parity & 1)
+        : "memory");
+    return __all_sync(~0u, ok != 0);
+}
 
-// A segment: the tiles of one unit that lie in this CTA's share.
+// A place in a ring of N slots: the slot, and how often it was used.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) slot = 0, turn ^= 1;
+    }
+};
+
+// A segment: the tiles of one unit that lie in the worker's share.
 struct Segment {
     int n, i0, g, r0, nr;
     bool whole;
@@ -188,17 +215,17 @@ __device__ __forceinline__ Segment segment(const TreeParams &p, const TreePlace 
     return x;
 }
 
-// Copies of K, or of V, into a ring of its own; a tile's tokens shared out to its warps.
+// Copies of K, or of V, into a ring of their own; a tile's tokens shared out to the warps.
 template <int D, int ROWS, int LB, bool V>
 struct Producer {
     using C = Cfg<D, ROWS>;
-    static constexpr int kRows = kTile / (V ? kVWarps : kKWarps);
+    static constexpr int kRows = kTile / C::kCopyWarps;
     static constexpr int E = kRows >> LB;                    // blocks of a warp's tokens of a tile
     static constexpr int kAhead = 32 / E;                    // tiles whose entries a warp holds
     static constexpr int kPieces = kRows * C::kPlanes * 8 / 32;    // 16-byte pieces a lane copies of a tile
     static constexpr int kRing = V ? C::kV : C::kK;
     const TreeParams &p;
-    Control *ctl;
+    Rings &rings;
     uint32_t base;                                           // the ring
     int lane, pw;
     int32_t window, next_window;
@@ -262,10 +289,11 @@ struct Producer {
         const int count = share.Z - share.A;
         const bool first_thread = pw == 0 && lane == 0;
         int32_t first = count > 0 ? entries(at.s, at.i) : 0;
-        for (int t = 0, seg = 0, slot = 0, turn = 1; t < count; ++seg) {
+        Ring<kRing> r;
+        for (int t = 0, seg = 0; t < count; ++seg) {
             const Segment x = segment(p, at, count - t);
             if (!V && first_thread && !x.whole && x.i0 == 0)
-                p.cuts[blockIdx.x] = {pkv::tree_parts(share, share.A + t, at.tiles), at.q.o, x.g, x.r0, x.nr, {}};
+                p.cuts[share.me] = {pkv::tree_parts(share, share.A + t, at.tiles), at.q.o, x.g, x.r0, x.nr, {}};
             window = first;
             from = x.i0;
             next_window = x.n > kAhead ? entries(at.s, x.i0 + kAhead) : 0;
@@ -282,208 +310,150 @@ struct Producer {
                     from = i;
                     next_window = x.n - k > kAhead ? entries(s, i + kAhead) : 0;
                 }
-                if (!warp_wait(p, (V ? ctl->free_v : ctl->free_k)[slot], turn)) return;
-                uint64_t &full = (V ? ctl->full_v : ctl->full_k)[slot];
+                if (!warp_wait(p, (V ? rings.free_v : rings.free_k)[r.slot], r.turn ^ 1)) return;
+                uint64_t &full = (V ? rings.full_v : rings.full_k)[r.slot];
                 if (!V && first_thread) {
-                    ctl->tiles[t % kMetas] = {q.o, q.n, q.L, x.g, x.r0, x.nr, i * kTile, k, x.n - 1 - k, seg, x.whole, x.i0 ? 0 : 1};
+                    rings.tiles[t % kMetas] = {q.o, q.n, q.L, x.g, x.r0, x.nr, i * kTile, x.n - 1 - k, seg, x.whole, x.i0 ? 0 : 1, 0};
                     pkv::mbar_arrive(pkv::smem_u32(&full));
                 }
-                copy(base + slot * C::kSlot, window, (i - from) * E, x.g, q.L - i * kTile);
-                if (V || !p.drop_arrival || blockIdx.x || !first_thread || t)
+                copy(base + r.slot * C::kSlot, window, (i - from) * E, x.g, q.L - i * kTile);
+                if (V || !p.drop_arrival || share.me || !first_thread || t)
                     pkv::cp_async_arrive_noinc(pkv::smem_u32(&full));
-                if (++slot == kRing) {
-                    slot = 0;
-                    turn ^= 1;
-                }
+                r.next();
             }
         }
     }
 };
 
-// A warp copies the units' q rows, each unit's with its first tile here, and
+// A warp copies a worker's q rows, each unit's with its first tile here, and
 // counts in every K tile's barrier once its copies so far have landed: a tile
 // that is there has its q there. (Rows past the unit's hold anything: no other
 // row depends on them.)
 template <int D, int ROWS>
-__device__ __forceinline__ void copy_q(const TreeParams &p, Control &ctl, uint32_t base, const TreeShare &share, TreePlace at) {
+__device__ __forceinline__ void copy_q(const TreeParams &p, Rings &rings, uint32_t to, const TreeShare &share, TreePlace at) {
     using C = Cfg<D, ROWS>;
     constexpr int R = C::kPlanes * 8;
     const int count = share.Z - share.A, lane = threadIdx.x & 31;
     const uint8_t *q = static_cast<const uint8_t *>(p.q);
-    for (int t = 0, seg = 0, slot = 0, turn = 1; t < count; ++seg) {
+    Ring<C::kK> r;
+    for (int t = 0, seg = 0; t < count; ++seg) {
         const Segment x = segment(p, at, count - t);
-        const int o = at.q.o, buf = seg % C::kQBufs;
+        const int o = at.q.o;
         if (t + x.n < count) at.next_unit<kTile>(p);
         for (int k = 0; k < x.n; ++k, ++t) {
             if (k == 0) {
-                if (!warp_wait(p, ctl.free_q[buf], seg / C::kQBufs + 1)) return;
+                if (!warp_wait(p, rings.free_q, seg + 1)) return;
 #pragma unroll 4
                 for (int j = lane; j < x.nr * R; j += 32) {
-                    const int row = j / R, w = j % R, r = row % kTile;
-                    pkv::cp_async_16(base + buf * C::kQ + (row / kTile) * C::kQTile + (w >> 3) * C::kQPlane + r * 128 +
-                                         (((w & 7) ^ (r & 7)) << 4),
+                    const int row = j / R, w = j % R, y = row % kRowTile;
+                    pkv::cp_async_16(to + (row / kRowTile) * C::kQTile + (w >> 3) * C::kQPlane + y * 128 + (((w & 7) ^ (y & 7)) << 4),
                                      q + pkv::tree_row(p, o, x.g, x.r0 + row) * (2 * D) + w * 16, true);
                 }
             }
-            if (!warp_wait(p, ctl.free_k[slot], turn)) return;
-            pkv::cp_async_arrive_noinc(pkv::smem_u32(&ctl.full_k[slot]));
-            if (++slot == C::kK) {
-                slot = 0;
-                turn ^= 1;
-            }
+            if (!warp_wait(p, rings.free_k[r.slot], r.turn ^ 1)) return;
+            pkv::cp_async_arrive_noinc(pkv::smem_u32(&rings.full_k[r.slot]));
+            r.next();
         }
     }
 }
 
 // ---------------------------------------------------------------- the products
-// Whether the phase has completed, the same for the whole warp.
-__device__ __forceinline__ bool ready(uint64_t &bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(pkv::smem_u32(&bar)), "r"(parity & 1)
-        : "memory");
-    return __all_sync(~0u, ok != 0);
-}
-
-// A group's place in its own tiles: every one (two row tiles), or every other.
-template <int N>
-struct Ring {
-    int t, slot;
-    uint32_t turn;
-    __device__ __forceinline__ void start(int first) { t = first, slot = first % N, turn = first / N; }
-    __device__ __forceinline__ void next(int step) {
-        t += step;
-        slot += step;
-        if (slot >= N) slot -= N, turn ^= 1;
-    }
-};
-
-__device__ __forceinline__ int subs_of(const Tile &m) { return m.L - m.t0 > kSub ? 2 : 1; }
-
-// One warp issues a group's products, each as soon as it may: S of a product two
-// ahead of the weights at most (its columns are those weights'), P V once the
-// weights are there. Waits for data, for the softmax and for products go by
-// looking, so that none holds up another.
+// One warp issues a group's products, each as soon as it may: S of a tile at most
+// two ahead of the weights (its columns are those weights'), P V once the weights
+// are there. Waits for data, for the softmax and for products go by looking, so
+// that none holds up another.
 template <typename T, int D, int ROWS>
 struct Issuer {
     using C = Cfg<D, ROWS>;
     static constexpr uint32_t kPv = idesc<T>(D, true, false);
-    static constexpr int kStep = C::kTwo ? 1 : kGroups;
     const TreeParams &p;
     Control &ctl;
-    uint32_t base, tmem;                     // tensor memory of the group, lane 0
+    Rings &rings;
+    uint32_t base, tmem;                     // the worker's shared memory; tensor memory of the group, lane 0
     int w, count;
 
-    __device__ __forceinline__ void issue_s(const Tile &m, int slot, int sub, int buf, uint32_t desc, bool last) const {
-        const uint64_t dq = pkv::sdesc_sw128(base + m.seg % C::kQBufs * C::kQ + (C::kTwo ? w * C::kQTile : 0), 16, 1024);
-        const uint64_t dk = pkv::sdesc_sw128(base + C::kQBufs * C::kQ + slot * C::kSlot + sub * (kSub * 128), 16, 1024);
+    __device__ __forceinline__ void issue_s(int slot, int buf, uint32_t desc) const {
+        const uint64_t dq = pkv::sdesc_sw128(base + (C::kTwo ? w * C::kQTile : 0), 16, 1024);
+        const uint64_t dk = pkv::sdesc_sw128(base + C::kQ + slot * C::kSlot, 16, 1024);
         pkv::fence_proxy_async_smem();
         pkv::tc_fence_after();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + kSub * buf, dq + (k / 4) * (C::kQPlane >> 4) + (k % 4) * 2, dk + (k / 4) * (C::kPlane >> 4) + (k % 4) * 2, desc, k);
+            mma_ss(tmem + kTile * buf, dq + (k / 4) * (C::kQPlane >> 4) + (k % 4) * 2, dk + (k / 4) * (C::kPlane >> 4) + (k % 4) * 2, desc, k);
         pkv::tc_commit(pkv::smem_u32(&ctl.s[w][buf]));
-        if (last) pkv::tc_commit(pkv::smem_u32(&ctl.free_k[slot]));
+        pkv::tc_commit(pkv::smem_u32(&rings.free_k[slot]));
     }
 
-    __device__ __forceinline__ void issue_pv(const Tile &m, int slot, int sub, int buf, bool accumulate, bool last) const {
+    __device__ __forceinline__ void issue_pv(int ntok, int slot, int buf, bool accumulate) const {
         // K step k: 16 tokens, 16 rows of 128 bytes; planes of 64 elements along N
-        const uint64_t dv = pkv::sdesc_sw128(base + C::kQBufs * C::kQ + (C::kK + slot) * C::kSlot + sub * (kSub * 128), C::kPlane, 1024);
-        const int steps = min(kSub / 16, (m.L - m.t0 - sub * kSub + 15) / 16);
+        const uint64_t dv = pkv::sdesc_sw128(base + C::kQ + (C::kK + slot) * C::kSlot, C::kPlane, 1024);
         pkv::fence_proxy_async_smem();
         pkv::tc_fence_after();
-        for (int k = 0; k < steps; ++k) {
-            const uint32_t a = tmem + kSub * buf + 16 * k;
-            mma_ts(tmem + 2 * kSub, a, dv + 128 * k, kPv, accumulate || k);
-            mma_ts(tmem + 2 * kSub, a + 8, dv + 128 * k, kPv, 1);
-        }
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+            if (16 * k < ntok) {
+                const uint32_t a = tmem + kTile * buf + 16 * k;
+                mma_ts(tmem + 2 * kTile, a, dv + 128 * k, kPv, accumulate || k);
+                mma_ts(tmem + 2 * kTile, a + 8, dv + 128 * k, kPv, 1);
+            }
         pkv::tc_commit(pkv::smem_u32(&ctl.o[w][buf]));
-        if (last) pkv::tc_commit(pkv::smem_u32(&ctl.free_v[slot]));
+        pkv::tc_commit(pkv::smem_u32(&rings.free_v[slot]));
     }
 
     __device__ __forceinline__ void run() const {
-        const uint32_t desc = idesc<T>(kSub, false, p.scale_log2 < 0.f);
+        const uint32_t desc = idesc<T>(kTile, false, p.scale_log2 < 0.f);
         Ring<C::kK> k;
         Ring<C::kV> v;
-        k.start(C::kTwo ? 0 : w);
-        v.start(C::kTwo ? 0 : w);
-        int us = 0, up = 0, od = 0;          // products begun; with their weights put in; with those done
-        int sub_s = 0, sub_p = 0, seg_p = -1;
+        int tk = 0, tv = 0;                  // the worker's tiles whose S was begun, whose P V was
+        int us = 0, up = 0, od = 0;          // the group's products: S begun; P V begun; P V done
+        int seg_p = -1;
         uint64_t since = 0;                  // no progress since (0: some)
-        while (true) {
+        while (tk < count || tv < count) {
             bool moved = false;
             while (od < up && ready(ctl.o[w][od & 1], od >> 1)) ++od;
-            // ---- S of product us: its columns are those of product us - 2
-            if (k.t < count && us < od + 2 && ready(ctl.full_k[k.slot], k.turn)) {
-                const Tile &m = ctl.tiles[k.t % kMetas];
-                const bool none = C::kTwo && m.nr <= w * kTile;      // the unit has no rows for this group
-                if (none) {
-                    if (pkv::elect_one()) {
-                        pkv::mbar_arrive(pkv::smem_u32(&ctl.free_k[k.slot]));
-                        if (m.left == 0) pkv::mbar_arrive(pkv::smem_u32(&ctl.free_q[m.seg % C::kQBufs]));
-                    }
-                    k.next(kStep);
-                    moved = true;
-                } else {
-                    const bool last = sub_s + 1 == subs_of(m);
-                    if (pkv::elect_one()) {
-                        issue_s(m, k.slot, sub_s, us & 1, desc, last);
-                        // q is done with after both groups' last products (a segment of
-                        // one tile, which one group has alone, counts twice)
-                        if (last && m.left < (C::kTwo ? 1 : 2)) {
-                            const uint32_t bar = pkv::smem_u32(&ctl.free_q[m.seg % C::kQBufs]);
-                            pkv::tc_commit(bar);
-                            if (!C::kTwo && m.left == 0 && m.at == 0) pkv::tc_commit(bar);
-                        }
-                        ctl.which[w][us & 1] = 2 * k.t + sub_s;
+            // ---- S of the next tile: its columns are those of the last but one
+            if (tk < count && us < od + 2 && ready(rings.full_k[k.slot], k.turn)) {
+                const Tile &m = rings.tiles[tk % kMetas];
+                const bool none = C::kTwo && m.nr <= w * kRowTile;   // the unit has no rows for this group
+                if (pkv::elect_one()) {
+                    if (none) {
+                        pkv::mbar_arrive(pkv::smem_u32(&rings.free_k[k.slot]));
+                        if (m.left == 0) pkv::mbar_arrive(pkv::smem_u32(&rings.free_q));
+                    } else {
+                        issue_s(k.slot, us & 1, desc);
+                        if (m.left == 0) pkv::tc_commit(pkv::smem_u32(&rings.free_q));
+                        ctl.which[w][us & 1] = tk;
                         pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
                     }
-                    ++us;
-                    sub_s ^= 1;
-                    if (last) {
-                        sub_s = 0;
-                        k.next(kStep);
-                    }
-                    moved = true;
                 }
                 __syncwarp();
+                us += !none;
+                ++tk;
+                k.next();
+                moved = true;
             }
-            // ---- P V of product up
-            if (v.t < count && v.t <= k.t) {
-                const Tile &m = ctl.tiles[v.t % kMetas];
-                if (C::kTwo && v.t < k.t && m.nr <= w * kTile) {
-                    if (ready(ctl.full_v[v.slot], v.turn)) {
-                        if (pkv::elect_one()) pkv::mbar_arrive(pkv::smem_u32(&ctl.free_v[v.slot]));
-                        v.next(kStep);
-                        moved = true;
-                    }
-                } else if (up < us && ready(ctl.p[w][up & 1], up >> 1) && ready(ctl.full_v[v.slot], v.turn)) {
-                    const bool last = sub_p + 1 == subs_of(m);
-                    const bool skip = *reinterpret_cast<volatile int *>(&ctl.skip[w][up & 1]) != 0;
+            // ---- P V of the next product
+            if (tv < tk) {
+                const Tile &m = rings.tiles[tv % kMetas];
+                const bool none = C::kTwo && m.nr <= w * kRowTile;
+                if ((none || ready(ctl.p[w][up & 1], up >> 1)) && ready(rings.full_v[v.slot], v.turn)) {
+                    const bool skip = !none && *reinterpret_cast<volatile int *>(&ctl.skip[w][up & 1]) != 0;
                     if (pkv::elect_one()) {
-                        if (skip) {
-                            pkv::mbar_arrive(pkv::smem_u32(&ctl.o[w][up & 1]));
-                            if (last) pkv::mbar_arrive(pkv::smem_u32(&ctl.free_v[v.slot]));
+                        if (none || skip) {
+                            if (skip) pkv::mbar_arrive(pkv::smem_u32(&ctl.o[w][up & 1]));
+                            pkv::mbar_arrive(pkv::smem_u32(&rings.free_v[v.slot]));
                         } else {
-                            issue_pv(m, v.slot, sub_p, up & 1, m.seg == seg_p, last);
+                            issue_pv(m.L - m.t0, v.slot, up & 1, m.seg == seg_p);
                         }
                     }
+                    __syncwarp();
                     seg_p = m.seg;
-                    ++up;
-                    sub_p ^= 1;
-                    if (last) {
-                        sub_p = 0;
-                        v.next(kStep);
-                    }
+                    up += !none;
+                    ++tv;
+                    v.next();
                     moved = true;
                 }
-                __syncwarp();
             }
-            if (k.t >= count && v.t >= count) break;
             if (moved) {
                 since = 0;
             } else {
@@ -491,18 +461,20 @@ struct Issuer {
                 if (since == 0) since = now;
                 else if (__any_sync(~0u, now - since > p.wait_ns)) {
                     if (pkv::elect_one()) atomicOr(p.b.err, PKV_DEVERR_TIMEOUT);
-                    return;
+                    break;
                 }
             }
         }
         // nothing more comes: the softmax leaves
-        if (pkv::elect_one()) {
-            ctl.which[w][us & 1] = -1;
-            pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
-            pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
+        if (tv >= count) {
+            if (pkv::elect_one()) {
+                ctl.which[w][us & 1] = -1;
+                pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
+                pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
+            }
+            __syncwarp();
         }
-        __syncwarp();
-        while (od < up && warp_wait(p, ctl.o[w][od & 1], od >> 1)) ++od;   // and its products are done
+        while (od < up && warp_wait(p, ctl.o[w][od & 1], od >> 1)) ++od;      // its products are done
     }
 };
 
@@ -514,13 +486,14 @@ struct Softmax {
     using El = pkv::Elem<T>;
     const TreeParams &p;
     Control &ctl;
-    uint32_t base, tm;                                       // tensor memory of the group, this lane quarter
+    Rings &rings;
+    uint32_t base, tm;                                       // the worker's shared memory; tensor memory of the group, this lane quarter
     int w, row;
     float scale, mu, room, l;
     bool have_o;
     uint32_t mask[2];                                        // the row's first mask words
 
-    __device__ __forceinline__ uint32_t O() const { return tm + 2 * kSub; }
+    __device__ __forceinline__ uint32_t O() const { return tm + 2 * kTile; }
     // The warp has done what the barrier counts; what it did to tensor memory is ordered.
     __device__ __forceinline__ void arrive(uint64_t &bar) const {
         pkv::tc_fence_before();
@@ -565,9 +538,9 @@ struct Softmax {
         }
     }
 
-    // Whether any V of the product's drafted tokens is not finite (told through *odd).
-    __device__ __forceinline__ void look_through(uint32_t slot, const Tile &m, int sub, int tag, volatile int *odd) const {
-        const int a = max(sub * kSub, m.L - m.n - m.t0), z = min((sub + 1) * kSub, m.L - m.t0);
+    // Whether any V of the tile's drafted tokens is not finite (told through *odd).
+    __device__ __forceinline__ void look_through(uint32_t slot, const Tile &m, int tag, volatile int *odd) const {
+        const int a = max(0, m.L - m.n - m.t0), z = min(kTile, m.L - m.t0);
         constexpr int R = C::kPlanes * 8;
         constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
         constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
@@ -582,7 +555,7 @@ struct Softmax {
         if (any) *odd = tag;
     }
 
-    // O += P V of a product on the CUDA cores, over what has weight.
+    // O += P V of a tile on the CUDA cores, over what has weight.
     __device__ __forceinline__ void slow_pv(uint32_t P, uint32_t slot, int ntok) const {
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
@@ -639,7 +612,7 @@ struct Softmax {
         tm_wait(x1);
         float a4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < kSub; j += 8)
+        for (int j = 0; j < kTile; j += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int c = j + 2 * e;
@@ -662,7 +635,7 @@ struct Softmax {
         const pkv::Pair s2 = pkv::pair_of(scale, scale), m2 = pkv::pair_of(-mu, -mu), minus = pkv::pair_of(-1.f, -1.f);
         pkv::Pair sum = 0;
 #pragma unroll
-        for (int c = 0; c < kSub; c += 16) {
+        for (int c = 0; c < kTile; c += 16) {
             uint32_t y[16];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -689,25 +662,12 @@ struct Softmax {
         return true;
     }
 
-    // The rows' outputs, or a piece: this group's state, and the other's (two).
-    __device__ __forceinline__ void finish(const Tile &m, int r0, int nr, bool two) {
-        float f0 = 1.f, f1 = 0.f;
-        if (two) {
-            const float2 s = ctl.told[row];
-            // a state without a weight has no reference of its own
-            const float top = l == 0.f ? s.x : s.y == 0.f ? mu : fmaxf(mu, s.x);
-            f0 = l == 0.f ? 0.f : pkv::ex2_approx(mu - top);
-            f1 = s.y == 0.f ? 0.f : pkv::ex2_approx(s.x - top);
-            l = l * f0 + s.y * f1;
-            mu = top;
-        }
+    // The rows' outputs, or a piece.
+    __device__ __forceinline__ void finish(const Tile &m, int me, int r0, int nr) const {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        f0 *= inv;
-        f1 *= inv;
         const bool mine = row < nr;
         const size_t at = m.whole ? pkv::tree_row(p, m.o, m.g, m.r0 + r0 + (mine ? row : 0))
-                                  : (size_t)(2 * blockIdx.x + m.slot) * p.RC + r0 + row;
-        const uint32_t other = O() + (w ? -256 : 256);
+                                  : (size_t)(2 * me + m.slot) * p.RC + r0 + row;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t x[32];
@@ -715,13 +675,7 @@ struct Softmax {
             tm_load(O() + c, x);
             tm_wait(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = f0 == 0.f ? 0.f : f32(x[i]) * f0;
-            if (two) {
-                tm_load(other + c, x);
-                tm_wait(x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = f1 == 0.f ? y[i] : fmaf(f32(x[i]), f1, y[i]);
-            }
+            for (int i = 0; i < 32; ++i) y[i] = l == 0.f ? 0.f : f32(x[i]) * inv;
             if (mine && m.whole) {
                 pkv::tree_store<32>(p, at * D + c, y);
             } else if (mine) {
@@ -739,25 +693,23 @@ struct Softmax {
         __syncwarp();
     }
 
-    __device__ __forceinline__ bool run() {
+    __device__ __forceinline__ bool run(int me) {
         int seg = -1, i = 0, r0 = 0, nr = 0;
-        uint32_t met = 0, seen = 0, taken = 0;               // uses of these barriers
-        bool shown = false;                                  // a state the other group has not taken yet
+        uint32_t met = 0;                                    // uses of that barrier
         for (int u = 0;; ++u) {
             const int buf = u & 1;
             if (!wait(ctl.s[w][buf], u >> 1)) return false;
-            const int which = *reinterpret_cast<volatile int *>(&ctl.which[w][buf]);
-            if (which < 0) return true;
-            const int t = which >> 1, sub = which & 1;
-            const Tile &m = ctl.tiles[t % kMetas];           // (stays until the tile is done, and some tiles longer)
+            const int t = *reinterpret_cast<volatile int *>(&ctl.which[w][buf]);
+            if (t < 0) return true;
+            const Tile &m = rings.tiles[t % kMetas];         // (stays until the tile is done, and some tiles longer)
             if (m.seg != seg) {
                 seg = m.seg;
                 mu = kNone;
                 room = -INFINITY;
                 l = 0.f;
                 have_o = false;
-                r0 = C::kTwo ? w * kTile : 0;
-                nr = min(kTile, m.nr - r0);
+                r0 = C::kTwo ? w * kRowTile : 0;
+                nr = min(kRowTile, m.nr - r0);
                 i = (m.r0 + r0 + min(row, nr - 1)) / p.G;
                 if (p.masks) {                               // asked for now, needed at the unit's end
                     const uint2 two = __ldg(reinterpret_cast<const uint2 *>(mask_row(m, i)));
@@ -766,44 +718,32 @@ struct Softmax {
                 }
             }
             const bool live = (row & ~31) < nr;              // warps without rows only keep the meetings
-            const int t0 = m.t0 + sub * kSub, d0 = t0 - (m.L - m.n);
-            const uint32_t at = tm + kSub * buf;
-            if (shown) {                                     // the outputs that the other group reads
-                if (!wait(ctl.taken[w], taken++)) return false;
-                shown = false;
-            }
-            if (d0 + kSub > 0) {                             // drafted tokens among them, or the context's end
+            const int d0 = m.t0 - (m.L - m.n);
+            const uint32_t at = tm + kTile * buf;
+            bool odd = false;
+            if (d0 + kTile > 0) {                            // drafted tokens among them, or the context's end
                 if (live && !weights<true>(at, m, i, d0, u)) return false;
-                const uint32_t slot = base + C::kQBufs * C::kQ + (C::kK + t % C::kV) * C::kSlot;
-                if (!wait(ctl.full_v[t % C::kV], t / C::kV)) return false;
+                const uint32_t slot = base + C::kQ + (C::kK + t % C::kV) * C::kSlot;
+                if (!wait(rings.full_v[t % C::kV], t / C::kV)) return false;
                 volatile int *flag = &ctl.odd[w][met & 1];   // (written again two meetings later)
-                look_through(slot, m, sub, u + 1, flag);
+                look_through(slot, m, t + 1, flag);
                 arrive(ctl.meet[w]);
                 if (!wait(ctl.meet[w], met++)) return false;
-                const bool odd = *flag == u + 1;
+                odd = *flag == t + 1;
                 if (odd) {
                     if (have_o && !wait_o(u - 1)) return false;
-                    if (live) slow_pv(at, slot + sub * (kSub * 128), min(kSub, m.L - t0));
+                    if (live) slow_pv(at, slot, min(kTile, m.L - m.t0));
                 }
-                if (row == 0) ctl.skip[w][buf] = odd;
             } else {
                 if (live && !weights<false>(at, m, i, d0, u)) return false;
-                if (row == 0) ctl.skip[w][buf] = 0;
             }
+            if (row == 0) ctl.skip[w][buf] = odd;
+            const int left = m.left;
             arrive(ctl.p[w][buf]);
             have_o = true;
-            if (sub + 1 < subs_of(m)) continue;
-            if (m.left == 0) {
-                const bool two = !C::kTwo && m.at > 0;
+            if (left == 0) {
                 if (!wait_o(u)) return false;
-                if (two && !wait(ctl.state[w ^ 1], seen++)) return false;
-                if (live) finish(m, r0, nr, two);
-                if (two) arrive(ctl.taken[w ^ 1]);
-            } else if (!C::kTwo && m.left == 1) {            // the other group has the last tile
-                if (!wait_o(u)) return false;
-                ctl.told[row] = make_float2(mu, l);
-                arrive(ctl.state[w]);
-                shown = true;
+                if (live) finish(m, me, r0, nr);
             }
         }
     }
@@ -820,53 +760,58 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
     if (tid == 32) {
         auto init = [](uint64_t &bar, int n) { pkv::mbar_init(pkv::smem_u32(&bar), n); };
         constexpr int users = C::kTwo ? 2 : 1;
-        for (int i = 0; i < 6; ++i) {
-            init(ctl.full_k[i], 32 * (kKWarps + 1) + 1);     // copies, q's, and the tile's record
-            init(ctl.full_v[i], 32 * kVWarps);
-            init(ctl.free_k[i], users);
-            init(ctl.free_v[i], users);
+        for (int i = 0; i < C::kWorkers; ++i) {
+            for (int b = 0; b < kMostSlots; ++b) {
+                init(ctl.rings[i].full_k[b], 32 * (C::kCopyWarps + 1) + 1);      // copies, q's, and the tile's record
+                init(ctl.rings[i].full_v[b], 32 * C::kCopyWarps);
+                init(ctl.rings[i].free_k[b], users);
+                init(ctl.rings[i].free_v[b], users);
+            }
+            init(ctl.rings[i].free_q, users);
         }
-        for (int i = 0; i < 2; ++i) init(ctl.free_q[i], 2);
         for (int i = 0; i < kGroups; ++i) {
             for (int b = 0; b < 2; ++b) {
                 init(ctl.s[i][b], 2);                        // the products, and which they are
                 init(ctl.p[i][b], kGroupWarps);
                 init(ctl.o[i][b], 1);
-                ctl.odd[i][b] = ctl.skip[i][b] = 0;
+                ctl.odd[i][b] = 0;
             }
             init(ctl.meet[i], kGroupWarps);
-            init(ctl.state[i], kGroupWarps);
-            init(ctl.taken[i], kGroupWarps);
         }
         pkv::fence_mbarrier_init();
     }
     pkv::tc_fence_before();
     pkv::grid_dependency_wait();
-    if (tid == 0) p.cuts[blockIdx.x].parts = 0;
+    if (tid < C::kWorkers) p.cuts[tid * gridDim.x + blockIdx.x].parts = 0;
+    int *prefix = reinterpret_cast<int *>(smem) + kThreads / 32;
+    const int total = pkv::tree_tiles<kTile, kThreads>(p, prefix, reinterpret_cast<int *>(smem));
+    // softmax warps, then by twos (worker or half of its copies): K, issue, V, q
+    // (so that the issuing warps share no scheduler with the softmax of rows 0..63)
+    const int x = warp - kSoftmaxThreads / 32, role = x < 0 ? -1 : x / 2, which = x < 0 ? tid / kGroupThreads : x & 1;
+    const int worker = C::kTwo ? 0 : which;
     TreePlace at;
-    const TreeShare share =
-        pkv::tree_share<kTile, kThreads>(p, reinterpret_cast<int *>(smem) + kThreads / 32, reinterpret_cast<int *>(smem), at);
+    const TreeShare share = pkv::tree_share<kTile>(p, prefix, total, worker * gridDim.x + blockIdx.x, C::kWorkers * gridDim.x, at);
     __syncthreads();
     pkv::tc_fence_after();
-    const uint32_t base = pkv::smem_u32(smem), tmem = ctl.tmem;
-    if (tid < kSoftmaxThreads) {
-        const int w = tid / kGroupThreads;
-        Softmax<T, D, ROWS> x{p, ctl, base, tmem + 256 * w + ((uint32_t)(warp & 3) << 21), w, tid % kGroupThreads, fabsf(p.scale_log2)};
-        x.run();
+    const uint32_t base = pkv::smem_u32(smem) + worker * C::kWorker, tmem = ctl.tmem;
+    Rings &rings = ctl.rings[worker];
+    if (role < 0) {
+        Softmax<T, D, ROWS> sm{p, ctl, rings, base, tmem + 256 * which + ((uint32_t)(warp & 3) << 21), which, tid % kGroupThreads,
+                               fabsf(p.scale_log2)};
+        sm.run(share.me);
     } else {
-        const int x = warp - kSoftmaxThreads / 32, lane = tid & 31, count = share.Z - share.A;
-        constexpr int kv = kGroups + kKWarps;
-        if (x < kGroups) {
-            Issuer<T, D, ROWS> is{p, ctl, base, tmem + 256 * x, x, count};
+        const int lane = tid & 31, part = C::kTwo ? which : 0;
+        if (role == 0) {
+            Producer<D, ROWS, LB, false> pr{p, rings, base + C::kQ, lane, part, 0, 0, 0};
+            pr.run(share, at);
+        } else if (role == 1) {
+            Issuer<T, D, ROWS> is{p, ctl, rings, base, tmem + 256 * which, which, share.Z - share.A};
             is.run();
-        } else if (x < kv) {
-            Producer<D, ROWS, LB, false> pr{p, &ctl, base + C::kQBufs * C::kQ, lane, x - kGroups, 0, 0, 0};
+        } else if (role == 2) {
+            Producer<D, ROWS, LB, true> pr{p, rings, base + C::kQ + C::kK * C::kSlot, lane, part, 0, 0, 0};
             pr.run(share, at);
-        } else if (x < kv + kVWarps) {
-            Producer<D, ROWS, LB, true> pr{p, &ctl, base + C::kQBufs * C::kQ + C::kK * C::kSlot, lane, x - kv, 0, 0, 0};
-            pr.run(share, at);
-        } else {
-            copy_q<D, ROWS>(p, ctl, base, share, at);
+        } else if (!C::kTwo || which == 0) {
+            copy_q<D, ROWS>(p, rings, base, share, at);
         }
         pkv::cp_async_wait_all();
     }
@@ -891,7 +836,7 @@ cudaError_t launch_one(const TreeParams &p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_chained(tree_mma_kernel<T, D, ROWS, LB>, dim3((unsigned)p.C), kThreads, bytes, stream, p);
+    return launch_chained(tree_mma_kernel<T, D, ROWS, LB>, dim3((unsigned)(p.C / Cfg<D, ROWS>::kWorkers)), kThreads, bytes, stream, p);
 }
 
 template <typename T, int D, int ROWS>
