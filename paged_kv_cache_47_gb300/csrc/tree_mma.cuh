@@ -601,24 +601,26 @@ struct Softmax {
     // place. d0: the first token's place among the drafted ones; u: the product.
     template <bool MASKED>
     __device__ __forceinline__ bool weights(uint32_t at, const Tile &m, int i, int d0, int u) {
-        uint32_t x[64];
-        uint32_t(&x0)[32] = *reinterpret_cast<uint32_t(*)[32]>(x), (&x1)[32] = *reinterpret_cast<uint32_t(*)[32]>(x + 32);
-        tm_load(at, x0);
-        tm_load(at + 32, x1);
         uint32_t bits[2];
         bits[0] = MASKED ? sees(m, i, d0) : ~0u;
         bits[1] = MASKED ? sees(m, i, d0 + 32) : ~0u;
-        tm_wait(x0);
-        tm_wait(x1);
         float a4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // (rolled: longer code is fetched more slowly than it runs)
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+            uint32_t x[32];
+            tm_load(at + c, x);
+            const uint32_t seen = c ? bits[1] : bits[0];
+            tm_wait(x);
 #pragma unroll
-        for (int j = 0; j < kTile; j += 8)
+            for (int j = 0; j < 32; j += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = j + 2 * e;
-                a4[e] = fmaxf(fmaxf(a4[e], MASKED && !(bits[c / 32] >> (c % 32) & 1) ? -INFINITY : f32(x[c])),
-                              MASKED && !(bits[c / 32] >> (c % 32 + 1) & 1) ? -INFINITY : f32(x[c + 1]));
-            }
+                for (int e = 0; e < 4; ++e) {
+                    const int k = j + 2 * e;
+                    a4[e] = fmaxf(fmaxf(a4[e], MASKED && !(seen >> k & 1) ? -INFINITY : f32(x[k])),
+                                  MASKED && !(seen >> (k + 1) & 1) ? -INFINITY : f32(x[k + 1]));
+                }
+        }
         const float top = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3])) * scale;    // (scale is not negative; NaN stays out)
         if (__any_sync(~0u, top > room)) {
             const bool none = mu == kNone;
@@ -634,18 +636,21 @@ struct Softmax {
         }
         const pkv::Pair s2 = pkv::pair_of(scale, scale), m2 = pkv::pair_of(-mu, -mu), minus = pkv::pair_of(-1.f, -1.f);
         pkv::Pair sum = 0;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kTile; c += 16) {
-            uint32_t y[16];
+            uint32_t x[16], y[16];
+            pkv::tmem_ld16(at + c, x);
+            const uint32_t seen = (c < 32 ? bits[0] : bits[1]) >> (c & 16);
+            pkv::tmem_ld_wait(x);
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
                 float a, b, ra, rb, la, lb;
-                pkv::unpair(pkv::fma2(pkv::pair_of(f32(x[c + j]), f32(x[c + j + 1])), s2, m2), a, b);
+                pkv::unpair(pkv::fma2(pkv::pair_of(f32(x[j]), f32(x[j + 1])), s2, m2), a, b);
                 a = pkv::ex2_approx(a);
                 b = pkv::ex2_approx(b);
                 if (MASKED) {
-                    a = bits[c / 32] >> (c % 32 + j) & 1 ? a : 0.f;
-                    b = bits[c / 32] >> (c % 32 + j + 1) & 1 ? b : 0.f;
+                    a = seen >> j & 1 ? a : 0.f;
+                    b = seen >> (j + 1) & 1 ? b : 0.f;
                 }
                 const pkv::Pair ab = pkv::pair_of(a, b);
                 sum = pkv::add2(sum, ab);
