@@ -190,8 +190,8 @@ cudaError_t launch(int dtype, const TreeParams &p, cudaStream_t stream) {
                     : dtype == PKV_F16 ? pkv::launch_tree_f16(D, p, stream)
                                        : pkv::launch_tree_bf16(D, p, stream);
     if (e != cudaSuccess) return e;
-    int y = (p.RC + pkv::kTreeJoinWarps - 1) / pkv::kTreeJoinWarps;
-    if (y > 8) y = 8;
+    // two rows a warp
+    const int y = (p.RC + 2 * pkv::kTreeJoinWarps - 1) / (2 * pkv::kTreeJoinWarps);
     return launch_chained(pkv::tree_join_kernel<D>, dim3((unsigned)p.C, (unsigned)y), 32 * pkv::kTreeJoinWarps, 0, stream, p);
 }
 

@@ -24,7 +24,7 @@
 namespace pkv {
 
 constexpr int kTreeMaxSeqs = 1024;       // sequences of one launch
-constexpr int kTreeJoinWarps = 8;
+constexpr int kTreeJoinWarps = 4;
 constexpr int kTreeMmaRows = 128;        // rows of a row tile on the tensor cores
 constexpr int kTreeMmaTile = 64;         // tokens of a tile there
 
@@ -198,23 +198,27 @@ __device__ __forceinline__ void tree_store(const TreeParams &p, size_t at, const
 }
 
 // The joins: CTA (c, y) takes rows y * warps.. of the unit cut that begins in
-// worker c, a warp a row, D / 32 elements a lane.
+// worker c, a warp a row, four elements a lane. Denominators are asked for beside
+// the record of the cut, and eight pieces' elements at once: two round trips of
+// memory for few pieces.
 template <int D>
 __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const __grid_constant__ TreeParams p) {
     grid_dependents_launch();
     grid_dependency_wait();
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int parts = __ldcg(&p.cuts[c].parts);
     const TreeCut cut = p.cuts[c];
-    if (cut.parts < 2) return;
-    for (int r = blockIdx.y * kTreeJoinWarps + warp; r < cut.nr; r += gridDim.y * kTreeJoinWarps) {
+    for (int r = blockIdx.y * kTreeJoinWarps + warp; r < p.RC; r += gridDim.y * kTreeJoinWarps) {
         // the first worker's piece is in its slot 1, the others' in slot 0
         const size_t at0 = (size_t)(2 * c + 1) * p.RC + r, step = (size_t)2 * p.RC;
+        float l0 = c + lane < p.C ? __ldcg(p.ws_lse + at0 + lane * step - (lane ? p.RC : 0)) : -INFINITY;
+        if (parts < 2 || r >= cut.nr) return;
         float mx = -INFINITY, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < cut.parts; k0 += 32) {
+        for (int k0 = 0; k0 < parts; k0 += 32) {
             const int k = k0 + lane;
-            const size_t at = at0 + k * step - (k ? p.RC : 0);
-            const float l = k < cut.parts ? __ldcg(p.ws_lse + at) : -INFINITY;
+            float l = -INFINITY;
+            if (k < parts) l = k0 ? __ldcg(p.ws_lse + at0 + k * step - p.RC) : l0;
             float m = l;
 #pragma unroll
             for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
@@ -226,17 +230,24 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const __
             sum = sum * f0 + s;
             mx = nm;
             o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
-            const int here = min(32, cut.parts - k0);
-#pragma unroll 4
-            for (int j = 0; j < here; ++j) {
-                const size_t a = at0 + (k0 + j) * step - (k0 + j ? p.RC : 0);
-                const float w = __shfl_sync(~0u, f, j);
-                if (lane * 4 < D) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + a * D) + lane);
-                    o.x = fmaf(x.x, w, o.x);
-                    o.y = fmaf(x.y, w, o.y);
-                    o.z = fmaf(x.z, w, o.z);
-                    o.w = fmaf(x.w, w, o.w);
+            const int here = min(32, parts - k0);
+            for (int j0 = 0; j0 < here; j0 += 8) {
+                float4 x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int q = k0 + min(j0 + j, here - 1);
+                    const size_t a = at0 + q * step - (q ? p.RC : 0);
+                    if (lane * 4 < D) x[j] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + a * D) + lane);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float w = __shfl_sync(~0u, f, min(j0 + j, here - 1));
+                    if (j0 + j < here && lane * 4 < D) {
+                        o.x = fmaf(x[j].x, w, o.x);
+                        o.y = fmaf(x[j].y, w, o.y);
+                        o.z = fmaf(x[j].z, w, o.z);
+                        o.w = fmaf(x[j].w, w, o.w);
+                    }
                 }
             }
         }

@@ -247,41 +247,25 @@ struct Producer {
         return D == 128 ? (at ^ ((2 * j & 6) << 4)) + j * 256 : (at ^ ((4 * j & 4) << 4)) + j * 512;
     }
 
-    // A context's last tile, or one with a block id outside the pool (its rows
-    // become zeros). Scores of rows past the context are not looked at, so those
-    // of K may hold anything; V's are zeros up to the product's last 16 tokens.
-    static __device__ __noinline__ void ragged(const TreeParams &p, const uint8_t *pool, uint32_t slot, int32_t ids, int at, int g,
-                                               int left, int pw) {
-        const int lane = threadIdx.x & 31;
-        constexpr int R = C::kPlanes * 8;                    // pieces of a row
-        const int rows = max(0, min(kRows, (V ? (left + 15) & ~15 : left) - pw * kRows));
-        const uint32_t to = slot + lane_at(pw, lane);
-#pragma unroll 4
-        for (int j = 0; j < (rows * R + 31) / 32; ++j) {
-            const int r = (lane + 32 * j) / R, w = (lane + 32 * j) % R;
-            const int id = __shfl_sync(~0u, ids, at + (r >> LB));
-            const bool in = pw * kRows + r < left, ok = (unsigned)id < (unsigned)p.NB;
-            if (in && !ok && !V) atomicOr(p.b.err, PKV_DEVERR_BLOCK_ID);
-            const size_t src = ((((size_t)(ok ? id : 0) * p.Hk + g) << LB) + (r & ((1 << LB) - 1))) * (2 * D) + w * 16;
-            pkv::cp_async_16(piece(to, j), pool + src, in && ok);
-        }
-    }
-
+    // The warp's rows of a tile, left of them in the context. What is past it, or
+    // in a block whose id lies outside the pool, becomes zeros: all that a product
+    // reads (16 tokens at a time) of V, as zero weights want them.
     __device__ __forceinline__ void copy(uint32_t slot, int32_t ids, int at, int g, int left) const {
-        const uint8_t *src = static_cast<const uint8_t *>(V ? p.v : p.k);
-        const int32_t mine = __shfl_sync(~0u, ids, at + lane % E);
-        if (left < kTile || __any_sync(~0u, (unsigned)mine >= (unsigned)p.NB)) {
-            ragged(p, src, slot, ids, at, g, left, pw);
-            return;
-        }
-        constexpr int PB = kPieces / E;                      // pieces of a block
-        const uint32_t to = slot + lane_at(pw, lane);
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
+        const uint8_t *src = static_cast<const uint8_t *>(V ? p.v : p.k) + lane * 16;
+        uint32_t to = slot + lane_at(pw, lane);
+        left -= pw * kRows;
+        const int rows = min(kRows, V ? (left + 15) & ~15 : left), row = lane / (C::kPlanes * 8);
+        constexpr int PB = kPieces / E, PR = 32 / (C::kPlanes * 8);    // pieces of a block, rows of a piece
+#pragma unroll 1
+        for (int k = 0; k << LB < rows; ++k) {
             const int id = __shfl_sync(~0u, ids, at + k);
-            const uint8_t *block = src + (((size_t)(uint32_t)id * p.Hk + g) << LB) * (2 * D) + lane * 16;
+            const bool ok = (unsigned)id < (unsigned)p.NB;
+            if (!ok && !V && lane == 0) atomicOr(p.b.err, PKV_DEVERR_BLOCK_ID);
+            const int here = ok ? left - (k << LB) - row : 0;          // rows from this lane's first on
+            const uint8_t *block = src + (((size_t)(ok ? id : 0) * p.Hk + g) << LB) * (2 * D);
 #pragma unroll
-            for (int j = 0; j < PB; ++j) pkv::cp_async_16(piece(to, k * PB + j), block + j * 512, true);
+            for (int j = 0; j < PB; ++j) pkv::cp_async_16(piece(to, j), block + j * 512, j * PR < here);
+            to += 128 << LB;
         }
     }
 
@@ -377,7 +361,7 @@ struct Issuer {
         const uint64_t dk = pkv::sdesc_sw128(base + C::kQ + slot * C::kSlot, 16, 1024);
         pkv::fence_proxy_async_smem();
         pkv::tc_fence_after();
-#pragma unroll
+#pragma unroll C::kTwo ? 8 : 1
         for (int k = 0; k < D / 16; ++k)
             mma_ss(tmem + kTile * buf, dq + (k / 4) * (C::kQPlane >> 4) + (k % 4) * 2, dk + (k / 4) * (C::kPlane >> 4) + (k % 4) * 2, desc, k);
         pkv::tc_commit(pkv::smem_u32(&ctl.s[w][buf]));
@@ -389,7 +373,7 @@ struct Issuer {
         const uint64_t dv = pkv::sdesc_sw128(base + C::kQ + (C::kK + slot) * C::kSlot, C::kPlane, 1024);
         pkv::fence_proxy_async_smem();
         pkv::tc_fence_after();
-#pragma unroll
+#pragma unroll C::kTwo ? 4 : 1
         for (int k = 0; k < kTile / 16; ++k)
             if (16 * k < ntok) {
                 const uint32_t a = tmem + kTile * buf + 16 * k;
