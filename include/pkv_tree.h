@@ -96,10 +96,11 @@ size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc *cache, int32_t num_
  * What a row does not see never reaches it, whatever the pool holds there
  * (infinities and NaN included).
  * masks: NULL for chains (i sees j <= i). q, out: [num_tokens][num_q_heads]
- * [head_dim], q and the pools in the cache's dtype, all 16-byte aligned. max_tree: drafted tokens of a sequence at
+ * [head_dim], q and the pools in the cache's dtype and 16-byte aligned, out
+ * 32-byte aligned. max_tree: drafted tokens of a sequence at
  * most, 1..PKV_TREE_MAX_TOKENS (and 64 * mask_words with masks); it sizes the
  * work, so a bound near the truth is best. Block ids outside the pool set
- * PKV_DEVERR_BLOCK_ID and read as zeros. workspace: 16-byte aligned, at least
+ * PKV_DEVERR_BLOCK_ID and read as zeros. workspace: 32-byte aligned, at least
  * pkv_decode_tree_workspace_bytes. options: NULL for the defaults.
  */
 pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,

@@ -276,11 +276,11 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
     if (!q || !k_pool || !v_pool || !block_tables || !context_lens || !token_offsets || !out)
         return pkv::set_last_error(PKV_ERR_INVALID_ARG, "a pointer argument is NULL");
     const int D = cache->head_dim, Hk = cache->num_kv_heads;
-    if (misaligned(q, 16) || misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(out, 16) ||
+    if (misaligned(q, 16) || misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(out, 32) ||
         misaligned(block_tables, 4) || misaligned(context_lens, 4) || misaligned(token_offsets, 4) ||
         misaligned(masks, 8) || (options && misaligned(options->lse_out, 4)))
         return pkv::set_last_error(PKV_ERR_INVALID_ARG,
-                                   "q, the pools and out must be 16-byte aligned, the others to their elements");
+                                   "q and the pools must be 16-byte aligned, out 32-byte aligned, the others to their elements");
     Shape shape = shape_of(cache, num_q_heads, max_tree);
     const int G = num_q_heads / Hk, RC = shape.rows;
     // the list's places fit 32 bits
@@ -295,8 +295,8 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
     if (!workspace || workspace_bytes < need)
         return pkv::set_last_error(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                                    workspace ? workspace_bytes : (size_t)0);
-    if (misaligned(workspace, 16))
-        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    if (misaligned(workspace, 32))
+        return pkv::set_last_error(PKV_ERR_INVALID_ARG, "workspace must be 32-byte aligned");
     TreeParams p = {};
     if ((st = pkv::device_error_word(&p.b.err)) != PKV_OK) return st;
     if (cache->dtype != PKV_F32) pkv::next_wait_fault(&p.wait_ns, &p.drop_arrival);

@@ -170,14 +170,31 @@ __device__ __forceinline__ size_t tree_row(const TreeParams &p, int o, int g, in
     return (size_t)(o + i) * p.Hq + g * p.G + (rr - i * p.G);
 }
 
+// 32 bytes in one store: a whole sector of memory, where rows lie apart.
+__device__ __forceinline__ void store_32(void *to, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // E neighbouring outputs in the output's type.
 template <int E>
 __device__ __forceinline__ void tree_store(const TreeParams &p, size_t at, const float (&o)[E]) {
     static_assert(E % 4 == 0, "");
     if (p.out_dtype == PKV_F32) {
+        if constexpr (E % 8 == 0) {
 #pragma unroll
-        for (int i = 0; i < E; i += 4)
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < E; i += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(o[i + j]);
+                store_32(static_cast<float *>(p.out) + at + i, w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; i += 4)
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
         return;
     }
     float a, b;
@@ -187,10 +204,12 @@ __device__ __forceinline__ void tree_store(const TreeParams &p, size_t at, const
         w[i / 2] = p.out_dtype == PKV_F16 ? Elem<__half>::pack2(o[i], o[i + 1], a, b)
                                           : Elem<__nv_bfloat16>::pack2(o[i], o[i + 1], a, b);
     uint16_t *dst = static_cast<uint16_t *>(p.out) + at;
-    if constexpr (E % 8 == 0) {
+    if constexpr (E % 16 == 0) {
 #pragma unroll
-        for (int i = 0; i < E; i += 8)
-            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
+        for (int i = 0; i < E; i += 16) {
+            const uint32_t x[8] = {w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3], w[i / 2 + 4], w[i / 2 + 5], w[i / 2 + 6], w[i / 2 + 7]};
+            store_32(dst + i, x);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < E; i += 4) *reinterpret_cast<uint2 *>(dst + i) = make_uint2(w[i / 2], w[i / 2 + 1]);

@@ -91,6 +91,10 @@ struct Cfg {
     static constexpr int kQPlane = (kTwo ? kRowTile : ROWS) * 128;
     static constexpr int kQTile = kPlanes * kQPlane;         // q of a row tile
     static constexpr int kQ = (kTwo ? 2 : 1) * kQTile;       // q of a unit
+    // Units of up to 64 rows: group 1 has them in rows 64..127 of its products, so
+    // that the groups' softmax warps run on schedulers of their own (a warp reaches
+    // a quarter of tensor memory's lanes). The other rows hold anything.
+    static constexpr int kShift = ROWS == 64 ? 64 : 0;
     // rings of K and of V: with q 224 KB (D 64: 208, 160 and 192)
     static constexpr int kK = kTwo ? (D == 128 ? 4 : 10) : D == 128 ? (ROWS == 64 ? 3 : 2) : ROWS == 64 ? 6 : 4;
     static constexpr int kV = kTwo ? (D == 128 ? 6 : 10) : D == 128 ? 3 : ROWS == 64 ? 6 : 4;
@@ -109,7 +113,8 @@ struct Control {
     uint64_t s[kGroups][2], p[kGroups][2], o[kGroups][2], meet[kGroups];
     int odd[kGroups][2];             // tile (+ 1) last found to have V that are not finite, by turns
     int skip[kGroups][2];            // by S: the weights are used up already
-    int which[kGroups][2];           // by S: the worker's tile; -1: no more
+    int4 which[kGroups][2];          // by S: the worker's tile (-1: no more), segment, first token's place
+                                     // among the drafted ones, tiles of the segment after it
     uint32_t tmem;
 };
 
@@ -357,7 +362,7 @@ struct Issuer {
     int w, count;
 
     __device__ __forceinline__ void issue_s(int slot, int buf, uint32_t desc) const {
-        const uint64_t dq = pkv::sdesc_sw128(base + (C::kTwo ? w * C::kQTile : 0), 16, 1024);
+        const uint64_t dq = pkv::sdesc_sw128(base + (C::kTwo ? w * C::kQTile : 0) - w * C::kShift * 128, 16, 1024);
         const uint64_t dk = pkv::sdesc_sw128(base + C::kQ + slot * C::kSlot, 16, 1024);
         pkv::fence_proxy_async_smem();
         pkv::tc_fence_after();
@@ -406,7 +411,7 @@ struct Issuer {
                     } else {
                         issue_s(k.slot, us & 1, desc);
                         if (m.left == 0) pkv::tc_commit(pkv::smem_u32(&rings.free_q));
-                        ctl.which[w][us & 1] = tk;
+                        ctl.which[w][us & 1] = make_int4(tk, m.seg, m.t0 - (m.L - m.n), m.left);
                         pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
                     }
                 }
@@ -452,7 +457,7 @@ struct Issuer {
         // nothing more comes: the softmax leaves
         if (tv >= count) {
             if (pkv::elect_one()) {
-                ctl.which[w][us & 1] = -1;
+                ctl.which[w][us & 1].x = -1;
                 pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
                 pkv::mbar_arrive(pkv::smem_u32(&ctl.s[w][us & 1]));
             }
@@ -472,7 +477,7 @@ struct Softmax {
     Control &ctl;
     Rings &rings;
     uint32_t base, tm;                                       // the worker's shared memory; tensor memory of the group, this lane quarter
-    int w, row;
+    int w, thread, row;                                      // group, thread of it, row of the unit (or none)
     float scale, mu, room, l;
     bool have_o;
     uint32_t mask[2];                                        // the row's first mask words
@@ -482,7 +487,7 @@ struct Softmax {
     __device__ __forceinline__ void arrive(uint64_t &bar) const {
         pkv::tc_fence_before();
         __syncwarp();
-        if ((row & 31) == 0) pkv::mbar_arrive(pkv::smem_u32(&bar));
+        if ((thread & 31) == 0) pkv::mbar_arrive(pkv::smem_u32(&bar));
     }
     __device__ __forceinline__ bool wait(uint64_t &bar, uint32_t parity) const {
         const bool ok = warp_wait(p, bar, parity);
@@ -529,7 +534,7 @@ struct Softmax {
         constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
         constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
         uint32_t any = 0;
-        for (int x = a * R + row; x < z * R; x += kGroupThreads) {
+        for (int x = a * R + thread; x < z * R; x += kGroupThreads) {
             // (the order of a row's pieces says nothing here)
             uint32_t y[4];
             pkv::lds_u32x4(slot + (x % R >> 3) * C::kPlane + (x / R) * 128 + (x % 8 << 4), y[0], y[1], y[2], y[3]);
@@ -654,7 +659,7 @@ struct Softmax {
     // The rows' outputs, or a piece.
     __device__ __forceinline__ void finish(const Tile &m, int me, int r0, int nr) const {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const bool mine = row < nr;
+        const bool mine = row < nr;                          // (of a live warp: row >= 0)
         const size_t at = m.whole ? pkv::tree_row(p, m.o, m.g, m.r0 + r0 + (mine ? row : 0))
                                   : (size_t)(2 * me + m.slot) * p.RC + r0 + row;
 #pragma unroll 1
@@ -669,8 +674,12 @@ struct Softmax {
                 pkv::tree_store<32>(p, at * D + c, y);
             } else if (mine) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4 *>(p.ws_o + at * D + c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                for (int i = 0; i < 32; i += 8) {
+                    uint32_t z[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[j] = __float_as_uint(y[i + j]);
+                    pkv::store_32(p.ws_o + at * D + c + i, z);
+                }
             }
             __syncwarp();
         }
@@ -688,26 +697,26 @@ struct Softmax {
         for (int u = 0;; ++u) {
             const int buf = u & 1;
             if (!wait(ctl.s[w][buf], u >> 1)) return false;
-            const int t = *reinterpret_cast<volatile int *>(&ctl.which[w][buf]);
+            const int4 it = ctl.which[w][buf];
+            const int t = it.x, d0 = it.z;
             if (t < 0) return true;
             const Tile &m = rings.tiles[t % kMetas];         // (stays until the tile is done, and some tiles longer)
-            if (m.seg != seg) {
-                seg = m.seg;
+            if (it.y != seg) {
+                seg = it.y;
                 mu = kNone;
                 room = -INFINITY;
                 l = 0.f;
                 have_o = false;
                 r0 = C::kTwo ? w * kRowTile : 0;
                 nr = min(kRowTile, m.nr - r0);
-                i = (m.r0 + r0 + min(row, nr - 1)) / p.G;
+                i = (m.r0 + r0 + max(0, min(row, nr - 1))) / p.G;
                 if (p.masks) {                               // asked for now, needed at the unit's end
                     const uint2 two = __ldg(reinterpret_cast<const uint2 *>(mask_row(m, i)));
                     mask[0] = two.x;
                     mask[1] = two.y;
                 }
             }
-            const bool live = (row & ~31) < nr;              // warps without rows only keep the meetings
-            const int d0 = m.t0 - (m.L - m.n);
+            const bool live = row >= 0 && (row & ~31) < nr;           // warps without rows only keep the meetings
             const uint32_t at = tm + kTile * buf;
             bool odd = false;
             if (d0 + kTile > 0) {                            // drafted tokens among them, or the context's end
@@ -726,11 +735,10 @@ struct Softmax {
             } else {
                 if (live && !weights<false>(at, m, i, d0, u)) return false;
             }
-            if (row == 0) ctl.skip[w][buf] = odd;
-            const int left = m.left;
+            if (thread == 0) ctl.skip[w][buf] = odd;
             arrive(ctl.p[w][buf]);
             have_o = true;
-            if (left == 0) {
+            if (it.w == 0) {
                 if (!wait_o(u)) return false;
                 if (live) finish(m, me, r0, nr);
             }
@@ -786,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
     Rings &rings = ctl.rings[worker];
     if (role < 0) {
         Softmax<T, D, ROWS> sm{p, ctl, rings, base, tmem + 256 * which + ((uint32_t)(warp & 3) << 21), which, tid % kGroupThreads,
+                               tid % kGroupThreads - which * C::kShift,
                                fabsf(p.scale_log2)};
         sm.run(share.me);
     } else {

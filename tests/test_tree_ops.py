@@ -52,7 +52,7 @@ def _commit(L, desc=None, S=2, T=8, N=4, path=16, cnt=16, offs=16, lens=16, tab=
 
 
 def _attend(L, desc=None, q=16, T=8, Hq=4, kp=16, vp=16, tab=16, S=2, M=4, lens=16, offs=16, masks=16, W=1, N=4, scale=1.0,
-            out=16, odt=2, ws=16, wsb=BIG, ctas=None, lse=None):
+            out=32, odt=2, ws=32, wsb=BIG, ctas=None, lse=None):
     o = b.TreeOptions(ctas or 0, 0, lse)
     return L.pkv_decode_attention_tree(REF(desc or _desc()), q, T, Hq, kp, vp, tab, S, M, lens, offs, masks, W, N, scale,
                                        out, odt, ws, wsb, None, REF(o) if ctas or lse else None)
