@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const float x[4] = {o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv};
-                if (whole) pkv::tree_store<4>(p, row * D + 4 * e + 32 * j, x);
+                if (whole) pkv::tree_store<4>(p.out, p.out_dtype, row * D + 4 * e + 32 * j, x);
                 else *reinterpret_cast<float4 *>(p.ws_o + row * D + 4 * e + 32 * j) = make_float4(x[0], x[1], x[2], x[3]);
             }
             if (e == 0) {

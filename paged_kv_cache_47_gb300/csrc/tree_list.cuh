@@ -177,23 +177,23 @@ __device__ __forceinline__ void store_32(void *to, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
-// E neighbouring outputs in the output's type.
+// E neighbouring outputs in this type.
 template <int E>
-__device__ __forceinline__ void tree_store(const TreeParams &p, size_t at, const float (&o)[E]) {
+__device__ __forceinline__ void tree_store(void *to, int dtype, size_t at, const float (&o)[E]) {
     static_assert(E % 4 == 0, "");
-    if (p.out_dtype == PKV_F32) {
+    if (dtype == PKV_F32) {
         if constexpr (E % 8 == 0) {
 #pragma unroll
             for (int i = 0; i < E; i += 8) {
                 uint32_t w[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(o[i + j]);
-                store_32(static_cast<float *>(p.out) + at + i, w);
+                store_32(static_cast<float *>(to) + at + i, w);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < E; i += 4)
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                *reinterpret_cast<float4 *>(static_cast<float *>(to) + at + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
         return;
     }
@@ -201,9 +201,9 @@ __device__ __forceinline__ void tree_store(const TreeParams &p, size_t at, const
     uint32_t w[E / 2];
 #pragma unroll
     for (int i = 0; i < E; i += 2)
-        w[i / 2] = p.out_dtype == PKV_F16 ? Elem<__half>::pack2(o[i], o[i + 1], a, b)
+        w[i / 2] = dtype == PKV_F16 ? Elem<__half>::pack2(o[i], o[i + 1], a, b)
                                           : Elem<__nv_bfloat16>::pack2(o[i], o[i + 1], a, b);
-    uint16_t *dst = static_cast<uint16_t *>(p.out) + at;
+    uint16_t *dst = static_cast<uint16_t *>(to) + at;
     if constexpr (E % 16 == 0) {
 #pragma unroll
         for (int i = 0; i < E; i += 16) {
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const __
         const size_t row = tree_row(p, cut.o, cut.g, cut.r0 + r);
         if (lane * 4 < D) {
             const float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-            tree_store<4>(p, row * D + lane * 4, x);
+            tree_store<4>(p.out, p.out_dtype, row * D + lane * 4, x);
         }
         if (p.lse_out && lane == 0) p.lse_out[row] = sum == 0.f ? -INFINITY : mx + log2f(sum);
     }

@@ -158,13 +158,11 @@ __device__ __forceinline__ void tm_load(uint32_t at, uint32_t (&r)[32]) {
 __device__ __forceinline__ void tm_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_M8(r, 0), PKV_M8(r, 8), PKV_M8(r, 16), PKV_M8(r, 24) : : "memory");
 }
-__device__ __forceinline__ void tm_store(uint32_t at, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
-        "%23, %24, %25, %26, %27, %28, %29, %30, %31};" ::PKV_W8(r, 0),
-        PKV_W8(r, 8), PKV_W8(r, 16), PKV_W8(r, 24), "r"(at)
-        : "memory");
+__device__ __forceinline__ uint32_t tm_load1(uint32_t at) {
+    uint32_t x;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x) : : "memory");
+    return x;
 }
 __device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile(
@@ -517,13 +515,13 @@ struct Softmax {
 
     __device__ __forceinline__ void scale_o(float f) const {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-            uint32_t x[32];
-            tm_load(O() + c, x);
-            tm_wait(x);
+        for (int c = 0; c < D; c += 16) {
+            uint32_t x[16];
+            pkv::tmem_ld16(O() + c, x);
+            pkv::tmem_ld_wait(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(f32(x[i]) * f);
-            tm_store(O() + c, x);
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(f32(x[i]) * f);
+            tm_store16(O() + c, x);
         }
     }
 
@@ -557,25 +555,20 @@ struct Softmax {
                 for (int i = 0; i < 16; ++i) o[i] = 0;
             }
 #pragma unroll 1
-            for (int t0 = 0; t0 < ntok; t0 += 16) {
-                uint32_t x[16];
-                pkv::tmem_ld16(P + t0, x);
-                pkv::tmem_ld_wait(x);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 hi = El::unpack2(x[j / 2]), lo = El::unpack2(x[8 + j / 2]);
-                    const float pj = j % 2 ? hi.y + lo.y : hi.x + lo.x;
-                    if (pj == 0.f || t0 + j >= ntok) continue;
+            for (int t = 0; t < ntok; ++t) {                 // weight of token t: hi and lo words of a pair
+                const uint32_t pair = P + (t & ~15) + (t & 15) / 2;
+                const float2 hi = El::unpack2(tm_load1(pair)), lo = El::unpack2(tm_load1(pair + 8));
+                const float pt = t & 1 ? hi.y + lo.y : hi.x + lo.x;
+                if (pt != 0.f) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t y[4];
-                        pkv::lds_u32x4(slot + (c >> 6) * C::kPlane + (t0 + j) * 128 + ((((c & 63) / 8 + k) ^ (j & 7)) << 4), y[0], y[1],
-                                       y[2], y[3]);
+                        pkv::lds_u32x4(slot + (c >> 6) * C::kPlane + t * 128 + ((((c & 63) / 8 + k) ^ (t & 7)) << 4), y[0], y[1], y[2], y[3]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float2 v = El::unpack2(y[e]);
-                            o[8 * k + 2 * e] = __float_as_uint(fmaf(pj, v.x, f32(o[8 * k + 2 * e])));
-                            o[8 * k + 2 * e + 1] = __float_as_uint(fmaf(pj, v.y, f32(o[8 * k + 2 * e + 1])));
+                            o[8 * k + 2 * e] = __float_as_uint(fmaf(pt, v.x, f32(o[8 * k + 2 * e])));
+                            o[8 * k + 2 * e + 1] = __float_as_uint(fmaf(pt, v.y, f32(o[8 * k + 2 * e + 1])));
                         }
                     }
                 }
@@ -643,7 +636,13 @@ struct Softmax {
                 }
                 const pkv::Pair ab = pkv::pair_of(a, b);
                 sum = pkv::add2(sum, ab);
-                y[j / 2] = El::pack2(a, b, ra, rb);
+                if constexpr (std::is_same<T, __half>::value) {
+                    y[j / 2] = El::pack2(a, b, ra, rb);
+                } else {                                     // (the upper halves, not rounded: fewer steps, and the rest in lo)
+                    y[j / 2] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+                    ra = f32(__float_as_uint(a) & 0xffff0000u);
+                    rb = f32(__float_as_uint(b) & 0xffff0000u);
+                }
                 pkv::unpair(pkv::fma2(pkv::pair_of(ra, rb), minus, ab), la, lb);
                 y[8 + j / 2] = El::pack2(la, lb, ra, rb);
             }
@@ -662,6 +661,7 @@ struct Softmax {
         const bool mine = row < nr;                          // (of a live warp: row >= 0)
         const size_t at = m.whole ? pkv::tree_row(p, m.o, m.g, m.r0 + r0 + (mine ? row : 0))
                                   : (size_t)(2 * me + m.slot) * p.RC + r0 + row;
+        void *to = m.whole ? p.out : p.ws_o;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t x[32];
@@ -669,18 +669,8 @@ struct Softmax {
             tm_load(O() + c, x);
             tm_wait(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = l == 0.f ? 0.f : f32(x[i]) * inv;
-            if (mine && m.whole) {
-                pkv::tree_store<32>(p, at * D + c, y);
-            } else if (mine) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint32_t z[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) z[j] = __float_as_uint(y[i + j]);
-                    pkv::store_32(p.ws_o + at * D + c + i, z);
-                }
-            }
+            for (int i = 0; i < 32; ++i) y[i] = inv == 0.f ? 0.f : f32(x[i]) * inv;
+            if (mine) pkv::tree_store<32>(to, m.whole ? p.out_dtype : PKV_F32, at * D + c, y);
             __syncwarp();
         }
         if (mine) {
