@@ -5,7 +5,7 @@ Tolerance of an output element, with Z the largest scale * sum |q_d k_d| and V t
 sees, L its context. Products of 16-bit values are exact in fp32, and a sum of D <= 128 of them is off by at most
 2^-23 of sum |q k| a step: a score by D 2^-23 Z <= 2^-16 Z, which moves softmax weights by as much, numerator and
 denominator, so the output by 2 2^-16 Z * 2 V / 2 (the weights' mean moves within [-V, V]). Weights enter the second product with 16 bits
-or more (half a step 2^-17), 2^x is off by 2^-22, a weight's exponent by 2^-23 times its size (at most ~2^7 for a
+or more (off by 2^-16 at most), 2^x is off by 2^-22, a weight's exponent by 2^-23 times its size (at most ~2^7 for a
 weight that counts: 2^-16); the second sum takes L / 16 + 16 steps of 2^-23 and rescalings of 2^-23 each. Together
 below V (2^-15 Z + 2^-15 + (L / 8 + 64) 2^-22), then half a step of the output's type. fp32: sums of D products,
 2^-24 of sum |q k| each step and product: within the same bound."""
@@ -327,6 +327,44 @@ def test_streams_graphs_and_two_calls_at_once():
     out = b.decode_attention_tree(*x.args(), max_tree=64, out_dtype=torch.float32, stream=st)
     st.synchronize()
     assert torch.equal(out, refs[0])
+    assert b.get_error() == 0
+
+
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1.3])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_any_scale(dt, scale):
+    x = Batch([300, 0, 65], [12, 40, 1], dt=dt, seed=7)
+    x.scale = scale
+    lse = torch.zeros(x.q.shape[:2], device="cuda")
+    for ctas in (0, 2):
+        x.check(x.run(lse_out=lse, num_ctas=ctas), lse=lse)
+    assert b.get_error() == 0
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_many_rows_a_kv_head(dt):
+    x = Batch([100], [256], G=41, Hk=1, D=64, dt=dt, seed=3)          # 41 chunks of 256 rows
+    x.check(x.run())
+    y = Batch([700, 3], [9, 14], G=16, Hk=2, dt=dt, seed=4)           # 129..256 rows, and fewer
+    for ctas in (0, 3):
+        y.check(y.run(num_ctas=ctas))
+    assert b.get_error() == 0
+
+
+@pytest.mark.parametrize("G", [4, 20])
+def test_a_wait_that_runs_out(G):
+    # the first copy's arrival is withheld: the call ends, says so, and leaves nothing behind
+    x = Batch([900, 40], [12, 7], G=G, dt="bf16", seed=9)
+    ref = x.run()
+    b.set_wait_fault(2_000_000, 1)
+    x.run()
+    status, word = b.get_error_status()
+    b.set_wait_fault(0, 0)
+    assert status == -5 and word & b.DEVERR_TIMEOUT
+    assert torch.equal(x.run(), ref)
+    b.set_wait_fault(2_000_000, 0)                         # the limit alone changes nothing
+    assert torch.equal(x.run(), ref)
+    b.set_wait_fault(0, 0)
     assert b.get_error() == 0
 
 
