@@ -1440,11 +1440,12 @@ def tree_workspace_bytes(k_pool, num_q_heads: int, max_tree: int, num_ctas: int 
 
 
 def alloc_tree_workspace(k_pool, num_q_heads: int, max_tree: int, num_ctas: int = 0) -> torch.Tensor:
-    """Workspace of decode_attention_tree; one for calls that may overlap."""
+    """Zero-filled workspace of decode_attention_tree (every call leaves its counters zero); one for calls
+    that may overlap."""
     n = tree_workspace_bytes(k_pool, num_q_heads, max_tree, num_ctas)
     if n == 0:
         raise PkvError(-1, lib().pkv_last_error_message().decode())
-    return torch.empty(n, dtype=torch.uint8, device=k_pool.device)
+    return torch.zeros(n, dtype=torch.uint8, device=k_pool.device)
 
 
 def prepared_decode_attention_tree(q, k_pool, v_pool, block_tables, context_lens, token_offsets, masks,

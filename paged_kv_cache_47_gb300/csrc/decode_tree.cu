@@ -36,12 +36,13 @@ struct Shared {
     float p[kRows][kTile + 1];
     int prefix[pkv::kTreeMaxSeqs + 1];
     int scan[kThreads / 32];
+    pkv::TreeCut cuts[2];
 };
 
 __device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_simt_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared<D> &sh = *reinterpret_cast<Shared<D> *>(raw);
     constexpr int V4 = D / 4, J = D / 32;            // vectors of a row; of a thread's outputs
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     TreePlace at;
     const int total = pkv::tree_tiles<kTile, kThreads>(p, sh.prefix, sh.scan);
     const TreeShare share = pkv::tree_share<kTile>(p, sh.prefix, total, blockIdx.x, gridDim.x, at);
-    if (tid == 0) p.cuts[blockIdx.x].parts = 0;
+    if (tid < 2) sh.cuts[tid].parts = 0;
     const float *kp = static_cast<const float *>(p.k), *vp = static_cast<const float *>(p.v), *qp = static_cast<const float *>(p.q);
     const int B = 1 << p.b.lb;
     for (int left = share.Z - share.A, done = 0; left > 0;) {
@@ -161,12 +162,15 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
                 else if (p.lse_out) p.lse_out[row] = lse;
             }
         }
-        if (!whole && i0 == 0 && tid == 0)
-            p.cuts[blockIdx.x] = {pkv::tree_parts(share, share.A + done, at.tiles), at.q.o, g, r0, nr, {}};
+        if (!whole && tid == 0) {
+            sh.cuts[i0 ? 0 : 1] = pkv::tree_cut(share, share.A + done - i0, at.tiles, at.q.o, g, r0, nr);
+            sh.cuts[i0 ? 0 : 1].due = 1;
+        }
         left -= count;
         done += count;
         if (left > 0) at.next_unit<kTile>(p);
     }
+    pkv::tree_join_cuts<D, kThreads / 32, 2, 2>(p, sh.cuts);
 }
 
 template <int D>
@@ -186,13 +190,9 @@ cudaError_t launch_simt(const TreeParams &p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch(int dtype, const TreeParams &p, cudaStream_t stream) {
-    cudaError_t e = dtype == PKV_F32   ? launch_simt<D>(p, stream)
-                    : dtype == PKV_F16 ? pkv::launch_tree_f16(D, p, stream)
-                                       : pkv::launch_tree_bf16(D, p, stream);
-    if (e != cudaSuccess) return e;
-    // two rows a warp
-    const int y = (p.RC + 2 * pkv::kTreeJoinWarps - 1) / (2 * pkv::kTreeJoinWarps);
-    return launch_chained(pkv::tree_join_kernel<D>, dim3((unsigned)p.C, (unsigned)y), 32 * pkv::kTreeJoinWarps, 0, stream, p);
+    return dtype == PKV_F32   ? launch_simt<D>(p, stream)
+           : dtype == PKV_F16 ? pkv::launch_tree_f16(D, p, stream)
+                              : pkv::launch_tree_bf16(D, p, stream);
 }
 
 // Rows of a unit, tokens of a tile, and workers of a launch.
@@ -212,13 +212,17 @@ pkv_status workers_of(const pkv_cache_desc *c, int ctas, Shape *s) {
         if (st != PKV_OK) return st;
         if (c->dtype == PKV_F32) ctas *= kCtasPerSm;
     }
-    // 16-bit units of one row tile: two workers a CTA
+    // 16-bit units of one row tile: two workers a CTA (at most 2 PKV_MAX_DECODE_CTAS counters)
+    if (ctas > PKV_MAX_DECODE_CTAS) ctas = PKV_MAX_DECODE_CTAS;
     s->workers = ctas * (c->dtype != PKV_F32 && s->rows <= pkv::kTreeMmaRows ? 2 : 1);
     return PKV_OK;
 }
 
+// workspace: counters (a fixed region, whatever the launch), then [workers][2]
+// pieces of rows and their denominators
+constexpr size_t kCounterBytes = 2 * PKV_MAX_DECODE_CTAS * sizeof(unsigned);
 size_t workspace_for(const Shape &s, int D) {
-    return (size_t)s.workers * (sizeof(pkv::TreeCut) + (size_t)2 * s.rows * (D + 1) * sizeof(float));
+    return kCounterBytes + (size_t)s.workers * 2 * s.rows * (D + 1) * sizeof(float);
 }
 
 pkv_status check_shape(const pkv_cache_desc *cache, int Hq, int max_tree, int ctas) {
@@ -320,9 +324,9 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
     p.RC = RC;
     p.C = shape.workers;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.ws_o = static_cast<float *>(workspace);
+    p.count = static_cast<unsigned *>(workspace);
+    p.ws_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
     p.ws_lse = p.ws_o + (size_t)p.C * 2 * RC * D;
-    p.cuts = reinterpret_cast<pkv::TreeCut *>(p.ws_lse + (size_t)p.C * 2 * RC);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     for (int s0 = 0; s0 < num_seqs; s0 += pkv::kTreeMaxSeqs) {
         p.S = num_seqs - s0 < pkv::kTreeMaxSeqs ? num_seqs - s0 : pkv::kTreeMaxSeqs;

@@ -115,6 +115,8 @@ struct Control {
     int skip[kGroups][2];            // by S: the weights are used up already
     int4 which[kGroups][2];          // by S: the worker's tile (-1: no more), segment, first token's place
                                      // among the drafted ones, tiles of the segment after it
+    pkv::TreeCut cuts[4];            // the workers' pieces of cut units
+    int last[kGroups];               // 1: the group counted its first unit's last piece
     uint32_t tmem;
 };
 
@@ -229,6 +231,7 @@ struct Producer {
     static constexpr int kRing = V ? C::kV : C::kK;
     const TreeParams &p;
     Rings &rings;
+    pkv::TreeCut *cuts;                                      // the worker's pieces
     uint32_t base;                                           // the ring
     int lane, pw;
     int32_t window, next_window;
@@ -279,8 +282,13 @@ struct Producer {
         Ring<kRing> r;
         for (int t = 0, seg = 0; t < count; ++seg) {
             const Segment x = segment(p, at, count - t);
-            if (!V && first_thread && !x.whole && x.i0 == 0)
-                p.cuts[share.me] = {pkv::tree_parts(share, share.A + t, at.tiles), at.q.o, x.g, x.r0, x.nr, {}};
+            if (!V && first_thread && !x.whole) {
+                pkv::TreeCut &c = cuts[x.i0 ? 0 : 1];
+                c = pkv::tree_cut(share, share.A + t - x.i0, at.tiles, at.q.o, x.g, x.r0, x.nr);
+                // pieces of units that began elsewhere are counted as soon as they are
+                // written, by each group that has rows of them: the others at the end
+                if (!x.i0) c.due = C::kTwo && x.nr > kRowTile ? 2 : 1;
+            }
             window = first;
             from = x.i0;
             next_window = x.n > kAhead ? entries(at.s, x.i0 + kAhead) : 0;
@@ -731,6 +739,17 @@ struct Softmax {
             if (it.w == 0) {
                 if (!wait_o(u)) return false;
                 if (live) finish(m, me, r0, nr);
+                if (!m.whole && m.slot == 0) {
+                    // a piece of a unit that began elsewhere, which that worker will join:
+                    // this one is hardly ever the last
+                    __threadfence();
+                    arrive(ctl.meet[w]);
+                    if (!wait(ctl.meet[w], met++)) return false;
+                    if (thread == 0) {
+                        pkv::TreeCut &c = ctl.cuts[C::kTwo ? 0 : 2 * w];
+                        if (c.count(p.count, 1, C::kTwo && m.nr > kRowTile ? 2 : 1)) ctl.last[w] = 1;
+                    }
+                }
             }
         }
     }
@@ -769,7 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
     }
     pkv::tc_fence_before();
     pkv::grid_dependency_wait();
-    if (tid < C::kWorkers) p.cuts[tid * gridDim.x + blockIdx.x].parts = 0;
+    if (tid < 4) ctl.cuts[tid].parts = ctl.cuts[tid].due = 0;
+    if (tid < kGroups) ctl.last[tid] = 0;
     int *prefix = reinterpret_cast<int *>(smem) + kThreads / 32;
     const int total = pkv::tree_tiles<kTile, kThreads>(p, prefix, reinterpret_cast<int *>(smem));
     // softmax warps, then by twos (worker or half of its copies): K, issue, V, q
@@ -790,13 +810,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
     } else {
         const int lane = tid & 31, part = C::kTwo ? which : 0;
         if (role == 0) {
-            Producer<D, ROWS, LB, false> pr{p, rings, base + C::kQ, lane, part, 0, 0, 0};
+            Producer<D, ROWS, LB, false> pr{p, rings, ctl.cuts + 2 * worker, base + C::kQ, lane, part, 0, 0, 0};
             pr.run(share, at);
         } else if (role == 1) {
             Issuer<T, D, ROWS> is{p, ctl, rings, base, tmem + 256 * which, which, share.Z - share.A};
             is.run();
         } else if (role == 2) {
-            Producer<D, ROWS, LB, true> pr{p, rings, base + C::kQ + C::kK * C::kSlot, lane, part, 0, 0, 0};
+            Producer<D, ROWS, LB, true> pr{p, rings, ctl.cuts + 2 * worker, base + C::kQ + C::kK * C::kSlot, lane, part, 0, 0, 0};
             pr.run(share, at);
         } else if (!C::kTwo || which == 0) {
             copy_q<D, ROWS>(p, rings, base, share, at);
@@ -809,6 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
         pkv::tc_fence_after();
         pkv::tmem_dealloc(tmem, kColumns);
     }
+    __syncthreads();
+    if (tid < C::kWorkers && !(C::kTwo ? ctl.last[0] | ctl.last[1] : ctl.last[tid])) ctl.cuts[2 * tid].parts = 0;
+    pkv::tree_join_cuts<D, kThreads / 32, 4, 4>(p, ctl.cuts);
 }
 
 template <typename T, int D, int ROWS, int LB>
