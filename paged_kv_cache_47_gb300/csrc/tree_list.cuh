@@ -147,7 +147,9 @@ __device__ __forceinline__ TreeShare tree_share(const TreeParams &p, const int *
     TreeShare r;
     r.me = me;
     r.NT = total;
-    r.CT = total < workers ? total : workers;
+    // two tiles each at least: half the pieces to join (one request of 1016 tokens
+    // with 16 drafted 17.0 us; one tile each 19.7, four 17.5)
+    r.CT = total < 2 * workers ? (total + 1) / 2 : workers;
     r.A = r.Z = 0;
     if (me < r.CT) {
         r.A = (int)((long long)me * total / r.CT);
