@@ -81,8 +81,9 @@ typedef struct {
 /* Bytes of workspace pkv_decode_attention_tree needs on the current device; 0
  * on invalid arguments. It must be zero-filled before its first use: it begins
  * with counters of the pieces that are to be joined (a region of one size,
- * whatever the call), which every call leaves zero. Calls that may overlap need
- * one each. */
+ * whatever the call), which every call leaves zero (but for one that sets
+ * PKV_DEVERR_TIMEOUT: zero the workspace again after it). Calls that may overlap
+ * need one each. */
 size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc *cache, int32_t num_q_heads,
                                        int32_t max_tree, int32_t num_ctas);
 

@@ -406,8 +406,9 @@ struct Issuer {
         while (tk < count || tv < count) {
             bool moved = false;
             while (od < up && ready(ctl.o[w][od & 1], od >> 1)) ++od;
-            // ---- S of the next tile: its columns are those of the last but one
-            if (tk < count && us < od + 2 && ready(rings.full_k[k.slot], k.turn)) {
+            // ---- S of the next tile: its columns are those of the last but one (a group
+            // without rows runs no further ahead than the tiles' records last)
+            if (tk < count && us < od + 2 && tk < tv + kMetas - C::kK && ready(rings.full_k[k.slot], k.turn)) {
                 const Tile &m = rings.tiles[tk % kMetas];
                 const bool none = C::kTwo && m.nr <= w * kRowTile;   // the unit has no rows for this group
                 if (pkv::elect_one()) {
@@ -698,7 +699,7 @@ struct Softmax {
             const int4 it = ctl.which[w][buf];
             const int t = it.x, d0 = it.z;
             if (t < 0) return true;
-            const Tile &m = rings.tiles[t % kMetas];         // (stays until the tile is done, and some tiles longer)
+            const Tile &m = rings.tiles[t % kMetas];         // stays until the weights are there
             if (it.y != seg) {
                 seg = it.y;
                 mu = kNone;
@@ -734,12 +735,14 @@ struct Softmax {
                 if (live && !weights<false>(at, m, i, d0, u)) return false;
             }
             if (thread == 0) ctl.skip[w][buf] = odd;
+            Tile end;
+            if (it.w == 0) end = m;
             arrive(ctl.p[w][buf]);
             have_o = true;
             if (it.w == 0) {
                 if (!wait_o(u)) return false;
-                if (live) finish(m, me, r0, nr);
-                if (!m.whole && m.slot == 0) {
+                if (live) finish(end, me, r0, nr);
+                if (!end.whole && end.slot == 0) {
                     // a piece of a unit that began elsewhere, which that worker will join:
                     // this one is hardly ever the last
                     __threadfence();
@@ -747,7 +750,7 @@ struct Softmax {
                     if (!wait(ctl.meet[w], met++)) return false;
                     if (thread == 0) {
                         pkv::TreeCut &c = ctl.cuts[C::kTwo ? 0 : 2 * w];
-                        if (c.count(p.count, 1, C::kTwo && m.nr > kRowTile ? 2 : 1)) ctl.last[w] = 1;
+                        if (c.count(p.count, 1, C::kTwo && end.nr > kRowTile ? 2 : 1)) ctl.last[w] = 1;
                     }
                 }
             }

@@ -380,3 +380,66 @@ def test_back_to_back_steps_on_one_cache():
         b.append(new[i], new[i + 1], slots, k, v)
         call()
         x.check(out)
+
+
+COUNTERS = 32768                       # bytes of counters, at the workspace's start
+
+
+def test_one_workspace_for_calls_of_all_shapes():
+    # the counters' region is one size, whatever the call, and every call leaves it zero
+    xs = [(Batch([900, 40, 0], [12, 7, 1], G=4, dt="bf16", seed=1), 0), (Batch([700, 90], [30, 60], G=8, Hk=1, dt="f16", seed=2), 3),
+          (Batch([500, 3], [9, 4], G=4, dt="f32", seed=3), 0), (Batch([3000], [16], G=20, D=64, dt="bf16", seed=4), 600)]
+    ws = torch.zeros(max(b.tree_workspace_bytes(x.k, x.Hq, int(x.n.max()), c) for x, c in xs), dtype=torch.uint8, device="cuda")
+    refs = [x.run(num_ctas=c) for x, c in xs]
+    for _ in range(3):
+        for (x, c), ref in zip(xs, refs):
+            assert torch.equal(x.run(num_ctas=c, workspace=ws), ref)
+            assert not ws[:COUNTERS].any()
+    # two captured graphs of one workspace, replayed in turn
+    outs, graphs = [torch.zeros_like(r) for r in refs[:2]], []
+    for (x, c), o in zip(xs, outs):
+        call = b.prepared_decode_attention_tree(*x.args(), max_tree=int(x.n.max()), out=o, workspace=ws, num_ctas=c)
+        graphs.append((torch.cuda.CUDAGraph(), call))
+        with torch.cuda.graph(graphs[-1][0]):
+            call()
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g, _call in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, r) for o, r in zip(outs, refs))
+    assert not ws[:COUNTERS].any() and b.get_error() == 0
+
+
+@pytest.mark.parametrize("G", [4, 20])
+def test_workspace_of_a_call_whose_wait_ran_out(G):
+    x = Batch([900, 40], [12, 7], G=G, dt="f16", seed=9)
+    ws = b.alloc_tree_workspace(x.k, x.Hq, 12)
+    ref = x.run()
+    b.set_wait_fault(2_000_000, 1)
+    x.run(workspace=ws)
+    status, word = b.get_error_status()
+    b.set_wait_fault(0, 0)
+    assert status == -5 and word & b.DEVERR_TIMEOUT
+    ws[:COUNTERS].zero_()                                  # as the interface asks for
+    for _ in range(2):
+        assert torch.equal(x.run(workspace=ws), ref)
+        assert not ws[:COUNTERS].any()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("ctas", [1, 2, 5])
+def test_large_and_small_units_by_turns(ctas, D, dt):
+    # units of two row tiles and of one follow each other in a worker's share: one group runs ahead of the other
+    rng = np.random.default_rng(ctas)
+    n = np.where(np.arange(90) % 3 == 0, rng.integers(33, 65, 90), rng.integers(1, 9, 90))
+    P = rng.integers(0, 200, 90)
+    P[1::9] = 1500
+    for B in (8, 32):
+        x = Batch(P, n, G=4, Hk=1, D=D, B=B, dt=dt, seed=ctas)
+        ref = x.run(num_ctas=ctas)
+        x.check(ref)
+        assert torch.equal(x.run(num_ctas=ctas), ref)
+    assert b.get_error() == 0
