@@ -102,7 +102,8 @@ size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc *cache, int32_t num_
  * [head_dim], q and the pools in the cache's dtype and 16-byte aligned, out
  * 32-byte aligned. max_tree: drafted tokens of a sequence at
  * most, 1..PKV_TREE_MAX_TOKENS (and 64 * mask_words with masks); it sizes the
- * work, so a bound near the truth is best. Block ids outside the pool set
+ * work, so a bound near the truth is best (and so is a table's width: trees of more
+ * than 128 rows a kv head are cut up by it). Block ids outside the pool set
  * PKV_DEVERR_BLOCK_ID and read as zeros. workspace: 32-byte aligned, at least
  * pkv_decode_tree_workspace_bytes. options: NULL for the defaults.
  */

@@ -195,34 +195,40 @@ cudaError_t launch(int dtype, const TreeParams &p, cudaStream_t stream) {
                               : pkv::launch_tree_bf16(D, p, stream);
 }
 
-// Rows of a unit, tokens of a tile, and workers of a launch.
+// Rows of a unit and workers of a launch.
 struct Shape {
-    int rows, tile, workers;
+    int rows, workers;
 };
-Shape shape_of(const pkv_cache_desc *c, int Hq, int max_tree) {
-    if (c->dtype == PKV_F32) return {kRows, kTile, 0};
-    // what the largest tree needs, up to two row tiles: they share each tile of K
-    // and V, which more rows would read again
-    const int64_t rows = (int64_t)max_tree * (Hq / c->num_kv_heads), most = 2 * pkv::kTreeMmaRows;
-    return {(int)(rows < most ? rows : most), pkv::kTreeMmaTile, 0};
+// Tables of fewer tokens: units of one row tile at most. Two row tiles share each
+// tile of K and V, which units of one read again; but their joins are twice as long
+// and a CTA has one worker instead of two that fill each other's gaps. 256 and 128
+// rows: one request of 1000 tokens with 64 drafted 66 and 46 us, 32 of 512 to 4096
+// tokens with 33 to 64 drafted 156 and 137, 8 of 4000 (32 drafted, 8 q heads a kv
+// head) 74 and 77, of 8000 107 and 115, of 32000 300 and 345; 32 of 8000 311 and 359.
+constexpr int kTwoRowTiles = 4096 + PKV_TREE_MAX_TOKENS;
+Shape shape_of(const pkv_cache_desc *c, int Hq, int max_tree, int64_t capacity, int ctas) {
+    if (c->dtype == PKV_F32) return {kRows, ctas};
+    const int64_t rows = (int64_t)max_tree * (Hq / c->num_kv_heads), one = pkv::kTreeMmaRows;
+    const int64_t most = capacity > kTwoRowTiles ? 2 * one : one;
+    // (one row tile: two workers a CTA, at most 2 PKV_MAX_DECODE_CTAS counters)
+    return {(int)(rows < most ? rows : most), rows > one && most > one ? ctas : 2 * ctas};
 }
-pkv_status workers_of(const pkv_cache_desc *c, int ctas, Shape *s) {
-    if (ctas == 0) {
-        const pkv_status st = pkv::device_sm_count(&ctas);
-        if (st != PKV_OK) return st;
-        if (c->dtype == PKV_F32) ctas *= kCtasPerSm;
-    }
-    // 16-bit units of one row tile: two workers a CTA (at most 2 PKV_MAX_DECODE_CTAS counters)
-    if (ctas > PKV_MAX_DECODE_CTAS) ctas = PKV_MAX_DECODE_CTAS;
-    s->workers = ctas * (c->dtype != PKV_F32 && s->rows <= pkv::kTreeMmaRows ? 2 : 1);
+pkv_status ctas_of(const pkv_cache_desc *c, int *ctas) {
+    if (*ctas) return PKV_OK;
+    const pkv_status st = pkv::device_sm_count(ctas);
+    if (st != PKV_OK) return st;
+    if (c->dtype == PKV_F32) *ctas *= kCtasPerSm;
+    if (*ctas > PKV_MAX_DECODE_CTAS) *ctas = PKV_MAX_DECODE_CTAS;
     return PKV_OK;
 }
 
 // workspace: counters (a fixed region, whatever the launch), then [workers][2]
-// pieces of rows and their denominators
+// pieces of rows and their denominators; as much for one worker of two row tiles as
+// for two of one, as it does not depend on the table's width
 constexpr size_t kCounterBytes = 2 * PKV_MAX_DECODE_CTAS * sizeof(unsigned);
-size_t workspace_for(const Shape &s, int D) {
-    return kCounterBytes + (size_t)s.workers * 2 * s.rows * (D + 1) * sizeof(float);
+size_t workspace_for(const pkv_cache_desc *c, int Hq, int max_tree, int ctas) {
+    const Shape s = shape_of(c, Hq, max_tree, 0, ctas);
+    return kCounterBytes + (size_t)s.workers * 2 * s.rows * (c->head_dim + 1) * sizeof(float);
 }
 
 pkv_status check_shape(const pkv_cache_desc *cache, int Hq, int max_tree, int ctas) {
@@ -249,9 +255,9 @@ extern "C" {
 size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc *cache, int32_t num_q_heads,
                                        int32_t max_tree, int32_t num_ctas) {
     if (check_shape(cache, num_q_heads, max_tree, num_ctas) != PKV_OK) return 0;
-    Shape s = shape_of(cache, num_q_heads, max_tree);
-    if (workers_of(cache, num_ctas, &s) != PKV_OK) return 0;
-    return workspace_for(s, cache->head_dim);
+    int ctas = num_ctas;
+    if (ctas_of(cache, &ctas) != PKV_OK) return 0;
+    return workspace_for(cache, num_q_heads, max_tree, ctas);
 }
 
 pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
@@ -285,17 +291,19 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
         misaligned(masks, 8) || (options && misaligned(options->lse_out, 4)))
         return pkv::set_last_error(PKV_ERR_INVALID_ARG,
                                    "q and the pools must be 16-byte aligned, out 32-byte aligned, the others to their elements");
-    Shape shape = shape_of(cache, num_q_heads, max_tree);
-    const int G = num_q_heads / Hk, RC = shape.rows;
+    const int64_t capacity = (int64_t)M * cache->block_size;
+    const int G = num_q_heads / Hk, RC = shape_of(cache, num_q_heads, max_tree, capacity, 1).rows;
+    const int tile = cache->dtype == PKV_F32 ? kTile : pkv::kTreeMmaTile;
     // the list's places fit 32 bits
-    const int64_t capacity = (int64_t)M * cache->block_size, seqs = num_seqs < pkv::kTreeMaxSeqs ? num_seqs : pkv::kTreeMaxSeqs;
+    const int64_t seqs = num_seqs < pkv::kTreeMaxSeqs ? num_seqs : pkv::kTreeMaxSeqs;
     const int64_t units = (int64_t)Hk * (((int64_t)max_tree * G + RC - 1) / RC);
-    if (capacity > INT32_MAX / 2 || seqs * units * ((capacity + shape.tile - 1) / shape.tile) >= (int64_t)INT32_MAX)
+    if (capacity > INT32_MAX / 2 || seqs * units * ((capacity + tile - 1) / tile) >= (int64_t)INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "batch x context too large for one launch");
     if ((int64_t)cache->num_blocks * Hk > INT32_MAX)
         return pkv::set_last_error(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is 2^31 or more");
-    if ((st = workers_of(cache, asked, &shape)) != PKV_OK) return st;
-    const size_t need = workspace_for(shape, D);
+    int ctas = asked;
+    if ((st = ctas_of(cache, &ctas)) != PKV_OK) return st;
+    const size_t need = workspace_for(cache, num_q_heads, max_tree, ctas);
     if (!workspace || workspace_bytes < need)
         return pkv::set_last_error(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                                    workspace ? workspace_bytes : (size_t)0);
@@ -322,7 +330,7 @@ pkv_status pkv_decode_attention_tree(const pkv_cache_desc *cache, const void *q,
     p.Hq = num_q_heads;
     p.G = G;
     p.RC = RC;
-    p.C = shape.workers;
+    p.C = shape_of(cache, num_q_heads, max_tree, capacity, ctas).workers;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.count = static_cast<unsigned *>(workspace);
     p.ws_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);

@@ -443,3 +443,37 @@ def test_large_and_small_units_by_turns(ctas, D, dt):
         x.check(ref)
         assert torch.equal(x.run(num_ctas=ctas), ref)
     assert b.get_error() == 0
+
+
+class WideTable(Batch):
+    """The same with tables far wider than the contexts: units may have two row tiles."""
+
+    def __init__(self, *a, **kw):
+        super().__init__(*a, **kw)
+        spare = 4608 // self.B
+        self.M += spare
+        self.tab = np.pad(self.tab, ((0, 0), (0, spare)), constant_values=-1)
+
+
+@pytest.mark.parametrize("what, args", [(test_matches_64_bits, (s, D, dt)) for s in (5, 6, 7, 8) for D in (64, 128) for dt in ("f16", "bf16")]
+                         + [(test_any_split, (c, "bf16")) for c in (1, 3, 40, 151, 600)]
+                         + [(test_bound_far_above_the_tokens_and_wide_masks, ())]
+                         + [(test_rows_that_see_nothing_and_any_masks, (dt,)) for dt in ("f16", "bf16")]
+                         + [(test_hidden_infinities_and_nans_reach_nobody, (D, dt, w)) for D, dt, w in
+                            ((128, "f16", math.inf), (128, "bf16", math.nan), (64, "bf16", -math.inf), (64, "f16", math.nan))]
+                         + [(test_large_scores_and_growing_maxima, ()), (test_bad_block_ids_read_as_zeros, ("f16",)),
+                            (test_any_scale, ("bf16", -0.11)), (test_a_wait_that_runs_out, (20,)),
+                            (test_workspace_of_a_call_whose_wait_ran_out, (20,)), (test_one_workspace_for_calls_of_all_shapes, ())]
+                         + [(test_many_rows_a_kv_head, (dt,)) for dt in ("f16", "bf16")]
+                         + [(test_large_and_small_units_by_turns, (c, D, "bf16")) for c in (1, 2, 5) for D in (64, 128)])
+def test_wide_tables(monkeypatch, what, args):
+    monkeypatch.setitem(globals(), "Batch", WideTable)
+    what(*args)
+
+
+def test_one_workspace_for_any_width_of_table():
+    for x in (Batch([700, 90], [40, 60], G=4), WideTable([700, 90], [40, 60], G=4)):
+        ws = b.alloc_tree_workspace(x.k, x.Hq, 60)
+        for _ in range(2):
+            x.check(x.run(workspace=ws))
+    assert not ws[:COUNTERS].any() and b.get_error() == 0
