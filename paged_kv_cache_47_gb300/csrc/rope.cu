@@ -17,6 +17,11 @@
 // of 40 q and 40 kv heads of 128 with the append (fp16, 503 MB in all) take
 // 74.5 us, 6.75 TB/s. A step of 64 tokens is a launch and two dependent loads:
 // 4.3 us, the host's call, and 2.5 replayed as a graph.
+//
+// Positions of several axes are a template argument: a pair's thread looks its axis
+// up in the plan (a byte in constant memory) and loads that axis's position; the
+// rest is the same. The same 8191 tokens with three axes take 76.0 us (0.98 of a
+// copy), 1024 tokens of 32 q and 8 kv heads 7.3 (host's call; 6.8 as a graph).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

