@@ -1440,8 +1440,8 @@ def tree_workspace_bytes(k_pool, num_q_heads: int, max_tree: int, num_ctas: int 
 
 
 def alloc_tree_workspace(k_pool, num_q_heads: int, max_tree: int, num_ctas: int = 0) -> torch.Tensor:
-    """Zero-filled workspace of decode_attention_tree, which every call leaves fit for the next (after
-    DEVERR_TIMEOUT it has to be zeroed again); calls that may overlap need one each."""
+    """Workspace of decode_attention_tree, zeroed on the current stream. Every call leaves it fit for the
+    next (after DEVERR_TIMEOUT it has to be zeroed again); calls that may overlap need one each."""
     n = tree_workspace_bytes(k_pool, num_q_heads, max_tree, num_ctas)
     if n == 0:
         raise PkvError(-1, lib().pkv_last_error_message().decode())

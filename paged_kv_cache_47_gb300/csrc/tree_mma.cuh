@@ -33,12 +33,12 @@
 // What bounds it. Up to 128 rows: a group's softmax, 1900 cycles a tile of 64 tokens
 // of 128 elements, and the memory, which gives a worker a tile in 2860, with 5 to 8
 // us of list and first copies before and 8 of pieces and joins behind. 64 requests
-// of 512 to 4096 tokens, 16 drafted, 32 q and 8 kv heads, bf16: 115 to 121
-// us, 5.2 to 5.4 TB/s (0.79 of a copy); 128 of 128 to 2048, one q head a kv head,
-// fp16: 503 to 562 us, 5.1 to 5.7 TB/s. 256 rows: softmax (1700), products (1800) and shared memory (1500)
-// all near one another, 2500 measured, and the power limit: 8 contexts of 32768 to
-// 131072 tokens, up to 26 drafted, 8 q heads a kv head, bf16: 655 to 732 us, 0.61 to
-// 0.69 PFLOP/s, 0.92 to 1.03 with the weights' low parts.
+// of 512 to 4096 tokens, 16 drafted, 32 q and 8 kv heads, bf16: 115 to 121 us, 5.2
+// to 5.4 TB/s (0.76 to 0.80 of a copy); 128 of 128 to 2048, one q head a kv head,
+// fp16: 503 to 562 us, 5.1 to 5.7 TB/s. 256 rows: softmax (1700), products (1800) and
+// shared memory (1500) near one another, 2500 measured, and the power limit: 8
+// contexts of 32768 to 131072 tokens, up to 26 drafted, 8 q heads a kv head, bf16:
+// 655 to 732 us, 0.61 to 0.69 PFLOP/s, 0.92 to 1.03 with the weights' low parts.
 //
 // Barriers. Each is waited for phase after phase by the same role, and no phase
 // can complete before the one waited for has been seen: a parity names it.
